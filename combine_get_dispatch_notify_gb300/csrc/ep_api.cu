@@ -1,5 +1,6 @@
 // C ABI of libep_gb300.so (declared in include/ep.h): argument checks on the
 // host, then one launch per step on the caller's stream.
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 #include <cuda_runtime.h>
@@ -184,6 +185,41 @@ bool array_ok(const void* p, long long n, unsigned align) {
 
 ep_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
 
+bool make_route(const Shape& sh, const ep_route_t* r, RouteCfg* out) {
+    if (r == nullptr) return false;
+    if (r->score < 0 || r->score > 1 || r->renormalize < 0 || r->renormalize > 1) return false;
+    if (r->num_groups < 1 || r->num_groups > 32 || sh.E % r->num_groups != 0) return false;
+    if (r->topk_groups < 1 || r->topk_groups > r->num_groups) return false;
+    const int per_group = sh.E / r->num_groups;
+    if (r->group_top < 1 || r->group_top > 2 || r->group_top > per_group) return false;
+    if (sh.K > static_cast<long long>(r->topk_groups) * per_group || !std::isfinite(r->scale)) return false;
+    *out = RouteCfg{r->score, r->num_groups, r->topk_groups, r->group_top, r->renormalize, r->scale};
+    return true;
+}
+
+bool gemm_shape_ok(const ep_gemm_shape_t* s, int n_multiple) {
+    if (s == nullptr) return false;
+    return s->num_experts >= 1 && s->num_experts <= 8192 && s->capacity >= 0 && s->capacity <= (1 << 24) &&
+           s->n >= n_multiple && s->n % n_multiple == 0 && s->n <= (1 << 20) && s->k >= 16 && s->k % 16 == 0 &&
+           s->k <= (1 << 20);
+}
+
+// Checks shared by the two products; `halves` is 2 when w holds a gate and an up matrix.
+ep_status_t ll_gemm(const ep_gemm_shape_t* s, int halves, const uint8_t* a, const float* a_scales, const uint8_t* w,
+                    const float* w_scales, const int32_t* count, void* y, float* y_scales, int32_t* status,
+                    cudaStream_t stream) {
+    if (!gemm_shape_ok(s, halves == 2 ? 16 : 8)) return EP_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(s->num_experts) * s->capacity;
+    if (!array_ok(a, rows, 16) || !array_ok(a_scales, rows, 16) || !aligned16(w) || !aligned16(w_scales) ||
+        !aligned4(count) || !array_ok(y, rows, 16) || (halves == 2 && !array_ok(y_scales, rows, 16)) ||
+        !aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (rows == 0) return EP_OK;
+    GemmArgs g = {s->num_experts, s->capacity, s->n, s->k, a, a_scales, w, w_scales, count, y,
+                  halves == 2 ? y_scales : nullptr, status};
+    return from_cuda(launch_ll_gemm_fp8(g, stream));
+}
+
 ep_status_t notify_common(const ep_shape_t* shape, const uint8_t* is_token_in_rank,
                           const int32_t* num_tokens_per_rank, const int32_t* num_tokens_per_rdma_rank,
                           const int32_t* num_tokens_per_expert, int32_t* rank_prefix_matrix,
@@ -304,7 +340,7 @@ const char* ep_status_string(ep_status_t status) {
         case EP_ERR_CAPACITY: return "receive capacity exceeded";
         case EP_ERR_TIMEOUT: return "device wait timed out";
         case EP_ERR_INCONSISTENT: return "count inputs disagree with is_token_in_rank";
-        case EP_ERR_INPUT: return "expert id outside [-1, num_experts)";
+        case EP_ERR_INPUT: return "expert id outside [-1, num_experts) or NaN router score";
     }
     return "unknown status";
 }
@@ -729,6 +765,76 @@ ep_status_t ep_ll_combine(const ep_shape_t* shape, const uint16_t* y, int32_t ex
         return EP_ERR_INVALID_ARG;
     return ep::from_cuda(ep::launch_ll_combine(sh, y, expert_capacity, topk_idx, topk_w, slot_pos, combined_x,
                                                status, stream));
+}
+
+ep_status_t ep_check_route(const ep_shape_t* shape, const ep_route_t* route) {
+    ep::Shape sh;
+    ep::RouteCfg rc;
+    return ep::make_shape(shape, &sh) && ep::make_route(sh, route, &rc) ? EP_OK : EP_ERR_INVALID_ARG;
+}
+
+ep_status_t ep_route(const ep_shape_t* shape, const ep_route_t* route, const void* logits, int32_t logits_bf16,
+                     const float* bias, int64_t* topk_idx, float* topk_w, int32_t* status, cudaStream_t stream) {
+    ep::Shape sh;
+    ep::RouteCfg rc;
+    if (!ep::make_shape(shape, &sh) || !ep::make_route(sh, route, &rc)) return EP_ERR_INVALID_ARG;
+    if (logits_bf16 < 0 || logits_bf16 > 1) return EP_ERR_INVALID_ARG;
+    const long long tokens = static_cast<long long>(sh.R) * sh.T;
+    if (!ep::array_ok(logits, tokens, 16) || (bias != nullptr && !ep::aligned16(bias)) ||
+        !ep::array_ok(topk_idx, tokens, 16) || !ep::array_ok(topk_w, tokens, 16) || !ep::aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (tokens == 0) return EP_OK;
+    return ep::from_cuda(
+        ep::launch_route(sh, rc, logits, logits_bf16 != 0, bias, topk_idx, topk_w, status, stream));
+}
+
+ep_status_t ep_route_backward(const ep_shape_t* shape, const ep_route_t* route, const void* logits,
+                              int32_t logits_bf16, const int64_t* topk_idx, const float* grad_topk_w,
+                              void* grad_logits, int32_t* status, cudaStream_t stream) {
+    ep::Shape sh;
+    ep::RouteCfg rc;
+    if (!ep::make_shape(shape, &sh) || !ep::make_route(sh, route, &rc)) return EP_ERR_INVALID_ARG;
+    if (logits_bf16 < 0 || logits_bf16 > 1) return EP_ERR_INVALID_ARG;
+    const long long tokens = static_cast<long long>(sh.R) * sh.T;
+    if (!ep::array_ok(logits, tokens, 16) || !ep::array_ok(topk_idx, tokens, 16) ||
+        !ep::array_ok(grad_topk_w, tokens, 16) || !ep::array_ok(grad_logits, tokens, 16) || !ep::aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (tokens == 0) return EP_OK;
+    return ep::from_cuda(ep::launch_route_backward(sh, rc, logits, logits_bf16 != 0, topk_idx, grad_topk_w,
+                                                   grad_logits, status, stream));
+}
+
+ep_status_t ep_ll_dispatch_fp8(const ep_shape_t* shape, const uint16_t* x, const int64_t* topk_idx,
+                               const int32_t* slot_pos, int32_t expert_capacity, uint8_t* recv_x,
+                               float* recv_x_scales, int32_t* recv_src_info, int32_t* status,
+                               cudaStream_t stream) {
+    ep::Shape sh;
+    if (!ep::make_shape(shape, &sh) || expert_capacity < 0 || sh.H % 16 != 0) return EP_ERR_INVALID_ARG;
+    const long long tokens = static_cast<long long>(sh.R) * sh.T;
+    const long long rows = static_cast<long long>(sh.E) * expert_capacity;
+    if (!ep::array_ok(x, tokens, 16) || !ep::array_ok(topk_idx, tokens, 8) || !ep::array_ok(slot_pos, tokens, 4) ||
+        !ep::array_ok(recv_x, rows, 16) || !ep::array_ok(recv_x_scales, rows, 16) ||
+        (recv_src_info != nullptr && !ep::aligned8(recv_src_info)) || !ep::aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (tokens == 0 || rows == 0) return EP_OK;
+    return ep::from_cuda(ep::launch_ll_dispatch_fp8(sh, x, topk_idx, slot_pos, expert_capacity, recv_x,
+                                                    recv_x_scales, recv_src_info, status, stream));
+}
+
+ep_status_t ep_check_gemm_shape(const ep_gemm_shape_t* shape) {
+    return ep::gemm_shape_ok(shape, 8) ? EP_OK : EP_ERR_INVALID_ARG;
+}
+
+ep_status_t ep_ll_gemm_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales, const uint8_t* w,
+                           const float* w_scales, const int32_t* count, uint16_t* y, int32_t* status,
+                           cudaStream_t stream) {
+    return ep::ll_gemm(shape, 1, a, a_scales, w, w_scales, count, y, nullptr, status, stream);
+}
+
+ep_status_t ep_ll_gemm_swiglu_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales,
+                                  const uint8_t* w, const float* w_scales, const int32_t* count, uint8_t* y,
+                                  float* y_scales, int32_t* status, cudaStream_t stream) {
+    return ep::ll_gemm(shape, 2, a, a_scales, w, w_scales, count, y, y_scales, status, stream);
 }
 
 ep_status_t ep_sync_status(const int32_t* status, cudaStream_t stream) {

@@ -148,4 +148,36 @@ cudaError_t launch_ll_combine(const Shape& sh, const uint16_t* y, int cap, const
                               const float* topk_w, const int32_t* slot_pos, uint16_t* combined_x,
                               int32_t* status, cudaStream_t stream);
 
+// Router (see ep_route): score 0 softmax, 1 sigmoid.
+struct RouteCfg {
+    int score, G, topk_groups, group_top, renorm;
+    float scale;
+};
+cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits, bool bf16, const float* bias,
+                         int64_t* topk_idx, float* topk_w, int32_t* status, cudaStream_t stream);
+cudaError_t launch_route_backward(const Shape& sh, const RouteCfg& rc, const void* logits, bool bf16,
+                                  const int64_t* topk_idx, const float* grad_topk_w, void* grad_logits,
+                                  int32_t* status, cudaStream_t stream);
+
+// LL dispatch with the rows cast to e4m3 on the way (H % 16 == 0).
+cudaError_t launch_ll_dispatch_fp8(const Shape& sh, const uint16_t* x, const int64_t* topk_idx,
+                                   const int32_t* slot_pos, int cap, uint8_t* recv_x, float* recv_x_scales,
+                                   int32_t* recv_src_info, int32_t* status, cudaStream_t stream);
+
+// Block-scaled e4m3 products of the experts' rows.  y_scales == NULL: y is
+// bf16 [E][cap][n] = the product; else w holds the gate and the up matrix and
+// y / y_scales are the gated activation cast to e4m3.
+struct GemmArgs {
+    int E, cap, n, k;
+    const uint8_t* a;
+    const float* a_scales;
+    const uint8_t* w;
+    const float* w_scales;
+    const int32_t* count;
+    void* y;
+    float* y_scales;
+    int32_t* status;
+};
+cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream);
+
 }  // namespace ep

@@ -1,0 +1,133 @@
+// Low-latency dispatch that casts its rows to e4m3 (ep_ll_dispatch_fp8): a
+// warp reads one slice of a token, casts it once and writes it to each of the
+// token's slots.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ep.h"
+#include "ep_device.cuh"
+#include "ep_internal.h"
+#include "fp8_cast.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kLaneCols = 16;                 // columns of one lane: 32 B in, 16 B out
+constexpr int kPass = kWarp * kLaneCols;      // 512 columns, 4 scale blocks
+constexpr int kPasses = 2;                    // passes of a unit, loads in flight together
+constexpr int kSlice = kPass * kPasses;       // 1024 columns, 8 scales: a 32-byte sector
+
+struct Args {
+    const uint16_t* x;
+    const int64_t* topk_idx;
+    const int32_t* slot_pos;
+    uint8_t* recv_x;
+    float* recv_scales;
+    int32_t* src_info;
+    long long units;  // tokens * slices
+    int slices, T, K, E, H, cap, blocks;
+};
+
+__global__ void __launch_bounds__(kWarps* kWarp) ll_dispatch_fp8_kernel(const Args p) {
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    griddep_launch_dependents();
+    griddep_wait();  // x, the ids and the row map are complete from here on
+    for (long long u = static_cast<long long>(blockIdx.x) * kWarps + warp; u < p.units;
+         u += static_cast<long long>(gridDim.x) * kWarps) {
+        const long long t = u / p.slices;
+        const int slice = static_cast<int>(u - t * p.slices);
+        uint4 v[kPasses][2];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int col = slice * kSlice + i * kPass + lane * kLaneCols;
+            v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+            if (col < p.H) {
+                v[i][0] = ld_nc_v4(p.x + t * p.H + col);
+                v[i][1] = ld_nc_v4(p.x + t * p.H + col + 8);
+            }
+        }
+        long long row = -1;  // lane k holds slot k's row
+        if (lane < p.K) {
+            const long long e = __ldg(p.topk_idx + t * p.K + lane);
+            const int pos = __ldg(p.slot_pos + t * p.K + lane);
+            if (e >= 0 && e < p.E && pos >= 0 && pos < p.cap) row = e * p.cap + pos;
+        }
+        uint4 q[kPasses];
+        float scale[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            float f[kLaneCols];
+            const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
+                                   v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f[2 * j] = __uint_as_float(w[j] << 16);
+                f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                amax = fmaxf(amax, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+            }
+            // eight neighbouring lanes hold one block of 128 columns
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+            scale[i] = block_scale(amax);
+#pragma unroll
+            for (int j = 0; j < kLaneCols; ++j) f[j] /= scale[i];
+            q[i].x = pack_e4m3x4(f[0], f[1], f[2], f[3]);
+            q[i].y = pack_e4m3x4(f[4], f[5], f[6], f[7]);
+            q[i].z = pack_e4m3x4(f[8], f[9], f[10], f[11]);
+            q[i].w = pack_e4m3x4(f[12], f[13], f[14], f[15]);
+        }
+        // lane j < 8 gathers the scale of the slice's block j
+        const float s0 = __shfl_sync(0xffffffffu, scale[0], (lane & 3) * 8);
+        const float s1 = __shfl_sync(0xffffffffu, scale[1], (lane & 3) * 8);
+        const float s = lane < 4 ? s0 : s1;
+        const int block = slice * (kSlice / kScaleBlock) + lane;
+        for (int k = 0; k < p.K; ++k) {
+            const long long r = __shfl_sync(0xffffffffu, row, k);
+            if (r < 0) continue;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int col = slice * kSlice + i * kPass + lane * kLaneCols;
+                if (col < p.H) st_v4(p.recv_x + r * p.H + col, q[i]);
+            }
+            if (lane < kSlice / kScaleBlock && block < p.blocks) p.recv_scales[r * p.blocks + block] = s;
+        }
+        if (slice == 0 && row >= 0 && p.src_info != nullptr)
+            reinterpret_cast<int2*>(p.src_info)[row] =
+                make_int2(static_cast<int>(t / p.T), static_cast<int>(t % p.T));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_ll_dispatch_fp8(const Shape& sh, const uint16_t* x, const int64_t* topk_idx,
+                                   const int32_t* slot_pos, int cap, uint8_t* recv_x, float* recv_x_scales,
+                                   int32_t* recv_src_info, int32_t* status, cudaStream_t stream) {
+    (void)status;  // nothing of this call can fail on the device
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    Args p = {};
+    p.x = x;
+    p.topk_idx = topk_idx;
+    p.slot_pos = slot_pos;
+    p.recv_x = recv_x;
+    p.recv_scales = recv_x_scales;
+    p.src_info = recv_src_info;
+    p.T = sh.T;
+    p.K = sh.K;
+    p.E = sh.E;
+    p.H = sh.H;
+    p.cap = cap;
+    p.blocks = scale_blocks(sh.H);
+    p.slices = (sh.H + kSlice - 1) / kSlice;
+    p.units = static_cast<long long>(sh.R) * sh.T * p.slices;
+    const long long want = (p.units + kWarps - 1) / kWarps;
+    const long long most = sms * 8LL;
+    return launch_pdl(ll_dispatch_fp8_kernel, dim3(static_cast<unsigned>(want < most ? want : most)),
+                      dim3(kWarps * kWarp), 0, stream, 0, false, p);
+}
+
+}  // namespace ep

@@ -58,6 +58,27 @@ class EpShape(ctypes.Structure):
         return self.num_experts // self.num_ranks
 
 
+class EpRoute(ctypes.Structure):
+    """Mirror of ep_route_t: how ep_route scores and selects experts."""
+
+    _fields_ = [("score", _i32), ("num_groups", _i32), ("topk_groups", _i32), ("group_top", _i32),
+                ("renormalize", _i32), ("scale", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, score="softmax", num_groups=1, topk_groups=1, group_top=1, renormalize=True,
+             scale=1.0) -> "EpRoute":
+        """``score`` is "softmax" or "sigmoid"."""
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+        return cls(int(score == "sigmoid"), num_groups, topk_groups, group_top, int(bool(renormalize)), scale)
+
+
+class EpGemmShape(ctypes.Structure):
+    """Mirror of ep_gemm_shape_t."""
+
+    _fields_ = [("num_experts", _i32), ("capacity", _i32), ("n", _i32), ("k", _i32)]
+
+
 class EpError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -88,6 +109,13 @@ _SIGS = {
     "ep_ll_layout": (_i32, [ctypes.POINTER(EpShape), _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
     "ep_ll_dispatch": (_i32, [ctypes.POINTER(EpShape), _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
     "ep_ll_combine": (_i32, [ctypes.POINTER(EpShape), _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "ep_check_route": (_i32, [ctypes.POINTER(EpShape), ctypes.POINTER(EpRoute)]),
+    "ep_route": (_i32, [ctypes.POINTER(EpShape), ctypes.POINTER(EpRoute), _vp, _i32] + [_vp] * 4 + [_vp]),
+    "ep_route_backward": (_i32, [ctypes.POINTER(EpShape), ctypes.POINTER(EpRoute), _vp, _i32] + [_vp] * 4 + [_vp]),
+    "ep_ll_dispatch_fp8": (_i32, [ctypes.POINTER(EpShape), _vp, _vp, _vp, _i32] + [_vp] * 4 + [_vp]),
+    "ep_check_gemm_shape": (_i32, [ctypes.POINTER(EpGemmShape)]),
+    "ep_ll_gemm_fp8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 7 + [_vp]),
+    "ep_ll_gemm_swiglu_fp8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_vp]),
     "ep_sync_status": (_i32, [_vp, _vp]),
     "ep_debug_notify_dispatch_stall": (_i32, [ctypes.POINTER(EpShape)] + [_vp] * 16 +
                                        [_sz, _vp, _i32, _i32, _vp]),
@@ -497,6 +525,103 @@ def ep_ll_combine(shape: EpShape, y, expert_capacity: int, topk_idx, topk_w, slo
         _t(slot_pos, torch.int32, (R, T, K), "slot_pos"), _t(combined_x, torch.bfloat16, (R, T, H), "combined_x"),
         _t(status, torch.int32, (1,), "status"), _stream(stream))
     _check("ep_ll_combine", rc)
+
+
+def ep_check_route(shape: EpShape, route: EpRoute) -> int:
+    return lib().ep_check_route(ctypes.byref(shape), ctypes.byref(route))
+
+
+def _logits(logits, shape: EpShape, name="logits"):
+    if logits is not None and logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    dtype = torch.float32 if logits is None else logits.dtype
+    return _t(logits, dtype, (shape.num_ranks, shape.num_tokens, shape.num_experts), name), dtype
+
+
+def ep_route(shape: EpShape, route: EpRoute, logits, bias, topk_idx, topk_w, status, stream=None) -> None:
+    """Router: ``logits`` [R, T, E] (fp32 or bf16) to the top-k map and weights the other
+    calls take; ``bias`` [E] fp32 (or None) is added to the scores for the selection only."""
+    R, T, K, E = shape.num_ranks, shape.num_tokens, shape.num_topk, shape.num_experts
+    lp, dtype = _logits(logits, shape)
+    rc = lib().ep_route(
+        ctypes.byref(shape), ctypes.byref(route), lp, _i32(int(dtype == torch.bfloat16)),
+        _t(bias, torch.float32, (E,), "bias", nullable=True), _t(topk_idx, torch.int64, (R, T, K), "topk_idx"),
+        _t(topk_w, torch.float32, (R, T, K), "topk_w"), _t(status, torch.int32, (1,), "status"), _stream(stream))
+    _check("ep_route", rc)
+
+
+def ep_route_backward(shape: EpShape, route: EpRoute, logits, topk_idx, grad_topk_w, grad_logits, status,
+                      stream=None) -> None:
+    """Gradient of :func:`ep_route`'s weights with respect to the logits
+    (``grad_logits`` has the logits' type; every element is written)."""
+    R, T, K = shape.num_ranks, shape.num_tokens, shape.num_topk
+    lp, dtype = _logits(logits, shape)
+    rc = lib().ep_route_backward(
+        ctypes.byref(shape), ctypes.byref(route), lp, _i32(int(dtype == torch.bfloat16)),
+        _t(topk_idx, torch.int64, (R, T, K), "topk_idx"), _t(grad_topk_w, torch.float32, (R, T, K), "grad_topk_w"),
+        _t(grad_logits, dtype, (R, T, shape.num_experts), "grad_logits"), _t(status, torch.int32, (1,), "status"),
+        _stream(stream))
+    _check("ep_route_backward", rc)
+
+
+def ep_ll_dispatch_fp8(shape: EpShape, x, topk_idx, slot_pos, expert_capacity: int, recv_x, recv_x_scales,
+                       recv_src_info, status, stream=None) -> None:
+    """:func:`ep_ll_dispatch` with the rows cast to e4m3 (uint8 bytes), one fp32 scale per
+    128 columns ([E, capacity, ceil(H / 128)])."""
+    R, T, K, E, H = shape.num_ranks, shape.num_tokens, shape.num_topk, shape.num_experts, shape.hidden
+    cap = expert_capacity
+    rc = lib().ep_ll_dispatch_fp8(
+        ctypes.byref(shape), _t(x, torch.bfloat16, (R, T, H), "x"),
+        _t(topk_idx, torch.int64, (R, T, K), "topk_idx"), _t(slot_pos, torch.int32, (R, T, K), "slot_pos"),
+        _i32(cap), _t(recv_x, torch.uint8, (E, cap, H), "recv_x"),
+        _t(recv_x_scales, torch.float32, (E, cap, scale_blocks(H)), "recv_x_scales"),
+        _t(recv_src_info, torch.int32, (E, cap, 2), "recv_src_info", nullable=True),
+        _t(status, torch.int32, (1,), "status"), _stream(stream))
+    _check("ep_ll_dispatch_fp8", rc)
+
+
+def scale_blocks(n: int) -> int:
+    """Scales of ``n`` columns: one per 128."""
+    return -(-n // 128)
+
+
+def ep_check_gemm_shape(shape: EpGemmShape) -> int:
+    return lib().ep_check_gemm_shape(ctypes.byref(shape))
+
+
+def _gemm_dims(a, w, w_dims: int):
+    for t, dims, name in ((a, 3, "a"), (w, w_dims, "w")):
+        if t is None or t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions")
+    return a.shape[0], a.shape[1], w.shape[-2], a.shape[2]
+
+
+def ep_ll_gemm_fp8(a, a_scales, w, w_scales, count, y, status, stream=None) -> None:
+    """Experts' product: ``a`` [E, capacity, k] and ``w`` [E, n, k] e4m3 (uint8 bytes) with
+    their 128-column and 128 x 128 block scales, ``count`` [E] rows per expert ->
+    ``y`` [E, capacity, n] bf16."""
+    E, cap, n, k = _gemm_dims(a, w, 3)
+    rc = lib().ep_ll_gemm_fp8(
+        ctypes.byref(EpGemmShape(E, cap, n, k)), _t(a, torch.uint8, (E, cap, k), "a"),
+        _t(a_scales, torch.float32, (E, cap, scale_blocks(k)), "a_scales"), _t(w, torch.uint8, (E, n, k), "w"),
+        _t(w_scales, torch.float32, (E, scale_blocks(n), scale_blocks(k)), "w_scales"),
+        _t(count, torch.int32, (E,), "count"), _t(y, torch.bfloat16, (E, cap, n), "y"),
+        _t(status, torch.int32, (1,), "status"), _stream(stream))
+    _check("ep_ll_gemm_fp8", rc)
+
+
+def ep_ll_gemm_swiglu_fp8(a, a_scales, w, w_scales, count, y, y_scales, status, stream=None) -> None:
+    """Gate and up products, silu(gate) * up and its cast in one launch: ``w`` [E, 2, n, k]
+    (gate, up) -> ``y`` [E, capacity, n] e4m3 (uint8 bytes), ``y_scales`` per 128 columns."""
+    E, cap, n, k = _gemm_dims(a, w, 4)
+    rc = lib().ep_ll_gemm_swiglu_fp8(
+        ctypes.byref(EpGemmShape(E, cap, n, k)), _t(a, torch.uint8, (E, cap, k), "a"),
+        _t(a_scales, torch.float32, (E, cap, scale_blocks(k)), "a_scales"), _t(w, torch.uint8, (E, 2, n, k), "w"),
+        _t(w_scales, torch.float32, (E, 2, scale_blocks(n), scale_blocks(k)), "w_scales"),
+        _t(count, torch.int32, (E,), "count"), _t(y, torch.uint8, (E, cap, n), "y"),
+        _t(y_scales, torch.float32, (E, cap, scale_blocks(n)), "y_scales"),
+        _t(status, torch.int32, (1,), "status"), _stream(stream))
+    _check("ep_ll_gemm_swiglu_fp8", rc)
 
 
 def ep_sync_status(status, stream=None) -> int:

@@ -66,7 +66,7 @@ typedef enum {
     EP_ERR_CAPACITY = -3,      /* receive pool smaller than the rows to place */
     EP_ERR_TIMEOUT = -4,       /* a bounded device wait ran out */
     EP_ERR_INCONSISTENT = -5,  /* count inputs disagree with is_token_in_rank */
-    EP_ERR_INPUT = -6          /* an expert id outside [-1, E) */
+    EP_ERR_INPUT = -6          /* an expert id outside [-1, E), or a NaN router score */
 } ep_status_t;
 
 /* Bits the kernels OR into the device status word. */
@@ -489,6 +489,146 @@ ep_status_t ep_ll_dispatch(const ep_shape_t* shape, const uint16_t* x, const int
 ep_status_t ep_ll_combine(const ep_shape_t* shape, const uint16_t* y, int32_t expert_capacity,
                           const int64_t* topk_idx, const float* topk_w, const int32_t* slot_pos,
                           uint16_t* combined_x, int32_t* status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Router.  Turns router logits into the top-k map and weights that every
+ * other call starts from.  For one token, with logit l_e of expert e:
+ *   eligible   l_e above the lowest finite value of its type: -inf, that
+ *              lowest value (the two usual masks) and NaN leave the expert
+ *              out; +inf counts as the largest finite value of the type
+ *   score      s_e = softmax of l over the eligible experts, or
+ *              s_e = 1 / (1 + exp(-l_e))
+ *   key        s_e + bias_e (no bias: s_e).  The bias only selects.  A key that
+ *              is -inf or NaN leaves the expert out of the selection
+ *   groups     num_groups runs of E / num_groups consecutive experts; a
+ *              group's key is the sum of its group_top largest keys; only
+ *              experts of the topk_groups groups with the largest keys stay.
+ *              A group without an eligible expert is never taken
+ *   selection  the K largest keys in descending order, ties to the lowest
+ *              index (groups too)
+ *   weights    w_k = scale * s_k, or scale * s_k / sum_j s_j over the kept
+ *              experts with renormalize (0 when that sum is 0)
+ * Slots beyond the experts that stay get expert -1 and weight 0: a row whose
+ * mask leaves nothing is all -1.  Softmax without bias selects by the logits
+ * themselves (the softmax keeps their order) where a group's key is one
+ * score.  Scores, sums and weights are fp32.
+ */
+typedef struct {
+    int32_t score;       /* 0: softmax, 1: sigmoid */
+    int32_t num_groups;  /* 1 .. 32, divides E; 1: no groups */
+    int32_t topk_groups; /* 1 .. num_groups */
+    int32_t group_top;   /* 1 or 2 (at most E / num_groups) */
+    int32_t renormalize; /* 0 or 1 */
+    float scale;         /* finite */
+} ep_route_t;
+
+/* EP_OK when `route` obeys the rules above for `shape` and K <= topk_groups *
+ * E / num_groups, else EP_ERR_INVALID_ARG. */
+ep_status_t ep_check_route(const ep_shape_t* shape, const ep_route_t* route);
+
+/* ep_route (uses R, T, K, E of `shape`)
+ *   logits       in  [R][T][E] fp32, or bf16 bits when logits_bf16 is 1
+ *   logits_bf16  0 or 1
+ *   bias         in  fp32 [E], or NULL
+ *   topk_idx     out int64 [R][T][K]  as ep_layout_notify / ep_ll_layout read it
+ *   topk_w       out fp32  [R][T][K]
+ * A NaN among the logits or the keys sets EP_DEV_INPUT.
+ */
+ep_status_t ep_route(const ep_shape_t* shape, const ep_route_t* route, const void* logits, int32_t logits_bf16,
+                     const float* bias, int64_t* topk_idx, float* topk_w, int32_t* status, cudaStream_t stream);
+
+/* ep_route_backward: gradient of ep_route's weights with respect to the
+ * logits, for the experts that were kept (the selection and the bias have
+ * none).  With g_k = grad_topk_w, S = sum_j s_j over the kept slots,
+ *   ds_k = scale * g_k, or scale / S * (g_k - sum_j g_j s_j / S)
+ *   softmax: grad l_e = s_e * (ds_e - sum_k s_k ds_k)   (every eligible e)
+ *   sigmoid: grad l_e = s_e * (1 - s_e) * ds_e          (0 where not kept)
+ * Softmax with renormalize depends on the kept logits alone: their softmax v
+ * gives grad l_k = scale * v_k * (g_k - sum_j v_j g_j), 0 elsewhere.
+ *   logits, logits_bf16  in  as for ep_route (score, renormalize and scale of
+ *                            `route` are used)
+ *   topk_idx             in  int64 [R][T][K]; -1 slots are skipped, a repeated
+ *                            expert's slots add up, an id outside [-1, E) sets
+ *                            EP_DEV_INPUT and is skipped
+ *   grad_topk_w          in  fp32 [R][T][K]
+ *   grad_logits          out [R][T][E], type of logits, every element written
+ */
+ep_status_t ep_route_backward(const ep_shape_t* shape, const ep_route_t* route, const void* logits,
+                              int32_t logits_bf16, const int64_t* topk_idx, const float* grad_topk_w,
+                              void* grad_logits, int32_t* status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Low-latency dispatch that casts.  ep_ll_dispatch with every row cast to
+ * e4m3 on the way, one fp32 scale for each block of 128 columns (the last one
+ * may be shorter): the token is read and cast once and written once per slot,
+ * half the bytes of a bf16 row.  For a block with largest magnitude m:
+ *   scale = max(m, 2^-100) / 448,  q = e4m3_rne(x / scale)
+ * (fp32 division; the floor keeps the scale of a zero block a normal number).
+ * m skips NaN elements, which stay NaN; a block with an infinity gets an
+ * infinite scale, so it reads back as NaN and not as a wrong number.
+ *   x              in  bf16 bits [R][T][H], H % 16 == 0
+ *   topk_idx       in  int64 [R][T][K]
+ *   slot_pos       in  int32 [R][T][K]  from ep_ll_layout
+ *   recv_x         out e4m3 bytes [E][expert_capacity][H]
+ *   recv_x_scales  out fp32 [E][expert_capacity][ceil(H / 128)]
+ *   recv_src_info  out int32 [E][expert_capacity][2] (source rank, token), or NULL
+ * A slot whose id is outside [0, E) or whose position is outside [0,
+ * expert_capacity) is skipped; rows not written are left as they are.
+ */
+ep_status_t ep_ll_dispatch_fp8(const ep_shape_t* shape, const uint16_t* x, const int64_t* topk_idx,
+                               const int32_t* slot_pos, int32_t expert_capacity, uint8_t* recv_x,
+                               float* recv_x_scales, int32_t* recv_src_info, int32_t* status,
+                               cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Experts' products on the per-expert packed layout.  Rows and weights are
+ * e4m3 with one fp32 scale for each 128 columns of a row and for each 128 x
+ * 128 block of a weight matrix (last blocks may be shorter):
+ *   p[e][m][n] = sum_b a_scales[e][m][b] * w_scales[e][n / 128][b] *
+ *                sum_{k in block b} a[e][m][k] * w[e][n][k]
+ * with fp32 sums.  Only rows m < min(count[e], capacity) are read and written;
+ * other output rows are left as they are.  An expert without rows costs
+ * nothing: its weights are not read.
+ */
+typedef struct {
+    int32_t num_experts; /* 1 .. 8192 */
+    int32_t capacity;    /* rows of each expert's buffer, 0 .. 2^24 */
+    int32_t n;           /* output columns, a multiple of 8 (16 for swiglu), at most 2^20 */
+    int32_t k;           /* input columns, a multiple of 16, at most 2^20 */
+} ep_gemm_shape_t;
+
+/* EP_OK when `shape` obeys the rules above, else EP_ERR_INVALID_ARG. */
+ep_status_t ep_check_gemm_shape(const ep_gemm_shape_t* shape);
+
+/* ep_ll_gemm_fp8: y = bf16(p), the product that ends an expert (its input
+ * gradient is the same call on the transposed weights: their blocks and scales
+ * transpose without another cast).
+ *   a         in  e4m3 bytes [num_experts][capacity][k]
+ *   a_scales  in  fp32 [num_experts][capacity][ceil(k / 128)]
+ *   w         in  e4m3 bytes [num_experts][n][k]
+ *   w_scales  in  fp32 [num_experts][ceil(n / 128)][ceil(k / 128)]
+ *   count     in  int32 [num_experts]  rows of each expert (ep_ll_layout's count)
+ *   y         out bf16 bits [num_experts][capacity][n]
+ * A device wait that runs out sets EP_DEV_TIMEOUT (y is then unspecified).
+ */
+ep_status_t ep_ll_gemm_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales, const uint8_t* w,
+                           const float* w_scales, const int32_t* count, uint16_t* y, int32_t* status,
+                           cudaStream_t stream);
+
+/* ep_ll_gemm_swiglu_fp8: the two products that begin a gated expert, their
+ * activation and its cast, without the products ever leaving the chip.  With
+ * gate and up = p for the two halves of w:
+ *   h = gate / (1 + exp(-gate)) * up
+ *   y, y_scales = h cast by blocks of 128 columns as in ep_ll_dispatch_fp8
+ *   w         in  e4m3 bytes [num_experts][2][n][k]  (gate matrix, up matrix)
+ *   w_scales  in  fp32 [num_experts][2][ceil(n / 128)][ceil(k / 128)]
+ *   y         out e4m3 bytes [num_experts][capacity][n]
+ *   y_scales  out fp32 [num_experts][capacity][ceil(n / 128)]
+ * other arguments as for ep_ll_gemm_fp8, whose a and a_scales y and y_scales are.
+ */
+ep_status_t ep_ll_gemm_swiglu_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales,
+                                  const uint8_t* w, const float* w_scales, const int32_t* count, uint8_t* y,
+                                  float* y_scales, int32_t* status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Waits for `stream`, reads the device status word (a 4-byte copy into host

@@ -201,7 +201,8 @@ bool gemm_shape_ok(const ep_gemm_shape_t* s, int n_multiple) {
     if (s == nullptr) return false;
     return s->num_experts >= 1 && s->num_experts <= 8192 && s->capacity >= 0 && s->capacity <= (1 << 24) &&
            s->n >= n_multiple && s->n % n_multiple == 0 && s->n <= (1 << 20) && s->k >= 16 && s->k % 16 == 0 &&
-           s->k <= (1 << 20);
+           s->k <= (1 << 20) && static_cast<long long>(s->capacity) * s->k < (1LL << 40) &&
+           static_cast<long long>(s->n) * s->k < (1LL << 40);
 }
 
 // Checks shared by the two products; `halves` is 2 when w holds a gate and an up matrix.

@@ -1,122 +1,449 @@
-// Experts' block-scaled e4m3 products (ep_ll_gemm_fp8, ep_ll_gemm_swiglu_fp8).
+// Experts' block-scaled e4m3 products on the tensor cores (ep_ll_gemm_fp8,
+// ep_ll_gemm_swiglu_fp8).
+//
+//   p[m][n] = sum_b as[m][b] ws[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
+//
+// A pair of CTAs (one cluster, two SMs) owns a tile of 256 rows x 256 weight
+// rows and walks the k-blocks of 128.  One tcgen05.mma chain of four (K = 32
+// each) leaves a block's plain sums in TMEM; two such accumulators (256
+// columns each, all of TMEM) take turns, so the next block multiplies while
+// the epilogue warps read this one, scale it by as * ws and add it to fp32
+// sums in their registers.  That scaling is what hardware block scales cannot
+// do for fp32 scales; it takes 32768 FMAs of an SM per block, half the time
+// the tensor core needs for it.
+//
+// Each CTA loads its own 128 rows of a and half of the weight rows with
+// swizzled TMA; the weights cross HBM once per 256 rows, and only the 32-row
+// chunks of a that hold rows are read.  For the gated product the weight rows
+// are 128 of the gate matrix (loaded by the leader) and the same 128 of the up
+// matrix (its peer), so gate and up of one output column meet in one thread.
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "ep.h"
 #include "ep_device.cuh"
 #include "ep_internal.h"
 #include "fp8_cast.cuh"
+#include "tcgen05.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kRows = 16;      // rows of a tile
-constexpr int kCols = 128;     // output columns of a tile: one scale block, one thread each
+constexpr int kTileM = 256;                    // rows of a pair's tile, 128 per CTA
+constexpr int kTileN = 256;                    // weight rows of a pair's tile
+constexpr int kHalf = 128;                     // rows of a, and of w, that one CTA loads
+constexpr int kChunk = 32;                     // rows of one TMA box of a
+constexpr int kBlockK = kScaleBlock;           // 128 e4m3: one 128-byte swizzled row
+constexpr int kTileBytes = kHalf * kBlockK;    // 16 KB, one operand of a stage
+constexpr int kStages = 6;
+constexpr int kThreads = 384;                  // producer, MMA, TMEM, spare | two epilogue warpgroups
+constexpr int kEpilogueWarps = 8;
+constexpr int kAccColumns = 256;               // TMEM columns of one accumulator
+constexpr int kTmemColumns = 512;
+constexpr long long kWaitLimitNs = 2000000000LL;
 
-__device__ __forceinline__ void unpack_e4m3x4(uint32_t v, float* f) {
-    uint32_t lo, hi;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(v)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(v >> 16)));
-    const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-    f[0] = a.x;
-    f[1] = a.y;
-    f[2] = b.x;
-    f[3] = b.y;
+struct Barriers {
+    uint64_t full[kStages];   // leader's: bytes of both CTAs have landed
+    uint64_t empty[kStages];  // both: the MMAs that read the stage are done
+    uint64_t acc_full[2];     // both: a block's sums are in TMEM
+    uint64_t acc_empty[2];    // leader's: every epilogue warp of the pair has read them
+};
+
+struct Shared {
+    Barriers bar;
+    float amax[2][2][kHalf];  // [tile parity][warpgroup][row]
+    int first[8192 / kWarp + 2];  // tiles before each group of 32 experts
+    uint32_t tmem;
+    int abort;
+};
+
+struct Params {
+    GemmArgs g;
+    int kb, nb, tiles_n;
+};
+
+// One wait of a role: false when the limit passes or another role gave up.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Shared* s) {
+    const uint32_t addr = smem_addr(bar);
+    if (mbar_try_wait_cluster(addr, parity)) return true;
+    long long start = 0;
+    uint32_t polls = 0;
+    while (!mbar_try_wait_cluster(addr, parity)) {
+        if ((++polls & 63u) != 0) continue;
+        if (*reinterpret_cast<volatile int*>(&s->abort) != 0) return false;
+        const long long now = globaltimer_ns();
+        if (start == 0) start = now;
+        if (now - start > kWaitLimitNs) {
+            *reinterpret_cast<volatile int*>(&s->abort) = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The pair's tiles: experts in order, then row tiles, then weight tiles.
+// `first` holds the tiles before each group of 32 experts; a role walks on
+// from the expert of its last tile.
+struct Walk {
+    int e = 0, before = 0;  // an expert, and the tiles before it
+};
+struct Tile {
+    int e, m0, n0, rows;  // rows: valid rows of the expert from m0 on
+};
+__device__ __forceinline__ int expert_rows(const Params& p, int e) {
+    return min(max(__ldg(p.g.count + e), 0), p.g.cap);
+}
+__device__ __forceinline__ Tile tile_at(int t, Walk& w, const int* first, const Params& p, int cols) {
+    if (first[w.e / kWarp + 1] <= t) {
+        int group = w.e / kWarp + 1;
+        while (first[group + 1] <= t) ++group;
+        w.e = group * kWarp;
+        w.before = first[group];
+    }
+    Tile r;
+    for (;;) {
+        r.rows = expert_rows(p, w.e);
+        const int n = (r.rows + kTileM - 1) / kTileM * p.tiles_n;
+        if (w.before + n > t) break;
+        w.before += n;
+        ++w.e;
+    }
+    const int local = t - w.before;
+    r.e = w.e;
+    r.m0 = local / p.tiles_n * kTileM;
+    r.n0 = local % p.tiles_n * cols;
+    r.rows -= r.m0;
+    return r;
+}
+
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Scales of four consecutive k-blocks for one row and two weight blocks.
+struct Scales {
+    float a[4], w0[4], w1[4];
+};
+__device__ __forceinline__ void load_scales(Scales& s, const float* as, const float* w0, const float* w1, int kb,
+                                            int end, bool on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool in = on && kb + i < end;
+        s.a[i] = in ? __ldg(as + kb + i) : 0.0f;
+        s.w0[i] = in ? __ldg(w0 + kb + i) : 0.0f;
+        s.w1[i] = in ? __ldg(w1 + kb + i) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void fma32(unsigned long long* acc, const uint32_t (&r)[32], unsigned long long s) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) fma2(acc[j], r[2 * j], r[2 * j + 1], s);
 }
 
 template <bool kSwiglu>
-__global__ void __launch_bounds__(kCols) gemm_kernel(const GemmArgs p) {
-    constexpr int kHalves = kSwiglu ? 2 : 1;
-    __shared__ float s_a[kRows][kScaleBlock];
-    __shared__ float s_scale[kRows];
-    __shared__ float s_amax[kCols / kWarp][kRows];
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ll_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                       const Params p) {
+    extern __shared__ uint8_t s_raw[];
+    // stages first, on a 1024-byte boundary as the swizzle needs, at the same offset in both CTAs
+    const uint32_t pad = (1024u - (smem_addr(s_raw) & 1023u)) & 1023u;
+    uint8_t* s_tiles = s_raw + pad;
+    Shared* s = reinterpret_cast<Shared*>(s_tiles + kStages * 2 * kTileBytes);
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int cols = kSwiglu ? kTileN / 2 : kTileN;  // output columns of a tile
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s->bar.full[i], 1);
+            mbar_init(&s->bar.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->bar.acc_full[i], 1);
+            mbar_init(&s->bar.acc_empty[i], 2 * kEpilogueWarps);
+        }
+        s->abort = 0;
+        fence_mbarrier_init();
+        prefetch_tensormap(&map_a);
+        prefetch_tensormap(&map_w);
+    }
+    if (warp == 2) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_launch_dependents();
-    griddep_wait();
-    const int tid = threadIdx.x, kb = scale_blocks(p.k), nb = scale_blocks(p.n);
-    const int n = blockIdx.x * kCols + tid;
-    const int e = blockIdx.z;
-    const int rows = min(p.count[e], p.cap);
-    for (int m0 = blockIdx.y * kRows; m0 < rows; m0 += gridDim.y * kRows) {
-        float acc[kHalves][kRows];
-        for (int h = 0; h < kHalves; ++h)
-            for (int i = 0; i < kRows; ++i) acc[h][i] = 0.0f;
-        for (int b = 0; b < kb; ++b) {
-            __syncthreads();
-            const int depth = min(kScaleBlock, p.k - b * kScaleBlock);
-            for (int i = tid; i < kRows * kScaleBlock / 4; i += kCols) {
-                const int r = i / (kScaleBlock / 4), c = i % (kScaleBlock / 4) * 4;
-                uint32_t v = 0;
-                if (m0 + r < rows && c < depth)
-                    v = *reinterpret_cast<const uint32_t*>(
-                        p.a + (static_cast<long long>(e) * p.cap + m0 + r) * p.k + b * kScaleBlock + c);
-                unpack_e4m3x4(v, &s_a[r][c]);
+    griddep_wait();  // counts, rows and scales are complete from here on
+    const int groups = (p.g.E + kWarp - 1) / kWarp;
+    if (warp == 1) {  // one warp counts the tiles
+        int base = 0;
+        for (int i = 0; i < groups; ++i) {
+            if (lane == 0) s->first[i] = base;
+            const int e = i * kWarp + lane;
+            const int n = e < p.g.E ? (expert_rows(p, e) + kTileM - 1) / kTileM * p.tiles_n : 0;
+            base += static_cast<int>(__reduce_add_sync(0xffffffffu, n));
+        }
+        if (lane == 0) s->first[groups] = base;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    const uint32_t tmem = s->tmem;
+    const int tiles = s->first[groups];
+
+    if (warp < 4) {
+        regs_down<48>();
+        if (warp == 0 && lane == 0) {
+            // ---- producer: this CTA's rows of a and its half of the weight rows ----
+            uint32_t it = 0;
+            Walk walk;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const Tile tl = tile_at(t, walk, s->first, p, cols);
+                const int chunks0 = (min(tl.rows, kHalf) + kChunk - 1) / kChunk;
+                const int chunks1 = (min(max(tl.rows - kHalf, 0), kHalf) + kChunk - 1) / kChunk;
+                const int chunks = rank == 0 ? chunks0 : chunks1;
+                const uint32_t bytes = 2 * kTileBytes + (chunks0 + chunks1) * kChunk * kBlockK;
+                const int wy = kSwiglu ? tl.n0 : tl.n0 + static_cast<int>(rank) * kHalf;
+                const int wz = kSwiglu ? 2 * tl.e + static_cast<int>(rank) : tl.e;
+                const int ay = tl.m0 + static_cast<int>(rank) * kHalf;
+                for (int b = 0; b < p.kb; ++b, ++it) {
+                    const uint32_t st = it % kStages, use = it / kStages;
+                    if (use > 0 && !(ok = wait_for(&s->bar.empty[st], (use - 1) & 1, s))) break;
+                    if (rank == 0) mbar_arrive_expect_tx(&s->bar.full[st], bytes);
+                    const uint32_t bar = mapa(smem_addr(&s->bar.full[st]), 0);
+                    const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
+                    tma_load_3d(ta + kTileBytes, &map_w, b * kBlockK, wy, wz, bar);
+                    for (int c = 0; c < chunks; ++c)
+                        tma_load_3d(ta + c * kChunk * kBlockK, &map_a, b * kBlockK, ay + c * kChunk, tl.e, bar);
+                }
             }
-            if (tid < kRows)
-                s_scale[tid] =
-                    m0 + tid < rows ? p.a_scales[(static_cast<long long>(e) * p.cap + m0 + tid) * kb + b] : 0.0f;
-            __syncthreads();
-            if (n < p.n) {
-                for (int h = 0; h < kHalves; ++h) {
-                    const long long mat = static_cast<long long>(e) * kHalves + h;
-                    const uint8_t* w = p.w + (mat * p.n + n) * p.k + b * kScaleBlock;
-                    float part[kRows];
-                    for (int i = 0; i < kRows; ++i) part[i] = 0.0f;
-                    for (int c = 0; c < depth; c += 16) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(w + c);
-                        float f[16];
-                        unpack_e4m3x4(v.x, f);
-                        unpack_e4m3x4(v.y, f + 4);
-                        unpack_e4m3x4(v.z, f + 8);
-                        unpack_e4m3x4(v.w, f + 12);
+            // every stage's last read is over before the CTA may leave
+            for (uint32_t i = it > kStages ? it - kStages : 0; i < it && ok; ++i)
+                ok = wait_for(&s->bar.empty[i % kStages], (i / kStages) & 1, s);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---- MMA: one thread feeds the pair's tensor cores ----
+            constexpr uint32_t idesc = e4m3_idesc(kTileM, kTileN);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                for (int b = 0; b < p.kb; ++b, ++it) {
+                    const uint32_t st = it % kStages, acc = it & 1, round = it / 2;
+                    if (round > 0 && !(ok = wait_for(&s->bar.acc_empty[acc], (round - 1) & 1, s))) break;
+                    if (!(ok = wait_for(&s->bar.full[st], (it / kStages) & 1, s))) break;
+                    tc_fence_after();
+                    const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
+                    const uint64_t da = sw128_desc(ta), dw = sw128_desc(ta + kTileBytes);
 #pragma unroll
-                        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) part[i] = fmaf(s_a[i][c + j], f[j], part[i]);
-                    }
-                    const float ws = p.w_scales[(mat * nb + blockIdx.x) * kb + b];
-                    for (int i = 0; i < kRows; ++i) acc[h][i] = fmaf(s_scale[i] * ws, part[i], acc[h][i]);
+                    for (int k = 0; k < kBlockK / 32; ++k)  // 32 bytes further inside the swizzled row
+                        mma_e4m3_pair(tmem + acc * kAccColumns, da + 2 * k, dw + 2 * k, idesc, k > 0);
+                    mma_commit_pair(smem_addr(&s->bar.empty[st]));
+                    mma_commit_pair(smem_addr(&s->bar.acc_full[acc]));
                 }
             }
         }
-        if (!kSwiglu) {
-            for (int i = 0; i < kRows; ++i)
-                if (m0 + i < rows && n < p.n)
-                    static_cast<__nv_bfloat16*>(p.y)[(static_cast<long long>(e) * p.cap + m0 + i) * p.n + n] =
-                        __float2bfloat16_rn(acc[0][i]);
-        } else {
-            for (int i = 0; i < kRows; ++i) {
-                acc[0][i] = acc[0][i] / (1.0f + expf(-acc[0][i])) * acc[kHalves - 1][i];
-                float m = fabsf(acc[0][i]);
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (tid % kWarp == 0) s_amax[tid / kWarp][i] = m;
+        __syncwarp();
+    } else {
+        // ---- epilogue: thread = one row; warpgroup g sums columns 64 g + [0, 64) of both weight blocks ----
+        regs_up<224>();
+        const int g = (warp - 4) / 4, quarter = warp % 4;
+        const int row = quarter * kWarp + lane;  // of this CTA's 128
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
+        uint32_t it = 0, parity = 0;
+        Walk walk;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
+            const Tile tl = tile_at(t, walk, s->first, p, cols);
+            const int left = tl.rows - static_cast<int>(rank) * kHalf;
+            const bool valid = row < left;
+            const bool warp_on = quarter * kWarp < left;
+            const long long r = static_cast<long long>(tl.e) * p.g.cap + tl.m0 + static_cast<int>(rank) * kHalf + row;
+            const float* as = p.g.a_scales + r * p.kb;
+            const int wb = tl.n0 / kScaleBlock;
+            const long long mat = static_cast<long long>(tl.e) * (kSwiglu ? 2 : 1);
+            const float* w0 = p.g.w_scales + (mat * p.nb + wb) * p.kb;
+            // the tile's second weight block: the up matrix, or the next 128 columns (the same again past the end)
+            const float* w1 = kSwiglu ? w0 + static_cast<long long>(p.nb) * p.kb : (wb + 1 < p.nb ? w0 + p.kb : w0);
+            unsigned long long acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            Scales cur, next;
+            load_scales(next, as, w0, w1, 0, p.kb, valid);
+            for (int b = 0; b < p.kb && ok; b += 4) {
+                cur = next;
+                load_scales(next, as, w0, w1, b + 4, p.kb, valid);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (b + i >= p.kb || !ok) break;
+                    const uint32_t buf = it & 1;
+                    ok = wait_for(&s->bar.acc_full[buf], (it / 2) & 1, s);
+                    ++it;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (warp_on) {
+                        const unsigned long long s0 = pair2(cur.a[i] * cur.w0[i]), s1 = pair2(cur.a[i] * cur.w1[i]);
+                        const uint32_t col = lanes + buf * kAccColumns + g * 64;
+                        uint32_t x[32], y[32];
+                        tmem_ld32(col, x);
+                        tmem_wait(x);
+                        tmem_ld32(col + 32, y);
+                        fma32(acc, x, s0);
+                        tmem_wait(y);
+                        tmem_ld32(col + 128, x);
+                        fma32(acc + 16, y, s0);
+                        tmem_wait(x);
+                        tmem_ld32(col + 160, y);
+                        fma32(acc + 32, x, s1);
+                        tmem_wait(y);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
+                        fma32(acc + 48, y, s1);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
+                    }
+                }
             }
-            __syncthreads();
-            for (int i = 0; i < kRows; ++i) {
-                const float scale =
-                    block_scale(fmaxf(fmaxf(s_amax[0][i], s_amax[1][i]), fmaxf(s_amax[2][i], s_amax[3][i])));
-                const long long row = static_cast<long long>(e) * p.cap + m0 + i;
-                if (m0 + i < rows && n < p.n) {
-                    static_cast<uint8_t*>(p.y)[row * p.n + n] =
-                        static_cast<uint8_t>(pack_e4m3x4(acc[0][i] / scale, 0.0f, 0.0f, 0.0f));
-                    if (tid == 0) p.y_scales[row * nb + blockIdx.x] = scale;
+            if (!ok) {
+                // the partner warp may be waiting for this one's maxima
+                if (kSwiglu && warp_on) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");
+                break;
+            }
+            if (!kSwiglu) {
+                if (valid) {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r * p.g.n;
+                    const bool wide = p.g.n % 16 == 0;  // rows on 32-byte boundaries
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {  // 16 columns
+                        const int col = tl.n0 + (j / 4) * 128 + g * 64 + (j % 4) * 16;
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 f = unpack2(acc[j * 8 + i]);
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                            v[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        if (wide) {
+                            if (col < p.g.n) store32(out + col, v);
+                        } else {
+                            if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
+                            if (col + 8 < p.g.n) st_v4(out + col + 8, make_uint4(v[4], v[5], v[6], v[7]));
+                        }
+                    }
+                }
+            } else if (warp_on) {
+                // h = gate / (1 + exp(-gate)) * up; columns past n have zero weights, so h = 0 there
+                float h[64];
+                float amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float2 a = unpack2(acc[j]), u = unpack2(acc[32 + j]);
+                    h[2 * j] = __fdividef(a.x, 1.0f + __expf(-a.x)) * u.x;
+                    h[2 * j + 1] = __fdividef(a.y, 1.0f + __expf(-a.y)) * u.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
+                }
+                // the other warpgroup has the block's other 64 columns
+                s->amax[parity][g][row] = amax;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                const float scale = block_scale(fmaxf(s->amax[parity][0][row], s->amax[parity][1][row]));
+                if (valid) {
+                    const float inv = 1.0f / scale;
+                    uint8_t* out = static_cast<uint8_t*>(p.g.y) + r * p.g.n;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {  // 16 columns
+                        const int col = tl.n0 + g * 64 + j * 16;
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = pack_e4m3x4(h[j * 16 + i * 4] * inv, h[j * 16 + i * 4 + 1] * inv,
+                                               h[j * 16 + i * 4 + 2] * inv, h[j * 16 + i * 4 + 3] * inv);
+                        if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
+                    }
+                    if (g == 0) p.g.y_scales[r * p.nb + wb] = scale;
                 }
             }
         }
     }
+    tc_fence_before();
+    __syncthreads();
+    if (s->abort != 0) {
+        // a wait ran out: let the copies and products still in flight land before shared memory and TMEM go
+        const long long start = globaltimer_ns();
+        while (globaltimer_ns() - start < 10000000LL) {
+        }
+        if (threadIdx.x == 0) flag_error(p.g.status, EP_DEV_TIMEOUT);
+    }
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc_pair(tmem, kTmemColumns);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (no device work), looked up once.
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// Map of [outer][rows][k] bytes, boxes of `box_rows` rows x 128 bytes.
+bool make_map(CUtensorMap* map, const void* base, int k, int rows, int outer, int box_rows) {
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(k) * rows};
+    const cuuint32_t box[3] = {kBlockK, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kSwiglu>
+cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
+    Params p = {};
+    p.g = g;
+    p.kb = scale_blocks(g.k);
+    p.nb = scale_blocks(g.n);
+    const int cols = kSwiglu ? kTileN / 2 : kTileN;
+    p.tiles_n = (g.n + cols - 1) / cols;
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    CUtensorMap map_a, map_w;
+    if (!make_map(&map_a, g.a, g.k, g.cap, g.E, kChunk) ||
+        !make_map(&map_w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + static_cast<size_t>(kStages) * 2 * kTileBytes + sizeof(Shared);
+    // an upper bound of the tiles: the counts are on the device
+    const long long most = static_cast<long long>(g.E) * ((g.cap + kTileM - 1) / kTileM) * p.tiles_n;
+    const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
+    return launch_pdl(ll_gemm_fp8_kernel<kSwiglu>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, map_a,
+                      map_w, p);
 }
 
 }  // namespace
 
 cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream) {
-    const int want = (g.cap + kRows - 1) / kRows;
-    const dim3 grid(static_cast<unsigned>(scale_blocks(g.n)), static_cast<unsigned>(want < 64 ? want : 64),
-                    static_cast<unsigned>(g.E));
-    return g.y_scales != nullptr ? launch_pdl(gemm_kernel<true>, grid, dim3(kCols), 0, stream, 0, false, g)
-                                 : launch_pdl(gemm_kernel<false>, grid, dim3(kCols), 0, stream, 0, false, g);
+    return g.y_scales != nullptr ? launch<true>(g, stream) : launch<false>(g, stream);
 }
 
 }  // namespace ep

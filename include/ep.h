@@ -595,7 +595,7 @@ typedef struct {
     int32_t capacity;    /* rows of each expert's buffer, 0 .. 2^24 */
     int32_t n;           /* output columns, a multiple of 8 (16 for swiglu), at most 2^20 */
     int32_t k;           /* input columns, a multiple of 16, at most 2^20 */
-} ep_gemm_shape_t;
+} ep_gemm_shape_t;       /* capacity * k and n * k below 2^40 */
 
 /* EP_OK when `shape` obeys the rules above, else EP_ERR_INVALID_ARG. */
 ep_status_t ep_check_gemm_shape(const ep_gemm_shape_t* shape);

@@ -48,11 +48,11 @@ def test_route_rules(ep):
 
 def test_gemm_shape_rules(ep):
     G = ep.EpGemmShape
-    for s in (G(1, 0, 8, 16), G(8192, 1 << 24, 1 << 20, 1 << 20), G(3, 5, 136, 144)):
+    for s in (G(1, 0, 8, 16), G(8192, 1 << 24, 1 << 20, 1 << 15), G(1, 1, 8, 1 << 20), G(3, 5, 136, 144)):
         assert ep.ep_check_gemm_shape(s) == ep.EP_OK
     for s in (G(0, 1, 8, 16), G(8193, 1, 8, 16), G(1, -1, 8, 16), G(1, (1 << 24) + 1, 8, 16), G(1, 1, 4, 16),
               G(1, 1, 0, 16), G(1, 1, 8, 8), G(1, 1, 8, 0), G(1, 1, 8, 24), G(1, 1, 12, 16), G(1, 1, (1 << 20) + 8, 16),
-              G(1, 1, 8, (1 << 20) + 16), G(1, 1, -8, 16), G(1, 1, 8, -16)):
+              G(1, 1, 8, (1 << 20) + 16), G(1, 1 << 20, 8, 1 << 20), G(1, 1, 1 << 20, 1 << 20), G(1, 1, -8, 16), G(1, 1, 8, -16)):
         assert ep.ep_check_gemm_shape(s) == ep.EP_ERR_INVALID_ARG
 
 

@@ -67,11 +67,10 @@ struct Params {
 
 // One wait of a role: false when the limit passes or another role gave up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Shared* s) {
-    const uint32_t addr = smem_addr(bar);
-    if (mbar_try_wait_cluster(addr, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     long long start = 0;
     uint32_t polls = 0;
-    while (!mbar_try_wait_cluster(addr, parity)) {
+    while (!mbar_try_wait(bar, parity)) {
         if ((++polls & 63u) != 0) continue;
         if (*reinterpret_cast<volatile int*>(&s->abort) != 0) return false;
         const long long now = globaltimer_ns();
@@ -302,12 +301,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_wait(y);
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
+                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
                         fma32(acc + 48, y, s1);
                     } else {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
+                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
                     }
                 }
             }

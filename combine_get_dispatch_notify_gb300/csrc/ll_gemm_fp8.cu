@@ -41,7 +41,7 @@ constexpr int kTileBytes = kHalf * kBlockK;    // 16 KB, one operand of a stage
 constexpr int kStages = 6;
 constexpr int kThreads = 384;                  // producer, MMA, TMEM, spare | two epilogue warpgroups
 constexpr int kEpilogueWarps = 8;
-constexpr int kAccColumns = 256;               // TMEM columns of one accumulator
+constexpr int kAccColumns = kTileN;            // TMEM columns of one accumulator
 constexpr int kTmemColumns = 512;
 constexpr long long kWaitLimitNs = 2000000000LL;
 
@@ -124,24 +124,37 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
                  : "memory");
 }
 
-// Scales of four consecutive k-blocks for one row and two weight blocks.
-struct Scales {
-    float a[4], w0[4], w1[4];
-};
-__device__ __forceinline__ void load_scales(Scales& s, const float* as, const float* w0, const float* w1, int kb,
-                                            int end, bool on) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = on && kb + i < end;
-        s.a[i] = in ? __ldg(as + kb + i) : 0.0f;
-        s.w0[i] = in ? __ldg(w0 + kb + i) : 0.0f;
-        s.w1[i] = in ? __ldg(w1 + kb + i) : 0.0f;
+// One row's scales, four k-blocks at a time, the next four on their way.
+struct RowScales {
+    float4 cur, next;
+    __device__ __forceinline__ static float4 load(const float* as, int b, int kb, bool on) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!on || b >= kb) return v;
+        if (kb % 4 == 0) return __ldg(reinterpret_cast<const float4*>(as + b));  // rows on 16-byte boundaries
+        v.x = __ldg(as + b);
+        if (b + 1 < kb) v.y = __ldg(as + b + 1);
+        if (b + 2 < kb) v.z = __ldg(as + b + 2);
+        if (b + 3 < kb) v.w = __ldg(as + b + 3);
+        return v;
     }
-}
+    __device__ __forceinline__ void start(const float* as, int kb, bool on) {
+        cur = load(as, 0, kb, on);
+        next = load(as, 4, kb, on);
+    }
+    __device__ __forceinline__ void advance(const float* as, int b, int kb, bool on) {
+        cur = make_float4(cur.y, cur.z, cur.w, 0.0f);
+        if (b % 4 == 3) {
+            cur = next;
+            next = load(as, b + 5, kb, on);
+        }
+    }
+};
 
-__device__ __forceinline__ void fma32(unsigned long long* acc, const uint32_t (&r)[32], unsigned long long s) {
+// Scalar FMAs: the packed form (fma.rn.f32x2) runs at the same rate on this
+// part (256 cycles for a block's 32768) and costs moves to pair its operands.
+__device__ __forceinline__ void fma32(float* acc, const float (&r)[32], float s) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) fma2(acc[j], r[2 * j], r[2 * j + 1], s);
+    for (int j = 0; j < 32; ++j) acc[j] = fmaf(r[j], s, acc[j]);
 }
 
 template <bool kSwiglu>
@@ -231,17 +244,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int b = 0; b < p.kb; ++b, ++it) {
-                    const uint32_t st = it % kStages, acc = it & 1, round = it / 2;
-                    if (round > 0 && !(ok = wait_for(&s->bar.acc_empty[acc], (round - 1) & 1, s))) break;
+                    const uint32_t st = it % kStages, buf = it & 1, round = it / 2;
                     if (!(ok = wait_for(&s->bar.full[st], (it / kStages) & 1, s))) break;
+                    if (round > 0 && !(ok = wait_for(&s->bar.acc_empty[buf], (round - 1) & 1, s))) break;
                     tc_fence_after();
                     const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
                     const uint64_t da = sw128_desc(ta), dw = sw128_desc(ta + kTileBytes);
 #pragma unroll
                     for (int k = 0; k < kBlockK / 32; ++k)  // 32 bytes further inside the swizzled row
-                        mma_e4m3_pair(tmem + acc * kAccColumns, da + 2 * k, dw + 2 * k, idesc, k > 0);
+                        mma_e4m3_pair(tmem + buf * kAccColumns, da + 2 * k, dw + 2 * k, idesc, k > 0);
+                    mma_commit_pair(smem_addr(&s->bar.acc_full[buf]));
                     mma_commit_pair(smem_addr(&s->bar.empty[st]));
-                    mma_commit_pair(smem_addr(&s->bar.acc_full[acc]));
                 }
             }
         }
@@ -252,6 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int g = (warp - 4) / 4, quarter = warp % 4;
         const int row = quarter * kWarp + lane;  // of this CTA's 128
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
+        const uint32_t empty[2] = {mapa(smem_addr(&s->bar.acc_empty[0]), 0), mapa(smem_addr(&s->bar.acc_empty[1]), 0)};
         uint32_t it = 0, parity = 0;
         Walk walk;
         bool ok = true;
@@ -267,47 +281,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float* w0 = p.g.w_scales + (mat * p.nb + wb) * p.kb;
             // the tile's second weight block: the up matrix, or the next 128 columns (the same again past the end)
             const float* w1 = kSwiglu ? w0 + static_cast<long long>(p.nb) * p.kb : (wb + 1 < p.nb ? w0 + p.kb : w0);
-            unsigned long long acc[64];
+            float acc[128];  // 64 columns of the first weight block, 64 of the second
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
-            Scales cur, next;
-            load_scales(next, as, w0, w1, 0, p.kb, valid);
-            for (int b = 0; b < p.kb && ok; b += 4) {
-                cur = next;
-                load_scales(next, as, w0, w1, b + 4, p.kb, valid);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (b + i >= p.kb || !ok) break;
-                    const uint32_t buf = it & 1;
-                    ok = wait_for(&s->bar.acc_full[buf], (it / 2) & 1, s);
-                    ++it;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (warp_on) {
-                        const unsigned long long s0 = pair2(cur.a[i] * cur.w0[i]), s1 = pair2(cur.a[i] * cur.w1[i]);
-                        const uint32_t col = lanes + buf * kAccColumns + g * 64;
-                        uint32_t x[32], y[32];
-                        tmem_ld32(col, x);
-                        tmem_wait(x);
-                        tmem_ld32(col + 32, y);
-                        fma32(acc, x, s0);
-                        tmem_wait(y);
-                        tmem_ld32(col + 128, x);
-                        fma32(acc + 16, y, s0);
-                        tmem_wait(x);
-                        tmem_ld32(col + 160, y);
-                        fma32(acc + 32, x, s1);
-                        tmem_wait(y);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
-                        fma32(acc + 48, y, s1);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa(smem_addr(&s->bar.acc_empty[buf]), 0));
-                    }
+            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            RowScales rs;
+            rs.start(as, p.kb, valid);
+            float c0 = __ldg(w0), c1 = __ldg(w1);
+#pragma unroll 1
+            for (int b = 0; b < p.kb; ++b, ++it) {
+                const uint32_t buf = it & 1;
+                const float s0 = rs.cur.x * c0, s1 = rs.cur.x * c1;
+                rs.advance(as, b, p.kb, valid);
+                if (b + 1 < p.kb) {
+                    c0 = __ldg(w0 + b + 1);
+                    c1 = __ldg(w1 + b + 1);
+                }
+                ok = __all_sync(0xffffffffu, wait_for(&s->bar.acc_full[buf], (it / 2) & 1, s));
+                if (!ok) break;
+                tc_fence_after();
+                if (warp_on) {
+                    const uint32_t col = lanes + buf * kAccColumns + g * 64;
+                    float x[32];
+                    tmem_read32(col, x);
+                    fma32(acc, x, s0);
+                    tmem_read32(col + 32, x);
+                    fma32(acc + 32, x, s0);
+                    tmem_read32(col + 128, x);
+                    fma32(acc + 64, x, s1);
+                    tmem_read32(col + 160, x);
+                    tc_fence_before();  // the block's sums have left TMEM
+                    if (lane == 0) mbar_arrive_cluster_relaxed(empty[buf]);
+                    fma32(acc + 96, x, s1);
+                } else {
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(empty[buf]);
                 }
             }
             if (!ok) {
@@ -325,8 +332,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float2 f = unpack2(acc[j * 8 + i]);
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                            const __nv_bfloat162 h =
+                                __floats2bfloat162_rn(acc[j * 16 + 2 * i], acc[j * 16 + 2 * i + 1]);
                             v[i] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                         if (wide) {
@@ -342,11 +349,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float h[64];
                 float amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float2 a = unpack2(acc[j]), u = unpack2(acc[32 + j]);
-                    h[2 * j] = __fdividef(a.x, 1.0f + __expf(-a.x)) * u.x;
-                    h[2 * j + 1] = __fdividef(a.y, 1.0f + __expf(-a.y)) * u.y;
-                    amax = fmaxf(amax, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
+                for (int j = 0; j < 64; ++j) {
+                    h[j] = __fdividef(acc[j], 1.0f + __expf(-acc[j])) * acc[64 + j];
+                    amax = fmaxf(amax, fabsf(h[j]));
                 }
                 // the other warpgroup has the block's other 64 columns
                 s->amax[parity][g][row] = amax;

@@ -39,8 +39,11 @@ constexpr int kChunk = 32;                     // rows of one TMA box of a
 constexpr int kBlockK = kScaleBlock;           // 128 e4m3: one 128-byte swizzled row
 constexpr int kTileBytes = kHalf * kBlockK;    // 16 KB, one operand of a stage
 constexpr int kStages = 6;
-constexpr int kThreads = 384;                  // producer, MMA, TMEM, spare | two epilogue warpgroups
-constexpr int kEpilogueWarps = 8;
+constexpr int kGroups = 4;                     // epilogue warpgroups, 64 columns of a tile each
+constexpr int kGroupCols = kHalf / kGroups;    // of each of the tile's two weight blocks
+constexpr int kThreads = 128 + 128 * kGroups;  // producer, MMA, two scale warps | epilogue
+constexpr int kEpilogueWarps = 4 * kGroups;
+constexpr int kScaleSlots = 4;
 constexpr int kAccColumns = kTileN;            // TMEM columns of one accumulator
 constexpr int kTmemColumns = 512;
 constexpr long long kWaitLimitNs = 2000000000LL;
@@ -48,13 +51,14 @@ constexpr long long kWaitLimitNs = 2000000000LL;
 struct Barriers {
     uint64_t full[kStages];   // leader's: bytes of both CTAs have landed
     uint64_t empty[kStages];  // both: the MMAs that read the stage are done
-    uint64_t acc_full[2];     // both: a block's sums are in TMEM
+    uint64_t acc_full[2];     // both: a block's sums are in TMEM, its scales in shared memory
     uint64_t acc_empty[2];    // leader's: every epilogue warp of the pair has read them
 };
 
 struct Shared {
     Barriers bar;
-    float amax[2][2][kHalf];  // [tile parity][warpgroup][row]
+    float2 scale[kScaleSlots][kHalf];   // of each row with the tile's two weight blocks
+    float amax[2][kGroups][kHalf];      // [tile parity][warpgroup][row]
     int first[8192 / kWarp + 2];  // tiles before each group of 32 experts
     uint32_t tmem;
     int abort;
@@ -118,43 +122,45 @@ __device__ __forceinline__ Tile tile_at(int t, Walk& w, const int* first, const 
     return r;
 }
 
+// Row `row` of this CTA's half of the tile, in the packed rows of all experts.
+__device__ __forceinline__ long long tile_row(const Tile& t, const Params& p, uint32_t rank, int row) {
+    return static_cast<long long>(t.e) * p.g.cap + t.m0 + static_cast<int>(rank) * kHalf + row;
+}
+// Scales of the tile's two weight blocks: gate and up, or two neighbours (the
+// last one twice when it has no neighbour; its columns are past n then).
+template <bool kSwiglu>
+__device__ __forceinline__ void weight_scales(const Tile& t, const Params& p, const float** w0, const float** w1) {
+    const int block = t.n0 / kScaleBlock;
+    *w0 = p.g.w_scales + (static_cast<long long>(t.e) * (kSwiglu ? 2 : 1) * p.nb + block) * p.kb;
+    *w1 = *w0 + (kSwiglu ? static_cast<long long>(p.nb) * p.kb : (block + 1 < p.nb ? p.kb : 0));
+}
+
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
 
-// One row's scales, four k-blocks at a time, the next four on their way.
-struct RowScales {
-    float4 cur, next;
-    __device__ __forceinline__ static float4 load(const float* as, int b, int kb, bool on) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!on || b >= kb) return v;
-        if (kb % 4 == 0) return __ldg(reinterpret_cast<const float4*>(as + b));  // rows on 16-byte boundaries
-        v.x = __ldg(as + b);
-        if (b + 1 < kb) v.y = __ldg(as + b + 1);
-        if (b + 2 < kb) v.z = __ldg(as + b + 2);
-        if (b + 3 < kb) v.w = __ldg(as + b + 3);
-        return v;
-    }
-    __device__ __forceinline__ void start(const float* as, int kb, bool on) {
-        cur = load(as, 0, kb, on);
-        next = load(as, 4, kb, on);
-    }
-    __device__ __forceinline__ void advance(const float* as, int b, int kb, bool on) {
-        cur = make_float4(cur.y, cur.z, cur.w, 0.0f);
-        if (b % 4 == 3) {
-            cur = next;
-            next = load(as, b + 5, kb, on);
-        }
-    }
-};
+// Four consecutive k-blocks' scales of a row or a weight block (0 past the end).
+__device__ __forceinline__ float4 load_scales(const float* p, int b, int kb, bool on) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!on || b >= kb) return v;
+    if (kb % 4 == 0) return __ldg(reinterpret_cast<const float4*>(p + b));  // rows on 16-byte boundaries
+    v.x = __ldg(p + b);
+    if (b + 1 < kb) v.y = __ldg(p + b + 1);
+    if (b + 2 < kb) v.z = __ldg(p + b + 2);
+    if (b + 3 < kb) v.w = __ldg(p + b + 3);
+    return v;
+}
+__device__ __forceinline__ float element(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Scalar FMAs: the packed form (fma.rn.f32x2) runs at the same rate on this
-// part (256 cycles for a block's 32768) and costs moves to pair its operands.
-__device__ __forceinline__ void fma32(float* acc, const float (&r)[32], float s) {
+// acc += s * (16 columns of TMEM).  Scalar FMAs: the packed form (fma.rn.f32x2)
+// runs at the same rate on this part and costs moves to pair its operands.
+__device__ __forceinline__ void add16(float* acc, uint32_t tmem, float s) {
+    float x[16];
+    tmem_read16(tmem, x);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) acc[j] = fmaf(r[j], s, acc[j]);
+    for (int j = 0; j < 16; ++j) acc[j] = fmaf(x[j], s, acc[j]);
 }
 
 template <bool kSwiglu>
@@ -177,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&s->bar.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s->bar.acc_full[i], 1);
+            mbar_init(&s->bar.acc_full[i], 3);  // the MMAs and two scale warps
             mbar_init(&s->bar.acc_empty[i], 2 * kEpilogueWarps);
         }
         s->abort = 0;
@@ -185,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_w);
     }
-    if (warp == 2) tmem_alloc_pair(&s->tmem, kTmemColumns);
+    if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_launch_dependents();
     griddep_wait();  // counts, rows and scales are complete from here on
     const int groups = (p.g.E + kWarp - 1) / kWarp;
@@ -208,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int tiles = s->first[groups];
 
     if (warp < 4) {
-        regs_down<48>();
+        regs_down<64>();
         if (warp == 0 && lane == 0) {
             // ---- producer: this CTA's rows of a and its half of the weight rows ----
             uint32_t it = 0;
@@ -258,77 +264,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (warp >= 2) {
+            // ---- scales: a row's scale times each weight block's, for two rows a thread, four k-blocks at a time ----
+            const int row = threadIdx.x - 64;
+            uint32_t it = 0;
+            Walk walk;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const Tile tl = tile_at(t, walk, s->first, p, cols);
+                const int left = tl.rows - static_cast<int>(rank) * kHalf;
+                const float* a0 = p.g.a_scales + tile_row(tl, p, rank, row) * p.kb;
+                const float* a1 = a0 + 64LL * p.kb;
+                const float *w0, *w1;
+                weight_scales<kSwiglu>(tl, p, &w0, &w1);
+                float4 na0 = load_scales(a0, 0, p.kb, row < left), na1 = load_scales(a1, 0, p.kb, row + 64 < left),
+                       nw0 = load_scales(w0, 0, p.kb, true), nw1 = load_scales(w1, 0, p.kb, true);
+                for (int b = 0; b < p.kb && ok; b += 4) {
+                    const float4 va0 = na0, va1 = na1, vw0 = nw0, vw1 = nw1;
+                    na0 = load_scales(a0, b + 4, p.kb, row < left);  // on their way while these are handed over
+                    na1 = load_scales(a1, b + 4, p.kb, row + 64 < left);
+                    nw0 = load_scales(w0, b + 4, p.kb, true);
+                    nw1 = load_scales(w1, b + 4, p.kb, true);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (b + i >= p.kb) break;
+                        // Sums of block it - 2 complete: its MMA waited for the reads of block it - 4, the slot's last user.
+                        const uint32_t buf = it & 1;
+                        ok = it < 2 || wait_for(&s->bar.acc_full[buf], (it / 2 - 1) & 1, s);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        float2* slot = s->scale[it % kScaleSlots];
+                        const float u = element(va0, i), v = element(va1, i), x = element(vw0, i), y = element(vw1, i);
+                        slot[row] = make_float2(u * x, u * y);
+                        slot[row + 64] = make_float2(v * x, v * y);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s->bar.acc_full[buf]);
+                        ++it;
+                    }
+                }
+            }
+        }
         __syncwarp();
     } else {
-        // ---- epilogue: thread = one row; warpgroup g sums columns 64 g + [0, 64) of both weight blocks ----
-        regs_up<224>();
+        // ---- epilogue: thread = one row; warpgroup g sums columns 32 g + [0, 32) of both weight blocks ----
+        regs_up<104>();
         const int g = (warp - 4) / 4, quarter = warp % 4;
         const int row = quarter * kWarp + lane;  // of this CTA's 128
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
-        const uint32_t empty[2] = {mapa(smem_addr(&s->bar.acc_empty[0]), 0), mapa(smem_addr(&s->bar.acc_empty[1]), 0)};
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g * kGroupCols;
+        const uint32_t empty = mapa(smem_addr(&s->bar.acc_empty[0]), 0);
         uint32_t it = 0, parity = 0;
         Walk walk;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
             const Tile tl = tile_at(t, walk, s->first, p, cols);
             const int left = tl.rows - static_cast<int>(rank) * kHalf;
-            const bool valid = row < left;
             const bool warp_on = quarter * kWarp < left;
-            const long long r = static_cast<long long>(tl.e) * p.g.cap + tl.m0 + static_cast<int>(rank) * kHalf + row;
-            const float* as = p.g.a_scales + r * p.kb;
-            const int wb = tl.n0 / kScaleBlock;
-            const long long mat = static_cast<long long>(tl.e) * (kSwiglu ? 2 : 1);
-            const float* w0 = p.g.w_scales + (mat * p.nb + wb) * p.kb;
-            // the tile's second weight block: the up matrix, or the next 128 columns (the same again past the end)
-            const float* w1 = kSwiglu ? w0 + static_cast<long long>(p.nb) * p.kb : (wb + 1 < p.nb ? w0 + p.kb : w0);
-            float acc[128];  // 64 columns of the first weight block, 64 of the second
+            float acc[2 * kGroupCols];  // of the first weight block, then of the second
 #pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-            RowScales rs;
-            rs.start(as, p.kb, valid);
-            float c0 = __ldg(w0), c1 = __ldg(w1);
+            for (int j = 0; j < 2 * kGroupCols; ++j) acc[j] = 0.0f;
 #pragma unroll 1
-            for (int b = 0; b < p.kb; ++b, ++it) {
+            for (int b = p.kb; b > 0; --b, ++it) {
                 const uint32_t buf = it & 1;
-                const float s0 = rs.cur.x * c0, s1 = rs.cur.x * c1;
-                rs.advance(as, b, p.kb, valid);
-                if (b + 1 < p.kb) {
-                    c0 = __ldg(w0 + b + 1);
-                    c1 = __ldg(w1 + b + 1);
-                }
                 ok = __all_sync(0xffffffffu, wait_for(&s->bar.acc_full[buf], (it / 2) & 1, s));
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_on) {
-                    const uint32_t col = lanes + buf * kAccColumns + g * 64;
-                    float x[32];
-                    tmem_read32(col, x);
-                    fma32(acc, x, s0);
-                    tmem_read32(col + 32, x);
-                    fma32(acc + 32, x, s0);
-                    tmem_read32(col + 128, x);
-                    fma32(acc + 64, x, s1);
-                    tmem_read32(col + 160, x);
+                    const float2 sc = s->scale[it % kScaleSlots][row];
+                    const uint32_t col = lanes + buf * kAccColumns;
+                    add16(acc, col, sc.x);
+                    add16(acc + 16, col + 16, sc.x);
+                    add16(acc + 32, col + kHalf, sc.y);
+                    float x[16];
+                    tmem_read16(col + kHalf + 16, x);
                     tc_fence_before();  // the block's sums have left TMEM
-                    if (lane == 0) mbar_arrive_cluster_relaxed(empty[buf]);
-                    fma32(acc + 96, x, s1);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[48 + j] = fmaf(x[j], sc.y, acc[48 + j]);
                 } else {
                     tc_fence_before();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(empty[buf]);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
                 }
             }
             if (!ok) {
-                // the partner warp may be waiting for this one's maxima
-                if (kSwiglu && warp_on) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");
+                // the quarter's other warps may be waiting for this one's maxima
+                if (kSwiglu && warp_on) asm volatile("bar.arrive %0, 128;" ::"r"(1 + quarter) : "memory");
                 break;
             }
+            const bool valid = row < left;
+            const long long r = tile_row(tl, p, rank, row);
             if (!kSwiglu) {
                 if (valid) {
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r * p.g.n;
                     const bool wide = p.g.n % 16 == 0;  // rows on 32-byte boundaries
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {  // 16 columns
-                        const int col = tl.n0 + (j / 4) * 128 + g * 64 + (j % 4) * 16;
+                    for (int j = 0; j < 4; ++j) {  // 16 columns
+                        const int col = tl.n0 + (j / 2) * kHalf + g * kGroupCols + (j % 2) * 16;
                         uint32_t v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -346,31 +378,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             } else if (warp_on) {
                 // h = gate / (1 + exp(-gate)) * up; columns past n have zero weights, so h = 0 there
-                float h[64];
                 float amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    h[j] = __fdividef(acc[j], 1.0f + __expf(-acc[j])) * acc[64 + j];
-                    amax = fmaxf(amax, fabsf(h[j]));
+                for (int j = 0; j < kGroupCols; ++j) {
+                    acc[j] = __fdividef(acc[j], 1.0f + __expf(-acc[j])) * acc[kGroupCols + j];
+                    amax = fmaxf(amax, fabsf(acc[j]));
                 }
-                // the other warpgroup has the block's other 64 columns
+                // the other warpgroups have the rest of the block's 128 columns
                 s->amax[parity][g][row] = amax;
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                const float scale = block_scale(fmaxf(s->amax[parity][0][row], s->amax[parity][1][row]));
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) amax = fmaxf(amax, s->amax[parity][i][row]);
+                const float scale = block_scale(amax);
                 if (valid) {
                     const float inv = 1.0f / scale;
                     uint8_t* out = static_cast<uint8_t*>(p.g.y) + r * p.g.n;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // 16 columns
-                        const int col = tl.n0 + g * 64 + j * 16;
+                    for (int j = 0; j < 2; ++j) {  // 16 columns
+                        const int col = tl.n0 + g * kGroupCols + j * 16;
                         uint32_t v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[i] = pack_e4m3x4(h[j * 16 + i * 4] * inv, h[j * 16 + i * 4 + 1] * inv,
-                                               h[j * 16 + i * 4 + 2] * inv, h[j * 16 + i * 4 + 3] * inv);
+                            v[i] = pack_e4m3x4(acc[j * 16 + i * 4] * inv, acc[j * 16 + i * 4 + 1] * inv,
+                                               acc[j * 16 + i * 4 + 2] * inv, acc[j * 16 + i * 4 + 3] * inv);
                         if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
                     }
-                    if (g == 0) p.g.y_scales[r * p.nb + wb] = scale;
+                    if (g == 0) p.g.y_scales[r * p.nb + tl.n0 / kScaleBlock] = scale;
                 }
             }
         }
@@ -387,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_arrive_release();
     cluster_wait_acquire();
     tc_fence_after();
-    if (warp == 2) tmem_dealloc_pair(tmem, kTmemColumns);
+    if (warp == 4) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

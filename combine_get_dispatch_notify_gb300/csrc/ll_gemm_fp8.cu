@@ -41,25 +41,27 @@ constexpr int kTileBytes = kHalf * kBlockK;    // 16 KB, one operand of a stage
 constexpr int kStages = 6;
 constexpr int kGroups = 4;                     // epilogue warpgroups, 64 columns of a tile each
 constexpr int kGroupCols = kHalf / kGroups;    // of each of the tile's two weight blocks
-constexpr int kThreads = 128 + 128 * kGroups;  // producer, MMA, two scale warps | epilogue
-constexpr int kEpilogueWarps = 4 * kGroups;
-constexpr int kScaleSlots = 4;
-constexpr int kAccColumns = kTileN;            // TMEM columns of one accumulator
+constexpr int kThreads = 128 + 128 * kGroups;  // producer, two MMA warps, scale warp | epilogue
+constexpr int kScaleSlots = 3;                 // of four k-blocks each
+constexpr int kHalfN = kTileN / 2;             // weight rows of one MMA: 64 of each CTA's 128; its TMEM columns
 constexpr int kTmemColumns = 512;
 constexpr long long kWaitLimitNs = 2000000000LL;
 
 struct Barriers {
-    uint64_t full[kStages];   // leader's: bytes of both CTAs have landed
-    uint64_t empty[kStages];  // both: the MMAs that read the stage are done
-    uint64_t acc_full[2];     // both: a block's sums are in TMEM, its scales in shared memory
-    uint64_t acc_empty[2];    // leader's: every epilogue warp of the pair has read them
+    uint64_t full[kStages];             // leader's: bytes of both CTAs have landed
+    uint64_t empty[kStages];            // both: the MMAs that read the stage are done
+    uint64_t acc_full[2][2];            // [half][buffer], both: a block's sums are in TMEM
+    uint64_t acc_empty[2][2];           // leader's: the half's epilogue warps of the pair have read them
+    uint64_t scale_full[kScaleSlots];   // both: the scales of four blocks are in shared memory
+    uint64_t scale_empty[kScaleSlots];  // both: every epilogue warp is done with them
 };
 
 struct Shared {
     Barriers bar;
-    float2 scale[kScaleSlots][kHalf];   // of each row with the tile's two weight blocks
-    float amax[2][kGroups][kHalf];      // [tile parity][warpgroup][row]
-    int first[8192 / kWarp + 2];  // tiles before each group of 32 experts
+    float row_scale[kScaleSlots][4][kHalf];  // of each row of the CTA
+    float2 w_scale[kScaleSlots][4];          // of the tile's two weight blocks
+    float amax[2][kGroups][kHalf];           // [tile parity][warpgroup][row]
+    int first[8192 / kWarp + 2];             // tiles before each group of 32 experts
     uint32_t tmem;
     int abort;
 };
@@ -69,22 +71,20 @@ struct Params {
     int kb, nb, tiles_n;
 };
 
-// One wait of a role: false when the limit passes or another role gave up.
+// One wait of a role: false when the limit passes.
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Shared* s) {
+    const long long start = globaltimer_ns();
+    do {
+        for (int i = 0; i < 1024; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+    } while (globaltimer_ns() - start < kWaitLimitNs);
+    *reinterpret_cast<volatile int*>(&s->abort) = 1;
+    return false;
+}
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Shared* s) {
-    if (mbar_try_wait(bar, parity)) return true;
-    long long start = 0;
-    uint32_t polls = 0;
-    while (!mbar_try_wait(bar, parity)) {
-        if ((++polls & 63u) != 0) continue;
-        if (*reinterpret_cast<volatile int*>(&s->abort) != 0) return false;
-        const long long now = globaltimer_ns();
-        if (start == 0) start = now;
-        if (now - start > kWaitLimitNs) {
-            *reinterpret_cast<volatile int*>(&s->abort) = 1;
-            return false;
-        }
-    }
-    return true;
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, s);
 }
 
 // The pair's tiles: experts in order, then row tiles, then weight tiles.
@@ -126,13 +126,13 @@ __device__ __forceinline__ Tile tile_at(int t, Walk& w, const int* first, const 
 __device__ __forceinline__ long long tile_row(const Tile& t, const Params& p, uint32_t rank, int row) {
     return static_cast<long long>(t.e) * p.g.cap + t.m0 + static_cast<int>(rank) * kHalf + row;
 }
-// Scales of the tile's two weight blocks: gate and up, or two neighbours (the
-// last one twice when it has no neighbour; its columns are past n then).
+// Scales of the tile's weight block `which` (0 or 1): gate and up, or two
+// neighbours (the last one again when it has no neighbour; those columns are past n).
 template <bool kSwiglu>
-__device__ __forceinline__ void weight_scales(const Tile& t, const Params& p, const float** w0, const float** w1) {
-    const int block = t.n0 / kScaleBlock;
-    *w0 = p.g.w_scales + (static_cast<long long>(t.e) * (kSwiglu ? 2 : 1) * p.nb + block) * p.kb;
-    *w1 = *w0 + (kSwiglu ? static_cast<long long>(p.nb) * p.kb : (block + 1 < p.nb ? p.kb : 0));
+__device__ __forceinline__ const float* weight_scales(const Tile& t, const Params& p, int which) {
+    const long long first = static_cast<long long>(t.e) * (kSwiglu ? 2 : 1) * p.nb + t.n0 / kScaleBlock;
+    const long long block = kSwiglu ? which * p.nb : min(which, p.nb - 1 - t.n0 / kScaleBlock);
+    return p.g.w_scales + (first + block) * p.kb;
 }
 
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
@@ -152,27 +152,21 @@ __device__ __forceinline__ float4 load_scales(const float* p, int b, int kb, boo
     if (b + 3 < kb) v.w = __ldg(p + b + 3);
     return v;
 }
-__device__ __forceinline__ float element(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// acc += s * (16 columns of TMEM).  Scalar FMAs: the packed form (fma.rn.f32x2)
-// runs at the same rate on this part and costs moves to pair its operands.
-__device__ __forceinline__ void add16(float* acc, uint32_t tmem, float s) {
-    float x[16];
-    tmem_read16(tmem, x);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = fmaf(x[j], s, acc[j]);
+__device__ __forceinline__ float element(const float4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 template <bool kSwiglu>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ll_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+    ll_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_a128, const __grid_constant__ CUtensorMap map_w,
                        const Params p) {
     extern __shared__ uint8_t s_raw[];
     // stages first, on a 1024-byte boundary as the swizzle needs, at the same offset in both CTAs
     const uint32_t pad = (1024u - (smem_addr(s_raw) & 1023u)) & 1023u;
     uint8_t* s_tiles = s_raw + pad;
     Shared* s = reinterpret_cast<Shared*>(s_tiles + kStages * 2 * kTileBytes);
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int cols = kSwiglu ? kTileN / 2 : kTileN;  // output columns of a tile
@@ -180,11 +174,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s->bar.full[i], 1);
-            mbar_init(&s->bar.empty[i], 1);
+            mbar_init(&s->bar.empty[i], 2);  // both halves' MMAs
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s->bar.acc_full[i], 3);  // the MMAs and two scale warps
-            mbar_init(&s->bar.acc_empty[i], 2 * kEpilogueWarps);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s->bar.acc_full[i / 2][i % 2], 1);
+            mbar_init(&s->bar.acc_empty[i / 2][i % 2], 4 * kGroups);  // half the epilogue warps, in both CTAs
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&s->bar.scale_full[i], 1);
+            mbar_init(&s->bar.scale_empty[i], 4 * kGroups);
         }
         s->abort = 0;
         fence_mbarrier_init();
@@ -217,9 +215,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         regs_down<64>();
         if (warp == 0 && lane == 0) {
             // ---- producer: this CTA's rows of a and its half of the weight rows ----
-            uint32_t it = 0;
+            uint32_t st = 0, phase = 1;  // a fresh barrier passes a wait for phase 1
             Walk walk;
             bool ok = true;
+            const uint32_t full = mapa(smem_addr(&s->bar.full[0]), 0);
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const Tile tl = tile_at(t, walk, s->first, p, cols);
                 const int chunks0 = (min(tl.rows, kHalf) + kChunk - 1) / kChunk;
@@ -229,79 +228,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int wy = kSwiglu ? tl.n0 : tl.n0 + static_cast<int>(rank) * kHalf;
                 const int wz = kSwiglu ? 2 * tl.e + static_cast<int>(rank) : tl.e;
                 const int ay = tl.m0 + static_cast<int>(rank) * kHalf;
-                for (int b = 0; b < p.kb; ++b, ++it) {
-                    const uint32_t st = it % kStages, use = it / kStages;
-                    if (use > 0 && !(ok = wait_for(&s->bar.empty[st], (use - 1) & 1, s))) break;
+                for (int b = 0; b < p.kb; ++b) {
+                    if (!(ok = wait_for(&s->bar.empty[st], phase, s))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&s->bar.full[st], bytes);
-                    const uint32_t bar = mapa(smem_addr(&s->bar.full[st]), 0);
+                    const uint32_t bar = full + st * sizeof(uint64_t);
                     const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
                     tma_load_3d(ta + kTileBytes, &map_w, b * kBlockK, wy, wz, bar);
-                    for (int c = 0; c < chunks; ++c)
-                        tma_load_3d(ta + c * kChunk * kBlockK, &map_a, b * kBlockK, ay + c * kChunk, tl.e, bar);
+                    if (chunks == kHalf / kChunk)
+                        tma_load_3d(ta, &map_a128, b * kBlockK, ay, tl.e, bar);
+                    else
+                        for (int c = 0; c < chunks; ++c)
+                            tma_load_3d(ta + c * kChunk * kBlockK, &map_a, b * kBlockK, ay + c * kChunk, tl.e, bar);
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             // every stage's last read is over before the CTA may leave
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it && ok; ++i)
-                ok = wait_for(&s->bar.empty[i % kStages], (i / kStages) & 1, s);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            // ---- MMA: one thread feeds the pair's tensor cores ----
-            constexpr uint32_t idesc = e4m3_idesc(kTileM, kTileN);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                for (int b = 0; b < p.kb; ++b, ++it) {
-                    const uint32_t st = it % kStages, buf = it & 1, round = it / 2;
-                    if (!(ok = wait_for(&s->bar.full[st], (it / kStages) & 1, s))) break;
-                    if (round > 0 && !(ok = wait_for(&s->bar.acc_empty[buf], (round - 1) & 1, s))) break;
-                    tc_fence_after();
-                    const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
-                    const uint64_t da = sw128_desc(ta), dw = sw128_desc(ta + kTileBytes);
+            for (int i = 0; i < kStages && ok; ++i) {
+                ok = wait_for(&s->bar.empty[st], phase, s);
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        } else if ((warp == 1 || warp == 2) && rank == 0) {
+            // ---- MMA: two warps feed the pair's tensor cores, one for each half of the tile's columns.  One half's
+            // sums cross to its epilogue warps, and its accumulator comes back, while the other half multiplies ----
+            constexpr uint32_t idesc = e4m3_idesc(kTileM, kHalfN);
+            const uint32_t half = warp - 1;
+            const uint32_t blocks = pair < tiles ? (tiles - pair + pairs - 1) / pairs * p.kb : 0;
+            uint32_t st = 0, full_phase = 0, buf = 0, empty_phase = 1;
+            for (uint32_t it = 0; it < blocks; ++it) {
+                // everything but the accumulator's hand-back is settled before the wait for it: what follows that
+                // wait is on the path of every block
+                bool ok = wait_for(&s->bar.full[st], full_phase, s);
+                const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
+                uint64_t da = sw128_desc(ta), dw = sw128_desc(ta + kTileBytes + half * (kTileBytes / 2));
+                asm volatile("" : "+l"(da), "+l"(dw));
+                ok = ok && wait_for(&s->bar.acc_empty[half][buf], empty_phase, s);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kBlockK / 32; ++k)  // 32 bytes further inside the swizzled row
-                        mma_e4m3_pair(tmem + buf * kAccColumns, da + 2 * k, dw + 2 * k, idesc, k > 0);
-                    mma_commit_pair(smem_addr(&s->bar.acc_full[buf]));
+                        mma_e4m3_pair(tmem + (2 * half + buf) * kHalfN, da + 2 * k, dw + 2 * k, idesc, k > 0);
+                    mma_commit_pair(smem_addr(&s->bar.acc_full[half][buf]));
                     mma_commit_pair(smem_addr(&s->bar.empty[st]));
+                }
+                __syncwarp();
+                buf ^= 1;
+                empty_phase ^= buf ^ 1;  // both buffers share a phase
+                if (++st == kStages) {
+                    st = 0;
+                    full_phase ^= 1;
                 }
             }
         }
-        if (warp >= 2) {
-            // ---- scales: a row's scale times each weight block's, for two rows a thread, four k-blocks at a time ----
-            const int row = threadIdx.x - 64;
-            uint32_t it = 0;
+        if (warp == 3) {
+            // ---- scales: four rows a lane, four k-blocks at a time, handed over through shared memory ----
+            uint32_t slot = 0, phase = 1;
             Walk walk;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const Tile tl = tile_at(t, walk, s->first, p, cols);
                 const int left = tl.rows - static_cast<int>(rank) * kHalf;
-                const float* a0 = p.g.a_scales + tile_row(tl, p, rank, row) * p.kb;
-                const float* a1 = a0 + 64LL * p.kb;
-                const float *w0, *w1;
-                weight_scales<kSwiglu>(tl, p, &w0, &w1);
-                float4 na0 = load_scales(a0, 0, p.kb, row < left), na1 = load_scales(a1, 0, p.kb, row + 64 < left),
-                       nw0 = load_scales(w0, 0, p.kb, true), nw1 = load_scales(w1, 0, p.kb, true);
-                for (int b = 0; b < p.kb && ok; b += 4) {
-                    const float4 va0 = na0, va1 = na1, vw0 = nw0, vw1 = nw1;
-                    na0 = load_scales(a0, b + 4, p.kb, row < left);  // on their way while these are handed over
-                    na1 = load_scales(a1, b + 4, p.kb, row + 64 < left);
-                    nw0 = load_scales(w0, b + 4, p.kb, true);
-                    nw1 = load_scales(w1, b + 4, p.kb, true);
+                const float* as = p.g.a_scales + tile_row(tl, p, rank, lane) * p.kb;
+                const long long step = static_cast<long long>(kWarp) * p.kb;
+                const float* ws = weight_scales<kSwiglu>(tl, p, lane & 1);
+                for (int b = 0; b < p.kb; b += 4) {
+                    float4 a[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < left);
+                    const float4 w = load_scales(ws, b, p.kb, lane < 2);
+                    ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_empty[slot], phase, s));
+                    if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (b + i >= p.kb) break;
-                        // Sums of block it - 2 complete: its MMA waited for the reads of block it - 4, the slot's last user.
-                        const uint32_t buf = it & 1;
-                        ok = it < 2 || wait_for(&s->bar.acc_full[buf], (it / 2 - 1) & 1, s);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        float2* slot = s->scale[it % kScaleSlots];
-                        const float u = element(va0, i), v = element(va1, i), x = element(vw0, i), y = element(vw1, i);
-                        slot[row] = make_float2(u * x, u * y);
-                        slot[row + 64] = make_float2(v * x, v * y);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s->bar.acc_full[buf]);
-                        ++it;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s->row_scale[slot][i][lane + j * kWarp] = element(a[j], i);
+                        if (lane < 2) reinterpret_cast<float*>(&s->w_scale[slot][i])[lane] = element(w, i);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->bar.scale_full[slot]);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
             }
@@ -312,39 +325,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         regs_up<104>();
         const int g = (warp - 4) / 4, quarter = warp % 4;
         const int row = quarter * kWarp + lane;  // of this CTA's 128
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g * kGroupCols;
-        const uint32_t empty = mapa(smem_addr(&s->bar.acc_empty[0]), 0);
-        uint32_t it = 0, parity = 0;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g / 2 * kTileN + g % 2 * kGroupCols;
+        uint64_t* full = s->bar.acc_full[g / 2];
+        const uint32_t empty = mapa(smem_addr(s->bar.acc_empty[g / 2]), 0);
+        const uint32_t scale_empty = mapa(smem_addr(s->bar.scale_empty), rank);
+        uint32_t it = 0, parity = 0, slot = 0, slot_phase = 0;
         Walk walk;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
             const Tile tl = tile_at(t, walk, s->first, p, cols);
             const int left = tl.rows - static_cast<int>(rank) * kHalf;
             const bool warp_on = quarter * kWarp < left;
-            float acc[2 * kGroupCols];  // of the first weight block, then of the second
+            uint64_t acc[kGroupCols];  // pairs of the first weight block, then of the second
 #pragma unroll
-            for (int j = 0; j < 2 * kGroupCols; ++j) acc[j] = 0.0f;
+            for (int j = 0; j < kGroupCols; ++j) acc[j] = 0;
 #pragma unroll 1
-            for (int b = p.kb; b > 0; --b, ++it) {
+            for (int b = 0; b < p.kb; ++b, ++it) {
                 const uint32_t buf = it & 1;
-                ok = __all_sync(0xffffffffu, wait_for(&s->bar.acc_full[buf], (it / 2) & 1, s));
+                ok = (b & 3) != 0 || wait_for(&s->bar.scale_full[slot], slot_phase, s);
+                const float2 ws = s->w_scale[slot][b & 3];
+                const float as = s->row_scale[slot][b & 3][row];
+                ok = __all_sync(0xffffffffu, ok && wait_for(&full[buf], (it / 2) & 1, s));
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_on) {
-                    const float2 sc = s->scale[it % kScaleSlots][row];
-                    const uint32_t col = lanes + buf * kAccColumns;
-                    add16(acc, col, sc.x);
-                    add16(acc + 16, col + 16, sc.x);
-                    add16(acc + 32, col + kHalf, sc.y);
-                    float x[16];
-                    tmem_read16(col + kHalf + 16, x);
+                    const uint32_t col = lanes + buf * kHalfN;
+                    const uint64_t s0 = pair2(as * ws.x), s1 = pair2(as * ws.y);
+                    uint64_t x[16];
+                    tmem_read32(col, x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[j], x[j], s0);
+                    tmem_read32(col + kHalfN / 2, x);
                     tc_fence_before();  // the block's sums have left TMEM
                     if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[48 + j] = fmaf(x[j], sc.y, acc[48 + j]);
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 + j], x[j], s1);
                 } else {
                     tc_fence_before();
                     if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
+                }
+                if ((b & 3) == 3 || b + 1 == p.kb) {
+                    if (lane == 0) mbar_arrive_cluster_relaxed(scale_empty + slot * 8);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        slot_phase ^= 1;
+                    }
                 }
             }
             if (!ok) {
@@ -364,8 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const __nv_bfloat162 h =
-                                __floats2bfloat162_rn(acc[j * 16 + 2 * i], acc[j * 16 + 2 * i + 1]);
+                            const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(acc[j * 8 + i]));
                             v[i] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                         if (wide) {
@@ -378,11 +402,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             } else if (warp_on) {
                 // h = gate / (1 + exp(-gate)) * up; columns past n have zero weights, so h = 0 there
+                float h[kGroupCols];
                 float amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kGroupCols; ++j) {
-                    acc[j] = __fdividef(acc[j], 1.0f + __expf(-acc[j])) * acc[kGroupCols + j];
-                    amax = fmaxf(amax, fabsf(acc[j]));
+                for (int j = 0; j < kGroupCols / 2; ++j) {
+                    const float2 a = unpack2(acc[j]), u = unpack2(acc[kGroupCols / 2 + j]);
+                    h[2 * j] = __fdividef(a.x, 1.0f + __expf(-a.x)) * u.x;
+                    h[2 * j + 1] = __fdividef(a.y, 1.0f + __expf(-a.y)) * u.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
                 }
                 // the other warpgroups have the rest of the block's 128 columns
                 s->amax[parity][g][row] = amax;
@@ -399,8 +426,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[i] = pack_e4m3x4(acc[j * 16 + i * 4] * inv, acc[j * 16 + i * 4 + 1] * inv,
-                                               acc[j * 16 + i * 4 + 2] * inv, acc[j * 16 + i * 4 + 3] * inv);
+                            v[i] = pack_e4m3x4(h[j * 16 + i * 4] * inv, h[j * 16 + i * 4 + 1] * inv,
+                                               h[j * 16 + i * 4 + 2] * inv, h[j * 16 + i * 4 + 3] * inv);
                         if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
                     }
                     if (g == 0) p.g.y_scales[r * p.nb + tl.n0 / kScaleBlock] = scale;
@@ -465,8 +492,8 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
     p.tiles_n = (g.n + cols - 1) / cols;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    CUtensorMap map_a, map_w;
-    if (!make_map(&map_a, g.a, g.k, g.cap, g.E, kChunk) ||
+    CUtensorMap map_a, map_a128, map_w;
+    if (!make_map(&map_a, g.a, g.k, g.cap, g.E, kChunk) || !make_map(&map_a128, g.a, g.k, g.cap, g.E, kHalf) ||
         !make_map(&map_w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + static_cast<size_t>(kStages) * 2 * kTileBytes + sizeof(Shared);
@@ -474,7 +501,7 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileM - 1) / kTileM) * p.tiles_n;
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
     return launch_pdl(ll_gemm_fp8_kernel<kSwiglu>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, map_a,
-                      map_w, p);
+                      map_a128, map_w, p);
 }
 
 }  // namespace

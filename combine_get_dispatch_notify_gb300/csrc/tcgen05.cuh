@@ -29,6 +29,10 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // ---- TMA: one box of a 3-D tensor map into this CTA's shared memory, its
 // bytes counted on an mbarrier of this CTA or of its pair's leader ----
 __device__ __forceinline__ void tma_load_3d(uint32_t smem, const CUtensorMap* map, int x, int y, int z,
@@ -58,18 +62,42 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t addr, uint32_t column
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 columns of this warp's 32 lanes.  The load and its wait are one
-// statement: the pair takes about 20 cycles, which the SM's other warps fill,
-// and registers that are still being written between two statements cost moves.
-__device__ __forceinline__ void tmem_read16(uint32_t addr, float (&r)[16]) {
+// 32 columns of this warp's 32 lanes as 16 pairs.  The load and its wait are
+// one statement: the two take about 20 cycles, which the SM's other warps fill,
+// and registers still being written between two statements cost moves.
+__device__ __forceinline__ void tmem_read32(uint32_t addr, uint64_t (&x)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        "{\n\t.reg .b32 r<32>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15, r16, r17, r18, r19, "
+        "r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {r0, r1}; mov.b64 %1, {r2, r3}; mov.b64 %2, {r4, r5}; mov.b64 %3, {r6, r7};\n\t"
+        "mov.b64 %4, {r8, r9}; mov.b64 %5, {r10, r11}; mov.b64 %6, {r12, r13}; mov.b64 %7, {r14, r15};\n\t"
+        "mov.b64 %8, {r16, r17}; mov.b64 %9, {r18, r19}; mov.b64 %10, {r20, r21}; mov.b64 %11, {r22, r23};\n\t"
+        "mov.b64 %12, {r24, r25}; mov.b64 %13, {r26, r27}; mov.b64 %14, {r28, r29}; mov.b64 %15, {r30, r31};\n\t"
+        "}"
+        : "=l"(x[0]), "=l"(x[1]), "=l"(x[2]), "=l"(x[3]), "=l"(x[4]), "=l"(x[5]), "=l"(x[6]), "=l"(x[7]),
+          "=l"(x[8]), "=l"(x[9]), "=l"(x[10]), "=l"(x[11]), "=l"(x[12]), "=l"(x[13]), "=l"(x[14]), "=l"(x[15])
         : "r"(addr)
         : "memory");
+}
+
+// ---- packed fp32 pairs ----
+// acc += x * s, each half rounded once.  The packed form runs at the scalar
+// form's rate (fma pipe) but takes half the issue slots.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t x, uint64_t s) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(s));
+}
+__device__ __forceinline__ uint64_t pair2(float v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(v)));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
 }
 
 // ---- tcgen05.mma on the pair, e4m3 x e4m3 -> fp32 in TMEM ----
@@ -99,6 +127,33 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
         "h"(static_cast<uint16_t>(3))
         : "memory");
 }
+
+// The same on the leader's barrier alone.
+__device__ __forceinline__ void mma_commit_leader(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// One lane of a converged warp.  MMAs and commits issued behind it, from
+// warp-uniform operands, take about 6 cycles each; behind `lane == 0` about 50.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// ---- 4-byte asynchronous copies ----
+__device__ __forceinline__ void copy_async4(float* smem, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(smem)), "l"(src) : "memory");
+}
+// Arrives on `bar` for this thread once its copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <int kRegs>
 __device__ __forceinline__ void regs_up() {

@@ -1,6 +1,12 @@
 // Router: scores, group and expert selection, weights (ep_route), and the
 // gradient of the weights with respect to the logits (ep_route_backward).
-// One warp works on one token; its E keys lie in shared memory.
+// One warp works on one token.
+//
+// ep_route has two kernels.  route_lists_kernel keeps a lane's keys as one
+// sorted list of 32-bit words in registers and takes the K winners off the
+// lists' heads; route_kernel keeps the keys in shared memory and covers what
+// the lists do not (more than 512 experts, groups that do not fall on lanes,
+// softmax keys that are sums).
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -50,7 +56,6 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
-constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
 __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
@@ -181,6 +186,287 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_kernel(const RouteAr
     }
 }
 
+// ---------------------------------------------------------------------------
+// Lists in registers.
+//
+// Lane i holds the N consecutive experts from i * N on.  A key becomes one word,
+// its order-preserving bits cut to 32 - kIdxBits with the complemented index
+// below them, so one unsigned maximum finds the largest key and, among equals,
+// the lowest index.  Each lane sorts its words once; a round is then a
+// redux.max over the list heads and one shift in the winner's lane.
+//
+// bf16 logits fit whole (16 bits of key, 16 of index).  A wider key is cut, and
+// a sigmoid key is first taken from ex2.approx and rcp.approx (about 2^-21 off):
+// the order that comes out is proven token by token.  The K winners' exact keys
+// must be ordered, and the runner-up must be further away than the cut and the
+// approximation together; so must the last group kept and the first one
+// dropped.  A token that fails (a few in a hundred) takes its rounds over exact
+// keys instead.  This way the exact sigmoid, some 20 instructions, is computed
+// for K experts and not for E.
+
+// What can separate two approximate keys from their exact order: the sigmoid's
+// errors, below 2^-20 each, and the cuts, 2^-14 of each key with nine index bits.
+__device__ __forceinline__ float key_margin(float a, float b) {
+    return 1.9073486328125e-06f + 1.220703125e-04f * fmaxf(fabsf(a), fabsf(b));
+}
+
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+    // odd-even merge sort (Batcher)
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+        for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+                        v[i + j] = hi;
+                        v[i + j + k] = lo;
+                    }
+}
+
+// The lane's logits (lowest value past E: masked).
+template <bool kBf16, int N>
+__device__ __forceinline__ void load_lane(const void* logits, long long base, int first, int E, bool vec,
+                                          float (&l)[N]) {
+    const bool whole = vec && first + N <= E;
+    if (whole && (kBf16 ? N % 8 == 0 : N % 4 == 0)) {
+        if (kBf16) {
+#pragma unroll
+            for (int i = 0; i < N / 8; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(logits) + base + first) + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    l[(8 * i + 2 * j) % N] = __uint_as_float(w[j] << 16);
+                    l[(8 * i + 2 * j + 1) % N] = __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(logits) + base + first) + i);
+                l[(4 * i) % N] = v.x;
+                l[(4 * i + 1) % N] = v.y;
+                l[(4 * i + 2) % N] = v.z;
+                l[(4 * i + 3) % N] = v.w;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) l[j] = first + j < E ? load_logit<kBf16>(logits, base + first + j) : -INFINITY;
+}
+
+__device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// Group keys of the lane's group from its two largest values (kNone: none).
+__device__ __forceinline__ float group_value(uint32_t k1, uint32_t k2, int group_top) {
+    if (k1 == kNone) return -INFINITY;
+    return group_top == 2 && k2 != kNone ? of_key(k1) + of_key(k2) : of_key(k1);
+}
+
+// Largest and second largest key of the `seg` lanes around this one.
+template <int N>
+__device__ __forceinline__ void segment_top2(const uint32_t (&k)[N], int seg, uint32_t& k1, uint32_t& k2) {
+    k1 = k[0];
+    k2 = kNone;
+#pragma unroll
+    for (int j = 1; j < N; ++j) {
+        k2 = max(k2, min(k1, k[j]));
+        k1 = max(k1, k[j]);
+    }
+    for (int o = 1; o < seg; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
+        k2 = max(min(k1, o1), max(k2, o2));
+        k1 = max(k1, o1);
+    }
+}
+
+// Whether this lane's group is one of the topk_groups largest, ties to the
+// lowest.  With `margin`, `near` tells that the margin could change that.
+__device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, int lane, bool margin, bool& near) {
+    const int g = lane / seg;
+    int above = 0, surely = 0, maybe = 0;  // groups above this one: as computed, for certain, possibly
+    for (int i = 0; i < G; ++i) {
+        const float o = __shfl_sync(kFull, v, i * seg);  // every lane takes part
+        const float m = key_margin(o, v);
+        above += o > v || (o == v && i < g) ? 1 : 0;
+        surely += o > v + m ? 1 : 0;
+        maybe += i != g && o + m >= v ? 1 : 0;
+    }
+    const bool kept = above < topk && v > -INFINITY;
+    near = margin && g < G && v > -INFINITY && (kept ? maybe >= topk : surely < topk);
+    return kept;
+}
+
+// kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.
+template <bool kBf16, int N, int kMode>
+__global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const RouteArgs p, int seg, int vec) {
+    constexpr bool kWhole = kBf16 && kMode == 0;  // the word holds the whole key
+    constexpr int kIdxBits = kWhole ? 16 : (N <= 8 ? 8 : 9);
+    constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1u;
+    const int lane = threadIdx.x % kWarp;
+    const float lim = largest<kBf16>();
+    griddep_launch_dependents();
+    griddep_wait();  // the logits are complete from here on
+    const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / kWarp);
+    const int first = lane * N;
+    const bool groups = p.rc.topk_groups < p.rc.G;
+    float bias[N];
+    if (kMode == 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) bias[j] = p.bias != nullptr && first + j < p.E ? __ldg(p.bias + first + j) : 0.0f;
+    }
+    long long t = static_cast<long long>(blockIdx.x) * (blockDim.x / kWarp) + threadIdx.x / kWarp;
+    float next[N];
+    if (t < p.tokens) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, vec != 0, next);
+    for (; t < p.tokens; t += step) {
+        const long long base = t * p.E;
+        float l[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) l[j] = next[j];
+        if (t + step < p.tokens) load_lane<kBf16, N>(p.logits, (t + step) * p.E, first, p.E, vec != 0, next);
+
+        // keys, approximate for the sigmoid
+        uint32_t k[N];
+        bool nan = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float v = fminf(l[j], lim);
+            if (kMode == 1) v = __fdividef(1.0f, 1.0f + __expf(-v)) + bias[j];
+            nan |= l[j] != l[j] || v != v;
+            k[j] = l[j] > -lim && v > -INFINITY ? key_of(v) : kNone;
+        }
+        if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
+        bool near = false;
+        if (groups) {
+            uint32_t k1, k2;
+            segment_top2<N>(k, seg, k1, k2);
+            const float v = group_value(k1, k2, p.rc.group_top);
+            const bool kept = group_kept(v, p.rc.G, seg, p.rc.topk_groups, lane, kMode == 1, near);
+#pragma unroll
+            for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
+        }
+        uint32_t w[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            w[j] = k[j] == kNone ? 0u : ((k[j] & ~kIdxMask) | (kIdxMask - static_cast<uint32_t>(first + j)));
+        sort_descending<N>(w);
+        uint32_t win = 0;  // lane i holds winner i, lane K the runner-up
+        const int rounds = kWhole ? p.K : min(p.K + 1, kWarp);
+        for (int r = 0; r < rounds; ++r) {
+            const uint32_t top = __reduce_max_sync(kFull, w[0]);
+            if (top == 0u) break;
+            if (lane == r) win = top;
+            if (w[0] == top) {
+#pragma unroll
+                for (int j = 0; j + 1 < N; ++j) w[j] = w[j + 1];
+                w[N - 1] = 0u;
+            }
+        }
+        int idx = win != 0u && lane < p.K ? static_cast<int>(kIdxMask - (win & kIdxMask)) : -1;
+        float logit = 0.0f, s = 0.0f;  // of the lane's winner
+        if (kWhole) {
+            // a negative float's ordered bits end in ones
+            logit = of_key(win >> 31 ? win & ~kIdxMask : win | kIdxMask);
+        } else {
+            const float approx = of_key(win & ~kIdxMask);
+            if (idx >= 0) logit = fminf(load_logit<kBf16>(p.logits, base + idx), lim);
+            float exact = logit;
+            if (kMode == 1) {
+                s = idx >= 0 ? sigmoid_exact(logit) : 0.0f;
+                exact = idx >= 0 && p.bias != nullptr ? s + __ldg(p.bias + idx) : s;
+            }
+            // winners in exact order, and the runner-up out of reach of the last of them
+            const uint32_t mine = idx >= 0 ? key_of(exact) : kNone;
+            const uint32_t after = __shfl_down_sync(kFull, mine, 1);
+            const int idx_after = __shfl_down_sync(kFull, idx, 1);
+            const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
+            bool bad = near;
+            if (lane + 1 < p.K && idx_after >= 0) bad |= mine < after || (mine == after && idx > idx_after);
+            if (lane < p.K && idx >= 0 && p.K < kWarp && runner != 0u) {
+                const float rv = of_key(runner & ~kIdxMask);
+                bad |= !(fminf(exact, approx) - rv > key_margin(approx, rv));  // also where both are infinite
+            }
+            if (p.K == kWarp) bad = true;  // no lane left for the runner-up
+            if (__any_sync(kFull, bad)) {  // rounds over exact keys
+                if (kMode == 1) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float v = sigmoid_exact(fminf(l[j], lim)) + bias[j];
+                        k[j] = l[j] > -lim && v > -INFINITY ? key_of(v) : kNone;
+                    }
+                    if (groups) {
+                        uint32_t k1, k2;
+                        bool unused = false;
+                        segment_top2<N>(k, seg, k1, k2);
+                        const bool kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg,
+                                                     p.rc.topk_groups, lane, false, unused);
+#pragma unroll
+                        for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
+                    }
+                }
+                idx = -1;
+                for (int r = 0; r < p.K; ++r) {
+                    uint32_t best = k[0];
+                    int at = 0;
+#pragma unroll
+                    for (int j = 1; j < N; ++j)
+                        if (k[j] > best) {
+                            best = k[j];
+                            at = j;
+                        }
+                    const uint32_t top = __reduce_max_sync(kFull, best);
+                    if (top == kNone) break;
+                    const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+                    const int from = __shfl_sync(kFull, first + at, owner);
+                    if (lane == r) idx = from;
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (lane == owner && j == at) k[j] = kNone;
+                }
+                logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
+                s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
+            }
+        }
+        float wt;
+        if (kMode == 0) {
+            // softmax: over the winners where their weights are renormalised, else over all experts
+            float m = idx >= 0 ? logit : -FLT_MAX;
+            if (!p.rc.renorm) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (l[j] > -lim) m = fmaxf(m, fminf(l[j], lim));
+            }
+            m = warp_max(m);
+            wt = idx >= 0 ? expf(logit - m) : 0.0f;
+            float total = wt;
+            if (!p.rc.renorm) {
+                total = 0.0f;
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (l[j] > -lim) total += expf(fminf(l[j], lim) - m);
+            }
+            total = warp_sum(total);
+            wt = total > 0.0f ? wt / total : 0.0f;
+        } else {
+            wt = s;
+            if (p.rc.renorm) {
+                const float total = warp_sum(wt);
+                wt = total > 0.0f ? wt / total : 0.0f;
+            }
+        }
+        if (lane < p.K) {
+            p.topk_idx[t * p.K + lane] = idx;
+            p.topk_w[t * p.K + lane] = wt * p.rc.scale;
+        }
+    }
+}
+
 struct RouteBwdArgs {
     const void* logits;
     const int64_t* topk_idx;
@@ -270,6 +556,28 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
     }
 }
 
+template <bool kBf16, int kMode, int N>
+cudaError_t launch_lists_n(const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
+    const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
+    const int resident =
+        max_blocks_per_sm(reinterpret_cast<const void*>(route_lists_kernel<kBf16, N, kMode>), kRouteWarps * kWarp, 0);
+    if (resident <= 0) return cudaErrorInvalidValue;
+    const long long most = static_cast<long long>(sms) * resident;
+    return launch_pdl(route_lists_kernel<kBf16, N, kMode>, dim3(static_cast<unsigned>(want < most ? want : most)),
+                      dim3(kRouteWarps * kWarp), 0, stream, 0, false, p, seg, vec);
+}
+
+template <bool kBf16, int kMode>
+cudaError_t launch_lists(int n, const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
+    switch (n) {
+        case 1: return launch_lists_n<kBf16, kMode, 1>(p, seg, vec, sms, stream);
+        case 2: return launch_lists_n<kBf16, kMode, 2>(p, seg, vec, sms, stream);
+        case 4: return launch_lists_n<kBf16, kMode, 4>(p, seg, vec, sms, stream);
+        case 8: return launch_lists_n<kBf16, kMode, 8>(p, seg, vec, sms, stream);
+        default: return launch_lists_n<kBf16, kMode, 16>(p, seg, vec, sms, stream);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits, bool bf16, const float* bias,
@@ -277,6 +585,20 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const RouteArgs p = {logits, bias, topk_idx, topk_w, status, static_cast<long long>(sh.R) * sh.T, sh.E, sh.K, rc};
+    const bool by_logit = rc.score == 0 && bias == nullptr && (rc.group_top == 1 || rc.topk_groups == rc.G);
+    if (sh.E <= 512 && (rc.score == 1 || by_logit)) {
+        const int n = sh.E <= 32 ? 1 : sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;
+        const int per_group = sh.E / rc.G, seg = per_group / n;
+        // groups are whole power-of-two runs of lanes
+        const bool on_lanes = rc.topk_groups == rc.G || (per_group % n == 0 && (seg & (seg - 1)) == 0);
+        if (on_lanes) {
+            const int vec = (static_cast<long long>(sh.E) * (bf16 ? 2 : 4)) % 16 == 0;
+            return bf16 ? (rc.score == 0 ? launch_lists<true, 0>(n, p, seg, vec, sms, stream)
+                                         : launch_lists<true, 1>(n, p, seg, vec, sms, stream))
+                        : (rc.score == 0 ? launch_lists<false, 0>(n, p, seg, vec, sms, stream)
+                                         : launch_lists<false, 1>(n, p, seg, vec, sms, stream));
+        }
+    }
     const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
     const long long most = sms * 16LL;
     const dim3 grid(static_cast<unsigned>(want < most ? want : most));

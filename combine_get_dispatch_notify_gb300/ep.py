@@ -147,9 +147,18 @@ def exported_symbols() -> list[str]:
 
 
 # --------------------------------------------------------------------------- helpers
+def _current_stream() -> int:
+    """Raw handle of torch's current stream on the current device.  The raw getter costs a
+    fraction of building a torch.cuda.Stream, which is most of a short call's host time."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
 def _stream(stream) -> _vp:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _vp(_current_stream())
     return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -164,7 +173,7 @@ def _t(t: torch.Tensor | None, dtype, shape, name: str, nullable=False) -> _vp:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return _vp(t.data_ptr())
 

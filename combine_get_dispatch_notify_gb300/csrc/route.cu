@@ -2,11 +2,12 @@
 // gradient of the weights with respect to the logits (ep_route_backward).
 // One warp works on one token.
 //
-// ep_route has two kernels.  route_lists_kernel keeps a lane's keys as one
-// sorted list of 32-bit words in registers and takes the K winners off the
-// lists' heads; route_kernel keeps the keys in shared memory and covers what
-// the lists do not (more than 512 experts, groups that do not fall on lanes,
-// softmax keys that are sums).
+// ep_route has three kernels.  route_lists_kernel, and route_bf16_kernel for
+// bf16 logits that are keys themselves, keep a lane's keys as one sorted list of
+// 32-bit words in registers and take the K winners off the lists' heads;
+// route_kernel keeps the keys in shared memory and covers what the lists do not
+// (more than 512 experts, groups that do not fall on lanes, softmax scores with
+// a bias or summed for groups).
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -194,21 +195,6 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_kernel(const RouteAr
 // below them, so one unsigned maximum finds the largest key and, among equals,
 // the lowest index.  Each lane sorts its words once; a round is then a
 // redux.max over the list heads and one shift in the winner's lane.
-//
-// bf16 logits fit whole (16 bits of key, 16 of index).  A wider key is cut, and
-// a sigmoid key is first taken from ex2.approx and rcp.approx (about 2^-21 off):
-// the order that comes out is proven token by token.  The K winners' exact keys
-// must be ordered, and the runner-up must be further away than the cut and the
-// approximation together; so must the last group kept and the first one
-// dropped.  A token that fails (a few in a hundred) takes its rounds over exact
-// keys instead.  This way the exact sigmoid, some 20 instructions, is computed
-// for K experts and not for E.
-
-// What can separate two approximate keys from their exact order: the sigmoid's
-// errors, below 2^-20 each, and the cuts, 2^-14 of each key with nine index bits.
-__device__ __forceinline__ float key_margin(float a, float b) {
-    return 1.9073486328125e-06f + 1.220703125e-04f * fmaxf(fabsf(a), fabsf(b));
-}
 
 template <int N>
 __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
@@ -228,16 +214,169 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
                     }
 }
 
-// The lane's logits (lowest value past E: masked).
+// Takes the `rounds` largest words off the lists; lane r gets the r-th (0 past
+// the end).  Up to kFew rounds are unrolled: round r then shifts only what the
+// rounds after it can still take.
+constexpr int kFew = 9;
+template <int N>
+__device__ __forceinline__ uint32_t take(uint32_t (&w)[N], int rounds, int lane) {
+    uint32_t win = 0;
+    if (rounds <= kFew) {
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+            if (r >= rounds) break;
+            const uint32_t top = __reduce_max_sync(kFull, w[0]);
+            if (lane == r) win = top;
+            if (w[0] == top) {
+#pragma unroll
+                for (int j = 0; j < N && j < kFew - 1 - r; ++j) w[j] = j + 1 < N ? w[j + 1] : 0u;
+            }
+        }
+    } else {
+        for (int r = 0; r < rounds; ++r) {
+            const uint32_t top = __reduce_max_sync(kFull, w[0]);
+            if (lane == r) win = top;
+            if (w[0] == top) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) w[j] = j + 1 < N ? w[j + 1] : 0u;
+            }
+        }
+    }
+    return win;
+}
+
+// Sum over lanes [0, K) (the others hold 0), valid in those lanes.
+__device__ __forceinline__ float sum_kept(float v, int K) {
+    for (int o = 1; o < K; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+__device__ __forceinline__ void store_slot(const RouteArgs& p, long long t, int slot, int idx, float w) {
+    p.topk_idx[t * p.K + slot] = idx;
+    p.topk_w[t * p.K + slot] = w * p.rc.scale;
+}
+
+// ---- bf16 logits that are the keys themselves: the word holds the whole key ----
+//
+// Two logits are ordered by two instructions: a negative half flips all its
+// bits, a positive one its sign.  In that order -inf, the lowest value and
+// negative NaNs come last (up to kLowest16), +inf and positive NaNs first (from
+// kInf16 on), so masked experts need no test.  Infinite and NaN logits, and zeros
+// of either sign among the winners (equal keys with different bits), are rare:
+// such a token runs once more over words cleaned one by one.
+constexpr uint32_t kLowest16 = 0x0080u, kMinusInf16 = 0x007fu, kInf16 = 0xff80u, kLargest16 = 0xff7fu;
+constexpr uint32_t kMinusZero16 = 0x7fffu, kZero16 = 0x8000u;
+
+// 0xffff in each half whose sign is set.
+__device__ __forceinline__ uint32_t half_signs(uint32_t v) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const RouteArgs p) {
+    const int lane = threadIdx.x % kWarp, first = lane * N;
+    griddep_launch_dependents();
+    griddep_wait();  // the logits are complete from here on
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
+    long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
+    const bool on = first < p.E;  // E is a multiple of N
+    const uint16_t* row = static_cast<const uint16_t*>(p.logits) + first;
+    uint32_t next[N / 2];
+    auto load = [&](long long token) {
+        const uint16_t* src = row + token * p.E;
+        if (N >= 8) {
+#pragma unroll
+            for (int i = 0; i < N / 8; ++i) {
+                const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+                next[(4 * i) % (N / 2)] = v.x;
+                next[(4 * i + 1) % (N / 2)] = v.y;
+                next[(4 * i + 2) % (N / 2)] = v.z;
+                next[(4 * i + 3) % (N / 2)] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) next[i] = on ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0u;
+        }
+    };
+    if (t < p.tokens) load(t);
+    for (; t < p.tokens; t += step) {
+        uint32_t raw[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) raw[j] = next[j];
+        if (t + step < p.tokens) load(t + step);
+        uint32_t w[N], win = 0;
+        for (int pass = 0;; ++pass) {
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const uint32_t flip = half_signs(raw[j]) | 0x80008000u;
+                const uint32_t o = raw[j] ^ flip;
+                w[2 * j] = on ? __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j), 0x1054) : 0u;
+                w[2 * j + 1] = on ? __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j + 1), 0x3254) : 0u;
+            }
+            bool nan = false;
+            if (pass == 1) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    uint32_t o = w[j] >> 16;
+                    nan |= on && (o > kInf16 || o < kMinusInf16);
+                    o = o > kInf16 || o <= kLowest16 ? 0u : o == kInf16 ? kLargest16 : o == kMinusZero16 ? kZero16 : o;
+                    w[j] = o == 0u ? 0u : (o << 16) | (w[j] & 0xffffu);
+                }
+                if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
+            }
+            sort_descending<N>(w);
+            bool special = w[0] >= (kInf16 << 16) || (on && w[N - 1] < (kMinusInf16 << 16));
+            win = take<N>(w, min(p.K + 1, kWarp), lane);
+            const uint32_t o = win >> 16;
+            special |= o == kMinusZero16 || o == kZero16;
+            if (pass == 1 || !__any_sync(kFull, special)) break;
+        }
+        const uint32_t o = win >> 16;
+        const bool kept = lane < p.K && o > kLowest16;
+        const float logit = __uint_as_float((o & 0x8000u ? o ^ 0x8000u : o ^ 0xffffu) << 16);
+        // softmax over the winners, the first of them the largest; or over all experts
+        const float m = __shfl_sync(kFull, logit, 0);
+        const float mine = kept ? expf(logit - m) : 0.0f;
+        float total;
+        if (p.rc.renorm) {
+            total = sum_kept(mine, p.K);
+        } else {
+            total = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float l = __uint_as_float(j % 2 == 0 ? raw[j / 2] << 16 : raw[j / 2] & 0xffff0000u);
+                if (on && l > -largest<true>()) total += expf(fminf(l, largest<true>()) - m);
+            }
+            total = warp_sum(total);
+        }
+        if (lane < p.K) store_slot(p, t, lane, kept ? static_cast<int>(0xffffu - (win & 0xffffu)) : -1, kept ? mine / total : 0.0f);
+    }
+}
+
+// ---- fp32 keys: cut, and approximate for the sigmoid ----
+//
+// A sigmoid key is first taken from ex2.approx and rcp.approx, below 2^-20 off;
+// the exact sigmoid, some 20 instructions, is computed for the K winners and not
+// for E experts.  What comes out is proven token by token: every winner's exact
+// key has to be out of the runner-up's reach (its cut and its approximation), and
+// the last group kept out of reach of the first one dropped.  The winners'
+// own order is settled by their exact keys.  A token that fails (about one in a
+// hundred) takes its rounds over exact keys.
+
+__device__ __forceinline__ float approx_error() { return 9.5367431640625e-07f; }  // 2^-20
+
+// The lane's logits (-inf past E).
 template <bool kBf16, int N>
 __device__ __forceinline__ void load_lane(const void* logits, long long base, int first, int E, bool vec,
                                           float (&l)[N]) {
-    const bool whole = vec && first + N <= E;
-    if (whole && (kBf16 ? N % 8 == 0 : N % 4 == 0)) {
+    if (vec && first + N <= E && (kBf16 ? N % 8 == 0 : N % 4 == 0)) {
         if (kBf16) {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(logits) + base + first) + i);
+                const uint4 v =
+                    __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(logits) + base + first) + i);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -248,7 +387,8 @@ __device__ __forceinline__ void load_lane(const void* logits, long long base, in
         } else {
 #pragma unroll
             for (int i = 0; i < N / 4; ++i) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(logits) + base + first) + i);
+                const float4 v =
+                    __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(logits) + base + first) + i);
                 l[(4 * i) % N] = v.x;
                 l[(4 * i + 1) % N] = v.y;
                 l[(4 * i + 2) % N] = v.z;
@@ -263,7 +403,7 @@ __device__ __forceinline__ void load_lane(const void* logits, long long base, in
 
 __device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Group keys of the lane's group from its two largest values (kNone: none).
+// A group's key from its two largest ones (-inf: no expert can be taken).
 __device__ __forceinline__ float group_value(uint32_t k1, uint32_t k2, int group_top) {
     if (k1 == kNone) return -INFINITY;
     return group_top == 2 && k2 != kNone ? of_key(k1) + of_key(k2) : of_key(k1);
@@ -287,16 +427,18 @@ __device__ __forceinline__ void segment_top2(const uint32_t (&k)[N], int seg, ui
 }
 
 // Whether this lane's group is one of the topk_groups largest, ties to the
-// lowest.  With `margin`, `near` tells that the margin could change that.
+// lowest.  With `margin`, `near` tells that approximate keys could change that.
 __device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, int lane, bool margin, bool& near) {
     const int g = lane / seg;
     int above = 0, surely = 0, maybe = 0;  // groups above this one: as computed, for certain, possibly
     for (int i = 0; i < G; ++i) {
         const float o = __shfl_sync(kFull, v, i * seg);  // every lane takes part
-        const float m = key_margin(o, v);
         above += o > v || (o == v && i < g) ? 1 : 0;
-        surely += o > v + m ? 1 : 0;
-        maybe += i != g && o + m >= v ? 1 : 0;
+        if (margin) {
+            const float m = 4.0f * approx_error() + 4.76837158203125e-07f * (fabsf(o) + fabsf(v));  // and 2^-21
+            surely += o > v + m ? 1 : 0;
+            maybe += i != g && o + m >= v ? 1 : 0;
+        }
     }
     const bool kept = above < topk && v > -INFINITY;
     near = margin && g < G && v > -INFINITY && (kept ? maybe >= topk : surely < topk);
@@ -306,164 +448,146 @@ __device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, in
 // kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.
 template <bool kBf16, int N, int kMode>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const RouteArgs p, int seg, int vec) {
-    constexpr bool kWhole = kBf16 && kMode == 0;  // the word holds the whole key
-    constexpr int kIdxBits = kWhole ? 16 : (N <= 8 ? 8 : 9);
+    constexpr int kIdxBits = N <= 8 ? 8 : 9;
     constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1u;
-    const int lane = threadIdx.x % kWarp;
+    constexpr float kCut = 1.0f / (1 << (23 - kIdxBits));  // of a key, lost below the index
+    const int lane = threadIdx.x % kWarp, first = lane * N;
     const float lim = largest<kBf16>();
     griddep_launch_dependents();
     griddep_wait();  // the logits are complete from here on
-    const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / kWarp);
-    const int first = lane * N;
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
     const bool groups = p.rc.topk_groups < p.rc.G;
     float bias[N];
     if (kMode == 1) {
 #pragma unroll
         for (int j = 0; j < N; ++j) bias[j] = p.bias != nullptr && first + j < p.E ? __ldg(p.bias + first + j) : 0.0f;
     }
-    long long t = static_cast<long long>(blockIdx.x) * (blockDim.x / kWarp) + threadIdx.x / kWarp;
+    // the lane's exact keys with the groups applied: the slow way
+    auto exact_keys = [&](long long base, uint32_t (&k)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float l = first + j < p.E ? load_logit<kBf16>(p.logits, base + first + j) : -INFINITY;
+            const float v = kMode == 1 ? sigmoid_exact(fminf(l, lim)) + bias[j] : fminf(l, lim);
+            k[j] = l > -lim && v > -INFINITY ? key_of(v) : kNone;
+        }
+        if (groups) {
+            uint32_t k1, k2;
+            bool unused;
+            segment_top2<N>(k, seg, k1, k2);
+            const bool kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane,
+                                         false, unused);
+#pragma unroll
+            for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
+        }
+    };
+    long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
     float next[N];
     if (t < p.tokens) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, vec != 0, next);
     for (; t < p.tokens; t += step) {
         const long long base = t * p.E;
-        float l[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) l[j] = next[j];
-        if (t + step < p.tokens) load_lane<kBf16, N>(p.logits, (t + step) * p.E, first, p.E, vec != 0, next);
-
-        // keys, approximate for the sigmoid
         uint32_t k[N];
         bool nan = false;
+        float m = -FLT_MAX, total = 0.0f;
+        if (kMode == 0 && !p.rc.renorm) {  // softmax over all experts
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (next[j] > -lim) m = fmaxf(m, fminf(next[j], lim));
+            m = warp_max(m);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (next[j] > -lim) total += expf(fminf(next[j], lim) - m);
+            total = warp_sum(total);
+        }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            float v = fminf(l[j], lim);
+            float v = fminf(next[j], lim);
             if (kMode == 1) v = __fdividef(1.0f, 1.0f + __expf(-v)) + bias[j];
-            nan |= l[j] != l[j] || v != v;
-            k[j] = l[j] > -lim && v > -INFINITY ? key_of(v) : kNone;
+            nan |= next[j] != next[j] || v != v;
+            k[j] = next[j] > -lim && v > -INFINITY ? key_of(v) : kNone;
         }
+        if (t + step < p.tokens) load_lane<kBf16, N>(p.logits, base + step * p.E, first, p.E, vec != 0, next);
         if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
-        bool near = false;
+        bool bad = false;
         if (groups) {
             uint32_t k1, k2;
             segment_top2<N>(k, seg, k1, k2);
-            const float v = group_value(k1, k2, p.rc.group_top);
-            const bool kept = group_kept(v, p.rc.G, seg, p.rc.topk_groups, lane, kMode == 1, near);
+            const bool kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane,
+                                         kMode == 1, bad);
 #pragma unroll
             for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
         }
-        uint32_t w[N];
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            w[j] = k[j] == kNone ? 0u : ((k[j] & ~kIdxMask) | (kIdxMask - static_cast<uint32_t>(first + j)));
-        sort_descending<N>(w);
-        uint32_t win = 0;  // lane i holds winner i, lane K the runner-up
-        const int rounds = kWhole ? p.K : min(p.K + 1, kWarp);
-        for (int r = 0; r < rounds; ++r) {
-            const uint32_t top = __reduce_max_sync(kFull, w[0]);
-            if (top == 0u) break;
-            if (lane == r) win = top;
-            if (w[0] == top) {
-#pragma unroll
-                for (int j = 0; j + 1 < N; ++j) w[j] = w[j + 1];
-                w[N - 1] = 0u;
-            }
-        }
+            k[j] = k[j] == kNone ? 0u : ((k[j] & ~kIdxMask) | (kIdxMask - static_cast<uint32_t>(first + j)));
+        sort_descending<N>(k);
+        const uint32_t win = take<N>(k, min(p.K + 1, kWarp), lane);  // lane K: the runner-up
+        const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
         int idx = win != 0u && lane < p.K ? static_cast<int>(kIdxMask - (win & kIdxMask)) : -1;
-        float logit = 0.0f, s = 0.0f;  // of the lane's winner
-        if (kWhole) {
-            // a negative float's ordered bits end in ones
-            logit = of_key(win >> 31 ? win & ~kIdxMask : win | kIdxMask);
-        } else {
-            const float approx = of_key(win & ~kIdxMask);
-            if (idx >= 0) logit = fminf(load_logit<kBf16>(p.logits, base + idx), lim);
-            float exact = logit;
-            if (kMode == 1) {
-                s = idx >= 0 ? sigmoid_exact(logit) : 0.0f;
-                exact = idx >= 0 && p.bias != nullptr ? s + __ldg(p.bias + idx) : s;
+        float logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
+        float s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
+        const float key = kMode == 1 ? (idx >= 0 && p.bias != nullptr ? s + __ldg(p.bias + idx) : s) : logit;
+        if (idx >= 0 && runner != 0u) {
+            const float reach = of_key(runner & ~kIdxMask);
+            bad |= !(key - reach > fabsf(reach) * kCut + approx_error());  // true also for two infinities
+        }
+        bad |= p.K == kWarp;  // no lane left for the runner-up
+        int slot = lane;
+        if (__any_sync(kFull, bad)) {  // rounds over exact keys
+            exact_keys(base, k);
+            idx = -1;
+            for (int r = 0; r < p.K; ++r) {
+                uint32_t best = k[0];
+                int at = 0;
+#pragma unroll
+                for (int j = 1; j < N; ++j)
+                    if (k[j] > best) {
+                        best = k[j];
+                        at = j;
+                    }
+                const uint32_t top = __reduce_max_sync(kFull, best);
+                if (top == kNone) break;
+                const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+                const int from = __shfl_sync(kFull, first + at, owner);
+                if (lane == r) idx = from;
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (lane == owner && j == at) k[j] = kNone;
             }
-            // winners in exact order, and the runner-up out of reach of the last of them
-            const uint32_t mine = idx >= 0 ? key_of(exact) : kNone;
+            logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
+            s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
+        } else {
+            const uint32_t mine = idx >= 0 ? key_of(key) : kNone;
             const uint32_t after = __shfl_down_sync(kFull, mine, 1);
             const int idx_after = __shfl_down_sync(kFull, idx, 1);
-            const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
-            bool bad = near;
-            if (lane + 1 < p.K && idx_after >= 0) bad |= mine < after || (mine == after && idx > idx_after);
-            if (lane < p.K && idx >= 0 && p.K < kWarp && runner != 0u) {
-                const float rv = of_key(runner & ~kIdxMask);
-                bad |= !(fminf(exact, approx) - rv > key_margin(approx, rv));  // also where both are infinite
-            }
-            if (p.K == kWarp) bad = true;  // no lane left for the runner-up
-            if (__any_sync(kFull, bad)) {  // rounds over exact keys
-                if (kMode == 1) {
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const float v = sigmoid_exact(fminf(l[j], lim)) + bias[j];
-                        k[j] = l[j] > -lim && v > -INFINITY ? key_of(v) : kNone;
-                    }
-                    if (groups) {
-                        uint32_t k1, k2;
-                        bool unused = false;
-                        segment_top2<N>(k, seg, k1, k2);
-                        const bool kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg,
-                                                     p.rc.topk_groups, lane, false, unused);
-#pragma unroll
-                        for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
-                    }
+            const bool swapped = lane + 1 < p.K && (mine < after || (mine == after && idx_after >= 0 && idx > idx_after));
+            if (__any_sync(kFull, swapped)) {  // order the winners by their exact keys
+                int rank = 0;
+                for (int j = 0; j < p.K; ++j) {
+                    const uint32_t other = __shfl_sync(kFull, mine, j);
+                    const int other_idx = __shfl_sync(kFull, idx, j);
+                    rank += other > mine || (other == mine && (idx < 0 ? j < lane : other_idx >= 0 && other_idx < idx));
                 }
-                idx = -1;
-                for (int r = 0; r < p.K; ++r) {
-                    uint32_t best = k[0];
-                    int at = 0;
-#pragma unroll
-                    for (int j = 1; j < N; ++j)
-                        if (k[j] > best) {
-                            best = k[j];
-                            at = j;
-                        }
-                    const uint32_t top = __reduce_max_sync(kFull, best);
-                    if (top == kNone) break;
-                    const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-                    const int from = __shfl_sync(kFull, first + at, owner);
-                    if (lane == r) idx = from;
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (lane == owner && j == at) k[j] = kNone;
-                }
-                logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
-                s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
+                slot = rank;
             }
         }
         float wt;
         if (kMode == 0) {
-            // softmax: over the winners where their weights are renormalised, else over all experts
-            float m = idx >= 0 ? logit : -FLT_MAX;
-            if (!p.rc.renorm) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (l[j] > -lim) m = fmaxf(m, fminf(l[j], lim));
+            if (p.rc.renorm) {
+                m = warp_max(idx >= 0 ? logit : -FLT_MAX);
+                wt = idx >= 0 ? expf(logit - m) : 0.0f;
+                total = sum_kept(wt, p.K);
+            } else {
+                wt = idx >= 0 ? expf(logit - m) : 0.0f;
             }
-            m = warp_max(m);
-            wt = idx >= 0 ? expf(logit - m) : 0.0f;
-            float total = wt;
-            if (!p.rc.renorm) {
-                total = 0.0f;
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (l[j] > -lim) total += expf(fminf(l[j], lim) - m);
-            }
-            total = warp_sum(total);
             wt = total > 0.0f ? wt / total : 0.0f;
         } else {
             wt = s;
             if (p.rc.renorm) {
-                const float total = warp_sum(wt);
+                total = sum_kept(wt, p.K);
                 wt = total > 0.0f ? wt / total : 0.0f;
             }
         }
-        if (lane < p.K) {
-            p.topk_idx[t * p.K + lane] = idx;
-            p.topk_w[t * p.K + lane] = wt * p.rc.scale;
-        }
+        if (lane < p.K) store_slot(p, t, slot, idx, wt);
     }
 }
 
@@ -556,25 +680,26 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
     }
 }
 
-template <bool kBf16, int kMode, int N>
-cudaError_t launch_lists_n(const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
+// One resident CTA of warps for each place on the SMs, or fewer.
+template <typename... Args>
+cudaError_t launch_tokens(void (*kernel)(RouteArgs, Args...), const RouteArgs& p, int sms, cudaStream_t stream,
+                          Args... args) {
     const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
-    const int resident =
-        max_blocks_per_sm(reinterpret_cast<const void*>(route_lists_kernel<kBf16, N, kMode>), kRouteWarps * kWarp, 0);
+    const int resident = max_blocks_per_sm(reinterpret_cast<const void*>(kernel), kRouteWarps * kWarp, 0);
     if (resident <= 0) return cudaErrorInvalidValue;
     const long long most = static_cast<long long>(sms) * resident;
-    return launch_pdl(route_lists_kernel<kBf16, N, kMode>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                      dim3(kRouteWarps * kWarp), 0, stream, 0, false, p, seg, vec);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kRouteWarps * kWarp), 0,
+                      stream, 0, false, p, args...);
 }
 
 template <bool kBf16, int kMode>
 cudaError_t launch_lists(int n, const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
     switch (n) {
-        case 1: return launch_lists_n<kBf16, kMode, 1>(p, seg, vec, sms, stream);
-        case 2: return launch_lists_n<kBf16, kMode, 2>(p, seg, vec, sms, stream);
-        case 4: return launch_lists_n<kBf16, kMode, 4>(p, seg, vec, sms, stream);
-        case 8: return launch_lists_n<kBf16, kMode, 8>(p, seg, vec, sms, stream);
-        default: return launch_lists_n<kBf16, kMode, 16>(p, seg, vec, sms, stream);
+        case 1: return launch_tokens<int, int>(route_lists_kernel<kBf16, 1, kMode>, p, sms, stream, seg, vec);
+        case 2: return launch_tokens<int, int>(route_lists_kernel<kBf16, 2, kMode>, p, sms, stream, seg, vec);
+        case 4: return launch_tokens<int, int>(route_lists_kernel<kBf16, 4, kMode>, p, sms, stream, seg, vec);
+        case 8: return launch_tokens<int, int>(route_lists_kernel<kBf16, 8, kMode>, p, sms, stream, seg, vec);
+        default: return launch_tokens<int, int>(route_lists_kernel<kBf16, 16, kMode>, p, sms, stream, seg, vec);
     }
 }
 
@@ -588,6 +713,14 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     const bool by_logit = rc.score == 0 && bias == nullptr && (rc.group_top == 1 || rc.topk_groups == rc.G);
     if (sh.E <= 512 && (rc.score == 1 || by_logit)) {
         const int n = sh.E <= 32 ? 1 : sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;
+        if (bf16 && by_logit && rc.topk_groups == rc.G && n > 1 && sh.E % n == 0 && sh.E % (n < 8 ? n : 8) == 0) {
+            switch (n) {
+                case 2: return launch_tokens<>(route_bf16_kernel<2>, p, sms, stream);
+                case 4: return launch_tokens<>(route_bf16_kernel<4>, p, sms, stream);
+                case 8: return launch_tokens<>(route_bf16_kernel<8>, p, sms, stream);
+                default: return launch_tokens<>(route_bf16_kernel<16>, p, sms, stream);
+            }
+        }
         const int per_group = sh.E / rc.G, seg = per_group / n;
         // groups are whole power-of-two runs of lanes
         const bool on_lanes = rc.topk_groups == rc.G || (per_group % n == 0 && (seg & (seg - 1)) == 0);

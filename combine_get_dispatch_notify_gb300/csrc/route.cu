@@ -215,19 +215,22 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
 }
 
 // Takes the `rounds` largest words off the lists; lane r gets the r-th (0 past
-// the end).  Up to kFew rounds are unrolled: round r then shifts only what the
-// rounds after it can still take.
+// the end).  A winner goes through shared memory, stored by the lane that had it:
+// the integer pipe, half rate, is what bounds these kernels, and a select in
+// every lane would use it twice a round.  Up to kFew rounds are unrolled: round r
+// then shifts only what the rounds after it can still take.
 constexpr int kFew = 9;
 template <int N>
-__device__ __forceinline__ uint32_t take(uint32_t (&w)[N], int rounds, int lane) {
-    uint32_t win = 0;
+__device__ __forceinline__ uint32_t take(uint32_t (&w)[N], int rounds, int lane, uint32_t* slots) {
+    slots[lane] = 0u;
+    __syncwarp();
     if (rounds <= kFew) {
 #pragma unroll
         for (int r = 0; r < kFew; ++r) {
             if (r >= rounds) break;
             const uint32_t top = __reduce_max_sync(kFull, w[0]);
-            if (lane == r) win = top;
             if (w[0] == top) {
+                slots[r] = top;
 #pragma unroll
                 for (int j = 0; j < N && j < kFew - 1 - r; ++j) w[j] = j + 1 < N ? w[j + 1] : 0u;
             }
@@ -235,13 +238,16 @@ __device__ __forceinline__ uint32_t take(uint32_t (&w)[N], int rounds, int lane)
     } else {
         for (int r = 0; r < rounds; ++r) {
             const uint32_t top = __reduce_max_sync(kFull, w[0]);
-            if (lane == r) win = top;
             if (w[0] == top) {
+                slots[r] = top;
 #pragma unroll
                 for (int j = 0; j < N; ++j) w[j] = j + 1 < N ? w[j + 1] : 0u;
             }
         }
     }
+    __syncwarp();
+    const uint32_t win = slots[lane];
+    __syncwarp();
     return win;
 }
 
@@ -276,20 +282,25 @@ __device__ __forceinline__ uint32_t half_signs(uint32_t v) {
 
 template <int N>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const RouteArgs p) {
+    __shared__ uint32_t s_slots[kRouteWarps][kWarp];
     const int lane = threadIdx.x % kWarp, first = lane * N;
+    uint32_t* slots = s_slots[threadIdx.x / kWarp];
     griddep_launch_dependents();
     griddep_wait();  // the logits are complete from here on
     const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
-    const bool on = first < p.E;  // E is a multiple of N
+    const bool on = first < p.E;  // E is a multiple of N; lanes past it hold masked logits
     const uint16_t* row = static_cast<const uint16_t*>(p.logits) + first;
     uint32_t next[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) next[i] = 0xff80ff80u;  // -inf
     auto load = [&](long long token) {
+        if (!on) return;
         const uint16_t* src = row + token * p.E;
         if (N >= 8) {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i) {
-                const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
                 next[(4 * i) % (N / 2)] = v.x;
                 next[(4 * i + 1) % (N / 2)] = v.y;
                 next[(4 * i + 2) % (N / 2)] = v.z;
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) next[i] = on ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0u;
+            for (int i = 0; i < N / 2; ++i) next[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
         }
     };
     if (t < p.tokens) load(t);
@@ -310,26 +321,26 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
         for (int pass = 0;; ++pass) {
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
-                const uint32_t flip = half_signs(raw[j]) | 0x80008000u;
-                const uint32_t o = raw[j] ^ flip;
-                w[2 * j] = on ? __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j), 0x1054) : 0u;
-                w[2 * j + 1] = on ? __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j + 1), 0x3254) : 0u;
+                const uint32_t o = raw[j] ^ (half_signs(raw[j]) | 0x80008000u);
+                w[2 * j] = __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j), 0x1054);
+                w[2 * j + 1] = __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j + 1), 0x3254);
             }
-            bool nan = false;
             if (pass == 1) {
+                bool nan = false;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     uint32_t o = w[j] >> 16;
-                    nan |= on && (o > kInf16 || o < kMinusInf16);
+                    nan |= o > kInf16 || o < kMinusInf16;
                     o = o > kInf16 || o <= kLowest16 ? 0u : o == kInf16 ? kLargest16 : o == kMinusZero16 ? kZero16 : o;
                     w[j] = o == 0u ? 0u : (o << 16) | (w[j] & 0xffffu);
                 }
                 if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
             }
             sort_descending<N>(w);
-            bool special = w[0] >= (kInf16 << 16) || (on && w[N - 1] < (kMinusInf16 << 16));
-            win = take<N>(w, min(p.K + 1, kWarp), lane);
+            bool special = w[0] >= (kInf16 << 16) || w[N - 1] < (kMinusInf16 << 16);
+            win = take<N>(w, p.K, lane, slots);
             const uint32_t o = win >> 16;
+            // a zero among the winners: a kept one is always seen, and with none kept no zero matters
             special |= o == kMinusZero16 || o == kZero16;
             if (pass == 1 || !__any_sync(kFull, special)) break;
         }
@@ -426,114 +437,124 @@ __device__ __forceinline__ void segment_top2(const uint32_t (&k)[N], int seg, ui
     }
 }
 
-// Whether this lane's group is one of the topk_groups largest, ties to the
-// lowest.  With `margin`, `near` tells that approximate keys could change that.
-__device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, int lane, bool margin, bool& near) {
+// Whether this lane's group (value v) is one of the topk_groups largest, ties to
+// the lowest; `near` when another group comes within `margin`.
+__device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, int lane, float margin, bool& near) {
     const int g = lane / seg;
-    int above = 0, surely = 0, maybe = 0;  // groups above this one: as computed, for certain, possibly
+    int above = 0;
     for (int i = 0; i < G; ++i) {
-        const float o = __shfl_sync(kFull, v, i * seg);  // every lane takes part
-        above += o > v || (o == v && i < g) ? 1 : 0;
-        if (margin) {
-            const float m = 4.0f * approx_error() + 4.76837158203125e-07f * (fabsf(o) + fabsf(v));  // and 2^-21
-            surely += o > v + m ? 1 : 0;
-            maybe += i != g && o + m >= v ? 1 : 0;
-        }
+        const float d = __shfl_sync(kFull, v, i * seg) - v;  // every lane takes part; NaN between two infinities
+        above += i < g ? !(d < 0.0f) : d > 0.0f;
+        near |= i != g && g < G && !(fabsf(d) > margin);
     }
-    const bool kept = above < topk && v > -INFINITY;
-    near = margin && g < G && v > -INFINITY && (kept ? maybe >= topk : surely < topk);
-    return kept;
+    return g < G && above < topk;
 }
 
-// kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.
+// kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.  E is a
+// multiple of N.
 template <bool kBf16, int N, int kMode>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const RouteArgs p, int seg, int vec) {
     constexpr int kIdxBits = N <= 8 ? 8 : 9;
     constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1u;
     constexpr float kCut = 1.0f / (1 << (23 - kIdxBits));  // of a key, lost below the index
+    __shared__ uint32_t s_slots[kRouteWarps][kWarp];
     const int lane = threadIdx.x % kWarp, first = lane * N;
+    uint32_t* slots = s_slots[threadIdx.x / kWarp];
     const float lim = largest<kBf16>();
     griddep_launch_dependents();
     griddep_wait();  // the logits are complete from here on
     const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
-    const bool groups = p.rc.topk_groups < p.rc.G;
+    const bool groups = p.rc.topk_groups < p.rc.G, on = first < p.E;
     float bias[N];
+    float largest_key = 1.0f;  // bound of the keys' magnitude
     if (kMode == 1) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) bias[j] = p.bias != nullptr && first + j < p.E ? __ldg(p.bias + first + j) : 0.0f;
-    }
-    // the lane's exact keys with the groups applied: the slow way
-    auto exact_keys = [&](long long base, uint32_t (&k)[N]) {
-#pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float l = first + j < p.E ? load_logit<kBf16>(p.logits, base + first + j) : -INFINITY;
-            const float v = kMode == 1 ? sigmoid_exact(fminf(l, lim)) + bias[j] : fminf(l, lim);
-            k[j] = l > -lim && v > -INFINITY ? key_of(v) : kNone;
+            bias[j] = p.bias != nullptr && on ? __ldg(p.bias + first + j) : 0.0f;
+            largest_key = fmaxf(largest_key, 1.0f + fabsf(bias[j]));
         }
-        if (groups) {
-            uint32_t k1, k2;
-            bool unused;
-            segment_top2<N>(k, seg, k1, k2);
-            const bool kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane,
-                                         false, unused);
-#pragma unroll
-            for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
-        }
-    };
+        largest_key = warp_max(largest_key);
+    }
+    // two groups closer than this could be ordered wrongly: two approximate keys in each, their sum's roundings
+    const float margin = kMode == 1 ? 4.0f * approx_error() + 4.76837158203125e-07f * largest_key : -1.0f;
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
     float next[N];
-    if (t < p.tokens) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, vec != 0, next);
+#pragma unroll
+    for (int j = 0; j < N; ++j) next[j] = 0.0f;
+    if (t < p.tokens && on) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, vec != 0, next);
     for (; t < p.tokens; t += step) {
         const long long base = t * p.E;
         uint32_t k[N];
-        bool nan = false;
         float m = -FLT_MAX, total = 0.0f;
         if (kMode == 0 && !p.rc.renorm) {  // softmax over all experts
+            if (on) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (next[j] > -lim) m = fmaxf(m, fminf(next[j], lim));
+                for (int j = 0; j < N; ++j)
+                    if (next[j] > -lim) m = fmaxf(m, fminf(next[j], lim));
+            }
             m = warp_max(m);
+            if (on) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (next[j] > -lim) total += expf(fminf(next[j], lim) - m);
+                for (int j = 0; j < N; ++j)
+                    if (next[j] > -lim) total += expf(fminf(next[j], lim) - m);
+            }
             total = warp_sum(total);
         }
+        // Logits that are infinite, NaN or at the lowest value, and keys that are not finite, leave a NaN here: such
+        // a token goes the exact way, so the keys below need no tests.
+        float odd = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            float v = fminf(next[j], lim);
-            if (kMode == 1) v = __fdividef(1.0f, 1.0f + __expf(-v)) + bias[j];
-            nan |= next[j] != next[j] || v != v;
-            k[j] = next[j] > -lim && v > -INFINITY ? key_of(v) : kNone;
+            odd = fmaf(next[j] * 4.0f, 0.0f, odd);
+            float v = next[j];
+            if (kMode == 1) {
+                v = __fdividef(1.0f, 1.0f + __expf(-v)) + bias[j];
+                odd = fmaf(v, 0.0f, odd);
+            }
+            k[j] = key_of(v);
         }
-        if (t + step < p.tokens) load_lane<kBf16, N>(p.logits, base + step * p.E, first, p.E, vec != 0, next);
-        if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
-        bool bad = false;
+        if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, base + step * p.E, first, p.E, vec != 0, next);
+        bool bad = odd != odd || p.K == kWarp;  // with 32 winners no lane is left for the runner-up
+        bool kept = on;
         if (groups) {
             uint32_t k1, k2;
             segment_top2<N>(k, seg, k1, k2);
-            const bool kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane,
-                                         kMode == 1, bad);
-#pragma unroll
-            for (int j = 0; j < N; ++j) k[j] = kept ? k[j] : kNone;
+            kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane, margin, bad);
         }
+        const uint32_t keep = kept ? ~kIdxMask : 0u, index = kept ? kIdxMask - static_cast<uint32_t>(first) : 0u;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            k[j] = k[j] == kNone ? 0u : ((k[j] & ~kIdxMask) | (kIdxMask - static_cast<uint32_t>(first + j)));
+        for (int j = 0; j < N; ++j) k[j] = (k[j] & keep) | (index - (kept ? static_cast<uint32_t>(j) : 0u));
         sort_descending<N>(k);
-        const uint32_t win = take<N>(k, min(p.K + 1, kWarp), lane);  // lane K: the runner-up
+        const uint32_t win = take<N>(k, min(p.K + 1, kWarp), lane, slots);  // lane K: the runner-up
         const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
         int idx = win != 0u && lane < p.K ? static_cast<int>(kIdxMask - (win & kIdxMask)) : -1;
-        float logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
+        float logit = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : 0.0f;
         float s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
         const float key = kMode == 1 ? (idx >= 0 && p.bias != nullptr ? s + __ldg(p.bias + idx) : s) : logit;
         if (idx >= 0 && runner != 0u) {
             const float reach = of_key(runner & ~kIdxMask);
-            bad |= !(key - reach > fabsf(reach) * kCut + approx_error());  // true also for two infinities
+            bad |= !(key - reach > fabsf(reach) * kCut + approx_error());
         }
-        bad |= p.K == kWarp;  // no lane left for the runner-up
         int slot = lane;
         if (__any_sync(kFull, bad)) {  // rounds over exact keys
-            exact_keys(base, k);
+            bool nan = false;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float l = on ? load_logit<kBf16>(p.logits, base + first + j) : -INFINITY;
+                const float v = kMode == 1 ? sigmoid_exact(fminf(l, lim)) + bias[j] : fminf(l, lim);
+                nan |= l != l || v != v;
+                k[j] = l > -lim && v > -INFINITY ? key_of(v) : kNone;
+            }
+            if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
+            if (groups) {
+                uint32_t k1, k2;
+                bool unused = false;
+                segment_top2<N>(k, seg, k1, k2);
+                const bool in = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane,
+                                           -1.0f, unused);
+#pragma unroll
+                for (int j = 0; j < N; ++j) k[j] = in ? k[j] : kNone;
+            }
             idx = -1;
             for (int r = 0; r < p.K; ++r) {
                 uint32_t best = k[0];
@@ -711,9 +732,9 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     if (sms <= 0) return cudaErrorInvalidDevice;
     const RouteArgs p = {logits, bias, topk_idx, topk_w, status, static_cast<long long>(sh.R) * sh.T, sh.E, sh.K, rc};
     const bool by_logit = rc.score == 0 && bias == nullptr && (rc.group_top == 1 || rc.topk_groups == rc.G);
-    if (sh.E <= 512 && (rc.score == 1 || by_logit)) {
-        const int n = sh.E <= 32 ? 1 : sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;
-        if (bf16 && by_logit && rc.topk_groups == rc.G && n > 1 && sh.E % n == 0 && sh.E % (n < 8 ? n : 8) == 0) {
+    const int n = sh.E <= 32 ? 1 : sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;  // experts of a lane
+    if (sh.E <= 512 && sh.E % n == 0 && (rc.score == 1 || by_logit)) {
+        if (bf16 && by_logit && rc.topk_groups == rc.G && n > 1) {
             switch (n) {
                 case 2: return launch_tokens<>(route_bf16_kernel<2>, p, sms, stream);
                 case 4: return launch_tokens<>(route_bf16_kernel<4>, p, sms, stream);

@@ -214,53 +214,68 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
                     }
 }
 
-// Takes the `rounds` largest words off the lists; lane r gets the r-th (0 past
-// the end).  A winner goes through shared memory, stored by the lane that had it:
-// the integer pipe, half rate, is what bounds these kernels, and a select in
-// every lane would use it twice a round.  Up to kFew rounds are unrolled: round r
-// then shifts only what the rounds after it can still take.
-constexpr int kFew = 9;
-template <int N>
+// Takes the largest words off the lists; lane r gets the r-th (0 past the end).
+// A winner goes through shared memory, stored by the lane that had it: the
+// integer pipe, half rate, is what bounds these kernels, and a select in every
+// lane would use it twice a round.  kRounds > 0: that many rounds, unrolled, and
+// round r shifts only what the rounds after it can still take; 0: `rounds` of
+// them.
+template <int N, int kRounds>
 __device__ __forceinline__ uint32_t take(uint32_t (&w)[N], int rounds, int lane, uint32_t* slots) {
-    slots[lane] = 0u;
-    __syncwarp();
-    if (rounds <= kFew) {
+    if (kRounds > 0) {
 #pragma unroll
-        for (int r = 0; r < kFew; ++r) {
-            if (r >= rounds) break;
+        for (int r = 0; r < kRounds; ++r) {
             const uint32_t top = __reduce_max_sync(kFull, w[0]);
-            if (w[0] == top) {
-                slots[r] = top;
+            const bool mine = w[0] == top;
+            if (mine) slots[r] = top;
 #pragma unroll
-                for (int j = 0; j < N && j < kFew - 1 - r; ++j) w[j] = j + 1 < N ? w[j + 1] : 0u;
-            }
+            for (int j = 0; j < N && j < kRounds - 1 - r; ++j) w[j] = mine ? (j + 1 < N ? w[(j + 1) % N] : 0u) : w[j];
         }
     } else {
         for (int r = 0; r < rounds; ++r) {
             const uint32_t top = __reduce_max_sync(kFull, w[0]);
-            if (w[0] == top) {
-                slots[r] = top;
+            const bool mine = w[0] == top;
+            if (mine) slots[r] = top;
 #pragma unroll
-                for (int j = 0; j < N; ++j) w[j] = j + 1 < N ? w[j + 1] : 0u;
-            }
+            for (int j = 0; j < N; ++j) w[j] = mine ? (j + 1 < N ? w[(j + 1) % N] : 0u) : w[j];
         }
     }
     __syncwarp();
-    const uint32_t win = slots[lane];
+    const uint32_t win = lane < (kRounds > 0 ? kRounds : rounds) ? slots[lane] : 0u;
     __syncwarp();
     return win;
 }
 
 // Sum over lanes [0, K) (the others hold 0), valid in those lanes.
-__device__ __forceinline__ float sum_kept(float v, int K) {
-    for (int o = 1; o < K; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
+template <int kFewK>
+__device__ __forceinline__ float sum_kept(float v) {
+    if (kFewK > 0) {  // K <= kFewK
+#pragma unroll
+        for (int o = 1; o < kFewK; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+        return v;
+    }
+    return warp_sum(v);
 }
 
-__device__ __forceinline__ void store_slot(const RouteArgs& p, long long t, int slot, int idx, float w) {
-    p.topk_idx[t * p.K + slot] = idx;
-    p.topk_w[t * p.K + slot] = w * p.rc.scale;
-}
+constexpr int kFewK = 8;  // K up to this has its rounds unrolled
+
+// Where a warp's slots go; moved along with its tokens, so that no token needs a
+// 64-bit product.
+struct SlotOut {
+    int64_t* idx;
+    float* w;
+    long long step;
+    __device__ __forceinline__ SlotOut(const RouteArgs& p, long long t, long long tokens)
+        : idx(p.topk_idx + t * p.K), w(p.topk_w + t * p.K), step(tokens * p.K) {}
+    __device__ __forceinline__ void put(int slot, int i, float v) {
+        idx[slot] = i;
+        w[slot] = v;
+    }
+    __device__ __forceinline__ void move() {
+        idx += step;
+        w += step;
+    }
+};
 
 // ---- bf16 logits that are the keys themselves: the word holds the whole key ----
 //
@@ -280,7 +295,7 @@ __device__ __forceinline__ uint32_t half_signs(uint32_t v) {
     return r;
 }
 
-template <int N>
+template <int N, bool kFew>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const RouteArgs p) {
     __shared__ uint32_t s_slots[kRouteWarps][kWarp];
     const int lane = threadIdx.x % kWarp, first = lane * N;
@@ -290,13 +305,13 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
     const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
     const bool on = first < p.E;  // E is a multiple of N; lanes past it hold masked logits
-    const uint16_t* row = static_cast<const uint16_t*>(p.logits) + first;
+    const uint16_t* src = static_cast<const uint16_t*>(p.logits) + t * p.E + first;
+    SlotOut out(p, t, step);
     uint32_t next[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) next[i] = 0xff80ff80u;  // -inf
-    auto load = [&](long long token) {
+    auto load = [&]() {
         if (!on) return;
-        const uint16_t* src = row + token * p.E;
         if (N >= 8) {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i) {
@@ -311,40 +326,44 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
             for (int i = 0; i < N / 2; ++i) next[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
         }
     };
-    if (t < p.tokens) load(t);
-    for (; t < p.tokens; t += step) {
+    if (t < p.tokens) load();
+    for (; t < p.tokens; t += step, out.move()) {
         uint32_t raw[N / 2];
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) raw[j] = next[j];
-        if (t + step < p.tokens) load(t + step);
-        uint32_t w[N], win = 0;
-        for (int pass = 0;; ++pass) {
+        src += step * p.E;
+        if (t + step < p.tokens) load();
+        uint32_t w[N];
+        auto words = [&]() {
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
                 const uint32_t o = raw[j] ^ (half_signs(raw[j]) | 0x80008000u);
                 w[2 * j] = __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j), 0x1054);
                 w[2 * j + 1] = __byte_perm(o, 0xffffu - static_cast<uint32_t>(first + 2 * j + 1), 0x3254);
             }
-            if (pass == 1) {
-                bool nan = false;
+        };
+        words();
+        sort_descending<N>(w);
+        bool special = w[0] >= (kInf16 << 16) || w[N - 1] < (kMinusInf16 << 16);
+        uint32_t win = take<N, kFew ? kFewK : 0>(w, p.K, lane, slots);
+        uint32_t o = win >> 16;
+        // a zero among the winners: a kept one is always seen, and with none kept no zero matters
+        special |= o - kMinusZero16 <= 1u;
+        if (__any_sync(kFull, special)) {
+            words();
+            bool nan = false;
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    uint32_t o = w[j] >> 16;
-                    nan |= o > kInf16 || o < kMinusInf16;
-                    o = o > kInf16 || o <= kLowest16 ? 0u : o == kInf16 ? kLargest16 : o == kMinusZero16 ? kZero16 : o;
-                    w[j] = o == 0u ? 0u : (o << 16) | (w[j] & 0xffffu);
-                }
-                if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
+            for (int j = 0; j < N; ++j) {
+                uint32_t c = w[j] >> 16;
+                nan |= c > kInf16 || c < kMinusInf16;
+                c = c > kInf16 || c <= kLowest16 ? 0u : c == kInf16 ? kLargest16 : c == kMinusZero16 ? kZero16 : c;
+                w[j] = c == 0u ? 0u : (c << 16) | (w[j] & 0xffffu);
             }
+            if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
             sort_descending<N>(w);
-            bool special = w[0] >= (kInf16 << 16) || w[N - 1] < (kMinusInf16 << 16);
-            win = take<N>(w, p.K, lane, slots);
-            const uint32_t o = win >> 16;
-            // a zero among the winners: a kept one is always seen, and with none kept no zero matters
-            special |= o == kMinusZero16 || o == kZero16;
-            if (pass == 1 || !__any_sync(kFull, special)) break;
+            win = take<N, 0>(w, p.K, lane, slots);
+            o = win >> 16;
         }
-        const uint32_t o = win >> 16;
         const bool kept = lane < p.K && o > kLowest16;
         const float logit = __uint_as_float((o & 0x8000u ? o ^ 0x8000u : o ^ 0xffffu) << 16);
         // softmax over the winners, the first of them the largest; or over all experts
@@ -352,17 +371,18 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
         const float mine = kept ? expf(logit - m) : 0.0f;
         float total;
         if (p.rc.renorm) {
-            total = sum_kept(mine, p.K);
+            total = sum_kept<kFew ? kFewK : 0>(mine);
         } else {
             total = 0.0f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float l = __uint_as_float(j % 2 == 0 ? raw[j / 2] << 16 : raw[j / 2] & 0xffff0000u);
-                if (on && l > -largest<true>()) total += expf(fminf(l, largest<true>()) - m);
+                if (l > -largest<true>()) total += expf(fminf(l, largest<true>()) - m);
             }
             total = warp_sum(total);
         }
-        if (lane < p.K) store_slot(p, t, lane, kept ? static_cast<int>(0xffffu - (win & 0xffffu)) : -1, kept ? mine / total : 0.0f);
+        const float weight = __fdividef(mine, total) * p.rc.scale;
+        if (lane < p.K) out.put(lane, kept ? static_cast<int>(0xffffu - (win & 0xffffu)) : -1, kept ? weight : 0.0f);
     }
 }
 
@@ -452,7 +472,7 @@ __device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, in
 
 // kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.  E is a
 // multiple of N.
-template <bool kBf16, int N, int kMode>
+template <bool kBf16, int N, int kMode, bool kFew>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const RouteArgs p, int seg, int vec) {
     constexpr int kIdxBits = N <= 8 ? 8 : 9;
     constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1u;
@@ -481,9 +501,11 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
     float next[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) next[j] = 0.0f;
-    if (t < p.tokens && on) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, vec != 0, next);
-    for (; t < p.tokens; t += step) {
-        const long long base = t * p.E;
+    long long base = t * p.E;
+    const long long base_step = step * p.E;
+    SlotOut out(p, t, step);
+    if (t < p.tokens && on) load_lane<kBf16, N>(p.logits, base, first, p.E, vec != 0, next);
+    for (; t < p.tokens; t += step, base += base_step, out.move()) {
         uint32_t k[N];
         float m = -FLT_MAX, total = 0.0f;
         if (kMode == 0 && !p.rc.renorm) {  // softmax over all experts
@@ -513,7 +535,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             }
             k[j] = key_of(v);
         }
-        if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, base + step * p.E, first, p.E, vec != 0, next);
+        if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, base + base_step, first, p.E, vec != 0, next);
         bool bad = odd != odd || p.K == kWarp;  // with 32 winners no lane is left for the runner-up
         bool kept = on;
         if (groups) {
@@ -525,7 +547,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
 #pragma unroll
         for (int j = 0; j < N; ++j) k[j] = (k[j] & keep) | (index - (kept ? static_cast<uint32_t>(j) : 0u));
         sort_descending<N>(k);
-        const uint32_t win = take<N>(k, min(p.K + 1, kWarp), lane, slots);  // lane K: the runner-up
+        const uint32_t win = take<N, kFew ? kFewK + 1 : 0>(k, min(p.K + 1, kWarp), lane, slots);  // lane K: the runner-up
         const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
         int idx = win != 0u && lane < p.K ? static_cast<int>(kIdxMask - (win & kIdxMask)) : -1;
         float logit = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : 0.0f;
@@ -591,24 +613,14 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
                 slot = rank;
             }
         }
-        float wt;
+        float wt = s;
         if (kMode == 0) {
-            if (p.rc.renorm) {
-                m = warp_max(idx >= 0 ? logit : -FLT_MAX);
-                wt = idx >= 0 ? expf(logit - m) : 0.0f;
-                total = sum_kept(wt, p.K);
-            } else {
-                wt = idx >= 0 ? expf(logit - m) : 0.0f;
-            }
-            wt = total > 0.0f ? wt / total : 0.0f;
-        } else {
-            wt = s;
-            if (p.rc.renorm) {
-                total = sum_kept(wt, p.K);
-                wt = total > 0.0f ? wt / total : 0.0f;
-            }
+            if (p.rc.renorm) m = warp_max(idx >= 0 ? logit : -FLT_MAX);
+            wt = idx >= 0 ? expf(logit - m) : 0.0f;
         }
-        if (lane < p.K) store_slot(p, t, slot, idx, wt);
+        if (p.rc.renorm) total = sum_kept<kFew ? kFewK : 0>(wt);
+        if (kMode == 0 || p.rc.renorm) wt = total > 0.0f ? wt / total : 0.0f;
+        if (lane < p.K) out.put(slot, idx, wt * p.rc.scale);
     }
 }
 
@@ -713,14 +725,25 @@ cudaError_t launch_tokens(void (*kernel)(RouteArgs, Args...), const RouteArgs& p
                       stream, 0, false, p, args...);
 }
 
+template <int N>
+cudaError_t launch_bf16(const RouteArgs& p, int sms, cudaStream_t stream) {
+    return p.K <= kFewK ? launch_tokens<>(route_bf16_kernel<N, true>, p, sms, stream)
+                        : launch_tokens<>(route_bf16_kernel<N, false>, p, sms, stream);
+}
+
+template <bool kBf16, int kMode, int N>
+cudaError_t launch_lists_n(const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
+    return p.K <= kFewK ? launch_tokens<int, int>(route_lists_kernel<kBf16, N, kMode, true>, p, sms, stream, seg, vec)
+                        : launch_tokens<int, int>(route_lists_kernel<kBf16, N, kMode, false>, p, sms, stream, seg, vec);
+}
+
 template <bool kBf16, int kMode>
 cudaError_t launch_lists(int n, const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
     switch (n) {
-        case 1: return launch_tokens<int, int>(route_lists_kernel<kBf16, 1, kMode>, p, sms, stream, seg, vec);
-        case 2: return launch_tokens<int, int>(route_lists_kernel<kBf16, 2, kMode>, p, sms, stream, seg, vec);
-        case 4: return launch_tokens<int, int>(route_lists_kernel<kBf16, 4, kMode>, p, sms, stream, seg, vec);
-        case 8: return launch_tokens<int, int>(route_lists_kernel<kBf16, 8, kMode>, p, sms, stream, seg, vec);
-        default: return launch_tokens<int, int>(route_lists_kernel<kBf16, 16, kMode>, p, sms, stream, seg, vec);
+        case 2: return launch_lists_n<kBf16, kMode, 2>(p, seg, vec, sms, stream);
+        case 4: return launch_lists_n<kBf16, kMode, 4>(p, seg, vec, sms, stream);
+        case 8: return launch_lists_n<kBf16, kMode, 8>(p, seg, vec, sms, stream);
+        default: return launch_lists_n<kBf16, kMode, 16>(p, seg, vec, sms, stream);
     }
 }
 
@@ -732,14 +755,14 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     if (sms <= 0) return cudaErrorInvalidDevice;
     const RouteArgs p = {logits, bias, topk_idx, topk_w, status, static_cast<long long>(sh.R) * sh.T, sh.E, sh.K, rc};
     const bool by_logit = rc.score == 0 && bias == nullptr && (rc.group_top == 1 || rc.topk_groups == rc.G);
-    const int n = sh.E <= 32 ? 1 : sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;  // experts of a lane
+    const int n = sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;  // experts of a lane
     if (sh.E <= 512 && sh.E % n == 0 && (rc.score == 1 || by_logit)) {
-        if (bf16 && by_logit && rc.topk_groups == rc.G && n > 1) {
+        if (bf16 && by_logit && rc.topk_groups == rc.G) {
             switch (n) {
-                case 2: return launch_tokens<>(route_bf16_kernel<2>, p, sms, stream);
-                case 4: return launch_tokens<>(route_bf16_kernel<4>, p, sms, stream);
-                case 8: return launch_tokens<>(route_bf16_kernel<8>, p, sms, stream);
-                default: return launch_tokens<>(route_bf16_kernel<16>, p, sms, stream);
+                case 2: return launch_bf16<2>(p, sms, stream);
+                case 4: return launch_bf16<4>(p, sms, stream);
+                case 8: return launch_bf16<8>(p, sms, stream);
+                default: return launch_bf16<16>(p, sms, stream);
             }
         }
         const int per_group = sh.E / rc.G, seg = per_group / n;

@@ -433,6 +433,12 @@ __device__ __forceinline__ void load_lane(const void* logits, long long base, in
 }
 
 __device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid_approx(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 
 // A group's key from its two largest ones (-inf: no expert can be taken).
 __device__ __forceinline__ float group_value(uint32_t k1, uint32_t k2, int group_top) {
@@ -530,7 +536,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             odd = fmaf(next[j] * 4.0f, 0.0f, odd);
             float v = next[j];
             if (kMode == 1) {
-                v = __fdividef(1.0f, 1.0f + __expf(-v)) + bias[j];
+                v = sigmoid_approx(v) + bias[j];
                 odd = fmaf(v, 0.0f, odd);
             }
             k[j] = key_of(v);
@@ -635,88 +641,181 @@ struct RouteBwdArgs {
     RouteCfg rc;
 };
 
+// The gradient's slot part: lane k's expert (-1: none), and what it adds to that
+// expert's gradient.  `m` and `inv` are the softmax's maximum and reciprocal sum
+// over all experts where it is not renormalised (dense), `dot` what every expert
+// then loses p_e times.
+struct SlotGrad {
+    int idx;
+    float own, dot;
+};
+template <bool kBf16>
+__device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, long long t, int lane, float m, float inv) {
+    const bool softmax = p.rc.score == 0, dense = softmax && !p.rc.renorm;
+    const float hi = largest<kBf16>();
+    long long id = lane < p.K ? __ldg(p.topk_idx + t * p.K + lane) : -1;
+    if (id < -1 || id >= p.E) {
+        flag_error(p.status, EP_DEV_INPUT);
+        id = -1;
+    }
+    SlotGrad r;
+    r.idx = static_cast<int>(id);
+    float l = r.idx >= 0 ? load_logit<kBf16>(p.logits, t * p.E + r.idx) : -INFINITY;
+    const bool on = l > -hi;  // a masked expert's score is 0 and stays 0
+    l = fminf(l, hi);
+    const float g = on ? __ldg(p.grad_w + t * p.K + lane) * p.rc.scale : 0.0f;
+    const float top = softmax && !dense ? warp_max(on ? l : -FLT_MAX) : m;
+    float s = 0.0f;  // the kept score
+    if (on) s = softmax ? expf(l - top) * (dense ? inv : 1.0f) : 1.0f / (1.0f + expf(-l));
+    float ds = g;  // its gradient
+    if (p.rc.renorm) {
+        const float total = warp_sum(s);
+        const float v = total > 0.0f ? s / total : 0.0f;
+        const float c = g - warp_sum(v * g);
+        ds = softmax ? c : (total > 0.0f ? c / total : 0.0f);
+        if (softmax) s = v;
+    }
+    r.dot = dense ? warp_sum(s * ds) : 0.0f;
+    r.own = softmax ? s * ds : s * (1.0f - s) * ds;
+    return r;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void store_grad(void* out, long long i, float d) {
+    if (kBf16)
+        static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(d);
+    else
+        static_cast<float*>(out)[i] = d;
+}
+
+// One token, any E, any logits, repeated experts added up in slot order.
+template <bool kBf16>
+__device__ __noinline__ void backward_token(const RouteBwdArgs& p, long long t, int lane) {
+    const bool dense = p.rc.score == 0 && !p.rc.renorm;
+    const float hi = largest<kBf16>();
+    const long long base = t * p.E;
+    float m = -FLT_MAX, inv = 0.0f;
+    if (dense) {
+        float sum = 0.0f;
+        for (int e = lane; e < p.E; e += kWarp) {
+            const float v = load_logit<kBf16>(p.logits, base + e);
+            if (v > -hi) m = fmaxf(m, fminf(v, hi));
+        }
+        m = warp_max(m);
+        for (int e = lane; e < p.E; e += kWarp) {
+            const float v = load_logit<kBf16>(p.logits, base + e);
+            if (v > -hi) sum += expf(fminf(v, hi) - m);
+        }
+        sum = warp_sum(sum);
+        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    const SlotGrad g = slot_gradient<kBf16>(p, t, lane, m, inv);
+    for (int e0 = 0; e0 < p.E; e0 += kWarp) {
+        const int e = e0 + lane;
+        float d = 0.0f;
+        if (dense && e < p.E) {
+            const float v = load_logit<kBf16>(p.logits, base + e);
+            if (v > -hi) d = -expf(fminf(v, hi) - m) * inv * g.dot;
+        }
+        for (int k = 0; k < p.K; ++k) {
+            const int ek = __shfl_sync(kFull, g.idx, k);
+            const float gk = __shfl_sync(kFull, g.own, k);
+            if (ek == e && ek >= 0) d += gk;
+        }
+        if (e < p.E) store_grad<kBf16>(p.grad_logits, base + e, d);
+    }
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(const RouteBwdArgs p) {
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     griddep_launch_dependents();
     griddep_wait();  // the logits, ids and gradients are complete from here on
-    const bool softmax = p.rc.score == 0;
-    const float hi = largest<kBf16>();
-    for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < p.tokens;
-         t += static_cast<long long>(gridDim.x) * kRouteWarps) {
-        const long long base = t * p.E;
-        // lane k holds slot k
-        long long id = lane < p.K ? __ldg(p.topk_idx + t * p.K + lane) : -1;
-        if (id < -1 || id >= p.E) {
-            flag_error(p.status, EP_DEV_INPUT);
-            id = -1;
-        }
-        const int idx = static_cast<int>(id);
-        float l = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : -INFINITY;
-        const bool on = l > -hi;  // a masked expert's score is 0 and stays 0
-        l = fminf(l, hi);
-        const float g = on ? __ldg(p.grad_w + t * p.K + lane) * p.rc.scale : 0.0f;
-        float m = 0.0f, inv = 0.0f;
-        const bool dense = softmax && !p.rc.renorm;
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
+    for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp; t < p.tokens; t += step)
+        backward_token<kBf16>(p, t, threadIdx.x % kWarp);
+}
+
+// Up to 512 experts in rows of whole 16-byte vectors: lane i holds the N experts
+// from i * N on, reads and writes them as vectors, and finds its slots' parts in
+// a shared row that is zero but for them.  Bound by HBM: the exponentials are
+// ex2.approx (2^-22, and 2^-24 of the exponent).  A token with unusual logits, or
+// with an expert in two slots, goes through backward_token.
+template <bool kBf16, int N>
+__global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
+    __shared__ alignas(16) float s_rows[kRouteWarps][kWarp * N];
+    const int lane = threadIdx.x % kWarp, first = lane * N;
+    float* row = s_rows[threadIdx.x / kWarp];
+#pragma unroll
+    for (int j = 0; j < N; ++j) row[first + j] = 0.0f;
+    __syncwarp();
+    griddep_launch_dependents();
+    griddep_wait();  // the logits, ids and gradients are complete from here on
+    const bool dense = p.rc.score == 0 && !p.rc.renorm, on = first < p.E;
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
+    long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
+    float next[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) next[j] = 0.0f;
+    if (dense && t < p.tokens && on) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, true, next);
+    for (; t < p.tokens; t += step) {
+        float d[N];
+        float m = -FLT_MAX, sum = 0.0f, odd = 0.0f;
         if (dense) {
-            m = -FLT_MAX;
-            float sum = 0.0f;
-            for (int e = lane; e < p.E; e += kWarp) {
-                const float v = load_logit<kBf16>(p.logits, base + e);
-                if (v > -hi) m = fmaxf(m, fminf(v, hi));
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                d[j] = next[j];
+                odd = fmaf(d[j] * 4.0f, 0.0f, odd);  // NaN: infinite, NaN or lowest values
+                if (on) m = fmaxf(m, d[j]);
             }
+            if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, (t + step) * p.E, first, p.E, true, next);
             m = warp_max(m);
-            for (int e = lane; e < p.E; e += kWarp) {
-                const float v = load_logit<kBf16>(p.logits, base + e);
-                if (v > -hi) sum += expf(fminf(v, hi) - m);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                d[j] = on ? __expf(d[j] - m) : 0.0f;
+                sum += d[j];
             }
             sum = warp_sum(sum);
-            inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         }
-        const float top = softmax && !dense ? warp_max(on ? l : -FLT_MAX) : 0.0f;
-        float s;  // the kept score
-        if (!softmax)
-            s = on ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-        else if (dense)
-            s = on ? expf(l - m) * inv : 0.0f;
-        else
-            s = on ? expf(l - top) : 0.0f;
-        float ds = g;  // gradient of the kept score
-        if (p.rc.renorm) {
-            const float total = warp_sum(s);
-            const float v = total > 0.0f ? s / total : 0.0f;
-            const float c = g - warp_sum(v * g);
-            ds = softmax ? c : (total > 0.0f ? c / total : 0.0f);
-            if (softmax) s = v;
+        const float inv = dense ? 1.0f / sum : 0.0f;
+        const SlotGrad g = slot_gradient<kBf16>(p, t, lane, m, inv);
+        // an expert in two slots: the lanes of one id, those without one aside
+        const unsigned same = __match_any_sync(kFull, g.idx >= 0 ? g.idx : -1 - lane);
+        if (__any_sync(kFull, odd != odd || (same & (same - 1u)) != 0u)) {
+            backward_token<kBf16>(p, t, lane);
+            continue;
         }
-        const float dot = dense ? warp_sum(s * ds) : 0.0f;
-        const float own = softmax ? s * ds : s * (1.0f - s) * ds;  // this slot's part of its expert's gradient
-        for (int e0 = 0; e0 < p.E; e0 += kWarp) {
-            const int e = e0 + lane;
-            float d = 0.0f;
-            if (dense && e < p.E) {
-                const float v = load_logit<kBf16>(p.logits, base + e);
-                if (v > -hi) d = -expf(fminf(v, hi) - m) * inv * dot;
+        if (g.idx >= 0) row[g.idx] = g.own;
+        __syncwarp();
+        const float c = inv * g.dot;
+#pragma unroll
+        for (int j = 0; j < N; ++j) d[j] = dense ? fmaf(-d[j], c, row[first + j]) : row[first + j];
+        __syncwarp();
+        if (g.idx >= 0) row[g.idx] = 0.0f;
+        if (!on) continue;
+        if (kBf16) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.grad_logits) + t * p.E + first);
+#pragma unroll
+            for (int i = 0; i < N / 8; ++i) {
+                uint32_t v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(d[8 * i + 2 * j], d[8 * i + 2 * j + 1]);
+                    v[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                out[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
-            for (int k = 0; k < p.K; ++k) {
-                const int ek = __shfl_sync(kFull, idx, k);
-                const float gk = __shfl_sync(kFull, own, k);
-                if (ek == e && ek >= 0) d += gk;
-            }
-            if (e < p.E) {
-                if (kBf16)
-                    static_cast<__nv_bfloat16*>(p.grad_logits)[base + e] = __float2bfloat16_rn(d);
-                else
-                    static_cast<float*>(p.grad_logits)[base + e] = d;
-            }
+        } else {
+            float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.grad_logits) + t * p.E + first);
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+                out[i] = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
         }
     }
 }
 
 // One resident CTA of warps for each place on the SMs, or fewer.
-template <typename... Args>
-cudaError_t launch_tokens(void (*kernel)(RouteArgs, Args...), const RouteArgs& p, int sms, cudaStream_t stream,
-                          Args... args) {
+template <typename P, typename... Args>
+cudaError_t launch_tokens(void (*kernel)(P, Args...), const P& p, int sms, cudaStream_t stream, Args... args) {
     const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
     const int resident = max_blocks_per_sm(reinterpret_cast<const void*>(kernel), kRouteWarps * kWarp, 0);
     if (resident <= 0) return cudaErrorInvalidValue;
@@ -727,14 +826,14 @@ cudaError_t launch_tokens(void (*kernel)(RouteArgs, Args...), const RouteArgs& p
 
 template <int N>
 cudaError_t launch_bf16(const RouteArgs& p, int sms, cudaStream_t stream) {
-    return p.K <= kFewK ? launch_tokens<>(route_bf16_kernel<N, true>, p, sms, stream)
-                        : launch_tokens<>(route_bf16_kernel<N, false>, p, sms, stream);
+    return p.K <= kFewK ? launch_tokens(route_bf16_kernel<N, true>, p, sms, stream)
+                        : launch_tokens(route_bf16_kernel<N, false>, p, sms, stream);
 }
 
 template <bool kBf16, int kMode, int N>
 cudaError_t launch_lists_n(const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
-    return p.K <= kFewK ? launch_tokens<int, int>(route_lists_kernel<kBf16, N, kMode, true>, p, sms, stream, seg, vec)
-                        : launch_tokens<int, int>(route_lists_kernel<kBf16, N, kMode, false>, p, sms, stream, seg, vec);
+    return p.K <= kFewK ? launch_tokens(route_lists_kernel<kBf16, N, kMode, true>, p, sms, stream, seg, vec)
+                        : launch_tokens(route_lists_kernel<kBf16, N, kMode, false>, p, sms, stream, seg, vec);
 }
 
 template <bool kBf16, int kMode>
@@ -791,11 +890,19 @@ cudaError_t launch_route_backward(const Shape& sh, const RouteCfg& rc, const voi
     if (sms <= 0) return cudaErrorInvalidDevice;
     const RouteBwdArgs p = {logits, topk_idx, grad_topk_w, grad_logits, status, static_cast<long long>(sh.R) * sh.T,
                             sh.E, sh.K, rc};
-    const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
-    const long long most = sms * 16LL;
-    const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-    return bf16 ? launch_pdl(route_backward_kernel<true>, grid, dim3(kRouteWarps * kWarp), 0, stream, 0, false, p)
-                : launch_pdl(route_backward_kernel<false>, grid, dim3(kRouteWarps * kWarp), 0, stream, 0, false, p);
+    if (sh.E <= 512 && (static_cast<long long>(sh.E) * (bf16 ? 2 : 4)) % 16 == 0) {
+        if (bf16)
+            return sh.E <= 256 ? launch_tokens(route_backward_lanes_kernel<true, 8>, p, sms, stream)
+                               : sh.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<true, 16>, p, sms, stream)
+                                                : launch_tokens(route_backward_kernel<true>, p, sms, stream);
+        return sh.E <= 128   ? launch_tokens(route_backward_lanes_kernel<false, 4>, p, sms, stream)
+               : sh.E % 8 != 0 ? launch_tokens(route_backward_kernel<false>, p, sms, stream)
+               : sh.E <= 256 ? launch_tokens(route_backward_lanes_kernel<false, 8>, p, sms, stream)
+               : sh.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<false, 16>, p, sms, stream)
+                                : launch_tokens(route_backward_kernel<false>, p, sms, stream);
+    }
+    return bf16 ? launch_tokens(route_backward_kernel<true>, p, sms, stream)
+                : launch_tokens(route_backward_kernel<false>, p, sms, stream);
 }
 
 }  // namespace ep

@@ -641,29 +641,39 @@ struct RouteBwdArgs {
     RouteCfg rc;
 };
 
-// The gradient's slot part: lane k's expert (-1: none), and what it adds to that
-// expert's gradient.  `m` and `inv` are the softmax's maximum and reciprocal sum
+// The gradient's slot part: lane k's expert and its incoming gradient; what it
+// adds to that expert's logit gradient.  `m` and `inv` are the softmax's maximum and reciprocal sum
 // over all experts where it is not renormalised (dense), `dot` what every expert
 // then loses p_e times.
+struct Slot {
+    long long id;
+    float g;
+};
+__device__ __forceinline__ Slot load_slot(const RouteBwdArgs& p, long long t, int lane) {
+    Slot s = {-1, 0.0f};
+    if (lane < p.K) {
+        s.id = __ldg(p.topk_idx + t * p.K + lane);
+        s.g = __ldg(p.grad_w + t * p.K + lane);
+    }
+    return s;
+}
+// The slot's expert, -1 for none.
+__device__ __forceinline__ int slot_expert(const RouteBwdArgs& p, const Slot& s) {
+    if (s.id >= 0 && s.id < p.E) return static_cast<int>(s.id);
+    if (s.id != -1) flag_error(p.status, EP_DEV_INPUT);
+    return -1;
+}
 struct SlotGrad {
-    int idx;
     float own, dot;
 };
 template <bool kBf16>
-__device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, long long t, int lane, float m, float inv) {
+__device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, float l, float grad, float m, float inv) {
     const bool softmax = p.rc.score == 0, dense = softmax && !p.rc.renorm;
     const float hi = largest<kBf16>();
-    long long id = lane < p.K ? __ldg(p.topk_idx + t * p.K + lane) : -1;
-    if (id < -1 || id >= p.E) {
-        flag_error(p.status, EP_DEV_INPUT);
-        id = -1;
-    }
     SlotGrad r;
-    r.idx = static_cast<int>(id);
-    float l = r.idx >= 0 ? load_logit<kBf16>(p.logits, t * p.E + r.idx) : -INFINITY;
     const bool on = l > -hi;  // a masked expert's score is 0 and stays 0
     l = fminf(l, hi);
-    const float g = on ? __ldg(p.grad_w + t * p.K + lane) * p.rc.scale : 0.0f;
+    const float g = on ? grad * p.rc.scale : 0.0f;
     const float top = softmax && !dense ? warp_max(on ? l : -FLT_MAX) : m;
     float s = 0.0f;  // the kept score
     if (on) s = softmax ? expf(l - top) * (dense ? inv : 1.0f) : 1.0f / (1.0f + expf(-l));
@@ -709,7 +719,10 @@ __device__ __noinline__ void backward_token(const RouteBwdArgs& p, long long t, 
         sum = warp_sum(sum);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    const SlotGrad g = slot_gradient<kBf16>(p, t, lane, m, inv);
+    const Slot slot = load_slot(p, t, lane);
+    const int idx = slot_expert(p, slot);
+    const float l = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : -INFINITY;
+    const SlotGrad g = slot_gradient<kBf16>(p, l, slot.g, m, inv);
     for (int e0 = 0; e0 < p.E; e0 += kWarp) {
         const int e = e0 + lane;
         float d = 0.0f;
@@ -718,7 +731,7 @@ __device__ __noinline__ void backward_token(const RouteBwdArgs& p, long long t, 
             if (v > -hi) d = -expf(fminf(v, hi) - m) * inv * g.dot;
         }
         for (int k = 0; k < p.K; ++k) {
-            const int ek = __shfl_sync(kFull, g.idx, k);
+            const int ek = __shfl_sync(kFull, idx, k);
             const float gk = __shfl_sync(kFull, g.own, k);
             if (ek == e && ek >= 0) d += gk;
         }
@@ -756,8 +769,17 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
     float next[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) next[j] = 0.0f;
-    if (dense && t < p.tokens && on) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, true, next);
+    Slot ahead = {-1, 0.0f};
+    if (t < p.tokens) {
+        if (dense && on) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, true, next);
+        ahead = load_slot(p, t, lane);
+    }
     for (; t < p.tokens; t += step) {
+        const Slot slot = ahead;
+        const int idx = slot_expert(p, slot);
+        const float l = idx >= 0 ? load_logit<kBf16>(p.logits, t * p.E + idx) : -INFINITY;
+        if (t + step < p.tokens) ahead = load_slot(p, t + step, lane);
+        if (idx >= 0) row[idx] = __int_as_float(lane);  // of two slots with one expert, one keeps its mark
         float d[N];
         float m = -FLT_MAX, sum = 0.0f, odd = 0.0f;
         if (dense) {
@@ -777,20 +799,23 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
             sum = warp_sum(sum);
         }
         const float inv = dense ? 1.0f / sum : 0.0f;
-        const SlotGrad g = slot_gradient<kBf16>(p, t, lane, m, inv);
-        // an expert in two slots: the lanes of one id, those without one aside
-        const unsigned same = __match_any_sync(kFull, g.idx >= 0 ? g.idx : -1 - lane);
-        if (__any_sync(kFull, odd != odd || (same & (same - 1u)) != 0u)) {
+        const SlotGrad g = slot_gradient<kBf16>(p, l, slot.g, m, inv);
+        __syncwarp();
+        const bool twice = idx >= 0 && __float_as_int(row[idx]) != lane;
+        if (__any_sync(kFull, odd != odd || twice)) {
             backward_token<kBf16>(p, t, lane);
+            if (idx >= 0) row[idx] = 0.0f;
+            __syncwarp();
             continue;
         }
-        if (g.idx >= 0) row[g.idx] = g.own;
+        if (idx >= 0) row[idx] = g.own;
         __syncwarp();
         const float c = inv * g.dot;
 #pragma unroll
         for (int j = 0; j < N; ++j) d[j] = dense ? fmaf(-d[j], c, row[first + j]) : row[first + j];
         __syncwarp();
-        if (g.idx >= 0) row[g.idx] = 0.0f;
+        if (idx >= 0) row[idx] = 0.0f;
+        __syncwarp();
         if (!on) continue;
         if (kBf16) {
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.grad_logits) + t * p.E + first);

@@ -1,5 +1,5 @@
 // Experts' block-scaled e4m3 products on the tensor cores (ep_ll_gemm_fp8,
-// ep_ll_gemm_swiglu_fp8).
+// ep_ll_gemm_swiglu_fp8): tiles of more than 128 rows.
 //
 //   p[m][n] = sum_b as[m][b] ws[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
 //
@@ -22,30 +22,22 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "ep.h"
-#include "ep_device.cuh"
-#include "ep_internal.h"
-#include "fp8_cast.cuh"
-#include "tcgen05.cuh"
+#include "ll_gemm_fp8.cuh"
 
 namespace ep {
+namespace gemm {
 
 namespace {
 
-constexpr int kTileM = 256;                    // rows of a pair's tile, 128 per CTA
 constexpr int kTileN = 256;                    // weight rows of a pair's tile
-constexpr int kHalf = 128;                     // rows of a, and of w, that one CTA loads
-constexpr int kChunk = 32;                     // rows of one TMA box of a
-constexpr int kBlockK = kScaleBlock;           // 128 e4m3: one 128-byte swizzled row
-constexpr int kTileBytes = kHalf * kBlockK;    // 16 KB, one operand of a stage
+constexpr int kHalf = kBoxRows;                // rows of a, and of w, that one CTA loads
+constexpr int kTileBytes = kBoxBytes;          // one operand of a stage
 constexpr int kStages = 6;
 constexpr int kGroups = 4;                     // epilogue warpgroups, 64 columns of a tile each
 constexpr int kGroupCols = kHalf / kGroups;    // of each of the tile's two weight blocks
 constexpr int kThreads = 128 + 128 * kGroups;  // producer, two MMA warps, scale warp | epilogue
 constexpr int kScaleSlots = 3;                 // of four k-blocks each
 constexpr int kHalfN = kTileN / 2;             // weight rows of one MMA: 64 of each CTA's 128; its TMEM columns
-constexpr int kTmemColumns = 512;
-constexpr long long kWaitLimitNs = 2000000000LL;
 
 struct Barriers {
     uint64_t full[kStages];             // leader's: bytes of both CTAs have landed
@@ -61,99 +53,19 @@ struct Shared {
     float row_scale[kScaleSlots][4][kHalf];  // of each row of the CTA
     float2 w_scale[kScaleSlots][4];          // of the tile's two weight blocks
     float amax[2][kGroups][kHalf];           // [tile parity][warpgroup][row]
-    int first[8192 / kWarp + 2];             // tiles before each group of 32 experts
+    int first[kMaxGroups + 2];               // tiles before each group of 32 experts
     uint32_t tmem;
     int abort;
 };
-
-struct Params {
-    GemmArgs g;
-    int kb, nb, tiles_n;
-};
-
-// One wait of a role: false when the limit passes.
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Shared* s) {
-    const long long start = globaltimer_ns();
-    do {
-        for (int i = 0; i < 1024; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-    } while (globaltimer_ns() - start < kWaitLimitNs);
-    *reinterpret_cast<volatile int*>(&s->abort) = 1;
-    return false;
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Shared* s) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return wait_slow(bar, parity, s);
-}
-
-// The pair's tiles: experts in order, then row tiles, then weight tiles.
-// `first` holds the tiles before each group of 32 experts; a role walks on
-// from the expert of its last tile.
-struct Walk {
-    int e = 0, before = 0;  // an expert, and the tiles before it
-};
-struct Tile {
-    int e, m0, n0, rows;  // rows: valid rows of the expert from m0 on
-};
-__device__ __forceinline__ int expert_rows(const Params& p, int e) {
-    return min(max(__ldg(p.g.count + e), 0), p.g.cap);
-}
-__device__ __forceinline__ Tile tile_at(int t, Walk& w, const int* first, const Params& p, int cols) {
-    if (first[w.e / kWarp + 1] <= t) {
-        int group = w.e / kWarp + 1;
-        while (first[group + 1] <= t) ++group;
-        w.e = group * kWarp;
-        w.before = first[group];
-    }
-    Tile r;
-    for (;;) {
-        r.rows = expert_rows(p, w.e);
-        const int n = (r.rows + kTileM - 1) / kTileM * p.tiles_n;
-        if (w.before + n > t) break;
-        w.before += n;
-        ++w.e;
-    }
-    const int local = t - w.before;
-    r.e = w.e;
-    r.m0 = local / p.tiles_n * kTileM;
-    r.n0 = local % p.tiles_n * cols;
-    r.rows -= r.m0;
-    return r;
-}
 
 // Row `row` of this CTA's half of the tile, in the packed rows of all experts.
 __device__ __forceinline__ long long tile_row(const Tile& t, const Params& p, uint32_t rank, int row) {
     return static_cast<long long>(t.e) * p.g.cap + t.m0 + static_cast<int>(rank) * kHalf + row;
 }
-// Scales of the tile's weight block `which` (0 or 1): gate and up, or two
-// neighbours (the last one again when it has no neighbour; those columns are past n).
-template <bool kSwiglu>
-__device__ __forceinline__ const float* weight_scales(const Tile& t, const Params& p, int which) {
-    const long long first = static_cast<long long>(t.e) * (kSwiglu ? 2 : 1) * p.nb + t.n0 / kScaleBlock;
-    const long long block = kSwiglu ? which * p.nb : min(which, p.nb - 1 - t.n0 / kScaleBlock);
-    return p.g.w_scales + (first + block) * p.kb;
-}
-
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-}
-
-// Four consecutive k-blocks' scales of a row or a weight block (0 past the end).
-__device__ __forceinline__ float4 load_scales(const float* p, int b, int kb, bool on) {
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (!on || b >= kb) return v;
-    if (kb % 4 == 0) return __ldg(reinterpret_cast<const float4*>(p + b));  // rows on 16-byte boundaries
-    v.x = __ldg(p + b);
-    if (b + 1 < kb) v.y = __ldg(p + b + 1);
-    if (b + 2 < kb) v.z = __ldg(p + b + 2);
-    if (b + 3 < kb) v.w = __ldg(p + b + 3);
-    return v;
-}
-__device__ __forceinline__ float element(const float4& v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 template <bool kSwiglu>
@@ -190,26 +102,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&map_w);
     }
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
-    griddep_launch_dependents();
     griddep_wait();  // counts, rows and scales are complete from here on
-    const int groups = (p.g.E + kWarp - 1) / kWarp;
-    if (warp == 1) {  // one warp counts the tiles
-        int base = 0;
-        for (int i = 0; i < groups; ++i) {
-            if (lane == 0) s->first[i] = base;
-            const int e = i * kWarp + lane;
-            const int n = e < p.g.E ? (expert_rows(p, e) + kTileM - 1) / kTileM * p.tiles_n : 0;
-            base += static_cast<int>(__reduce_add_sync(0xffffffffu, n));
-        }
-        if (lane == 0) s->first[groups] = base;
-    }
+    griddep_launch_dependents();  // after the wait: the few-rows kernel starts on these inputs beside this one
+    if (warp == 1) count_tiles<false>(s->first, p, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive_release();
     cluster_wait_acquire();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
-    const int tiles = s->first[groups];
+    const int tiles = s->first[(p.g.E + kWarp - 1) / kWarp];
 
     if (warp < 4) {
         regs_down<64>();
@@ -220,7 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             const uint32_t full = mapa(smem_addr(&s->bar.full[0]), 0);
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const Tile tl = tile_at(t, walk, s->first, p, cols);
+                const Tile tl = tile_at<false>(t, walk, s->first, p, cols);
                 const int chunks0 = (min(tl.rows, kHalf) + kChunk - 1) / kChunk;
                 const int chunks1 = (min(max(tl.rows - kHalf, 0), kHalf) + kChunk - 1) / kChunk;
                 const int chunks = rank == 0 ? chunks0 : chunks1;
@@ -229,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int wz = kSwiglu ? 2 * tl.e + static_cast<int>(rank) : tl.e;
                 const int ay = tl.m0 + static_cast<int>(rank) * kHalf;
                 for (int b = 0; b < p.kb; ++b) {
-                    if (!(ok = wait_for(&s->bar.empty[st], phase, s))) break;
+                    if (!(ok = wait_for(&s->bar.empty[st], phase, &s->abort))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&s->bar.full[st], bytes);
                     const uint32_t bar = full + st * sizeof(uint64_t);
                     const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
@@ -247,7 +149,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // every stage's last read is over before the CTA may leave
             for (int i = 0; i < kStages && ok; ++i) {
-                ok = wait_for(&s->bar.empty[st], phase, s);
+                ok = wait_for(&s->bar.empty[st], phase, &s->abort);
                 if (++st == kStages) {
                     st = 0;
                     phase ^= 1;
@@ -263,11 +165,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (uint32_t it = 0; it < blocks; ++it) {
                 // everything but the accumulator's hand-back is settled before the wait for it: what follows that
                 // wait is on the path of every block
-                bool ok = wait_for(&s->bar.full[st], full_phase, s);
+                bool ok = wait_for(&s->bar.full[st], full_phase, &s->abort);
                 const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
                 uint64_t da = sw128_desc(ta), dw = sw128_desc(ta + kTileBytes + half * (kTileBytes / 2));
                 asm volatile("" : "+l"(da), "+l"(dw));
-                ok = ok && wait_for(&s->bar.acc_empty[half][buf], empty_phase, s);
+                ok = ok && wait_for(&s->bar.acc_empty[half][buf], empty_phase, &s->abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -292,7 +194,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Walk walk;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const Tile tl = tile_at(t, walk, s->first, p, cols);
+                const Tile tl = tile_at<false>(t, walk, s->first, p, cols);
                 const int left = tl.rows - static_cast<int>(rank) * kHalf;
                 const float* as = p.g.a_scales + tile_row(tl, p, rank, lane) * p.kb;
                 const long long step = static_cast<long long>(kWarp) * p.kb;
@@ -302,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < left);
                     const float4 w = load_scales(ws, b, p.kb, lane < 2);
-                    ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_empty[slot], phase, s));
+                    ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_empty[slot], phase, &s->abort));
                     if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -333,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Walk walk;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
-            const Tile tl = tile_at(t, walk, s->first, p, cols);
+            const Tile tl = tile_at<false>(t, walk, s->first, p, cols);
             const int left = tl.rows - static_cast<int>(rank) * kHalf;
             const bool warp_on = quarter * kWarp < left;
             uint64_t acc[kGroupCols];  // pairs of the first weight block, then of the second
@@ -342,10 +244,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int b = 0; b < p.kb; ++b, ++it) {
                 const uint32_t buf = it & 1;
-                ok = (b & 3) != 0 || wait_for(&s->bar.scale_full[slot], slot_phase, s);
+                ok = (b & 3) != 0 || wait_for(&s->bar.scale_full[slot], slot_phase, &s->abort);
                 const float2 ws = s->w_scale[slot][b & 3];
                 const float as = s->row_scale[slot][b & 3][row];
-                ok = __all_sync(0xffffffffu, ok && wait_for(&full[buf], (it / 2) & 1, s));
+                ok = __all_sync(0xffffffffu, ok && wait_for(&full[buf], (it / 2) & 1, &s->abort));
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_on) {
@@ -407,8 +309,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kGroupCols / 2; ++j) {
                     const float2 a = unpack2(acc[j]), u = unpack2(acc[kGroupCols / 2 + j]);
-                    h[2 * j] = __fdividef(a.x, 1.0f + __expf(-a.x)) * u.x;
-                    h[2 * j + 1] = __fdividef(a.y, 1.0f + __expf(-a.y)) * u.y;
+                    h[2 * j] = gated(a.x, u.x);
+                    h[2 * j + 1] = gated(a.y, u.y);
                     amax = fmaxf(amax, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
                 }
                 // the other warpgroups have the rest of the block's 128 columns
@@ -450,38 +352,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (no device work), looked up once.
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeTiled>(f);
-    }();
-    return fn;
-}
-
-// Map of [outer][rows][k] bytes, boxes of `box_rows` rows x 128 bytes.
-bool make_map(CUtensorMap* map, const void* base, int k, int rows, int outer, int box_rows) {
-    const EncodeTiled encode = encode_tiled();
-    if (encode == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows),
-                                static_cast<cuuint64_t>(outer)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(k) * rows};
-    const cuuint32_t box[3] = {kBlockK, static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t step[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool kSwiglu>
 cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
     Params p = {};
@@ -505,9 +375,17 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
 }
 
 }  // namespace
+}  // namespace gemm
 
 cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream) {
-    return g.y_scales != nullptr ? launch<true>(g, stream) : launch<false>(g, stream);
+    // With up to 128 rows an expert there is nothing for the pairs.  Otherwise the few-rows kernel follows them and
+    // takes over SMs as they run dry: it starts on the inputs the pairs started on and waits for the pairs at its end.
+    const bool pairs = g.cap > gemm::kFewRows;
+    if (pairs) {
+        const cudaError_t e = g.y_scales != nullptr ? gemm::launch<true>(g, stream) : gemm::launch<false>(g, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return gemm::launch_few(g, !pairs, stream);
 }
 
 }  // namespace ep

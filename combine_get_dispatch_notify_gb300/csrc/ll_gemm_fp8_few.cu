@@ -1,0 +1,364 @@
+// Experts' block-scaled e4m3 products on the tensor cores, tiles of up to 128
+// rows (serving's few tokens an expert, and the rest of a longer one).
+//
+// Here the weights are the tensor cores' row operand: one CTA works alone on 256
+// weight rows (two blocks of 128, for the gated product gate and up of the same
+// 128 columns) and the rows of a are the columns of its accumulators, 16 to 128
+// of them as needed.  Such a tile is bound by the weights' bytes, so they are all
+// that is read in full: 32 KB a k-block for each SM, with four stages in flight.  A
+// row operand of a's few rows would multiply mostly padding, and its
+// accumulators would fill TMEM two blocks deep whatever the row count.
+//
+//   D[n][m] = sum_{k in block} w[n][k] a[m][k];  acc[n][m] += (as[m] ws) * D[n][m]
+//
+// An epilogue thread owns one weight row; the scales of its columns, as * ws, come
+// from shared memory in pairs.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ll_gemm_fp8.cuh"
+
+namespace ep {
+namespace gemm {
+
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kStageBytes = 3 * kBoxBytes;  // two blocks of weight rows, up to 128 rows of a
+constexpr int kThreads = 384;               // producer, MMA, scales, spare | two epilogue warpgroups
+constexpr int kAccColumns = 256;            // TMEM columns of one buffer: both weight blocks, 128 each
+constexpr int kScaleSlots = 3;              // of four k-blocks each
+constexpr int kExchange = 32;               // rows of a that pass between the warpgroups at once
+
+struct Shared {
+    uint64_t full[kStages];   // the stage's bytes have landed
+    uint64_t empty[kStages];  // its MMAs are done
+    uint64_t acc_full[2];     // a block's sums are in TMEM
+    uint64_t acc_empty[2];    // every epilogue warp has read them
+    uint64_t scale_full[kScaleSlots];
+    uint64_t scale_empty[kScaleSlots];
+    alignas(16) float scale[kScaleSlots][4][2][kFewRows];  // [k-block][weight block][row of a]
+    float up[kExchange][kBoxRows];                         // the up products on their way to the gates
+    float amax[kExchange][4];                              // of each row of a, by warp
+    int first[kMaxGroups + 2];
+    uint32_t tmem;
+    int abort;
+};
+
+// Barrier of the 256 epilogue threads, or of the first warpgroup's 128.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void gate_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+// Whether `ok` holds in all 256 epilogue threads.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return all != 0;
+}
+
+template <bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 1)
+    ll_gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                           const Params p, const int wait_first) {
+    extern __shared__ uint8_t s_raw[];
+    uint8_t* s_tiles = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);  // as the swizzle needs
+    Shared* s = reinterpret_cast<Shared*>(s_tiles + kStages * kStageBytes);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
+    constexpr int kCols = kSwiglu ? kBoxRows : 2 * kBoxRows;  // output columns of a tile
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s->full[i], 1);
+            mbar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], 8);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&s->scale_full[i], 1);
+            mbar_init(&s->scale_empty[i], 8);
+        }
+        s->abort = 0;
+        fence_mbarrier_init();
+        prefetch_tensormap(&map_a);
+        prefetch_tensormap(&map_w);
+    }
+    if (warp == 4) tmem_alloc(&s->tmem, kTmemColumns);
+    // Alone in its call, this kernel waits for what came before.  Behind the pairs it starts while they run: they let
+    // it start only once what came before them was complete, and it waits for them at its end.
+    if (wait_first) griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 1) count_tiles<true>(s->first, p, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s->tmem;
+    const int tiles = s->first[(p.g.E + kWarp - 1) / kWarp];
+    const int cta = blockIdx.x, ctas = gridDim.x;
+
+    if (warp < 4) {
+        regs_down<88>();
+        if (warp == 0 && lane == 0) {
+            // ---- producer ----
+            uint32_t st = 0, phase = 1;  // a fresh barrier passes a wait for phase 1
+            Walk walk;
+            bool ok = true;
+            for (int t = cta; t < tiles && ok; t += ctas) {
+                const Tile tl = tile_at<true>(t, walk, s->first, p, kCols);
+                const int chunks = (tl.rows + kChunk - 1) / kChunk;
+                const uint32_t bytes = 2 * kBoxBytes + chunks * kChunk * kBlockK;
+                const int y1 = kSwiglu ? tl.n0 : tl.n0 + kBoxRows;
+                const int z0 = kSwiglu ? 2 * tl.e : tl.e, z1 = kSwiglu ? z0 + 1 : z0;
+                for (int b = 0; b < p.kb; ++b) {
+                    if (!(ok = wait_for(&s->empty[st], phase, &s->abort))) break;
+                    const uint32_t bar = smem_addr(&s->full[st]), to = smem_addr(s_tiles) + st * kStageBytes;
+                    mbar_arrive_expect_tx(&s->full[st], bytes);
+                    tma_load_3d_alone(to, &map_w, b * kBlockK, tl.n0, z0, bar);
+                    tma_load_3d_alone(to + kBoxBytes, &map_w, b * kBlockK, y1, z1, bar);
+                    for (int c = 0; c < chunks; ++c)
+                        tma_load_3d_alone(to + 2 * kBoxBytes + c * kChunk * kBlockK, &map_a, b * kBlockK,
+                                          tl.m0 + c * kChunk, tl.e, bar);
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // every stage's last read is over before the CTA may leave
+            for (int i = 0; i < kStages && ok; ++i) {
+                ok = wait_for(&s->empty[st], phase, &s->abort);
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        } else if (warp == 1) {
+            // ---- MMA ----
+            uint32_t st = 0, full_phase = 0, buf = 0, empty_phase = 1;
+            Walk walk;
+            bool ok = true;
+            for (int t = cta; t < tiles && ok; t += ctas) {
+                const int rows = __shfl_sync(0xffffffffu, tile_at<true>(t, walk, s->first, p, kCols).rows, 0);
+                const uint32_t idesc = e4m3_idesc(kBoxRows, (rows + 15) / 16 * 16);
+                for (int b = 0; b < p.kb; ++b) {
+                    ok = wait_for(&s->full[st], full_phase, &s->abort);
+                    const uint32_t at = smem_addr(s_tiles) + st * kStageBytes;
+                    uint64_t dw = sw128_desc(at), da = sw128_desc(at + 2 * kBoxBytes);
+                    asm volatile("" : "+l"(da), "+l"(dw));
+                    ok = ok && wait_for(&s->acc_empty[buf], empty_phase, &s->abort);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int k = 0; k < kBlockK / 32; ++k)  // 32 bytes further inside the swizzled row
+                                mma_e4m3(tmem + buf * kAccColumns + h * kBoxRows, dw + h * (kBoxBytes >> 4) + 2 * k,
+                                         da + 2 * k, idesc, k > 0);
+                        mma_commit(smem_addr(&s->acc_full[buf]));
+                        mma_commit(smem_addr(&s->empty[st]));
+                    }
+                    __syncwarp();
+                    buf ^= 1;
+                    empty_phase ^= buf ^ 1;  // both buffers share a phase
+                    if (++st == kStages) {
+                        st = 0;
+                        full_phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == 2) {
+            // ---- scales: four rows of a to a lane, four k-blocks at a time ----
+            uint32_t slot = 0, phase = 1;
+            Walk walk;
+            bool ok = true;
+            for (int t = cta; t < tiles && ok; t += ctas) {
+                const Tile tl = tile_at<true>(t, walk, s->first, p, kCols);
+                const float* as = p.g.a_scales + (static_cast<long long>(tl.e) * p.g.cap + tl.m0 + lane) * p.kb;
+                const long long step = static_cast<long long>(kWarp) * p.kb;
+                const float* w0 = weight_scales<kSwiglu>(tl, p, 0);
+                const float* w1 = weight_scales<kSwiglu>(tl, p, 1);
+                for (int b = 0; b < p.kb; b += 4) {
+                    float4 a[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < tl.rows);
+                    const float4 v0 = load_scales(w0, b, p.kb, true), v1 = load_scales(w1, b, p.kb, true);
+                    ok = __all_sync(0xffffffffu, wait_for(&s->scale_empty[slot], phase, &s->abort));
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            s->scale[slot][i][0][lane + j * kWarp] = element(a[j], i) * element(v0, i);
+                            s->scale[slot][i][1][lane + j * kWarp] = element(a[j], i) * element(v1, i);
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->scale_full[slot]);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue: warpgroup g has weight block g, a thread one of its rows and the sums of every row of a ----
+        regs_up<208>();
+        const int g = (warp - 4) / 4, quarter = warp % 4;
+        const int row = quarter * kWarp + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g * kBoxRows;
+        const uint32_t empty = mapa(smem_addr(s->acc_empty), 0), scale_empty = mapa(smem_addr(s->scale_empty), 0);
+        uint32_t it = 0, slot = 0, slot_phase = 0;
+        Walk walk;
+        bool ok = true;
+        for (int t = cta; t < tiles && ok; t += ctas) {
+            const Tile tl = tile_at<true>(t, walk, s->first, p, kCols);
+            const int parts = (tl.rows + 31) / 32;  // of 32 rows of a
+            uint64_t acc[kFewRows / 2];
+#pragma unroll
+            for (int j = 0; j < kFewRows / 2; ++j) acc[j] = 0;
+#pragma unroll 1
+            for (int b = 0; b < p.kb; ++b, ++it) {
+                const uint32_t buf = it & 1;
+                ok = (b & 3) != 0 || wait_for(&s->scale_full[slot], slot_phase, &s->abort);
+                const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s->scale[slot][b & 3][g]);
+                ok = __all_sync(0xffffffffu, ok && wait_for(&s->acc_full[buf], (it / 2) & 1, &s->abort));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t col = lanes + buf * kAccColumns;
+#pragma unroll
+                for (int c = 0; c < kFewRows / 32; ++c) {
+                    if (c >= parts) break;
+                    uint64_t x[16];
+                    tmem_read32(col + c * 32, x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const ulonglong2 v = sc[c * 8 + j];
+                        fma2(acc[c * 16 + 2 * j], x[2 * j], v.x);
+                        fma2(acc[c * 16 + 2 * j + 1], x[2 * j + 1], v.y);
+                    }
+                }
+                tc_fence_before();  // the block's sums have left TMEM
+                if (lane == 0) {
+                    mbar_arrive_cluster_relaxed(empty + buf * 8);
+                    if ((b & 3) == 3 || b + 1 == p.kb) mbar_arrive_cluster_relaxed(scale_empty + slot * 8);
+                }
+                if (((b & 3) == 3 || b + 1 == p.kb) && ++slot == kScaleSlots) {
+                    slot = 0;
+                    slot_phase ^= 1;
+                }
+            }
+            ok = epilogue_all(ok);  // every epilogue warp comes here, also when a wait ran out
+            if (!ok) break;
+            const long long r0 = static_cast<long long>(tl.e) * p.g.cap + tl.m0;
+            if (!kSwiglu) {
+                const int n = tl.n0 + g * kBoxRows + row;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r0 * p.g.n + n;
+#pragma unroll
+                for (int j = 0; j < kFewRows / 2; ++j) {
+                    if (2 * j >= tl.rows) break;
+                    const float2 v = unpack2(acc[j]);
+                    if (n < p.g.n) {
+                        out[0] = __float2bfloat16_rn(v.x);
+                        if (2 * j + 1 < tl.rows) out[p.g.n] = __float2bfloat16_rn(v.y);
+                    }
+                    out += 2LL * p.g.n;
+                }
+            } else {
+                // The second warpgroup's up products pass to the first, 32 rows of a at a time.
+                const int n = tl.n0 + row;
+                uint8_t* out = static_cast<uint8_t*>(p.g.y) + r0 * p.g.n + n;
+#pragma unroll
+                for (int c = 0; c < kFewRows / kExchange; ++c) {
+                    if (c >= parts) break;
+                    if (g == 1) {
+#pragma unroll
+                        for (int j = 0; j < kExchange / 2; ++j) {
+                            const float2 v = unpack2(acc[c * kExchange / 2 + j]);
+                            s->up[2 * j][row] = v.x;
+                            s->up[2 * j + 1][row] = v.y;
+                        }
+                    }
+                    epilogue_sync();
+                    if (g == 0) {
+                        float h[kExchange];
+                        float mine = 0.0f;  // lane j: the largest of row j among the warp's 32 columns
+#pragma unroll
+                        for (int j = 0; j < kExchange; ++j) {
+                            const float2 v = unpack2(acc[c * kExchange / 2 + j / 2]);
+                            h[j] = gated(j % 2 == 0 ? v.x : v.y, s->up[j][row]);
+                            const float m = h[j] == h[j] ? fabsf(h[j]) : 0.0f;
+                            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+                            if (lane == j) mine = __uint_as_float(top);
+                        }
+                        s->amax[lane][quarter] = mine;
+                        gate_sync();
+                        const float4 m = *reinterpret_cast<const float4*>(s->amax[lane]);
+                        const float scale = block_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+                        const float inv = 1.0f / scale;
+                        if (quarter == 0 && c * kExchange + lane < tl.rows)
+                            p.g.y_scales[(r0 + c * kExchange + lane) * p.nb + tl.n0 / kScaleBlock] = scale;
+#pragma unroll
+                        for (int j = 0; j < kExchange; ++j) {
+                            const float q = h[j] * __shfl_sync(0xffffffffu, inv, j);
+                            if (n < p.g.n && c * kExchange + j < tl.rows)
+                                out[static_cast<long long>(c * kExchange + j) * p.g.n] =
+                                    static_cast<uint8_t>(pack_e4m3x4(q, 0.0f, 0.0f, 0.0f));
+                        }
+                    }
+                    epilogue_sync();  // before the next rows overwrite them
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s->abort != 0) {
+        // a wait ran out: let the copies and products still in flight land before shared memory and TMEM go
+        const long long start = globaltimer_ns();
+        while (globaltimer_ns() - start < 10000000LL) {
+        }
+        if (threadIdx.x == 0) flag_error(p.g.status, EP_DEV_TIMEOUT);
+    }
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc(tmem, kTmemColumns);
+    if (!wait_first) griddep_wait();  // this kernel's end is the call's: the pairs are done too
+}
+
+template <bool kSwiglu>
+cudaError_t launch(const GemmArgs& g, bool wait_first, cudaStream_t stream) {
+    Params p = {};
+    p.g = g;
+    p.kb = scale_blocks(g.k);
+    p.nb = scale_blocks(g.n);
+    const int cols = kSwiglu ? kBoxRows : 2 * kBoxRows;
+    p.tiles_n = (g.n + cols - 1) / cols;
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    CUtensorMap map_a, map_w;
+    if (!make_map(&map_a, g.a, g.k, g.cap, g.E, kChunk) ||
+        !make_map(&map_w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kBoxRows))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
+    const long long most = static_cast<long long>(g.E) * p.tiles_n;  // the counts are on the device
+    return launch_pdl(ll_gemm_fp8_few_kernel<kSwiglu>, dim3(static_cast<unsigned>(most < sms ? most : sms)),
+                      dim3(kThreads), smem, stream, 0, true, map_a, map_w, p, wait_first ? 1 : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_few(const GemmArgs& g, bool wait_first, cudaStream_t stream) {
+    return g.y_scales != nullptr ? launch<true>(g, wait_first, stream) : launch<false>(g, wait_first, stream);
+}
+
+}  // namespace gemm
+}  // namespace ep

@@ -433,8 +433,8 @@ __device__ __forceinline__ void load_lane(const void* logits, long long base, in
 }
 
 __device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
-__device__ __forceinline__ float sigmoid_approx(float l) {
-    float e, r;
+__device__ __forceinline__ float sigmoid_approx(float l, float& e) {  // e: exp(-l)
+    float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
@@ -464,14 +464,13 @@ __device__ __forceinline__ void segment_top2(const uint32_t (&k)[N], int seg, ui
 }
 
 // Whether this lane's group (value v) is one of the topk_groups largest, ties to
-// the lowest; `near` when another group comes within `margin`.
-__device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, int lane, float margin, bool& near) {
+// the lowest.
+__device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, int lane) {
     const int g = lane / seg;
     int above = 0;
     for (int i = 0; i < G; ++i) {
         const float d = __shfl_sync(kFull, v, i * seg) - v;  // every lane takes part; NaN between two infinities
         above += i < g ? !(d < 0.0f) : d > 0.0f;
-        near |= i != g && g < G && !(fabsf(d) > margin);
     }
     return g < G && above < topk;
 }
@@ -497,12 +496,13 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             bias[j] = p.bias != nullptr && on ? __ldg(p.bias + first + j) : 0.0f;
-            largest_key = fmaxf(largest_key, 1.0f + fabsf(bias[j]));
+            largest_key = !(fabsf(bias[j]) < INFINITY) ? INFINITY : fmaxf(largest_key, 1.0f + fabsf(bias[j]));
         }
         largest_key = warp_max(largest_key);
     }
+    const bool odd_bias = !(largest_key < INFINITY);  // infinite or NaN: every token goes the exact way
     // two groups closer than this could be ordered wrongly: two approximate keys in each, their sum's roundings
-    const float margin = kMode == 1 ? 4.0f * approx_error() + 4.76837158203125e-07f * largest_key : -1.0f;
+    const float margin = kMode == 1 ? 4.0f * approx_error() + 4.76837158203125e-07f * largest_key : 0.0f;
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
     float next[N];
 #pragma unroll
@@ -528,26 +528,38 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             }
             total = warp_sum(total);
         }
-        // Logits that are infinite, NaN or at the lowest value, and keys that are not finite, leave a NaN here: such
-        // a token goes the exact way, so the keys below need no tests.
+        // Masked and NaN logits leave a NaN here, and so does any below -88 with the sigmoid: such a token goes the
+        // exact way, so the keys below need no tests.
         float odd = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            odd = fmaf(next[j] * 4.0f, 0.0f, odd);
             float v = next[j];
             if (kMode == 1) {
-                v = sigmoid_approx(v) + bias[j];
-                odd = fmaf(v, 0.0f, odd);
+                float e;
+                v = sigmoid_approx(v, e) + bias[j];
+                odd = fmaf(e, 0.0f, odd);
+            } else {
+                odd = fmaf(v * 4.0f, 0.0f, odd);
             }
             k[j] = key_of(v);
         }
         if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, base + base_step, first, p.E, vec != 0, next);
-        bool bad = odd != odd || p.K == kWarp;  // with 32 winners no lane is left for the runner-up
+        bool bad = odd != odd || odd_bias || p.K == kWarp;  // with 32 winners no lane is left for the runner-up
         bool kept = on;
         if (groups) {
             uint32_t k1, k2;
             segment_top2<N>(k, seg, k1, k2);
-            kept = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane, margin, bad);
+            // one word a group, as for the experts; the last one kept has to be clear of the first one dropped
+            const float v = p.rc.group_top == 2 ? of_key(k1) + of_key(k2) : of_key(k1);
+            const uint32_t mine = on ? (key_of(v) & ~31u) | (31u - static_cast<uint32_t>(lane / seg)) : 0u;
+            uint32_t left = mine, last = 0;
+            for (int r = 0; r < p.rc.topk_groups; ++r) {
+                last = __reduce_max_sync(kFull, left);
+                if (left == last) left = 0;
+            }
+            kept = on && mine >= last;
+            const float a = of_key(last & ~31u), b = of_key(__reduce_max_sync(kFull, left) & ~31u);
+            bad |= !(a - b > margin + 3.814697265625e-06f * fabsf(b));  // the cut, 2^-18
         }
         const uint32_t keep = kept ? ~kIdxMask : 0u, index = kept ? kIdxMask - static_cast<uint32_t>(first) : 0u;
 #pragma unroll
@@ -556,7 +568,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
         const uint32_t win = take<N, kFew ? kFewK + 1 : 0>(k, min(p.K + 1, kWarp), lane, slots);  // lane K: the runner-up
         const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
         int idx = win != 0u && lane < p.K ? static_cast<int>(kIdxMask - (win & kIdxMask)) : -1;
-        float logit = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : 0.0f;
+        float logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
         float s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
         const float key = kMode == 1 ? (idx >= 0 && p.bias != nullptr ? s + __ldg(p.bias + idx) : s) : logit;
         if (idx >= 0 && runner != 0u) {
@@ -576,10 +588,9 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
             if (groups) {
                 uint32_t k1, k2;
-                bool unused = false;
                 segment_top2<N>(k, seg, k1, k2);
-                const bool in = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane,
-                                           -1.0f, unused);
+                const bool in =
+                    group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane);
 #pragma unroll
                 for (int j = 0; j < N; ++j) k[j] = in ? k[j] : kNone;
             }

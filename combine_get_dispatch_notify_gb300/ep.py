@@ -716,3 +716,69 @@ class Pipeline:
         ep_combine(sh, D["recv_x"] if y is None else y, None, Nt["send_pos"], Nt["recv_base"],
                    C["combined_x"], None, self.status, stream)
         return C["combined_x"]
+
+
+def cast_weight_blocks(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Weights [..., n, k] as the experts' products take them: e4m3 bytes (uint8) and one
+    fp32 scale per 128 x 128 block ([..., ceil(n / 128), ceil(k / 128)]), the block's largest
+    magnitude over 448.  Plain torch, for use once when weights are loaded."""
+    n, k = w.shape[-2:]
+    nb, kb = scale_blocks(n), scale_blocks(k)
+    blocks = torch.nn.functional.pad(w.float(), (0, kb * 128 - k, 0, nb * 128 - n))
+    blocks = blocks.unflatten(-1, (kb, 128)).unflatten(-3, (nb, 128))
+    scales = (blocks.abs().amax((-3, -1)).clamp(min=2.0 ** -100) / 448.0).contiguous()
+    q = (blocks / scales.unsqueeze(-1).unsqueeze(-3)).to(torch.float8_e4m3fn)
+    return q.view(torch.uint8).flatten(-4, -3).flatten(-2)[..., :n, :k].contiguous(), scales
+
+
+@dataclass
+class MoELayer:
+    """A mixture-of-experts layer on the low-latency layout: router, layout, casting
+    dispatch, gated e4m3 experts, weighted combine.  Owns every buffer; :meth:`run`
+    launches the calls on the current stream without synchronising.
+
+    ``ffn`` is the experts' inner size; ``expert_capacity`` bounds the rows of an expert
+    (slots beyond it are dropped and reported as EP_ERR_CAPACITY)."""
+
+    shape: EpShape
+    route: EpRoute
+    ffn: int
+    expert_capacity: int
+    device: str = "cuda"
+
+    def __post_init__(self):
+        sh, cap, F, dev = self.shape, self.expert_capacity, self.ffn, self.device
+        R, T, K, E, H = sh.num_ranks, sh.num_tokens, sh.num_topk, sh.num_experts, sh.hidden
+        z = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.topk_idx, self.topk_w = z(R, T, K, dt=torch.int64), z(R, T, K, dt=torch.float32)
+        # the layout counts for itself where one cluster of R CTAs can; else the counts come from the layout step
+        self.layout = None if R <= 16 and R * E <= 16384 else alloc_layout(sh, dev)
+        self.slot_pos, self.layout_range, self.count = z(R, T, K), z(E, R, 2), z(E)
+        self.rows = z(E, cap, H, dt=torch.uint8)
+        self.row_scales = z(E, cap, scale_blocks(H), dt=torch.float32)
+        self.inner = z(E, cap, F, dt=torch.uint8)
+        self.inner_scales = z(E, cap, scale_blocks(F), dt=torch.float32)
+        self.y = z(E, cap, H, dt=torch.bfloat16)
+        self.combined_x = z(R, T, H, dt=torch.bfloat16)
+
+    def run(self, x, logits, bias, w13, w13_scales, w2, w2_scales, stream=None):
+        """``x`` [R, T, H] bf16 and router ``logits`` [R, T, E] -> combined_x [R, T, H] bf16.
+        Weights as :func:`cast_weight_blocks` makes them: ``w13`` [E, 2, ffn, H] (gate, up) and
+        ``w2`` [E, H, ffn]; ``bias`` [E] of the selection, or None."""
+        sh, cap = self.shape, self.expert_capacity
+        ep_route(sh, self.route, logits, bias, self.topk_idx, self.topk_w, self.status, stream)
+        counts = None
+        if self.layout is not None:
+            L = self.layout
+            ep_get_dispatch_layout(sh, self.topk_idx, L["num_tokens_per_rank"], L["num_tokens_per_rdma_rank"],
+                                   L["num_tokens_per_expert"], L["is_token_in_rank"], self.status, stream)
+            counts = L["num_tokens_per_expert"]
+        ep_ll_layout(sh, self.topk_idx, counts, cap, self.slot_pos, self.layout_range, self.count, self.status, stream)
+        ep_ll_dispatch_fp8(sh, x, self.topk_idx, self.slot_pos, cap, self.rows, self.row_scales, None, self.status,
+                           stream)
+        ep_ll_gemm_swiglu_fp8(self.rows, self.row_scales, w13, w13_scales, self.count, self.inner, self.inner_scales,
+                              self.status, stream)
+        ep_ll_gemm_fp8(self.inner, self.inner_scales, w2, w2_scales, self.count, self.y, self.status, stream)
+        ep_ll_combine(sh, self.y, cap, self.topk_idx, self.topk_w, self.slot_pos, self.combined_x, self.status, stream)
+        return self.combined_x

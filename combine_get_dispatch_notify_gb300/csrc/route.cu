@@ -6,8 +6,7 @@
 // bf16 logits that are keys themselves, keep a lane's keys as one sorted list of
 // 32-bit words in registers and take the K winners off the lists' heads;
 // route_kernel keeps the keys in shared memory and covers what the lists do not
-// (more than 512 experts, groups that do not fall on lanes, softmax scores with
-// a bias or summed for groups).
+// (more than 512 experts, softmax scores with a bias or summed for groups).
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -446,7 +445,15 @@ __device__ __forceinline__ float group_value(uint32_t k1, uint32_t k2, int group
     return group_top == 2 && k2 != kNone ? of_key(k1) + of_key(k2) : of_key(k1);
 }
 
-// Largest and second largest key of the `seg` lanes around this one.
+// Largest and second largest key of the `seg` lanes around this one, from each lane's own two.
+__device__ __forceinline__ void segment_merge2(int seg, uint32_t& k1, uint32_t& k2) {
+    for (int o = 1; o < seg; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
+        k2 = max(min(k1, o1), max(k2, o2));
+        k1 = max(k1, o1);
+    }
+}
+// The same from each lane's N keys.
 template <int N>
 __device__ __forceinline__ void segment_top2(const uint32_t (&k)[N], int seg, uint32_t& k1, uint32_t& k2) {
     k1 = k[0];
@@ -456,11 +463,7 @@ __device__ __forceinline__ void segment_top2(const uint32_t (&k)[N], int seg, ui
         k2 = max(k2, min(k1, k[j]));
         k1 = max(k1, k[j]);
     }
-    for (int o = 1; o < seg; o <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
-        k2 = max(min(k1, o1), max(k2, o2));
-        k1 = max(k1, o1);
-    }
+    segment_merge2(seg, k1, k2);
 }
 
 // Whether this lane's group (value v) is one of the topk_groups largest, ties to
@@ -475,34 +478,79 @@ __device__ __forceinline__ bool group_kept(float v, int G, int seg, int topk, in
     return g < G && above < topk;
 }
 
-// kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.  E is a
-// multiple of N.
-template <bool kBf16, int N, int kMode, bool kFew>
+// kMode: 0 the logit is the key (softmax keeps its order), 1 sigmoid.
+// kAny false: E is a multiple of N, lane i holds the experts from i * N on, groups
+// are runs of `seg` lanes (a power of two).  kAny true: any E and any groups; lane
+// i holds every 32nd expert from i on, and the groups' keys pass through a shared
+// row from which `seg` lanes scan each group.
+template <bool kBf16, int N, int kMode, bool kFew, bool kAny>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const RouteArgs p, int seg, int vec) {
     constexpr int kIdxBits = N <= 8 ? 8 : 9;
     constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1u;
     constexpr float kCut = 1.0f / (1 << (23 - kIdxBits));  // of a key, lost below the index
     __shared__ uint32_t s_slots[kRouteWarps][kWarp];
-    const int lane = threadIdx.x % kWarp, first = lane * N;
+    __shared__ uint32_t s_rows[kRouteWarps][kAny ? N * kWarp : 1];
+    const int lane = threadIdx.x % kWarp;
     uint32_t* slots = s_slots[threadIdx.x / kWarp];
+    uint32_t* row = s_rows[threadIdx.x / kWarp];
     const float lim = largest<kBf16>();
     griddep_launch_dependents();
     griddep_wait();  // the logits are complete from here on
     const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
-    const bool groups = p.rc.topk_groups < p.rc.G, on = first < p.E;
+    const bool groups = p.rc.topk_groups < p.rc.G;
+    const int per_group = p.E / p.rc.G;
+    auto expert = [&](int j) { return kAny ? lane + kWarp * j : lane * N + j; };
+    auto has = [&](int j) { return expert(kAny ? j : 0) < p.E; };  // an expert there
     float bias[N];
+    uint32_t group_bit[kAny ? N : 1];
     float largest_key = 1.0f;  // bound of the keys' magnitude
-    if (kMode == 1) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            bias[j] = p.bias != nullptr && on ? __ldg(p.bias + first + j) : 0.0f;
+    for (int j = 0; j < N; ++j) {
+        if (kMode == 1) {
+            bias[j] = p.bias != nullptr && has(j) ? __ldg(p.bias + expert(j)) : 0.0f;
             largest_key = !(fabsf(bias[j]) < INFINITY) ? INFINITY : fmaxf(largest_key, 1.0f + fabsf(bias[j]));
         }
-        largest_key = warp_max(largest_key);
+        if (kAny) group_bit[j % (kAny ? N : 1)] = has(j) ? 1u << (expert(j) / per_group) : 0u;
     }
+    if (kMode == 1) largest_key = warp_max(largest_key);
     const bool odd_bias = !(largest_key < INFINITY);  // infinite or NaN: every token goes the exact way
     // two groups closer than this could be ordered wrongly: two approximate keys in each, their sum's roundings
     const float margin = kMode == 1 ? 4.0f * approx_error() + 4.76837158203125e-07f * largest_key : 0.0f;
+    auto load = [&](long long base, float (&l)[N]) {
+        if (kAny) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (has(j)) l[j] = load_logit<kBf16>(p.logits, base + expert(j));
+        } else if (has(0)) {
+            load_lane<kBf16, N>(p.logits, base, lane * N, p.E, vec != 0, l);
+        }
+    };
+    // the two largest keys of the lane's group
+    auto group_top2 = [&](const uint32_t (&k)[N], uint32_t& k1, uint32_t& k2) {
+        if (kAny) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (has(j)) row[expert(j)] = k[j];
+            __syncwarp();
+            k1 = k2 = kNone;
+            const int g = lane / seg;
+            if (g < p.rc.G)
+                for (int i = lane % seg; i < per_group; i += seg) {
+                    const uint32_t v = row[g * per_group + i];
+                    k2 = max(k2, min(k1, v));
+                    k1 = max(k1, v);
+                }
+            __syncwarp();
+            segment_merge2(seg, k1, k2);
+        } else {
+            segment_top2<N>(k, seg, k1, k2);
+        }
+    };
+    // whether the lane's expert j is in a group kept, from the kept flags of the groups' lanes
+    auto group_mask = [&](bool kept) { return kAny ? __reduce_or_sync(kFull, kept ? 1u << (lane / seg) : 0u) : 0u; };
+    auto in_group = [&](int j, bool kept, uint32_t mask) {
+        return kAny ? (mask & group_bit[j % (kAny ? N : 1)]) != 0u : kept;
+    };
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
     float next[N];
 #pragma unroll
@@ -510,22 +558,18 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
     long long base = t * p.E;
     const long long base_step = step * p.E;
     SlotOut out(p, t, step);
-    if (t < p.tokens && on) load_lane<kBf16, N>(p.logits, base, first, p.E, vec != 0, next);
+    if (t < p.tokens) load(base, next);
     for (; t < p.tokens; t += step, base += base_step, out.move()) {
         uint32_t k[N];
         float m = -FLT_MAX, total = 0.0f;
         if (kMode == 0 && !p.rc.renorm) {  // softmax over all experts
-            if (on) {
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (next[j] > -lim) m = fmaxf(m, fminf(next[j], lim));
-            }
+            for (int j = 0; j < N; ++j)
+                if (has(j) && next[j] > -lim) m = fmaxf(m, fminf(next[j], lim));
             m = warp_max(m);
-            if (on) {
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (next[j] > -lim) total += expf(fminf(next[j], lim) - m);
-            }
+            for (int j = 0; j < N; ++j)
+                if (has(j) && next[j] > -lim) total += expf(fminf(next[j], lim) - m);
             total = warp_sum(total);
         }
         // Masked and NaN logits leave a NaN here, and so does any below -88 with the sigmoid: such a token goes the
@@ -543,27 +587,31 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             }
             k[j] = key_of(v);
         }
-        if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, base + base_step, first, p.E, vec != 0, next);
+        if (t + step < p.tokens) load(base + base_step, next);
         bool bad = odd != odd || odd_bias || p.K == kWarp;  // with 32 winners no lane is left for the runner-up
-        bool kept = on;
+        bool kept = true;
+        uint32_t mask = 0xffffffffu;
         if (groups) {
             uint32_t k1, k2;
-            segment_top2<N>(k, seg, k1, k2);
+            group_top2(k, k1, k2);
             // one word a group, as for the experts; the last one kept has to be clear of the first one dropped
             const float v = p.rc.group_top == 2 ? of_key(k1) + of_key(k2) : of_key(k1);
-            const uint32_t mine = on ? (key_of(v) & ~31u) | (31u - static_cast<uint32_t>(lane / seg)) : 0u;
-            uint32_t left = mine, last = 0;
+            const bool mine = lane / seg < p.rc.G;
+            const uint32_t word = mine ? (key_of(v) & ~31u) | (31u - static_cast<uint32_t>(lane / seg)) : 0u;
+            uint32_t left = word, last = 0;
             for (int r = 0; r < p.rc.topk_groups; ++r) {
                 last = __reduce_max_sync(kFull, left);
                 if (left == last) left = 0;
             }
-            kept = on && mine >= last;
+            kept = mine && word >= last;
             const float a = of_key(last & ~31u), b = of_key(__reduce_max_sync(kFull, left) & ~31u);
             bad |= !(a - b > margin + 3.814697265625e-06f * fabsf(b));  // the cut, 2^-18
+            mask = group_mask(kept);
         }
-        const uint32_t keep = kept ? ~kIdxMask : 0u, index = kept ? kIdxMask - static_cast<uint32_t>(first) : 0u;
 #pragma unroll
-        for (int j = 0; j < N; ++j) k[j] = (k[j] & keep) | (index - (kept ? static_cast<uint32_t>(j) : 0u));
+        for (int j = 0; j < N; ++j)
+            k[j] = has(j) && in_group(j, kept, mask) ? (k[j] & ~kIdxMask) | (kIdxMask - static_cast<uint32_t>(expert(j)))
+                                                     : 0u;
         sort_descending<N>(k);
         const uint32_t win = take<N, kFew ? kFewK + 1 : 0>(k, min(p.K + 1, kWarp), lane, slots);  // lane K: the runner-up
         const uint32_t runner = __shfl_sync(kFull, win, p.K & 31);
@@ -580,7 +628,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             bool nan = false;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float l = on ? load_logit<kBf16>(p.logits, base + first + j) : -INFINITY;
+                const float l = has(j) ? load_logit<kBf16>(p.logits, base + expert(j)) : -INFINITY;
                 const float v = kMode == 1 ? sigmoid_exact(fminf(l, lim)) + bias[j] : fminf(l, lim);
                 nan |= l != l || v != v;
                 k[j] = l > -lim && v > -INFINITY ? key_of(v) : kNone;
@@ -588,11 +636,12 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
             if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
             if (groups) {
                 uint32_t k1, k2;
-                segment_top2<N>(k, seg, k1, k2);
+                group_top2(k, k1, k2);
                 const bool in =
                     group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane);
+                const uint32_t exact_mask = group_mask(in);
 #pragma unroll
-                for (int j = 0; j < N; ++j) k[j] = in ? k[j] : kNone;
+                for (int j = 0; j < N; ++j) k[j] = in_group(j, in, exact_mask) ? k[j] : kNone;
             }
             idx = -1;
             for (int r = 0; r < p.K; ++r) {
@@ -606,12 +655,12 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
                     }
                 const uint32_t top = __reduce_max_sync(kFull, best);
                 if (top == kNone) break;
-                const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-                const int from = __shfl_sync(kFull, first + at, owner);
+                const int from = static_cast<int>(
+                    __reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(expert(at)) : 0xffffffffu));
                 if (lane == r) idx = from;
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    if (lane == owner && j == at) k[j] = kNone;
+                    if (expert(j) == from) k[j] = kNone;
             }
             logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
             s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
@@ -759,30 +808,42 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
         backward_token<kBf16>(p, t, threadIdx.x % kWarp);
 }
 
-// Up to 512 experts in rows of whole 16-byte vectors: lane i holds the N experts
-// from i * N on, reads and writes them as vectors, and finds its slots' parts in
-// a shared row that is zero but for them.  Bound by HBM: the exponentials are
+// Up to 512 experts.  With kVec rows are whole 16-byte vectors: lane i holds the N
+// experts from i * N on and reads and writes them as vectors; else it holds every
+// 32nd expert from i on.  It finds its slots' parts in a shared row that is zero
+// but for them.  Bound by HBM: the exponentials are
 // ex2.approx (2^-22, and 2^-24 of the exponent).  A token with unusual logits, or
 // with an expert in two slots, goes through backward_token.
-template <bool kBf16, int N>
+template <bool kBf16, int N, bool kVec>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
     __shared__ alignas(16) float s_rows[kRouteWarps][kWarp * N];
     const int lane = threadIdx.x % kWarp, first = lane * N;
     float* row = s_rows[threadIdx.x / kWarp];
+    auto expert = [&](int j) { return kVec ? first + j : lane + kWarp * j; };
+    auto has = [&](int j) { return expert(kVec ? 0 : j) < p.E; };  // kVec: E is a multiple of N
 #pragma unroll
     for (int j = 0; j < N; ++j) row[first + j] = 0.0f;
     __syncwarp();
     griddep_launch_dependents();
     griddep_wait();  // the logits, ids and gradients are complete from here on
-    const bool dense = p.rc.score == 0 && !p.rc.renorm, on = first < p.E;
+    const bool dense = p.rc.score == 0 && !p.rc.renorm;
     const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
+    auto load = [&](long long token, float (&l)[N]) {
+        if (kVec) {
+            if (has(0)) load_lane<kBf16, N>(p.logits, token * p.E, first, p.E, true, l);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (has(j)) l[j] = load_logit<kBf16>(p.logits, token * p.E + expert(j));
+        }
+    };
     float next[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) next[j] = 0.0f;
     Slot ahead = {-1, 0.0f};
     if (t < p.tokens) {
-        if (dense && on) load_lane<kBf16, N>(p.logits, t * p.E, first, p.E, true, next);
+        if (dense) load(t, next);
         ahead = load_slot(p, t, lane);
     }
     for (; t < p.tokens; t += step) {
@@ -798,13 +859,13 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
             for (int j = 0; j < N; ++j) {
                 d[j] = next[j];
                 odd = fmaf(d[j] * 4.0f, 0.0f, odd);  // NaN: infinite, NaN or lowest values
-                if (on) m = fmaxf(m, d[j]);
+                if (has(j)) m = fmaxf(m, d[j]);
             }
-            if (t + step < p.tokens && on) load_lane<kBf16, N>(p.logits, (t + step) * p.E, first, p.E, true, next);
+            if (t + step < p.tokens) load(t + step, next);
             m = warp_max(m);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                d[j] = on ? __expf(d[j] - m) : 0.0f;
+                d[j] = has(j) ? __expf(d[j] - m) : 0.0f;
                 sum += d[j];
             }
             sum = warp_sum(sum);
@@ -823,11 +884,17 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         __syncwarp();
         const float c = inv * g.dot;
 #pragma unroll
-        for (int j = 0; j < N; ++j) d[j] = dense ? fmaf(-d[j], c, row[first + j]) : row[first + j];
+        for (int j = 0; j < N; ++j) d[j] = dense ? fmaf(-d[j], c, row[expert(j)]) : row[expert(j)];
         __syncwarp();
         if (idx >= 0) row[idx] = 0.0f;
         __syncwarp();
-        if (!on) continue;
+        if (!kVec) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (has(j)) store_grad<kBf16>(p.grad_logits, t * p.E + expert(j), d[j]);
+            continue;
+        }
+        if (!has(0)) continue;
         if (kBf16) {
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.grad_logits) + t * p.E + first);
 #pragma unroll
@@ -867,19 +934,39 @@ cudaError_t launch_bf16(const RouteArgs& p, int sms, cudaStream_t stream) {
 }
 
 template <bool kBf16, int kMode, int N>
-cudaError_t launch_lists_n(const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
-    return p.K <= kFewK ? launch_tokens(route_lists_kernel<kBf16, N, kMode, true>, p, sms, stream, seg, vec)
-                        : launch_tokens(route_lists_kernel<kBf16, N, kMode, false>, p, sms, stream, seg, vec);
+cudaError_t launch_lists_n(const RouteArgs& p, int seg, int vec, bool any, int sms, cudaStream_t stream) {
+    if (any)
+        return p.K <= kFewK
+                   ? launch_tokens(route_lists_kernel<kBf16, N, kMode, true, true>, p, sms, stream, seg, vec)
+                   : launch_tokens(route_lists_kernel<kBf16, N, kMode, false, true>, p, sms, stream, seg, vec);
+    return p.K <= kFewK ? launch_tokens(route_lists_kernel<kBf16, N, kMode, true, false>, p, sms, stream, seg, vec)
+                        : launch_tokens(route_lists_kernel<kBf16, N, kMode, false, false>, p, sms, stream, seg, vec);
 }
 
 template <bool kBf16, int kMode>
-cudaError_t launch_lists(int n, const RouteArgs& p, int seg, int vec, int sms, cudaStream_t stream) {
+cudaError_t launch_lists(int n, const RouteArgs& p, int seg, int vec, bool any, int sms, cudaStream_t stream) {
     switch (n) {
-        case 2: return launch_lists_n<kBf16, kMode, 2>(p, seg, vec, sms, stream);
-        case 4: return launch_lists_n<kBf16, kMode, 4>(p, seg, vec, sms, stream);
-        case 8: return launch_lists_n<kBf16, kMode, 8>(p, seg, vec, sms, stream);
-        default: return launch_lists_n<kBf16, kMode, 16>(p, seg, vec, sms, stream);
+        case 2: return launch_lists_n<kBf16, kMode, 2>(p, seg, vec, any, sms, stream);
+        case 4: return launch_lists_n<kBf16, kMode, 4>(p, seg, vec, any, sms, stream);
+        case 8: return launch_lists_n<kBf16, kMode, 8>(p, seg, vec, any, sms, stream);
+        default: return launch_lists_n<kBf16, kMode, 16>(p, seg, vec, any, sms, stream);
     }
+}
+
+template <bool kBf16>
+cudaError_t launch_backward(const RouteBwdArgs& p, int sms, cudaStream_t stream) {
+    constexpr int kFewest = kBf16 ? 8 : 4;  // a 16-byte vector
+    const bool vec = p.E % kFewest == 0;
+    if (p.E <= kFewest * kWarp) {
+        if (vec) return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, true>, p, sms, stream);
+        if (p.E <= 2 * kWarp) return launch_tokens(route_backward_lanes_kernel<kBf16, 2, false>, p, sms, stream);
+        return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, false>, p, sms, stream);
+    }
+    if (p.E <= 8 * kWarp)
+        return p.E % 8 == 0 ? launch_tokens(route_backward_lanes_kernel<kBf16, 8, true>, p, sms, stream)
+                            : launch_tokens(route_backward_lanes_kernel<kBf16, 8, false>, p, sms, stream);
+    return p.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<kBf16, 16, true>, p, sms, stream)
+                         : launch_tokens(route_backward_lanes_kernel<kBf16, 16, false>, p, sms, stream);
 }
 
 }  // namespace
@@ -891,8 +978,9 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     const RouteArgs p = {logits, bias, topk_idx, topk_w, status, static_cast<long long>(sh.R) * sh.T, sh.E, sh.K, rc};
     const bool by_logit = rc.score == 0 && bias == nullptr && (rc.group_top == 1 || rc.topk_groups == rc.G);
     const int n = sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;  // experts of a lane
-    if (sh.E <= 512 && sh.E % n == 0 && (rc.score == 1 || by_logit)) {
-        if (bf16 && by_logit && rc.topk_groups == rc.G) {
+    if (sh.E <= 512 && (rc.score == 1 || by_logit)) {
+        const bool grouped = rc.topk_groups < rc.G;
+        if (bf16 && by_logit && !grouped && sh.E % n == 0) {
             switch (n) {
                 case 2: return launch_bf16<2>(p, sms, stream);
                 case 4: return launch_bf16<4>(p, sms, stream);
@@ -900,16 +988,19 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
                 default: return launch_bf16<16>(p, sms, stream);
             }
         }
-        const int per_group = sh.E / rc.G, seg = per_group / n;
-        // groups are whole power-of-two runs of lanes
-        const bool on_lanes = rc.topk_groups == rc.G || (per_group % n == 0 && (seg & (seg - 1)) == 0);
-        if (on_lanes) {
-            const int vec = (static_cast<long long>(sh.E) * (bf16 ? 2 : 4)) % 16 == 0;
-            return bf16 ? (rc.score == 0 ? launch_lists<true, 0>(n, p, seg, vec, sms, stream)
-                                         : launch_lists<true, 1>(n, p, seg, vec, sms, stream))
-                        : (rc.score == 0 ? launch_lists<false, 0>(n, p, seg, vec, sms, stream)
-                                         : launch_lists<false, 1>(n, p, seg, vec, sms, stream));
-        }
+        // Runs of experts in a lane (vector loads, groups by shuffles) where E and the groups fall on lanes, else
+        // every 32nd expert and groups through shared memory: 32768 x 256 sigmoid keys in 8 groups take 26 us in
+        // runs, 32 us the other way.
+        const int per_group = sh.E / rc.G;
+        int seg = per_group / n;
+        bool any = sh.E % n != 0 || (grouped && (per_group % n != 0 || (seg & (seg - 1)) != 0));
+        if (any)
+            for (seg = kWarp; seg * rc.G > kWarp;) seg /= 2;
+        const int vec = (static_cast<long long>(sh.E) * (bf16 ? 2 : 4)) % 16 == 0;
+        return bf16 ? (rc.score == 0 ? launch_lists<true, 0>(n, p, seg, vec, any, sms, stream)
+                                     : launch_lists<true, 1>(n, p, seg, vec, any, sms, stream))
+                    : (rc.score == 0 ? launch_lists<false, 0>(n, p, seg, vec, any, sms, stream)
+                                     : launch_lists<false, 1>(n, p, seg, vec, any, sms, stream));
     }
     const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
     const long long most = sms * 16LL;
@@ -926,17 +1017,7 @@ cudaError_t launch_route_backward(const Shape& sh, const RouteCfg& rc, const voi
     if (sms <= 0) return cudaErrorInvalidDevice;
     const RouteBwdArgs p = {logits, topk_idx, grad_topk_w, grad_logits, status, static_cast<long long>(sh.R) * sh.T,
                             sh.E, sh.K, rc};
-    if (sh.E <= 512 && (static_cast<long long>(sh.E) * (bf16 ? 2 : 4)) % 16 == 0) {
-        if (bf16)
-            return sh.E <= 256 ? launch_tokens(route_backward_lanes_kernel<true, 8>, p, sms, stream)
-                               : sh.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<true, 16>, p, sms, stream)
-                                                : launch_tokens(route_backward_kernel<true>, p, sms, stream);
-        return sh.E <= 128   ? launch_tokens(route_backward_lanes_kernel<false, 4>, p, sms, stream)
-               : sh.E % 8 != 0 ? launch_tokens(route_backward_kernel<false>, p, sms, stream)
-               : sh.E <= 256 ? launch_tokens(route_backward_lanes_kernel<false, 8>, p, sms, stream)
-               : sh.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<false, 16>, p, sms, stream)
-                                : launch_tokens(route_backward_kernel<false>, p, sms, stream);
-    }
+    if (sh.E <= 512) return bf16 ? launch_backward<true>(p, sms, stream) : launch_backward<false>(p, sms, stream);
     return bf16 ? launch_tokens(route_backward_kernel<true>, p, sms, stream)
                 : launch_tokens(route_backward_kernel<false>, p, sms, stream);
 }

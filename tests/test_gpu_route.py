@@ -258,3 +258,33 @@ def test_backward_masks_repeats_and_bad_ids(score, renorm):
     got, rc = run_backward(l, bad, g, score, renorm, 1.0)
     want, ok = run_backward(l, clean, g, score, renorm, 1.0)
     assert rc == ep.EP_ERR_INPUT and ok == ep.EP_OK and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("E,G,tg,gt,K", [(130, 13, 5, 2, 9), (45, 9, 4, 1, 3), (217, 7, 3, 2, 17), (31, 1, 1, 1, 12),
+                                         (390, 6, 2, 2, 8), (511, 1, 1, 1, 8), (66, 33 // 11, 2, 2, 32)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_route_groups_of_any_size(E, G, tg, gt, K, dtype):
+    bias = torch.round(torch.randn(E, generator=torch.Generator().manual_seed(5)) * 8) / 32
+    l = logits_of(1, 29, E, dtype, 6, _mask_some(-float("inf")))
+    l[0, 5:] = logits_of(1, 24, E, dtype, 7)[0]
+    for score in ("sigmoid", "softmax"):
+        check_route(l, None, K, score=score, G=G, topk_groups=tg, group_top=1)
+    check_route(l, bias, K, score="sigmoid", G=G, topk_groups=tg, group_top=gt)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_route_close_keys_keep_their_exact_order(dtype):
+    """Keys a few ulp apart, below what a cut or an approximate key can tell: the order is the exact
+    sigmoid's (fp32, as 1 / (1 + exp(-l)) rounds), ties to the lowest index."""
+    g = torch.Generator().manual_seed(8)
+    l = (2.0 + torch.randint(-40, 40, (1, 64, 256), generator=g) * 2.0 ** -22).to(dtype)
+    bias = torch.randint(-3, 4, (256,), generator=g) * 2.0 ** -23
+    idx, _, rc = run_route(l, bias, 8, score="sigmoid", G=8, topk_groups=4, group_top=2)
+    s = (1.0 / (1.0 + torch.exp(-l.float().cuda())) + bias.cuda()).cpu()
+    per = s.view(64, 8, 32)
+    two = per.sort(dim=-1, descending=True).values[..., :2].sum(-1)
+    keep = two.sort(dim=-1, descending=True, stable=True).indices[:, :4]
+    mask = torch.zeros(64, 8, dtype=torch.bool).scatter_(1, keep, True)
+    key = torch.where(mask.unsqueeze(-1), per, -9.0).view(64, 256)
+    want = key.sort(dim=-1, descending=True, stable=True).indices[:, :8]
+    assert rc == ep.EP_OK and torch.equal(idx.view(64, 8), want)

@@ -156,16 +156,18 @@ def _current_stream() -> int:
     return raw(torch.cuda.current_device())
 
 
-def _stream(stream) -> _vp:
+def _stream(stream) -> int:
     if stream is None:
-        return _vp(_current_stream())
-    return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return _current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _t(t: torch.Tensor | None, dtype, shape, name: str, nullable=False) -> _vp:
+def _t(t: torch.Tensor | None, dtype, shape, name: str, nullable=False) -> int | None:
+    """Device address of a checked tensor (None for a missing one), as ctypes takes it for a
+    ``void*``."""
     if t is None:
         if nullable:
-            return _vp(None)
+            return None
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
@@ -175,7 +177,7 @@ def _t(t: torch.Tensor | None, dtype, shape, name: str, nullable=False) -> _vp:
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _vp(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str) -> int:

@@ -11,8 +11,10 @@
 //
 //   D[n][m] = sum_{k in block} w[n][k] a[m][k];  acc[n][m] += (as[m] ws) * D[n][m]
 //
-// An epilogue thread owns one weight row; the scales of its columns, as * ws, come
-// from shared memory in pairs.
+// An epilogue thread owns one row of each weight block and every other 16
+// columns, so a scale read from shared memory serves two products (the reads, 512
+// bytes to the registers of a warp each, would else take as long as everything else),
+// and gate and up of one output column meet in one thread.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -30,7 +32,8 @@ constexpr int kStageBytes = 3 * kBoxBytes;  // two blocks of weight rows, up to 
 constexpr int kThreads = 384;               // producer, MMA, scales, spare | two epilogue warpgroups
 constexpr int kAccColumns = 256;            // TMEM columns of one buffer: both weight blocks, 128 each
 constexpr int kScaleSlots = 3;              // of four k-blocks each
-constexpr int kExchange = 32;               // rows of a that pass between the warpgroups at once
+constexpr int kPart = 16;                   // rows of a, taken in turn by the two epilogue warpgroups
+constexpr int kParts = kFewRows / kPart / 2;  // of one of them
 
 struct Shared {
     uint64_t full[kStages];   // the stage's bytes have landed
@@ -39,26 +42,25 @@ struct Shared {
     uint64_t acc_empty[2];    // every epilogue warp has read them
     uint64_t scale_full[kScaleSlots];
     uint64_t scale_empty[kScaleSlots];
-    alignas(16) float scale[kScaleSlots][4][2][kFewRows];  // [k-block][weight block][row of a]
-    float up[kExchange][kBoxRows];                         // the up products on their way to the gates
-    float amax[kExchange][4];                              // of each row of a, by warp
+    alignas(16) float row_scale[kScaleSlots][4][kFewRows];  // [k-block][row of a]
+    float2 w_scale[kScaleSlots][4];                         // of the two weight blocks
+    alignas(16) float amax[2][2][kPart][4];                 // [warpgroup][in turn][row of a][warp]
     int first[kMaxGroups + 2];
     uint32_t tmem;
     int abort;
 };
 
-// Barrier of the 256 epilogue threads, or of the first warpgroup's 128.
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void gate_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-// Whether `ok` holds in all 256 epilogue threads.
-__device__ __forceinline__ bool epilogue_all(bool ok) {
+// Barrier of an epilogue warpgroup.
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+// Whether `ok` holds in all its threads.
+__device__ __forceinline__ bool group_all(int g, bool ok) {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.aligned.pred q, 1, 256, p;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
-        : "r"(static_cast<uint32_t>(ok))
+        : "r"(static_cast<uint32_t>(ok)), "r"(1 + g)
         : "memory");
     return all != 0;
 }
@@ -184,22 +186,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile tl = tile_at<true>(t, walk, s->first, p, kCols);
                 const float* as = p.g.a_scales + (static_cast<long long>(tl.e) * p.g.cap + tl.m0 + lane) * p.kb;
                 const long long step = static_cast<long long>(kWarp) * p.kb;
-                const float* w0 = weight_scales<kSwiglu>(tl, p, 0);
-                const float* w1 = weight_scales<kSwiglu>(tl, p, 1);
+                const float* ws = weight_scales<kSwiglu>(tl, p, lane & 1);
                 for (int b = 0; b < p.kb; b += 4) {
                     float4 a[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < tl.rows);
-                    const float4 v0 = load_scales(w0, b, p.kb, true), v1 = load_scales(w1, b, p.kb, true);
+                    const float4 w = load_scales(ws, b, p.kb, lane < 2);
                     ok = __all_sync(0xffffffffu, wait_for(&s->scale_empty[slot], phase, &s->abort));
                     if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            s->scale[slot][i][0][lane + j * kWarp] = element(a[j], i) * element(v0, i);
-                            s->scale[slot][i][1][lane + j * kWarp] = element(a[j], i) * element(v1, i);
-                        }
+                        for (int j = 0; j < 4; ++j) s->row_scale[slot][i][lane + j * kWarp] = element(a[j], i);
+                        if (lane < 2) reinterpret_cast<float*>(&s->w_scale[slot][i])[lane] = element(w, i);
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s->scale_full[slot]);
                     if (++slot == kScaleSlots) {
@@ -211,40 +211,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue: warpgroup g has weight block g, a thread one of its rows and the sums of every row of a ----
+        // ---- epilogue: thread = one row of each weight block; warpgroup g has parts g, g + 2, ... of a's rows ----
         regs_up<208>();
         const int g = (warp - 4) / 4, quarter = warp % 4;
         const int row = quarter * kWarp + lane;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g * kBoxRows;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g * kPart;
         const uint32_t empty = mapa(smem_addr(s->acc_empty), 0), scale_empty = mapa(smem_addr(s->scale_empty), 0);
-        uint32_t it = 0, slot = 0, slot_phase = 0;
+        uint32_t it = 0, slot = 0, slot_phase = 0, turn = 0;
         Walk walk;
         bool ok = true;
         for (int t = cta; t < tiles && ok; t += ctas) {
             const Tile tl = tile_at<true>(t, walk, s->first, p, kCols);
-            const int parts = (tl.rows + 31) / 32;  // of 32 rows of a
-            uint64_t acc[kFewRows / 2];
+            const int parts = (tl.rows + kPart - 1) / kPart;
+            uint64_t acc[kParts][2][kPart / 2];
 #pragma unroll
-            for (int j = 0; j < kFewRows / 2; ++j) acc[j] = 0;
+            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                for (int j = 0; j < kPart / 2; ++j) acc[i][0][j] = acc[i][1][j] = 0;
 #pragma unroll 1
             for (int b = 0; b < p.kb; ++b, ++it) {
                 const uint32_t buf = it & 1;
                 ok = (b & 3) != 0 || wait_for(&s->scale_full[slot], slot_phase, &s->abort);
-                const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s->scale[slot][b & 3][g]);
+                const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s->row_scale[slot][b & 3] + g * kPart);
+                const float2 ws = s->w_scale[slot][b & 3];
                 ok = __all_sync(0xffffffffu, ok && wait_for(&s->acc_full[buf], (it / 2) & 1, &s->abort));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t col = lanes + buf * kAccColumns;
+                const uint64_t w0 = pair2(ws.x), w1 = pair2(ws.y);
 #pragma unroll
-                for (int c = 0; c < kFewRows / 32; ++c) {
-                    if (c >= parts) break;
-                    uint64_t x[16];
-                    tmem_read32(col + c * 32, x);
+                for (int i = 0; i < kParts; ++i) {
+                    if (2 * i + g >= parts) break;
+                    uint64_t x0[kPart / 2], x1[kPart / 2];
+                    tmem_read16x2(col + 2 * i * kPart, col + 2 * i * kPart + kBoxRows, x0, x1);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const ulonglong2 v = sc[c * 8 + j];
-                        fma2(acc[c * 16 + 2 * j], x[2 * j], v.x);
-                        fma2(acc[c * 16 + 2 * j + 1], x[2 * j + 1], v.y);
+                    for (int j = 0; j < kPart / 4; ++j) {
+                        const ulonglong2 v = sc[i * (2 * kPart / 4) + j];
+                        fma2(acc[i][0][2 * j], x0[2 * j], mul2(v.x, w0));
+                        fma2(acc[i][0][2 * j + 1], x0[2 * j + 1], mul2(v.y, w0));
+                        fma2(acc[i][1][2 * j], x1[2 * j], mul2(v.x, w1));
+                        fma2(acc[i][1][2 * j + 1], x1[2 * j + 1], mul2(v.y, w1));
                     }
                 }
                 tc_fence_before();  // the block's sums have left TMEM
@@ -257,65 +263,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot_phase ^= 1;
                 }
             }
-            ok = epilogue_all(ok);  // every epilogue warp comes here, also when a wait ran out
+            ok = group_all(g, ok);  // every warp of the group comes here, also when a wait ran out
             if (!ok) break;
-            const long long r0 = static_cast<long long>(tl.e) * p.g.cap + tl.m0;
-            if (!kSwiglu) {
-                const int n = tl.n0 + g * kBoxRows + row;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r0 * p.g.n + n;
 #pragma unroll
-                for (int j = 0; j < kFewRows / 2; ++j) {
-                    if (2 * j >= tl.rows) break;
-                    const float2 v = unpack2(acc[j]);
-                    if (n < p.g.n) {
-                        out[0] = __float2bfloat16_rn(v.x);
-                        if (2 * j + 1 < tl.rows) out[p.g.n] = __float2bfloat16_rn(v.y);
-                    }
-                    out += 2LL * p.g.n;
-                }
-            } else {
-                // The second warpgroup's up products pass to the first, 32 rows of a at a time.
+            for (int i = 0; i < kParts; ++i) {
+                if (2 * i + g >= parts) break;
+                const int m0 = (2 * i + g) * kPart;  // the part's first row, and how many are valid
+                const int valid = tl.rows - m0;
+                const long long r0 = static_cast<long long>(tl.e) * p.g.cap + tl.m0 + m0;
                 const int n = tl.n0 + row;
-                uint8_t* out = static_cast<uint8_t*>(p.g.y) + r0 * p.g.n + n;
+                if (!kSwiglu) {
 #pragma unroll
-                for (int c = 0; c < kFewRows / kExchange; ++c) {
-                    if (c >= parts) break;
-                    if (g == 1) {
+                    for (int w = 0; w < 2; ++w) {
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r0 * p.g.n + n + w * kBoxRows;
+                        const bool on = n + w * kBoxRows < p.g.n;
 #pragma unroll
-                        for (int j = 0; j < kExchange / 2; ++j) {
-                            const float2 v = unpack2(acc[c * kExchange / 2 + j]);
-                            s->up[2 * j][row] = v.x;
-                            s->up[2 * j + 1][row] = v.y;
+                        for (int j = 0; j < kPart / 2; ++j) {
+                            const float2 v = unpack2(acc[i][w][j]);
+                            if (on && 2 * j < valid) out[0] = __float2bfloat16_rn(v.x);
+                            if (on && 2 * j + 1 < valid) out[p.g.n] = __float2bfloat16_rn(v.y);
+                            out += 2LL * p.g.n;
                         }
                     }
-                    epilogue_sync();
-                    if (g == 0) {
-                        float h[kExchange];
-                        float mine = 0.0f;  // lane j: the largest of row j among the warp's 32 columns
+                } else {
+                    float h[kPart];
+                    float mine = 0.0f;  // lane j: the largest of row j among the warp's 32 columns
 #pragma unroll
-                        for (int j = 0; j < kExchange; ++j) {
-                            const float2 v = unpack2(acc[c * kExchange / 2 + j / 2]);
-                            h[j] = gated(j % 2 == 0 ? v.x : v.y, s->up[j][row]);
-                            const float m = h[j] == h[j] ? fabsf(h[j]) : 0.0f;
-                            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-                            if (lane == j) mine = __uint_as_float(top);
-                        }
-                        s->amax[lane][quarter] = mine;
-                        gate_sync();
-                        const float4 m = *reinterpret_cast<const float4*>(s->amax[lane]);
-                        const float scale = block_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
-                        const float inv = 1.0f / scale;
-                        if (quarter == 0 && c * kExchange + lane < tl.rows)
-                            p.g.y_scales[(r0 + c * kExchange + lane) * p.nb + tl.n0 / kScaleBlock] = scale;
-#pragma unroll
-                        for (int j = 0; j < kExchange; ++j) {
-                            const float q = h[j] * __shfl_sync(0xffffffffu, inv, j);
-                            if (n < p.g.n && c * kExchange + j < tl.rows)
-                                out[static_cast<long long>(c * kExchange + j) * p.g.n] =
-                                    static_cast<uint8_t>(pack_e4m3x4(q, 0.0f, 0.0f, 0.0f));
-                        }
+                    for (int j = 0; j < kPart; ++j) {
+                        const float2 a = unpack2(acc[i][0][j / 2]), u = unpack2(acc[i][1][j / 2]);
+                        h[j] = gated(j % 2 == 0 ? a.x : a.y, j % 2 == 0 ? u.x : u.y);
+                        const float m = h[j] == h[j] ? fabsf(h[j]) : 0.0f;
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+                        if (lane == j) mine = __uint_as_float(top);
                     }
-                    epilogue_sync();  // before the next rows overwrite them
+                    // the other warps have the rest of the block's 128 columns; the buffers take turns, so one barrier
+                    // a part is enough
+                    float(*amax)[4] = s->amax[g][turn];
+                    turn ^= 1;
+                    if (lane < kPart) amax[lane][quarter] = mine;
+                    group_sync(g);
+                    const float4 m = *reinterpret_cast<const float4*>(amax[lane % kPart]);
+                    const float scale = block_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)));
+                    const float inv = 1.0f / scale;
+                    if (quarter == 0 && lane < kPart && lane < valid)
+                        p.g.y_scales[(r0 + lane) * p.nb + tl.n0 / kScaleBlock] = scale;
+                    uint8_t* out = static_cast<uint8_t*>(p.g.y) + r0 * p.g.n + n;
+#pragma unroll
+                    for (int j = 0; j < kPart; ++j) {
+                        const float q = h[j] * __shfl_sync(0xffffffffu, inv, j);
+                        if (n < p.g.n && j < valid)
+                            out[static_cast<long long>(j) * p.g.n] =
+                                static_cast<uint8_t>(pack_e4m3x4(q, 0.0f, 0.0f, 0.0f));
+                    }
                 }
             }
         }

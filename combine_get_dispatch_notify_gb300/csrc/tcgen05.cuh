@@ -99,11 +99,36 @@ __device__ __forceinline__ void tmem_read32(uint32_t addr, uint64_t (&x)[16]) {
         : "memory");
 }
 
+// 16 columns from each of two places, as 8 pairs each.
+__device__ __forceinline__ void tmem_read16x2(uint32_t addr0, uint32_t addr1, uint64_t (&x)[8], uint64_t (&y)[8]) {
+    asm volatile(
+        "{\n\t.reg .b32 r<32>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{r16, r17, r18, r19, r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {r0, r1}; mov.b64 %1, {r2, r3}; mov.b64 %2, {r4, r5}; mov.b64 %3, {r6, r7};\n\t"
+        "mov.b64 %4, {r8, r9}; mov.b64 %5, {r10, r11}; mov.b64 %6, {r12, r13}; mov.b64 %7, {r14, r15};\n\t"
+        "mov.b64 %8, {r16, r17}; mov.b64 %9, {r18, r19}; mov.b64 %10, {r20, r21}; mov.b64 %11, {r22, r23};\n\t"
+        "mov.b64 %12, {r24, r25}; mov.b64 %13, {r26, r27}; mov.b64 %14, {r28, r29}; mov.b64 %15, {r30, r31};\n\t"
+        "}"
+        : "=l"(x[0]), "=l"(x[1]), "=l"(x[2]), "=l"(x[3]), "=l"(x[4]), "=l"(x[5]), "=l"(x[6]), "=l"(x[7]),
+          "=l"(y[0]), "=l"(y[1]), "=l"(y[2]), "=l"(y[3]), "=l"(y[4]), "=l"(y[5]), "=l"(y[6]), "=l"(y[7])
+        : "r"(addr0), "r"(addr1)
+        : "memory");
+}
+
 // ---- packed fp32 pairs ----
 // acc += x * s, each half rounded once.  The packed form runs at the scalar
 // form's rate (fma pipe) but takes half the issue slots.
 __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t x, uint64_t s) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(s));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t s) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(s));
+    return r;
 }
 __device__ __forceinline__ uint64_t pair2(float v) {
     uint64_t r;

@@ -32,16 +32,22 @@ namespace {
 constexpr int kTileN = 256;                    // weight rows of a pair's tile
 constexpr int kHalf = kBoxRows;                // rows of a, and of w, that one CTA loads
 constexpr int kTileBytes = kBoxBytes;          // one operand of a stage
-constexpr int kStages = 6;
+template <bool kSwiglu>
+constexpr int kStages = kSwiglu ? 6 : 4;       // four leave room for the output tile
+constexpr int kMostStages = 6;
 constexpr int kGroups = 4;                     // epilogue warpgroups, 64 columns of a tile each
-constexpr int kGroupCols = kHalf / kGroups;    // of each of the tile's two weight blocks
+constexpr int kSums = kTileN / kGroups;        // sums of an epilogue thread
+constexpr int kGroupCols = kSums / 2;          // gated: columns of each of the tile's two weight blocks
 constexpr int kThreads = 128 + 128 * kGroups;  // producer, two MMA warps, scale warp | epilogue
-constexpr int kScaleSlots = 3;                 // of four k-blocks each
+constexpr int kOutRow = 128;                   // bytes of one epilogue thread's bf16 results: 64 columns
+constexpr int kOutBytes = kWarp * kOutRow;     // of a warp's
+constexpr int kScaleSlots = 4;                 // of four k-blocks each
+constexpr int kTileRing = 2 * kScaleSlots;     // more than slots: a tile is overwritten once the one after it is summed
 constexpr int kHalfN = kTileN / 2;             // weight rows of one MMA: 64 of each CTA's 128; its TMEM columns
 
 struct Barriers {
-    uint64_t full[kStages];             // leader's: bytes of both CTAs have landed
-    uint64_t empty[kStages];            // both: the MMAs that read the stage are done
+    uint64_t full[kMostStages];             // leader's: bytes of both CTAs have landed
+    uint64_t empty[kMostStages];            // both: the MMAs that read the stage are done
     uint64_t acc_full[2][2];            // [half][buffer], both: a block's sums are in TMEM
     uint64_t acc_empty[2][2];           // leader's: the half's epilogue warps of the pair have read them
     uint64_t scale_full[kScaleSlots];   // both: the scales of four blocks are in shared memory
@@ -52,6 +58,7 @@ struct Shared {
     Barriers bar;
     float row_scale[kScaleSlots][4][kHalf];  // of each row of the CTA
     float2 w_scale[kScaleSlots][4];          // of the tile's two weight blocks
+    Tile tile[kTileRing];                    // the tiles in turn, each handed over with its first scales
     float amax[2][kGroups][kHalf];           // [tile parity][warpgroup][row]
     int first[kMaxGroups + 2];               // tiles before each group of 32 experts
     uint32_t tmem;
@@ -62,22 +69,19 @@ struct Shared {
 __device__ __forceinline__ long long tile_row(const Tile& t, const Params& p, uint32_t rank, int row) {
     return static_cast<long long>(t.e) * p.g.cap + t.m0 + static_cast<int>(rank) * kHalf + row;
 }
-__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 
 template <bool kSwiglu>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ll_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_a128, const __grid_constant__ CUtensorMap map_w,
-                       const Params p) {
+                       const __grid_constant__ CUtensorMap map_y, const Params p) {
     extern __shared__ uint8_t s_raw[];
     // stages first, on a 1024-byte boundary as the swizzle needs, at the same offset in both CTAs
     const uint32_t pad = (1024u - (smem_addr(s_raw) & 1023u)) & 1023u;
     uint8_t* s_tiles = s_raw + pad;
-    Shared* s = reinterpret_cast<Shared*>(s_tiles + kStages * 2 * kTileBytes);
+    constexpr int kStages = gemm::kStages<kSwiglu>;
+    uint8_t* s_out = s_tiles + kStages * 2 * kTileBytes;  // of each epilogue warp (bf16 results)
+    Shared* s = reinterpret_cast<Shared*>(s_out + (kSwiglu ? 0 : 4 * kGroups * kOutBytes));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -100,6 +104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbarrier_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_w);
+        if (!kSwiglu) prefetch_tensormap(&map_y);
     }
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and scales are complete from here on
@@ -112,6 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s->tmem;
     const int tiles = s->first[(p.g.E + kWarp - 1) / kWarp];
+    const int mine = pair < tiles ? (tiles - pair + pairs - 1) / pairs : 0;  // tiles of this pair
 
     if (warp < 4) {
         regs_down<64>();
@@ -160,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // sums cross to its epilogue warps, and its accumulator comes back, while the other half multiplies ----
             constexpr uint32_t idesc = e4m3_idesc(kTileM, kHalfN);
             const uint32_t half = warp - 1;
-            const uint32_t blocks = pair < tiles ? (tiles - pair + pairs - 1) / pairs * p.kb : 0;
+            const uint32_t blocks = mine * p.kb;
             uint32_t st = 0, full_phase = 0, buf = 0, empty_phase = 1;
             for (uint32_t it = 0; it < blocks; ++it) {
                 // everything but the accumulator's hand-back is settled before the wait for it: what follows that
@@ -190,61 +196,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (warp == 3) {
             // ---- scales: four rows a lane, four k-blocks at a time, handed over through shared memory ----
-            uint32_t slot = 0, phase = 1;
+            uint32_t q = 0;  // slots so far
             Walk walk;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                const Tile tl = tile_at<false>(t, walk, s->first, p, cols);
+            for (int i = 0; i < mine && ok; ++i) {
+                const Tile tl = tile_at<false>(pair + i * pairs, walk, s->first, p, cols);
                 const int left = tl.rows - static_cast<int>(rank) * kHalf;
                 const float* as = p.g.a_scales + tile_row(tl, p, rank, lane) * p.kb;
                 const long long step = static_cast<long long>(kWarp) * p.kb;
                 const float* ws = weight_scales<kSwiglu>(tl, p, lane & 1);
-                for (int b = 0; b < p.kb; b += 4) {
+                for (int b = 0; b < p.kb; b += 4, ++q) {
+                    const uint32_t slot = q % kScaleSlots;
                     float4 a[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < left);
                     const float4 w = load_scales(ws, b, p.kb, lane < 2);
+                    const uint32_t phase = q / kScaleSlots & 1 ^ 1;  // a fresh barrier passes a wait for phase 1
                     ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_empty[slot], phase, &s->abort));
                     if (!ok) break;
+                    if (b == 0 && lane == 0) s->tile[i % kTileRing] = tl;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s->row_scale[slot][i][lane + j * kWarp] = element(a[j], i);
-                        if (lane < 2) reinterpret_cast<float*>(&s->w_scale[slot][i])[lane] = element(w, i);
+                        for (int j = 0; j < 4; ++j) s->row_scale[slot][k][lane + j * kWarp] = element(a[j], k);
+                        if (lane < 2) reinterpret_cast<float*>(&s->w_scale[slot][k])[lane] = element(w, k);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s->bar.scale_full[slot]);
-                    if (++slot == kScaleSlots) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
                 }
             }
         }
         __syncwarp();
     } else {
-        // ---- epilogue: thread = one row; warpgroup g sums columns 32 g + [0, 32) of both weight blocks ----
+        // ---- epilogue: thread = one row.  Warpgroup g sums 64 columns: 32 g + [0, 32) of both weight blocks where
+        // gate and up have to meet, else 64 (g / 2) + [0, 64) of block g % 2, which leave as whole lines ----
         regs_up<104>();
+        // Columns of one TMEM read.  Sums, read and addresses have to fit 104 registers, or moves crowd the loop: gated
+        // 794 us with 16 and 917 with 32 (32 experts, 1024 rows, 7168 -> 2 x 2048), plain 425 and 406 (32768 rows of
+        // Zipf-distributed experts, 2048 -> 7168).
+        constexpr int kRead = kSwiglu ? 16 : 32;
         const int g = (warp - 4) / 4, quarter = warp % 4;
         const int row = quarter * kWarp + lane;  // of this CTA's 128
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g / 2 * kTileN + g % 2 * kGroupCols;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g / 2 * kTileN +
+                               g % 2 * (kSwiglu ? kGroupCols : kHalfN / 2);
         uint64_t* full = s->bar.acc_full[g / 2];
         const uint32_t empty = mapa(smem_addr(s->bar.acc_empty[g / 2]), 0);
         const uint32_t scale_empty = mapa(smem_addr(s->bar.scale_empty), rank);
-        uint32_t it = 0, parity = 0, slot = 0, slot_phase = 0;
-        Walk walk;
-        bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
-            const Tile tl = tile_at<false>(t, walk, s->first, p, cols);
-            const int left = tl.rows - static_cast<int>(rank) * kHalf;
-            const bool warp_on = quarter * kWarp < left;
-            uint64_t acc[kGroupCols];  // pairs of the first weight block, then of the second
+        uint32_t it = 0, q = 0;  // blocks and slots so far
+        for (int i = 0; i < mine; ++i) {
+            // the tile comes with its first scales: walking here would hold up the sums, some 800 cycles a tile
+            const uint32_t first = q % kScaleSlots;
+            bool ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_full[first], q / kScaleSlots & 1, &s->abort));
+            const bool warp_on = quarter * kWarp < s->tile[i % kTileRing].rows - static_cast<int>(rank) * kHalf;
+            uint64_t acc[kSums / 2];  // gated: the gates, then the ups
 #pragma unroll
-            for (int j = 0; j < kGroupCols; ++j) acc[j] = 0;
+            for (int j = 0; j < kSums / 2; ++j) acc[j] = 0;
 #pragma unroll 1
-            for (int b = 0; b < p.kb; ++b, ++it) {
-                const uint32_t buf = it & 1;
-                ok = (b & 3) != 0 || wait_for(&s->bar.scale_full[slot], slot_phase, &s->abort);
+            for (int b = 0; ok && b < p.kb; ++b, ++it) {
+                const uint32_t buf = it & 1, slot = q % kScaleSlots;
+                ok = b == 0 || (b & 3) != 0 || wait_for(&s->bar.scale_full[slot], q / kScaleSlots & 1, &s->abort);
                 const float2 ws = s->w_scale[slot][b & 3];
                 const float as = s->row_scale[slot][b & 3][row];
                 ok = __all_sync(0xffffffffu, ok && wait_for(&full[buf], (it / 2) & 1, &s->abort));
@@ -252,55 +262,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (warp_on) {
                     const uint32_t col = lanes + buf * kHalfN;
-                    const uint64_t s0 = pair2(as * ws.x), s1 = pair2(as * ws.y);
-                    uint64_t x[16];
-                    tmem_read32(col, x);
+                    const uint64_t s0 = pair2(as * (kSwiglu || g % 2 == 0 ? ws.x : ws.y));
+                    const uint64_t s1 = kSwiglu ? pair2(as * ws.y) : s0;
+                    uint64_t x[kRead / 2];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[j], x[j], s0);
-                    tmem_read32(col + kHalfN / 2, x);
-                    tc_fence_before();  // the block's sums have left TMEM
-                    if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
+                    for (int c = 0; c < kSums; c += kRead) {
+                        tmem_read(col + (kSwiglu ? c / kGroupCols * (kHalfN / 2) + c % kGroupCols : c), x);
+                        if (c + kRead == kSums) {  // the block's sums have left TMEM
+                            tc_fence_before();
+                            if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
+                        }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 + j], x[j], s1);
+                        for (int j = 0; j < kRead / 2; ++j) fma2(acc[c / 2 + j], x[j], c < kSums / 2 ? s0 : s1);
+                    }
                 } else {
                     tc_fence_before();
                     if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
                 }
                 if ((b & 3) == 3 || b + 1 == p.kb) {
                     if (lane == 0) mbar_arrive_cluster_relaxed(scale_empty + slot * 8);
-                    if (++slot == kScaleSlots) {
-                        slot = 0;
-                        slot_phase ^= 1;
-                    }
+                    ++q;
                 }
             }
             if (!ok) {
                 // the quarter's other warps may be waiting for this one's maxima
-                if (kSwiglu && warp_on) asm volatile("bar.arrive %0, 128;" ::"r"(1 + quarter) : "memory");
+                if (kSwiglu) asm volatile("bar.arrive %0, 128;" ::"r"(1 + quarter) : "memory");
                 break;
             }
+            const Tile tl = s->tile[i % kTileRing];
+            const int left = tl.rows - static_cast<int>(rank) * kHalf;
             const bool valid = row < left;
             const long long r = tile_row(tl, p, rank, row);
             if (!kSwiglu) {
-                if (valid) {
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r * p.g.n;
-                    const bool wide = p.g.n % 16 == 0;  // rows on 32-byte boundaries
+                const int col = tl.n0 + g % 2 * kHalf + g / 2 * (kHalfN / 2);
+                uint4 v[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // 16 columns
-                        const int col = tl.n0 + (j / 2) * kHalf + g * kGroupCols + (j % 2) * 16;
-                        uint32_t v[8];
+                for (int j = 0; j < 8; ++j) {  // 8 columns
+                    uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(acc[j * 8 + i]));
-                            v[i] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                        if (wide) {
-                            if (col < p.g.n) store32(out + col, v);
-                        } else {
-                            if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
-                            if (col + 8 < p.g.n) st_v4(out + col + 8, make_uint4(v[4], v[5], v[6], v[7]));
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(acc[4 * j + k]));
+                        w[k] = *reinterpret_cast<const uint32_t*>(&h);
                     }
+                    v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (col < p.g.n && quarter * kWarp + kWarp <= left) {
+                    // all 32 rows: through shared memory, in swizzled rows, and out by TMA while the next tile's blocks
+                    // are summed (stores straight from here would hold them up: each touches 32 lines)
+                    uint8_t* to = s_out + (warp - 4) * kOutBytes;
+                    if (lane == 0) bulk_wait_read<0>();  // the last tile's store has left the buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(to + lane * kOutRow + ((j ^ (lane & 7)) << 4)) = v[j];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&map_y, smem_addr(to), col, tl.m0 + static_cast<int>(rank) * kHalf + quarter * kWarp,
+                                     tl.e);
+                        bulk_commit();
+                    }
+                } else if (valid) {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.g.y) + r * p.g.n + col;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (col + 8 * j < p.g.n) st_v4(out + 8 * j, v[j]);
                 }
             } else if (warp_on) {
                 // h = gate / (1 + exp(-gate)) * up; columns past n have zero weights, so h = 0 there
@@ -314,10 +340,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     amax = fmaxf(amax, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
                 }
                 // the other warpgroups have the rest of the block's 128 columns
-                s->amax[parity][g][row] = amax;
+                s->amax[i & 1][g][row] = amax;
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) amax = fmaxf(amax, s->amax[parity][i][row]);
+                for (int k = 0; k < kGroups; ++k) amax = fmaxf(amax, s->amax[i & 1][k][row]);
                 const float scale = block_scale(amax);
                 if (valid) {
                     const float inv = 1.0f / scale;
@@ -327,15 +353,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int col = tl.n0 + g * kGroupCols + j * 16;
                         uint32_t v[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = pack_e4m3x4(h[j * 16 + i * 4] * inv, h[j * 16 + i * 4 + 1] * inv,
-                                               h[j * 16 + i * 4 + 2] * inv, h[j * 16 + i * 4 + 3] * inv);
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = pack_e4m3x4(h[j * 16 + k * 4] * inv, h[j * 16 + k * 4 + 1] * inv,
+                                               h[j * 16 + k * 4 + 2] * inv, h[j * 16 + k * 4 + 3] * inv);
                         if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
                     }
                     if (g == 0) p.g.y_scales[r * p.nb + tl.n0 / kScaleBlock] = scale;
                 }
             }
         }
+        if (!kSwiglu && lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -362,16 +389,18 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
     p.tiles_n = (g.n + cols - 1) / cols;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    CUtensorMap map_a, map_a128, map_w;
+    CUtensorMap map_a, map_a128, map_w, map_y = {};
     if (!make_map(&map_a, g.a, g.k, g.cap, g.E, kChunk) || !make_map(&map_a128, g.a, g.k, g.cap, g.E, kHalf) ||
-        !make_map(&map_w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf))
+        !make_map(&map_w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf) ||
+        (!kSwiglu && !make_map_bf16(&map_y, g.y, g.n, g.cap, g.E, kWarp)))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + static_cast<size_t>(kStages) * 2 * kTileBytes + sizeof(Shared);
+    const size_t smem = 1024 + static_cast<size_t>(kStages<kSwiglu>) * 2 * kTileBytes +
+                        (kSwiglu ? 0 : 4 * kGroups * kOutBytes) + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileM - 1) / kTileM) * p.tiles_n;
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
     return launch_pdl(ll_gemm_fp8_kernel<kSwiglu>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, map_a,
-                      map_a128, map_w, p);
+                      map_a128, map_w, map_y, p);
 }
 
 }  // namespace

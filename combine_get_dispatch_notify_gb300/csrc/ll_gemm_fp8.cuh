@@ -155,18 +155,26 @@ inline EncodeTiled encode_tiled() {
     return fn;
 }
 
-// Map of [outer][rows][k] bytes, boxes of `box_rows` rows x 128 bytes.
-inline bool make_map(CUtensorMap* map, const void* base, int k, int rows, int outer, int box_rows) {
+// Map of [outer][rows][cols], boxes of `box_rows` rows x 128 bytes.
+inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void* base, int cols, int rows,
+                     int outer, int box_rows) {
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows),
+    const cuuint64_t row = static_cast<cuuint64_t>(cols) * bytes;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(outer)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(k) * rows};
-    const cuuint32_t box[3] = {kBlockK, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint64_t strides[2] = {row, row * rows};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / bytes), static_cast<cuuint32_t>(box_rows), 1};
     const cuuint32_t step[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool make_map(CUtensorMap* map, const void* base, int k, int rows, int outer, int box_rows) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, k, rows, outer, box_rows);
+}
+inline bool make_map_bf16(CUtensorMap* map, const void* base, int n, int rows, int outer, int box_rows) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, n, rows, outer, box_rows);
 }
 
 cudaError_t launch_few(const GemmArgs& g, bool wait_first, cudaStream_t stream);

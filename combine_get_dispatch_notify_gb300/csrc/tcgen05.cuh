@@ -50,6 +50,14 @@ __device__ __forceinline__ void tma_load_3d_alone(uint32_t smem, const CUtensorM
         : "memory");
 }
 
+// One box from this CTA's shared memory, written by this thread's copies (bulk_commit, bulk_wait_all).  What
+// other threads wrote there has to be fenced first (fence_proxy_async_smem).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t smem, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                 "r"(smem), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -78,10 +86,10 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t columns) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 columns of this warp's 32 lanes as 16 pairs.  The load and its wait are
+// 32 or 16 columns of this warp's 32 lanes as pairs.  The load and its wait are
 // one statement: the two take about 20 cycles, which the SM's other warps fill,
 // and registers still being written between two statements cost moves.
-__device__ __forceinline__ void tmem_read32(uint32_t addr, uint64_t (&x)[16]) {
+__device__ __forceinline__ void tmem_read(uint32_t addr, uint64_t (&x)[16]) {
     asm volatile(
         "{\n\t.reg .b32 r<32>;\n\t"
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -95,6 +103,20 @@ __device__ __forceinline__ void tmem_read32(uint32_t addr, uint64_t (&x)[16]) {
         "}"
         : "=l"(x[0]), "=l"(x[1]), "=l"(x[2]), "=l"(x[3]), "=l"(x[4]), "=l"(x[5]), "=l"(x[6]), "=l"(x[7]),
           "=l"(x[8]), "=l"(x[9]), "=l"(x[10]), "=l"(x[11]), "=l"(x[12]), "=l"(x[13]), "=l"(x[14]), "=l"(x[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_read(uint32_t addr, uint64_t (&x)[8]) {
+    asm volatile(
+        "{\n\t.reg .b32 r<16>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {r0, r1}; mov.b64 %1, {r2, r3}; mov.b64 %2, {r4, r5}; mov.b64 %3, {r6, r7};\n\t"
+        "mov.b64 %4, {r8, r9}; mov.b64 %5, {r10, r11}; mov.b64 %6, {r12, r13}; mov.b64 %7, {r14, r15};\n\t"
+        "}"
+        : "=l"(x[0]), "=l"(x[1]), "=l"(x[2]), "=l"(x[3]), "=l"(x[4]), "=l"(x[5]), "=l"(x[6]), "=l"(x[7])
         : "r"(addr)
         : "memory");
 }

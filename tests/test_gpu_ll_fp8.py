@@ -279,3 +279,28 @@ def test_large_offsets():
     got = y[-1, -4:].double().cpu()
     assert ((got - want).abs() <= want.abs() * 2.0 ** -8 + mag * moe_ref.sum_error(k)).all()
     assert (y[-1, :-4] == 0).all()
+
+
+def off16(t):
+    """A copy of `t` on the device that starts on a 16-byte boundary and on no wider one."""
+    step = 16 // t.element_size()
+    buf = torch.empty(t.numel() + step, dtype=t.dtype, device="cuda")
+    assert buf.data_ptr() % 32 == 0
+    return buf[step:].view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("cap,n,k", [(300, 512, 384), (40, 272, 256)])
+def test_products_with_arrays_on_16_byte_boundaries(cap, n, k):
+    E = 3
+    a, a_s, w, w_s, count = gemm_inputs(E, cap, n, k, 8)
+    y = off16(torch.full((E, cap, n), -7.0, dtype=torch.bfloat16))
+    status = status_word()
+    ep.ep_ll_gemm_fp8(off16(a), off16(a_s), off16(w), off16(w_s), count.cuda(), y, status)
+    assert ep.ep_sync_status(status) == ep.EP_OK
+    check_gemm((a, a_s, w, w_s, count), y.cpu(), n)
+    a, a_s, w, w_s, count = gemm_inputs(E, cap, n, k, 9, halves=2)
+    y = off16(torch.full((E, cap, n), 0x55, dtype=torch.uint8))
+    ys = off16(torch.full((E, cap, ep.scale_blocks(n)), -7.0))
+    ep.ep_ll_gemm_swiglu_fp8(off16(a), off16(a_s), off16(w), off16(w_s), count.cuda(), y, ys, status)
+    assert ep.ep_sync_status(status) == ep.EP_OK
+    check_swiglu((a, a_s, w, w_s, count), y.cpu(), ys.cpu(), n)

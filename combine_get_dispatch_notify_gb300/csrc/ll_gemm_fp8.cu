@@ -4,13 +4,22 @@
 //   p[m][n] = sum_b as[m][b] ws[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
 //
 // A pair of CTAs (one cluster, two SMs) owns a tile of 256 rows x 256 weight
-// rows and walks the k-blocks of 128.  One tcgen05.mma chain of four (K = 32
-// each) leaves a block's plain sums in TMEM; two such accumulators (256
-// columns each, all of TMEM) take turns, so the next block multiplies while
-// the epilogue warps read this one, scale it by as * ws and add it to fp32
-// sums in their registers.  That scaling is what hardware block scales cannot
-// do for fp32 scales; it takes 32768 FMAs of an SM per block, half the time
-// the tensor core needs for it.
+// rows and walks the k-blocks of 128.  A block's plain sums are made in TMEM, in
+// two halves of 128 columns with an MMA warp each (a chain of four tcgen05.mma,
+// K = 32 each) and two accumulators that take turns (2 x 2 x 128 columns, all of
+// TMEM): one half multiplies while the epilogue warps read the other, scale it by
+// as * ws and add it to fp32 sums in their registers.  That scaling is what
+// hardware block scales cannot do for fp32 scales: 32768 FMAs of an SM per block.
+//
+// What bounds it: a block's products take the tensor core 512 cycles, its operands
+// (32 KB to each SM; up to 49 bytes a cycle arrive from L2) 669, and the sixteen
+// epilogue warps' instructions about 550 of the four schedulers; together they run at
+// 860 cycles a block.  The tile is as large as TMEM and the registers for its sums
+// allow: with a smaller one the operands would take longer still.  Measured: 32
+// experts with 1024 rows each, gated, 7168 -> 2 x 2048: 800 us, 2405 TFLOP/s (tensor
+// pipe busy 58 %); 32768 rows in 32 experts by Zipf popularity, 2048 -> 7168: 407 us,
+// 2365 TFLOP/s.  With one warp for both halves' MMAs, or eight epilogue warps, the
+// first takes 900 us and more.
 //
 // Each CTA loads its own 128 rows of a and half of the weight rows with
 // swizzled TMA; the weights cross HBM once per 256 rows, and only the 32-row

@@ -7,6 +7,12 @@
 // 32-bit words in registers and take the K winners off the lists' heads;
 // route_kernel keeps the keys in shared memory and covers what the lists do not
 // (more than 512 experts, softmax scores with a bias or summed for groups).
+// Where two of them could take a case, measured: 32768 tokens x 256 fp32 sigmoid
+// keys in 8 groups 27 us with lists, 95 us in shared memory; 524288 x 256 bf16 logits
+// 148 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 763 us in
+// shared memory.  The bytes alone would take 5 and 48 us: selection is bound by the
+// integer pipe, which minima, maxima, compares and selects share at half rate (70 %
+// busy in route_bf16_kernel, 57 % in route_lists_kernel, 260 instructions a token).
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -57,12 +63,17 @@ __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// Over the `W` neighbouring lanes around this one.
+template <int W = kWarp>
 __device__ __forceinline__ float warp_max(float v) {
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
     return v;
 }
+template <int W = kWarp>
 __device__ __forceinline__ float warp_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
 }
 
@@ -256,7 +267,9 @@ __device__ __forceinline__ float sum_kept(float v) {
     return warp_sum(v);
 }
 
-constexpr int kFewK = 8;  // K up to this has its rounds unrolled
+// K up to this has its rounds unrolled, each shifting no more than the rest can take: 524288 x 256 bf16, K = 8, 148 us
+// and 174 us in a loop; 32768 x 256 fp32 in groups 27 and 29 us.
+constexpr int kFewK = 8;
 
 // Where a warp's slots go; moved along with its tokens, so that no token needs a
 // 64-bit product.
@@ -701,10 +714,17 @@ struct RouteBwdArgs {
     RouteCfg rc;
 };
 
-// The gradient's slot part: lane k's expert and its incoming gradient; what it
-// adds to that expert's logit gradient.  `m` and `inv` are the softmax's maximum and reciprocal sum
-// over all experts where it is not renormalised (dense), `dot` what every expert
-// then loses p_e times.
+// ---- gradient ----
+//
+// With s the scores, w = scale s / sum_kept(s) where they are renormalised, else scale s,
+// and g the weights' gradient:
+//
+//   ds_k = (scale g_k - sum_j scale g_j v_j) / sum_kept(s), v = s / sum_kept(s)   or   scale g_k
+//   sigmoid:                dl_k = s_k (1 - s_k) ds_k, 0 for the other experts
+//   softmax, renormalised:  dl_k = v_k (scale g_k - sum_j scale g_j v_j), 0 for the others
+//   softmax over all:       dl_e = [e kept] s_e ds_e - s_e sum_k s_k ds_k: dense
+
+// A slot's expert and its incoming gradient.
 struct Slot {
     long long id;
     float g;
@@ -723,29 +743,42 @@ __device__ __forceinline__ int slot_expert(const RouteBwdArgs& p, const Slot& s)
     if (s.id != -1) flag_error(p.status, EP_DEV_INPUT);
     return -1;
 }
+// What a slot adds to its expert's logit gradient, and (dense) what every expert then loses
+// s_e times.  `W` lanes have a token's slots; `m` and `inv` are the dense softmax's
+// maximum and reciprocal sum.
 struct SlotGrad {
     float own, dot;
 };
-template <bool kBf16>
+template <bool kBf16, bool kDense, int W>
 __device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, float l, float grad, float m, float inv) {
-    const bool softmax = p.rc.score == 0, dense = softmax && !p.rc.renorm;
+    const bool softmax = kDense || p.rc.score == 0;
     const float hi = largest<kBf16>();
     SlotGrad r;
     const bool on = l > -hi;  // a masked expert's score is 0 and stays 0
     l = fminf(l, hi);
     const float g = on ? grad * p.rc.scale : 0.0f;
-    const float top = softmax && !dense ? warp_max(on ? l : -FLT_MAX) : m;
+    if (kDense) {
+        const float s = on ? expf(l - m) * inv : 0.0f;
+        r.own = s * g;
+        r.dot = warp_sum<W>(r.own);
+        return r;
+    }
     float s = 0.0f;  // the kept score
-    if (on) s = softmax ? expf(l - top) * (dense ? inv : 1.0f) : 1.0f / (1.0f + expf(-l));
+    if (softmax) {
+        const float top = warp_max<W>(on ? l : -FLT_MAX);
+        if (on) s = expf(l - top);
+    } else if (on) {
+        s = 1.0f / (1.0f + expf(-l));
+    }
     float ds = g;  // its gradient
     if (p.rc.renorm) {
-        const float total = warp_sum(s);
+        const float total = warp_sum<W>(s);
         const float v = total > 0.0f ? s / total : 0.0f;
-        const float c = g - warp_sum(v * g);
+        const float c = g - warp_sum<W>(v * g);
         ds = softmax ? c : (total > 0.0f ? c / total : 0.0f);
         if (softmax) s = v;
     }
-    r.dot = dense ? warp_sum(s * ds) : 0.0f;
+    r.dot = 0.0f;
     r.own = softmax ? s * ds : s * (1.0f - s) * ds;
     return r;
 }
@@ -758,35 +791,31 @@ __device__ __forceinline__ void store_grad(void* out, long long i, float d) {
         static_cast<float*>(out)[i] = d;
 }
 
-// One token, any E, any logits, repeated experts added up in slot order.
+// One token's dense gradient, any E, any logits, repeated experts added up in slot order.
 template <bool kBf16>
 __device__ __noinline__ void backward_token(const RouteBwdArgs& p, long long t, int lane) {
-    const bool dense = p.rc.score == 0 && !p.rc.renorm;
     const float hi = largest<kBf16>();
     const long long base = t * p.E;
-    float m = -FLT_MAX, inv = 0.0f;
-    if (dense) {
-        float sum = 0.0f;
-        for (int e = lane; e < p.E; e += kWarp) {
-            const float v = load_logit<kBf16>(p.logits, base + e);
-            if (v > -hi) m = fmaxf(m, fminf(v, hi));
-        }
-        m = warp_max(m);
-        for (int e = lane; e < p.E; e += kWarp) {
-            const float v = load_logit<kBf16>(p.logits, base + e);
-            if (v > -hi) sum += expf(fminf(v, hi) - m);
-        }
-        sum = warp_sum(sum);
-        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    float m = -FLT_MAX, sum = 0.0f;
+    for (int e = lane; e < p.E; e += kWarp) {
+        const float v = load_logit<kBf16>(p.logits, base + e);
+        if (v > -hi) m = fmaxf(m, fminf(v, hi));
     }
+    m = warp_max(m);
+    for (int e = lane; e < p.E; e += kWarp) {
+        const float v = load_logit<kBf16>(p.logits, base + e);
+        if (v > -hi) sum += expf(fminf(v, hi) - m);
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const Slot slot = load_slot(p, t, lane);
     const int idx = slot_expert(p, slot);
     const float l = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : -INFINITY;
-    const SlotGrad g = slot_gradient<kBf16>(p, l, slot.g, m, inv);
+    const SlotGrad g = slot_gradient<kBf16, true, kWarp>(p, l, slot.g, m, inv);
     for (int e0 = 0; e0 < p.E; e0 += kWarp) {
         const int e = e0 + lane;
         float d = 0.0f;
-        if (dense && e < p.E) {
+        if (e < p.E) {
             const float v = load_logit<kBf16>(p.logits, base + e);
             if (v > -hi) d = -expf(fminf(v, hi) - m) * inv * g.dot;
         }
@@ -799,6 +828,62 @@ __device__ __noinline__ void backward_token(const RouteBwdArgs& p, long long t, 
     }
 }
 
+// Zeros elements [lo, hi) of an array on a 16-byte boundary.
+template <bool kBf16>
+__device__ __forceinline__ void zero_elements(void* out, long long lo, long long hi, int lane) {
+    constexpr int kVec = kBf16 ? 8 : 4;
+    const long long a = (lo + kVec - 1) / kVec, b = hi / kVec;  // whole vectors
+    if (a >= b) {
+        for (long long i = lo + lane; i < hi; i += kWarp) store_grad<kBf16>(out, i, 0.0f);
+        return;
+    }
+    for (long long i = a + lane; i < b; i += kWarp) static_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+    if (lo + lane < a * kVec) store_grad<kBf16>(out, lo + lane, 0.0f);
+    if (b * kVec + lane < hi) store_grad<kBf16>(out, b * kVec + lane, 0.0f);
+}
+
+// Gradients that are zero but for the slots' experts (sigmoid, and softmax over
+// the kept experts): W >= K lanes to a token, so a warp has 32 / W tokens at
+// once.  Their rows, one after another in memory, are zeroed as vectors and the
+// slots' parts stored on top.  Bound by HBM's writes and the gathered logits: 131072
+// tokens x 256 bf16, K = 8, @SPARSE@.
+template <bool kBf16, int W>
+__global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_sparse_kernel(const RouteBwdArgs p) {
+    constexpr int kTokens = kWarp / W;
+    const int lane = threadIdx.x % kWarp, sub = lane / W;
+    griddep_launch_dependents();
+    griddep_wait();  // the logits, ids and gradients are complete from here on
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps * kTokens;
+    auto load = [&](long long t) {
+        return t < p.tokens ? load_slot(p, t, lane % W) : Slot{-1, 0.0f};
+    };
+    long long t0 = (static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp) * kTokens;
+    Slot ahead = load(t0 + sub);
+    for (; t0 < p.tokens; t0 += step) {
+        const Slot slot = ahead;
+        const int idx = slot_expert(p, slot);
+        const long long at = (t0 + sub) * p.E + idx;
+        const float l = idx >= 0 ? load_logit<kBf16>(p.logits, at) : -INFINITY;
+        ahead = load(t0 + step + sub);
+        zero_elements<kBf16>(p.grad_logits, t0 * p.E, min(t0 + kTokens, p.tokens) * p.E, lane);
+        float own = slot_gradient<kBf16, false, W>(p, l, slot.g, 0.0f, 0.0f).own;
+        // the token's slots with the same expert: the first one gets their sum, in slot order
+        const uint32_t key = idx >= 0 ? static_cast<uint32_t>(idx) * kTokens + sub : 0x80000000u + lane;
+        const uint32_t same = __match_any_sync(kFull, key);
+        if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+            float sum = 0.0f;
+            for (int j = 0; j < kWarp; ++j) {
+                const float v = __shfl_sync(kFull, own, j);
+                if (same >> j & 1u) sum += v;
+            }
+            own = sum;
+        }
+        __syncwarp();  // after the zeros
+        if (idx >= 0 && (same & ((1u << lane) - 1u)) == 0u) store_grad<kBf16>(p.grad_logits, at, own);
+        __syncwarp();
+    }
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(const RouteBwdArgs p) {
     griddep_launch_dependents();
@@ -808,12 +893,14 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
         backward_token<kBf16>(p, t, threadIdx.x % kWarp);
 }
 
-// Up to 512 experts.  With kVec rows are whole 16-byte vectors: lane i holds the N
+// Dense gradients of up to 512 experts.  With kVec rows are whole 16-byte vectors: lane i holds the N
 // experts from i * N on and reads and writes them as vectors; else it holds every
 // 32nd expert from i on.  It finds its slots' parts in a shared row that is zero
 // but for them.  Bound by HBM: the exponentials are
 // ex2.approx (2^-22, and 2^-24 of the exponent).  A token with unusual logits, or
-// with an expert in two slots, goes through backward_token.
+// with an expert in two slots, goes through backward_token.  131072 tokens x 256 fp32
+// take 56 us (5.0 TB/s, 75 % of the copy rate), 57 us with kVec off; route_backward_kernel takes
+// 282 us.
 template <bool kBf16, int N, bool kVec>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
     __shared__ alignas(16) float s_rows[kRouteWarps][kWarp * N];
@@ -826,7 +913,6 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
     __syncwarp();
     griddep_launch_dependents();
     griddep_wait();  // the logits, ids and gradients are complete from here on
-    const bool dense = p.rc.score == 0 && !p.rc.renorm;
     const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
     long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
     auto load = [&](long long token, float (&l)[N]) {
@@ -843,7 +929,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
     for (int j = 0; j < N; ++j) next[j] = 0.0f;
     Slot ahead = {-1, 0.0f};
     if (t < p.tokens) {
-        if (dense) load(t, next);
+        load(t, next);
         ahead = load_slot(p, t, lane);
     }
     for (; t < p.tokens; t += step) {
@@ -854,24 +940,21 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         if (idx >= 0) row[idx] = __int_as_float(lane);  // of two slots with one expert, one keeps its mark
         float d[N];
         float m = -FLT_MAX, sum = 0.0f, odd = 0.0f;
-        if (dense) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                d[j] = next[j];
-                odd = fmaf(d[j] * 4.0f, 0.0f, odd);  // NaN: infinite, NaN or lowest values
-                if (has(j)) m = fmaxf(m, d[j]);
-            }
-            if (t + step < p.tokens) load(t + step, next);
-            m = warp_max(m);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                d[j] = has(j) ? __expf(d[j] - m) : 0.0f;
-                sum += d[j];
-            }
-            sum = warp_sum(sum);
+        for (int j = 0; j < N; ++j) {
+            d[j] = next[j];
+            odd = fmaf(d[j] * 4.0f, 0.0f, odd);  // NaN: infinite, NaN or lowest values
+            if (has(j)) m = fmaxf(m, d[j]);
         }
-        const float inv = dense ? 1.0f / sum : 0.0f;
-        const SlotGrad g = slot_gradient<kBf16>(p, l, slot.g, m, inv);
+        if (t + step < p.tokens) load(t + step, next);
+        m = warp_max(m);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            d[j] = has(j) ? __expf(d[j] - m) : 0.0f;
+            sum += d[j];
+        }
+        const float inv = 1.0f / warp_sum(sum);
+        const SlotGrad g = slot_gradient<kBf16, true, kWarp>(p, l, slot.g, m, inv);
         __syncwarp();
         const bool twice = idx >= 0 && __float_as_int(row[idx]) != lane;
         if (__any_sync(kFull, odd != odd || twice)) {
@@ -884,7 +967,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         __syncwarp();
         const float c = inv * g.dot;
 #pragma unroll
-        for (int j = 0; j < N; ++j) d[j] = dense ? fmaf(-d[j], c, row[expert(j)]) : row[expert(j)];
+        for (int j = 0; j < N; ++j) d[j] = fmaf(-d[j], c, row[expert(j)]);
         __syncwarp();
         if (idx >= 0) row[idx] = 0.0f;
         __syncwarp();
@@ -954,6 +1037,13 @@ cudaError_t launch_lists(int n, const RouteArgs& p, int seg, int vec, bool any, 
 }
 
 template <bool kBf16>
+cudaError_t launch_sparse(const RouteBwdArgs& p, int sms, cudaStream_t stream) {
+    if (p.K <= 8) return launch_tokens(route_backward_sparse_kernel<kBf16, 8>, p, sms, stream);
+    if (p.K <= 16) return launch_tokens(route_backward_sparse_kernel<kBf16, 16>, p, sms, stream);
+    return launch_tokens(route_backward_sparse_kernel<kBf16, 32>, p, sms, stream);
+}
+
+template <bool kBf16>
 cudaError_t launch_backward(const RouteBwdArgs& p, int sms, cudaStream_t stream) {
     constexpr int kFewest = kBf16 ? 8 : 4;  // a 16-byte vector
     const bool vec = p.E % kFewest == 0;
@@ -1017,6 +1107,8 @@ cudaError_t launch_route_backward(const Shape& sh, const RouteCfg& rc, const voi
     if (sms <= 0) return cudaErrorInvalidDevice;
     const RouteBwdArgs p = {logits, topk_idx, grad_topk_w, grad_logits, status, static_cast<long long>(sh.R) * sh.T,
                             sh.E, sh.K, rc};
+    if (rc.score != 0 || rc.renorm)
+        return bf16 ? launch_sparse<true>(p, sms, stream) : launch_sparse<false>(p, sms, stream);
     if (sh.E <= 512) return bf16 ? launch_backward<true>(p, sms, stream) : launch_backward<false>(p, sms, stream);
     return bf16 ? launch_tokens(route_backward_kernel<true>, p, sms, stream)
                 : launch_tokens(route_backward_kernel<false>, p, sms, stream);

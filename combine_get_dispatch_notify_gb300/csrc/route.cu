@@ -77,6 +77,23 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Two sums over the warp in six exchanges: half the lanes go on with each.
+__device__ __forceinline__ void warp_sum2(float& a, float& b, int lane) {
+    const bool low = lane < kWarp / 2;
+    float v = (low ? a : b) + __shfl_xor_sync(kFull, low ? b : a, kWarp / 2);
+#pragma unroll
+    for (int o = kWarp / 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    const float w = __shfl_xor_sync(kFull, v, kWarp / 2);
+    a = low ? v : w;
+    b = low ? w : v;
+}
+
 // Largest key of keys[lo, hi) and its lowest index (kNone, -1 when none is left).
 __device__ __forceinline__ uint32_t warp_best(const uint32_t* keys, int lo, int hi, int lane, int& at) {
     uint32_t best = kNone;
@@ -846,7 +863,8 @@ __device__ __forceinline__ void zero_elements(void* out, long long lo, long long
 // the kept experts): W >= K lanes to a token, so a warp has 32 / W tokens at
 // once.  Their rows, one after another in memory, are zeroed as vectors and the
 // slots' parts stored on top.  Bound by HBM's writes and the gathered logits: 131072
-// tokens x 256 bf16, K = 8, @SPARSE@.
+// tokens x 256, K = 8, bf16 26 us, fp32 41 us (with a whole warp to each token, and its row put
+// together in shared memory, bf16 took 66 us).
 template <bool kBf16, int W>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_sparse_kernel(const RouteBwdArgs p) {
     constexpr int kTokens = kWarp / W;
@@ -857,16 +875,20 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_sparse_kern
     auto load = [&](long long t) {
         return t < p.tokens ? load_slot(p, t, lane % W) : Slot{-1, 0.0f};
     };
+    auto logit = [&](long long t, int idx) {
+        return idx >= 0 ? load_logit<kBf16>(p.logits, t * p.E + idx) : -INFINITY;
+    };
+    // a group's logits are fetched one group ahead, its slots two
     long long t0 = (static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp) * kTokens;
-    Slot ahead = load(t0 + sub);
+    Slot now = load(t0 + sub), next = load(t0 + step + sub);
+    int idx = slot_expert(p, now);
+    float l = logit(t0 + sub, idx);
     for (; t0 < p.tokens; t0 += step) {
-        const Slot slot = ahead;
-        const int idx = slot_expert(p, slot);
-        const long long at = (t0 + sub) * p.E + idx;
-        const float l = idx >= 0 ? load_logit<kBf16>(p.logits, at) : -INFINITY;
-        ahead = load(t0 + step + sub);
+        const Slot after = load(t0 + 2 * step + sub);
+        const int next_idx = slot_expert(p, next);
+        const float next_l = logit(t0 + step + sub, next_idx);
         zero_elements<kBf16>(p.grad_logits, t0 * p.E, min(t0 + kTokens, p.tokens) * p.E, lane);
-        float own = slot_gradient<kBf16, false, W>(p, l, slot.g, 0.0f, 0.0f).own;
+        float own = slot_gradient<kBf16, false, W>(p, l, now.g, 0.0f, 0.0f).own;
         // the token's slots with the same expert: the first one gets their sum, in slot order
         const uint32_t key = idx >= 0 ? static_cast<uint32_t>(idx) * kTokens + sub : 0x80000000u + lane;
         const uint32_t same = __match_any_sync(kFull, key);
@@ -879,8 +901,13 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_sparse_kern
             own = sum;
         }
         __syncwarp();  // after the zeros
-        if (idx >= 0 && (same & ((1u << lane) - 1u)) == 0u) store_grad<kBf16>(p.grad_logits, at, own);
+        if (idx >= 0 && (same & ((1u << lane) - 1u)) == 0u)
+            store_grad<kBf16>(p.grad_logits, (t0 + sub) * p.E + idx, own);
         __syncwarp();
+        now = next;
+        next = after;
+        idx = next_idx;
+        l = next_l;
     }
 }
 
@@ -896,11 +923,12 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
 // Dense gradients of up to 512 experts.  With kVec rows are whole 16-byte vectors: lane i holds the N
 // experts from i * N on and reads and writes them as vectors; else it holds every
 // 32nd expert from i on.  It finds its slots' parts in a shared row that is zero
-// but for them.  Bound by HBM: the exponentials are
-// ex2.approx (2^-22, and 2^-24 of the exponent).  A token with unusual logits, or
-// with an expert in two slots, goes through backward_token.  131072 tokens x 256 fp32
-// take 56 us (5.0 TB/s, 75 % of the copy rate), 57 us with kVec off; route_backward_kernel takes
-// 282 us.
+// but for them.  Bound by HBM: the exponentials are ex2.approx (2^-22, and 2^-24 of
+// the exponent), and rows are brought into L2 three tokens ahead, because the warps that fit
+// hold too few bytes in flight (bf16 50 us without).  A token with unusual logits, or
+// with an expert in two slots, goes through backward_token.  131072 tokens x 256:
+// fp32 50 us (5.7 TB/s, 85 % of the copy rate), bf16 46 us; kVec off costs 2 % and 21 %.
+// route_backward_kernel takes 282 us for the fp32 ones.
 template <bool kBf16, int N, bool kVec>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
     __shared__ alignas(16) float s_rows[kRouteWarps][kWarp * N];
@@ -924,6 +952,12 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
                 if (has(j)) l[j] = load_logit<kBf16>(p.logits, token * p.E + expert(j));
         }
     };
+    constexpr int kAhead = 3;
+    auto prefetch_row = [&](long long token) {
+        constexpr int kLine = kBf16 ? 64 : 32;  // logits of 128 bytes
+        if (lane * kLine < p.E)
+            prefetch_l2(static_cast<const char*>(p.logits) + (token * p.E + lane * kLine) * (kBf16 ? 2 : 4));
+    };
     float next[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) next[j] = 0.0f;
@@ -939,33 +973,39 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         if (t + step < p.tokens) ahead = load_slot(p, t + step, lane);
         if (idx >= 0) row[idx] = __int_as_float(lane);  // of two slots with one expert, one keeps its mark
         float d[N];
-        float m = -FLT_MAX, sum = 0.0f, odd = 0.0f;
+        float m = -FLT_MAX, sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             d[j] = next[j];
-            odd = fmaf(d[j] * 4.0f, 0.0f, odd);  // NaN: infinite, NaN or lowest values
             if (has(j)) m = fmaxf(m, d[j]);
         }
         if (t + step < p.tokens) load(t + step, next);
-        m = warp_max(m);
+        if (t + kAhead * step < p.tokens) prefetch_row(t + kAhead * step);
+        m = redux_max(m);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             d[j] = has(j) ? __expf(d[j] - m) : 0.0f;
             sum += d[j];
         }
-        const float inv = 1.0f / warp_sum(sum);
-        const SlotGrad g = slot_gradient<kBf16, true, kWarp>(p, l, slot.g, m, inv);
+        const float hi = largest<kBf16>();
+        const float g = l > -hi ? slot.g * p.rc.scale : 0.0f;  // a masked expert's score is 0 and stays 0
+        const float e = l > -hi ? expf(l - m) : 0.0f;
+        float dot = e * g;
+        warp_sum2(sum, dot, lane);
+        const float inv = 1.0f / sum;
+        // masked logits came out as 0; infinite or NaN ones as NaN, and with all masked m tells
+        const bool odd = !(sum > 0.0f) || m <= -hi;
         __syncwarp();
         const bool twice = idx >= 0 && __float_as_int(row[idx]) != lane;
-        if (__any_sync(kFull, odd != odd || twice)) {
+        if (__any_sync(kFull, odd || twice)) {
             backward_token<kBf16>(p, t, lane);
             if (idx >= 0) row[idx] = 0.0f;
             __syncwarp();
             continue;
         }
-        if (idx >= 0) row[idx] = g.own;
+        if (idx >= 0) row[idx] = e * g * inv;
         __syncwarp();
-        const float c = inv * g.dot;
+        const float c = inv * (inv * dot);
 #pragma unroll
         for (int j = 0; j < N; ++j) d[j] = fmaf(-d[j], c, row[expert(j)]);
         __syncwarp();

@@ -11,6 +11,14 @@
  *                           and source info) into each destination's region
  *   ep_combine              gather the rows back and sum them in fp32
  *
+ * Around the per-expert packed (low-latency) layout stand the rest of an MoE
+ * layer's operators:
+ *   ep_route, ep_route_backward   router logits to top-k ids and weights, and
+ *                                 the weights' gradient
+ *   ep_ll_dispatch_fp8            rows cast to e4m3 as they are packed
+ *   ep_ll_gemm_swiglu_fp8,        the experts' block-scaled products, with the
+ *   ep_ll_gemm_fp8                gated activation and without
+ *
  * Pages the operations come from (cited by title and section):
  *   [IN] "notify_dispatch (internode.cu)" notes on DeepEP: sm0 stages 3-6 and
  *        sm1..x stages 1-3.

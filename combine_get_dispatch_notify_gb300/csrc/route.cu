@@ -8,8 +8,8 @@
 // route_kernel keeps the keys in shared memory and covers what the lists do not
 // (more than 512 experts, softmax scores with a bias or summed for groups).
 // Where two of them could take a case, measured: 32768 tokens x 256 fp32 sigmoid
-// keys in 8 groups 27 us with lists, 95 us in shared memory; 524288 x 256 bf16 logits
-// 148 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 763 us in
+// keys in 8 groups 27 us with lists, 63 us in shared memory; 524288 x 256 bf16 logits
+// 148 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 617 us in
 // shared memory.  The bytes alone would take 5 and 48 us: selection is bound by the
 // integer pipe, which minima, maxima, compares and selects share at half rate (70 %
 // busy in route_bf16_kernel, 57 % in route_lists_kernel, 260 instructions a token).
@@ -92,126 +92,6 @@ __device__ __forceinline__ void warp_sum2(float& a, float& b, int lane) {
     const float w = __shfl_xor_sync(kFull, v, kWarp / 2);
     a = low ? v : w;
     b = low ? w : v;
-}
-
-// Largest key of keys[lo, hi) and its lowest index (kNone, -1 when none is left).
-__device__ __forceinline__ uint32_t warp_best(const uint32_t* keys, int lo, int hi, int lane, int& at) {
-    uint32_t best = kNone;
-    int idx = 0x7fffffff;
-    for (int e = lo + lane; e < hi; e += kWarp)
-        if (keys[e] > best) {
-            best = keys[e];
-            idx = e;
-        }
-    const uint32_t top = __reduce_max_sync(kFull, best);
-    at = static_cast<int>(__reduce_min_sync(kFull, best == top && top != kNone ? idx : 0x7fffffff));
-    return top;
-}
-
-template <bool kBf16>
-__global__ void __launch_bounds__(kRouteWarps* kWarp) route_kernel(const RouteArgs p) {
-    extern __shared__ uint32_t s_keys[];
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    uint32_t* keys = s_keys + static_cast<size_t>(warp) * p.E;
-    griddep_launch_dependents();
-    griddep_wait();  // the logits are complete from here on
-    const int per_group = p.E / p.rc.G;
-    const bool softmax = p.rc.score == 0;
-    for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < p.tokens;
-         t += static_cast<long long>(gridDim.x) * kRouteWarps) {
-        const long long base = t * p.E;
-        bool nan = false;
-        float m = -FLT_MAX;
-        float sum = 0.0f;
-        if (softmax) {
-            for (int e = lane; e < p.E; e += kWarp) {
-                const float l = load_logit<kBf16>(p.logits, base + e);
-                if (l > -largest<kBf16>()) m = fmaxf(m, fminf(l, largest<kBf16>()));
-            }
-            m = warp_max(m);
-            for (int e = lane; e < p.E; e += kWarp) {
-                const float l = load_logit<kBf16>(p.logits, base + e);
-                if (l > -largest<kBf16>()) sum += expf(fminf(l, largest<kBf16>()) - m);
-            }
-            sum = warp_sum(sum);
-        }
-        // softmax keeps the logits' order, so where a key is one score the logit serves
-        const bool by_logit = softmax && p.bias == nullptr && (p.rc.group_top == 1 || p.rc.topk_groups == p.rc.G);
-        auto score = [&](float l) {
-            l = fminf(l, largest<kBf16>());
-            return softmax ? expf(l - m) / sum : 1.0f / (1.0f + expf(-l));
-        };
-        for (int e = lane; e < p.E; e += kWarp) {
-            const float l = load_logit<kBf16>(p.logits, base + e);
-            uint32_t k = kNone;
-            nan |= l != l;
-            if (l > -largest<kBf16>()) {
-                const float v = by_logit ? fminf(l, largest<kBf16>())
-                                         : (p.bias != nullptr ? score(l) + __ldg(p.bias + e) : score(l));
-                nan |= v != v;
-                if (v > -INFINITY) k = key_of(v);
-            }
-            keys[e] = k;
-        }
-        if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
-        __syncwarp();
-        if (p.rc.topk_groups < p.rc.G) {
-            uint32_t mine = kNone;  // lane g holds the key of group g
-            for (int g = 0; g < p.rc.G; ++g) {
-                int at;
-                uint32_t k = warp_best(keys, g * per_group, (g + 1) * per_group, lane, at);
-                if (p.rc.group_top == 2 && k != kNone) {
-                    // the second largest: the best one but for `at`
-                    const uint32_t first = k;
-                    __syncwarp();
-                    if (lane == 0) keys[at] = kNone;
-                    __syncwarp();
-                    int at2;
-                    const uint32_t second = warp_best(keys, g * per_group, (g + 1) * per_group, lane, at2);
-                    __syncwarp();
-                    if (lane == 0) keys[at] = first;
-                    __syncwarp();
-                    if (second != kNone) k = key_of(of_key(first) + of_key(second));
-                }
-                if (lane == g) mine = k;
-            }
-            unsigned kept = 0;
-            for (int j = 0; j < p.rc.topk_groups; ++j) {
-                const uint32_t top = __reduce_max_sync(kFull, mine);
-                if (top == kNone) break;
-                const int g = __ffs(__ballot_sync(kFull, mine == top)) - 1;
-                kept |= 1u << g;
-                if (lane == g) mine = kNone;
-            }
-            for (int e = lane; e < p.E; e += kWarp)
-                if (!((kept >> (e / per_group)) & 1u)) keys[e] = kNone;
-            __syncwarp();
-        }
-        int idx = -1;  // lane k holds slot k
-        for (int k = 0; k < p.K; ++k) {
-            int at;
-            if (warp_best(keys, 0, p.E, lane, at) == kNone) break;
-            if (lane == k) idx = at;
-            __syncwarp();
-            if (lane == 0) keys[at] = kNone;
-            __syncwarp();
-        }
-        const float l = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : 0.0f;
-        float w = idx >= 0 ? score(l) : 0.0f;
-        if (p.rc.renorm) {
-            if (softmax) {
-                const float top = warp_max(idx >= 0 ? fminf(l, largest<kBf16>()) : -FLT_MAX);
-                w = idx >= 0 ? expf(fminf(l, largest<kBf16>()) - top) : 0.0f;
-            }
-            const float total = warp_sum(w);
-            w = total > 0.0f ? w / total : 0.0f;
-        }
-        if (lane < p.K) {
-            p.topk_idx[t * p.K + lane] = idx;
-            p.topk_w[t * p.K + lane] = w * p.rc.scale;
-        }
-        __syncwarp();
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -720,6 +600,157 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
     }
 }
 
+// ---- keys in shared memory: any number of experts, any score ----
+//
+// Lane i owns every 32nd expert from i on: it brings their logits in, turns them
+// into keys and knows the best of them (of those in groups kept).  A round takes the best
+// of all; the warp then finds its owner's next best together, from a column of
+// the padded rows.  Bound by the instructions spent on every key.  55512 tokens x 1536
+// fp32, softmax, 8 groups: 186 us (1.8 TB/s); 32768 x 1024 bf16: 73 us; 32768 x 256 fp32
+// softmax with bias and sums of two: 67 us.
+__device__ __forceinline__ int padded(int e) { return e + (e >> 5); }  // rows of 33 words: columns without bank conflicts
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kRouteWarps* kWarp) route_kernel(const RouteArgs p, int seg) {
+    extern __shared__ uint32_t s_keys[];
+    constexpr int kNowhere = 0x7fffffff, kRow = kWarp + 1;
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    uint32_t* keys = s_keys + static_cast<size_t>(warp) * (padded(p.E) + 1);
+    const float lim = largest<kBf16>();
+    griddep_launch_dependents();
+    griddep_wait();  // the logits are complete from here on
+    const bool softmax = p.rc.score == 0, groups = p.rc.topk_groups < p.rc.G;
+    const int per_group = p.E / p.rc.G;
+    const float to_group = 1.0f / per_group;
+    // softmax keeps the logits' order, so where a key is one score the logit serves; the scores are needed where
+    // they are keys, or weights as they are
+    const bool by_logit = softmax && p.bias == nullptr && (p.rc.group_top == 1 || !groups);
+    const bool statistics = softmax && !(by_logit && p.rc.renorm);
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
+    for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < p.tokens; t += step) {
+        const long long base = t * p.E;
+        bool nan = false;
+        float m = -FLT_MAX, sum = 0.0f;
+        uint32_t* at = keys + lane;  // the lane's column
+#pragma unroll 8
+        for (int e = lane; e < p.E; e += kWarp, at += kRow) {
+            const float l = load_logit<kBf16>(p.logits, base + e);
+            if (statistics && l > -lim) m = fmaxf(m, fminf(l, lim));
+            *at = __float_as_uint(l);
+        }
+        if (statistics) {
+            m = redux_max(m);
+            at = keys + lane;
+#pragma unroll 4
+            for (int e = lane; e < p.E; e += kWarp, at += kRow) {
+                const float l = __uint_as_float(*at);
+                if (l > -lim) sum += expf(fminf(l, lim) - m);
+            }
+            sum = warp_sum(sum);
+        }
+        auto score = [&](float l) {
+            l = fminf(l, lim);
+            return softmax ? expf(l - m) / sum : sigmoid_exact(l);
+        };
+        uint32_t best = kNone;  // of the lane's experts, and where it is
+        int best_at = kNowhere;
+        auto key = [&](float l, int e) {
+            uint32_t k = kNone;
+            nan |= l != l;
+            if (l > -lim) {
+                float v = by_logit ? fminf(l, lim) : score(l);
+                if (p.bias != nullptr) v += __ldg(p.bias + e);
+                nan |= v != v;
+                if (v > -INFINITY) k = key_of(v);
+            }
+            if (k > best) {
+                best = k;
+                best_at = e;
+            }
+            return k;
+        };
+        at = keys + lane;
+#pragma unroll 4
+        for (int e = lane; e < p.E; e += kWarp, at += kRow) *at = key(__uint_as_float(*at), e);
+        if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
+        uint32_t kept = 0xffffffffu;  // groups
+        if (groups) {
+            // `seg` lanes scan each group
+            __syncwarp();
+            uint32_t k1 = kNone, k2 = kNone;
+            const int g = lane / seg;
+            if (g < p.rc.G)
+#pragma unroll 4
+                for (int e = g * per_group + lane % seg; e < (g + 1) * per_group; e += seg) {
+                    const uint32_t v = keys[padded(e)];
+                    k2 = max(k2, min(k1, v));
+                    k1 = max(k1, v);
+                }
+            __syncwarp();
+            segment_merge2(seg, k1, k2);
+            const bool in = group_kept(group_value(k1, k2, p.rc.group_top), p.rc.G, seg, p.rc.topk_groups, lane);
+            kept = __reduce_or_sync(kFull, in ? 1u << g : 0u);
+            best = kNone;
+            best_at = kNowhere;
+            for (uint32_t left = kept; left != 0u; left &= left - 1u) {
+                const int lo = (__ffs(left) - 1) * per_group;
+#pragma unroll 4
+                for (int e = lo + ((lane - lo) & (kWarp - 1)); e < lo + per_group; e += kWarp) {
+                    const uint32_t k = keys[padded(e)];
+                    if (k > best) {
+                        best = k;
+                        best_at = e;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        int idx = -1;  // lane k holds slot k
+        for (int k = 0; k < p.K; ++k) {
+            const uint32_t top = __reduce_max_sync(kFull, best);
+            if (top == kNone) break;
+            const int at = static_cast<int>(__reduce_min_sync(kFull, best == top ? best_at : kNowhere));
+            if (lane == k) idx = at;
+            if (lane == 0) keys[padded(at)] = kNone;
+            __syncwarp();
+            uint32_t next = kNone;
+            int next_at = kNowhere;
+            for (int e = at % kWarp + kWarp * lane; e < p.E; e += kWarp * kWarp) {
+                const uint32_t v = keys[padded(e)];
+                // (e + 1/2) / per_group is far enough from a whole number for fp32
+                if (v > next && (kept >> static_cast<int>((e + 0.5f) * to_group) & 1u)) {
+                    next = v;
+                    next_at = e;
+                }
+            }
+            const uint32_t most = __reduce_max_sync(kFull, next);
+            next_at = static_cast<int>(__reduce_min_sync(kFull, next == most && most != kNone ? next_at : kNowhere));
+            if (lane == at % kWarp) {
+                best = most;
+                best_at = next_at;
+            }
+            __syncwarp();
+        }
+        const float l = idx >= 0 ? load_logit<kBf16>(p.logits, base + idx) : 0.0f;
+        float w = 0.0f;
+        if (softmax && p.rc.renorm) {
+            const float top = warp_max(idx >= 0 ? fminf(l, lim) : -FLT_MAX);
+            w = idx >= 0 ? expf(fminf(l, lim) - top) : 0.0f;
+        } else if (idx >= 0) {
+            w = score(l);
+        }
+        if (p.rc.renorm) {
+            const float total = warp_sum(w);
+            w = total > 0.0f ? w / total : 0.0f;
+        }
+        if (lane < p.K) {
+            p.topk_idx[t * p.K + lane] = idx;
+            p.topk_w[t * p.K + lane] = w * p.rc.scale;
+        }
+        __syncwarp();
+    }
+}
+
 struct RouteBwdArgs {
     const void* logits;
     const int64_t* topk_idx;
@@ -1132,12 +1163,14 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
                     : (rc.score == 0 ? launch_lists<false, 0>(n, p, seg, vec, any, sms, stream)
                                      : launch_lists<false, 1>(n, p, seg, vec, any, sms, stream));
     }
+    int seg = kWarp;  // lanes that scan a group
+    while (seg * rc.G > kWarp) seg /= 2;
     const long long want = (p.tokens + kRouteWarps - 1) / kRouteWarps;
     const long long most = sms * 16LL;
     const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-    const size_t smem = sizeof(uint32_t) * kRouteWarps * static_cast<size_t>(sh.E);
-    return bf16 ? launch_pdl(route_kernel<true>, grid, dim3(kRouteWarps * kWarp), smem, stream, 0, false, p)
-                : launch_pdl(route_kernel<false>, grid, dim3(kRouteWarps * kWarp), smem, stream, 0, false, p);
+    const size_t smem = sizeof(uint32_t) * kRouteWarps * static_cast<size_t>(sh.E + sh.E / 32 + 1);
+    return bf16 ? launch_pdl(route_kernel<true>, grid, dim3(kRouteWarps * kWarp), smem, stream, 0, false, p, seg)
+                : launch_pdl(route_kernel<false>, grid, dim3(kRouteWarps * kWarp), smem, stream, 0, false, p, seg);
 }
 
 cudaError_t launch_route_backward(const Shape& sh, const RouteCfg& rc, const void* logits, bool bf16,

@@ -124,7 +124,7 @@ struct OccKey {
     int blocks;
 };
 std::mutex g_occ_mu;
-OccKey g_occ_cache[64];
+OccKey g_occ_cache[256];
 int g_occ_count = 0;
 }  // namespace
 
@@ -142,7 +142,7 @@ int max_blocks_per_sm(const void* kernel, int threads, size_t smem) {
         cudaGetLastError();
         return 0;
     }
-    if (g_occ_count < 64) g_occ_cache[g_occ_count++] = OccKey{kernel, dev, threads, smem, blocks};
+    if (g_occ_count < 256) g_occ_cache[g_occ_count++] = OccKey{kernel, dev, threads, smem, blocks};
     return blocks;
 }
 

@@ -288,3 +288,37 @@ def test_route_close_keys_keep_their_exact_order(dtype):
     key = torch.where(mask.unsqueeze(-1), per, -9.0).view(64, 256)
     want = key.sort(dim=-1, descending=True, stable=True).indices[:, :8]
     assert rc == ep.EP_OK and torch.equal(idx.view(64, 8), want)
+
+
+@pytest.mark.parametrize("E,G,tg,gt,K", [(1536, 8, 1, 1, 3), (2080, 13, 4, 2, 8), (576, 8, 7, 2, 31), (4096, 32, 5, 1, 6)],
+                         ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_route_many_experts(E, G, tg, gt, K, dtype):
+    bias = torch.round(torch.randn(E, generator=torch.Generator().manual_seed(5)) * 8) / 32
+    l = logits_of(1, 9, E, dtype, 6, _mask_some(-float("inf")))
+    l[0, 5:] = logits_of(1, 4, E, dtype, 7)[0]
+    for score in ("sigmoid", "softmax"):
+        check_route(l, None, K, score=score, G=G, topk_groups=tg, group_top=1)
+    check_route(l, bias, K, score="sigmoid", G=G, topk_groups=tg, group_top=gt)
+
+
+@pytest.mark.parametrize("E,K,bias,score", [(8, 2, False, "softmax"), (64, 8, True, "sigmoid"), (40, 5, True, "softmax"),
+                                            (640, 4, False, "softmax"), (33, 17, False, "sigmoid")], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_long_calls_repeat_short_ones(E, K, bias, score, dtype):
+    """More tokens than the GPU holds warps for, ending in part of a warp's tokens: every token's
+    results are those of a call of 61 tokens, bit for bit, forward and backward."""
+    short, times = 61, 2201  # 134261 tokens
+    base = logits_of(1, short, E, dtype, 11)
+    b = torch.randn(E, generator=torch.Generator().manual_seed(12)) if bias else None
+    idx, w, rc = run_route(base, b, K, score=score, renorm=False)
+    many_idx, many_w, many_rc = run_route(base.repeat(1, times, 1), b, K, score=score, renorm=False)
+    assert rc == many_rc == ep.EP_OK
+    assert torch.equal(many_idx, idx.repeat(1, times, 1)) and torch.equal(many_w, w.repeat(1, times, 1))
+    g = torch.randn(1, short, K, generator=torch.Generator().manual_seed(13))
+    idx[0, 7, 0], idx[0, 11] = -1, idx[0, 11, :1]  # an empty slot, and one expert in every slot
+    for renorm in (False, True):
+        d, rc = run_backward(base, idx, g, score, renorm, 1.5)
+        many, many_rc = run_backward(base.repeat(1, times, 1), idx.repeat(1, times, 1), g.repeat(1, times, 1), score,
+                                     renorm, 1.5)
+        assert rc == many_rc == ep.EP_OK and torch.equal(many, d.repeat(1, times, 1))

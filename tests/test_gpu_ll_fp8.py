@@ -304,3 +304,15 @@ def test_products_with_arrays_on_16_byte_boundaries(cap, n, k):
     ep.ep_ll_gemm_swiglu_fp8(off16(a), off16(a_s), off16(w), off16(w_s), count.cuda(), y, ys, status)
     assert ep.ep_sync_status(status) == ep.EP_OK
     check_swiglu((a, a_s, w, w_s, count), y.cpu(), ys.cpu(), n)
+
+
+@pytest.mark.parametrize("E,cap,n,k", [(48, 300, 512, 128), (40, 270, 768, 640), (90, 140, 1024, 48), (150, 40, 512, 272)],
+                         ids=str)
+def test_products_with_many_tiles(E, cap, n, k):
+    """Several tiles for every SM, of few k-blocks each: the tiles' hand-over runs ahead as far as it can."""
+    args = gemm_inputs(E, cap, n, k, 10)
+    args[4][1::3] = cap
+    check_gemm(args, run_gemm(args, n), n)
+    args = gemm_inputs(E, cap, n, k, 11, halves=2)
+    args[4][1::3] = cap
+    check_swiglu(args, *run_swiglu(args, n), n)

@@ -18,8 +18,9 @@
 // allow: with a smaller one the operands would take longer still.  Measured: 32
 // experts with 1024 rows each, gated, 7168 -> 2 x 2048: 800 us, 2405 TFLOP/s (tensor
 // pipe busy 58 %); 32768 rows in 32 experts by Zipf popularity, 2048 -> 7168: 407 us,
-// 2365 TFLOP/s.  With one warp for both halves' MMAs, or eight epilogue warps, the
-// first takes 900 us and more.
+// 2365 TFLOP/s.  One MMA of 256 columns in place of the halves took 791 us for the
+// first and 481 for the second when the halves took 806 and 460; eight epilogue warps
+// take 900 us and more for the first.
 //
 // Each CTA loads its own 128 rows of a and half of the weight rows with
 // swizzled TMA; the weights cross HBM once per 256 rows, and only the 32-row

@@ -3,15 +3,15 @@
 // One warp works on one token.
 //
 // ep_route has three kernels.  route_lists_kernel, and route_bf16_kernel for
-// bf16 logits that are keys themselves, keep a lane's keys as one sorted list of
-// 32-bit words in registers and take the K winners off the lists' heads;
+// bf16 logits whose order the keys keep (no bias, no groups), keep a lane's keys as
+// one sorted list of 32-bit words in registers and take the K winners off the lists' heads;
 // route_kernel keeps the keys in shared memory and covers what the lists do not
 // (more than 512 experts, softmax scores with a bias or summed for groups).
 // Where two of them could take a case, measured: 32768 tokens x 256 fp32 sigmoid
 // keys in 8 groups 27 us with lists, 63 us in shared memory; 524288 x 256 bf16 logits
 // 148 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 617 us in
-// shared memory.  The bytes alone would take 5 and 48 us: selection is bound by the
-// integer pipe, which minima, maxima, compares and selects share at half rate (70 %
+// shared memory; 131072 x 256 bf16, sigmoid without a bias, 47 and 89 us.  The bytes
+// alone would take 5 and 48 us of the first two: selection is bound by the integer pipe, which minima, maxima, compares and selects share at half rate (70 %
 // busy in route_bf16_kernel, 57 % in route_lists_kernel, 260 instructions a token).
 #include <cfloat>
 #include <cstdint>
@@ -153,6 +153,31 @@ __device__ __forceinline__ uint32_t take(uint32_t (&w)[N], int rounds, int lane,
     return win;
 }
 
+// The K largest of whole keys, ties to the lowest index: lane r gets the r-th one's expert (-1 past the end).
+template <int N, typename Expert>
+__device__ __forceinline__ int exact_rounds(uint32_t (&k)[N], int K, int lane, Expert expert) {
+    int idx = -1;
+    for (int r = 0; r < K; ++r) {
+        uint32_t best = k[0];
+        int at = 0;
+#pragma unroll
+        for (int j = 1; j < N; ++j)
+            if (k[j] > best) {
+                best = k[j];
+                at = j;
+            }
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        if (top == kNone) break;
+        const int from = static_cast<int>(
+            __reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(expert(at)) : 0xffffffffu));
+        if (lane == r) idx = from;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (expert(j) == from) k[j] = kNone;
+    }
+    return idx;
+}
+
 // Sum over lanes [0, K) (the others hold 0), valid in those lanes.
 template <int kFewK>
 __device__ __forceinline__ float sum_kept(float v) {
@@ -186,6 +211,8 @@ struct SlotOut {
     }
 };
 
+__device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
+
 // ---- bf16 logits that are the keys themselves: the word holds the whole key ----
 //
 // Two logits are ordered by two instructions: a negative half flips all its
@@ -194,6 +221,12 @@ struct SlotOut {
 // kInf16 on), so masked experts need no test.  Infinite and NaN logits, and zeros
 // of either sign among the winners (equal keys with different bits), are rare:
 // such a token runs once more over words cleaned one by one.
+//
+// A sigmoid without a bias keeps the logits' order, but two logits may share one
+// fp32 sigmoid, and then the lower index comes first.  With neighbouring bf16 values at least
+// 2^-9 |l| apart, sigmoids are more than four roundings apart where (1 - s) |l| > 2^-13,
+// as it is for 2^-10 <= |l| with -80 <= l <= 11: such a winner is above every lower
+// logit.  A token with another winner takes its rounds over exact sigmoids.
 constexpr uint32_t kLowest16 = 0x0080u, kMinusInf16 = 0x007fu, kInf16 = 0xff80u, kLargest16 = 0xff7fu;
 constexpr uint32_t kMinusZero16 = 0x7fffu, kZero16 = 0x8000u;
 
@@ -204,7 +237,7 @@ __device__ __forceinline__ uint32_t half_signs(uint32_t v) {
     return r;
 }
 
-template <int N, bool kFew>
+template <int N, bool kFew, bool kSigmoid>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const RouteArgs p) {
     __shared__ uint32_t s_slots[kRouteWarps][kWarp];
     const int lane = threadIdx.x % kWarp, first = lane * N;
@@ -256,42 +289,71 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
         bool special = w[0] >= (kInf16 << 16) || w[N - 1] < (kMinusInf16 << 16);
         uint32_t win = take<N, kFew ? kFewK : 0>(w, p.K, lane, slots);
         uint32_t o = win >> 16;
-        // a zero among the winners: a kept one is always seen, and with none kept no zero matters
-        special |= o - kMinusZero16 <= 1u;
+        auto value = [](uint32_t half) { return __uint_as_float((half & 0x8000u ? half ^ 0x8000u : half ^ 0xffffu) << 16); };
+        bool kept = lane < p.K && o > kLowest16;
+        float logit = value(o);
+        int idx = kept ? static_cast<int>(0xffffu - (win & 0xffffu)) : -1;
+        if (kSigmoid)
+            special |= kept && !(logit >= -80.0f && logit <= 11.0f && fabsf(logit) >= 9.765625e-4f);
+        else  // a zero among the winners: a kept one is always seen, and with none kept no zero matters
+            special |= o - kMinusZero16 <= 1u;
         if (__any_sync(kFull, special)) {
-            words();
             bool nan = false;
+            if (kSigmoid) {
+                const float lim = largest<true>();
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                uint32_t c = w[j] >> 16;
-                nan |= c > kInf16 || c < kMinusInf16;
-                c = c > kInf16 || c <= kLowest16 ? 0u : c == kInf16 ? kLargest16 : c == kMinusZero16 ? kZero16 : c;
-                w[j] = c == 0u ? 0u : (c << 16) | (w[j] & 0xffffu);
+                for (int j = 0; j < N; ++j) {
+                    const float l = __uint_as_float(j % 2 == 0 ? raw[j / 2] << 16 : raw[j / 2] & 0xffff0000u);
+                    nan |= l != l;
+                    w[j] = l > -lim ? key_of(sigmoid_exact(fminf(l, lim))) : kNone;
+                }
+                idx = exact_rounds<N>(w, p.K, lane, [&](int j) { return first + j; });
+                kept = idx >= 0;
+                logit = kept ? fminf(load_logit<true>(p.logits, t * p.E + idx), lim) : 0.0f;
+            } else {
+                words();
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    uint32_t c = w[j] >> 16;
+                    nan |= c > kInf16 || c < kMinusInf16;
+                    c = c > kInf16 || c <= kLowest16 ? 0u : c == kInf16 ? kLargest16 : c == kMinusZero16 ? kZero16 : c;
+                    w[j] = c == 0u ? 0u : (c << 16) | (w[j] & 0xffffu);
+                }
+                sort_descending<N>(w);
+                win = take<N, 0>(w, p.K, lane, slots);
+                o = win >> 16;
+                kept = lane < p.K && o > kLowest16;
+                logit = value(o);
+                idx = kept ? static_cast<int>(0xffffu - (win & 0xffffu)) : -1;
             }
             if (__any_sync(kFull, nan) && lane == 0) flag_error(p.status, EP_DEV_INPUT);
-            sort_descending<N>(w);
-            win = take<N, 0>(w, p.K, lane, slots);
-            o = win >> 16;
         }
-        const bool kept = lane < p.K && o > kLowest16;
-        const float logit = __uint_as_float((o & 0x8000u ? o ^ 0x8000u : o ^ 0xffffu) << 16);
-        // softmax over the winners, the first of them the largest; or over all experts
-        const float m = __shfl_sync(kFull, logit, 0);
-        const float mine = kept ? expf(logit - m) : 0.0f;
-        float total;
-        if (p.rc.renorm) {
-            total = sum_kept<kFew ? kFewK : 0>(mine);
-        } else {
-            total = 0.0f;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float l = __uint_as_float(j % 2 == 0 ? raw[j / 2] << 16 : raw[j / 2] & 0xffff0000u);
-                if (l > -largest<true>()) total += expf(fminf(l, largest<true>()) - m);
+        float weight;
+        if (kSigmoid) {
+            weight = kept ? sigmoid_exact(logit) : 0.0f;
+            if (p.rc.renorm) {
+                const float total = sum_kept<kFew ? kFewK : 0>(weight);
+                weight = total > 0.0f ? weight / total : 0.0f;
             }
-            total = warp_sum(total);
+        } else {
+            // softmax over the winners, the first of them the largest; or over all experts
+            const float m = __shfl_sync(kFull, logit, 0);
+            const float mine = kept ? expf(logit - m) : 0.0f;
+            float total;
+            if (p.rc.renorm) {
+                total = sum_kept<kFew ? kFewK : 0>(mine);
+            } else {
+                total = 0.0f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float l = __uint_as_float(j % 2 == 0 ? raw[j / 2] << 16 : raw[j / 2] & 0xffff0000u);
+                    if (l > -largest<true>()) total += expf(fminf(l, largest<true>()) - m);
+                }
+                total = warp_sum(total);
+            }
+            weight = __fdividef(mine, total);
         }
-        const float weight = __fdividef(mine, total) * p.rc.scale;
-        if (lane < p.K) out.put(lane, kept ? static_cast<int>(0xffffu - (win & 0xffffu)) : -1, kept ? weight : 0.0f);
+        if (lane < p.K) out.put(lane, idx, kept ? weight * p.rc.scale : 0.0f);
     }
 }
 
@@ -341,7 +403,6 @@ __device__ __forceinline__ void load_lane(const void* logits, long long base, in
     for (int j = 0; j < N; ++j) l[j] = first + j < E ? load_logit<kBf16>(logits, base + first + j) : -INFINITY;
 }
 
-__device__ __forceinline__ float sigmoid_exact(float l) { return 1.0f / (1.0f + expf(-l)); }
 __device__ __forceinline__ float sigmoid_approx(float l, float& e) {  // e: exp(-l)
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
@@ -553,25 +614,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_lists_kernel(const R
 #pragma unroll
                 for (int j = 0; j < N; ++j) k[j] = in_group(j, in, exact_mask) ? k[j] : kNone;
             }
-            idx = -1;
-            for (int r = 0; r < p.K; ++r) {
-                uint32_t best = k[0];
-                int at = 0;
-#pragma unroll
-                for (int j = 1; j < N; ++j)
-                    if (k[j] > best) {
-                        best = k[j];
-                        at = j;
-                    }
-                const uint32_t top = __reduce_max_sync(kFull, best);
-                if (top == kNone) break;
-                const int from = static_cast<int>(
-                    __reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(expert(at)) : 0xffffffffu));
-                if (lane == r) idx = from;
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (expert(j) == from) k[j] = kNone;
-            }
+            idx = exact_rounds<N>(k, p.K, lane, expert);
             logit = idx >= 0 ? fminf(load_logit<kBf16>(p.logits, base + idx), lim) : 0.0f;
             s = kMode == 1 && idx >= 0 ? sigmoid_exact(logit) : 0.0f;
         } else {
@@ -1083,8 +1126,11 @@ cudaError_t launch_tokens(void (*kernel)(P, Args...), const P& p, int sms, cudaS
 
 template <int N>
 cudaError_t launch_bf16(const RouteArgs& p, int sms, cudaStream_t stream) {
-    return p.K <= kFewK ? launch_tokens(route_bf16_kernel<N, true>, p, sms, stream)
-                        : launch_tokens(route_bf16_kernel<N, false>, p, sms, stream);
+    if (p.rc.score == 1)
+        return p.K <= kFewK ? launch_tokens(route_bf16_kernel<N, true, true>, p, sms, stream)
+                            : launch_tokens(route_bf16_kernel<N, false, true>, p, sms, stream);
+    return p.K <= kFewK ? launch_tokens(route_bf16_kernel<N, true, false>, p, sms, stream)
+                        : launch_tokens(route_bf16_kernel<N, false, false>, p, sms, stream);
 }
 
 template <bool kBf16, int kMode, int N>
@@ -1141,7 +1187,7 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     const int n = sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;  // experts of a lane
     if (sh.E <= 512 && (rc.score == 1 || by_logit)) {
         const bool grouped = rc.topk_groups < rc.G;
-        if (bf16 && by_logit && !grouped && sh.E % n == 0) {
+        if (bf16 && bias == nullptr && !grouped && sh.E % n == 0) {
             switch (n) {
                 case 2: return launch_bf16<2>(p, sms, stream);
                 case 4: return launch_bf16<4>(p, sms, stream);

@@ -322,3 +322,18 @@ def test_long_calls_repeat_short_ones(E, K, bias, score, dtype):
         many, many_rc = run_backward(base.repeat(1, times, 1), idx.repeat(1, times, 1), g.repeat(1, times, 1), score,
                                      renorm, 1.5)
         assert rc == many_rc == ep.EP_OK and torch.equal(many, d.repeat(1, times, 1))
+
+
+@pytest.mark.parametrize("E,K", [(48, 6), (256, 8), (512, 20)], ids=str)
+def test_route_bf16_sigmoids_that_coincide(E, K):
+    """Large and tiny bf16 logits whose fp32 sigmoids are equal or a few ulp apart: the order is the
+    sigmoids', ties to the lowest index, not the logits'."""
+    g = torch.Generator().manual_seed(14)
+    scale = torch.tensor([2.0 ** -14, 2.0 ** -9, 1.0, 11.0, 30.0, 100.0])
+    l = torch.randn(1, 240, E, generator=g) * scale[torch.arange(240) % 6].view(1, 240, 1)
+    l[0, ::7] = -l[0, ::7].abs()       # only the negative side
+    l = l.to(torch.bfloat16)
+    idx, _, rc = run_route(l, None, K, score="sigmoid")
+    s = (1.0 / (1.0 + torch.exp(-l.float().cuda()))).cpu().view(240, E)
+    want = s.sort(dim=-1, descending=True, stable=True).indices[:, :K]
+    assert rc == ep.EP_OK and torch.equal(idx.view(240, K), want)

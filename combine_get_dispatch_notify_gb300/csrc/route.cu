@@ -254,7 +254,14 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
     for (int i = 0; i < N / 2; ++i) next[i] = 0xff80ff80u;  // -inf
     auto load = [&]() {
         if (!on) return;
-        if (N >= 8) {
+        if (N % 8 == 4 && N > 4) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + i);
+                next[(2 * i) % (N / 2)] = v.x;
+                next[(2 * i + 1) % (N / 2)] = v.y;
+            }
+        } else if (N >= 8) {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i) {
                 const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
@@ -1187,8 +1194,11 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     const int n = sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : 16;  // experts of a lane
     if (sh.E <= 512 && (rc.score == 1 || by_logit)) {
         const bool grouped = rc.topk_groups < rc.G;
-        if (bf16 && bias == nullptr && !grouped && sh.E % n == 0) {
-            switch (n) {
+        // twelve experts a lane where they are enough: 131072 x 384 take 53 us, 84 us with sixteen
+        const int n16 = n == 16 && sh.E <= 384 && sh.E % 12 == 0 ? 12 : n;
+        if (bf16 && bias == nullptr && !grouped && sh.E % n16 == 0) {
+            switch (n16) {
+                case 12: return launch_bf16<12>(p, sms, stream);
                 case 2: return launch_bf16<2>(p, sms, stream);
                 case 4: return launch_bf16<4>(p, sms, stream);
                 case 8: return launch_bf16<8>(p, sms, stream);

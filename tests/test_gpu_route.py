@@ -303,7 +303,8 @@ def test_route_many_experts(E, G, tg, gt, K, dtype):
 
 
 @pytest.mark.parametrize("E,K,bias,score", [(8, 2, False, "softmax"), (64, 8, True, "sigmoid"), (40, 5, True, "softmax"),
-                                            (640, 4, False, "softmax"), (33, 17, False, "sigmoid")], ids=str)
+                                            (640, 4, False, "softmax"), (33, 17, False, "sigmoid"),
+                                            (384, 8, False, "softmax")], ids=str)
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 def test_long_calls_repeat_short_ones(E, K, bias, score, dtype):
     """More tokens than the GPU holds warps for, ending in part of a warp's tokens: every token's
@@ -324,7 +325,7 @@ def test_long_calls_repeat_short_ones(E, K, bias, score, dtype):
         assert rc == many_rc == ep.EP_OK and torch.equal(many, d.repeat(1, times, 1))
 
 
-@pytest.mark.parametrize("E,K", [(48, 6), (256, 8), (512, 20)], ids=str)
+@pytest.mark.parametrize("E,K", [(48, 6), (256, 8), (512, 20), (300, 8), (384, 3)], ids=str)
 def test_route_bf16_sigmoids_that_coincide(E, K):
     """Large and tiny bf16 logits whose fp32 sigmoids are equal or a few ulp apart: the order is the
     sigmoids', ties to the lowest index, not the logits'."""

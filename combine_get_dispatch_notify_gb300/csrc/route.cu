@@ -1007,23 +1007,24 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
 // but for them.  Bound by HBM: the exponentials are ex2.approx (2^-22, and 2^-24 of
 // the exponent), and rows are brought into L2 three tokens ahead, because the warps that fit
 // hold too few bytes in flight (bf16 50 us without).  A token with unusual logits, or
-// with an expert in two slots, goes through backward_token.  131072 tokens x 256:
+// with an expert in two slots, goes through backward_token.  W lanes have a token.  131072 tokens x 256:
 // fp32 50 us (5.7 TB/s, 85 % of the copy rate), bf16 46 us; kVec off costs 2 % and 21 %.
 // route_backward_kernel takes 282 us for the fp32 ones.
-template <bool kBf16, int N, bool kVec>
+template <bool kBf16, int N, bool kVec, int W>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
     __shared__ alignas(16) float s_rows[kRouteWarps][kWarp * N];
-    const int lane = threadIdx.x % kWarp, first = lane * N;
-    float* row = s_rows[threadIdx.x / kWarp];
-    auto expert = [&](int j) { return kVec ? first + j : lane + kWarp * j; };
+    constexpr int kTokens = kWarp / W;
+    const int lane = threadIdx.x % kWarp, sub = lane / W, at = lane % W, first = at * N;
+    float* row = s_rows[threadIdx.x / kWarp] + sub * (W * N);
+    auto expert = [&](int j) { return kVec ? first + j : at + W * j; };
     auto has = [&](int j) { return expert(kVec ? 0 : j) < p.E; };  // kVec: E is a multiple of N
 #pragma unroll
     for (int j = 0; j < N; ++j) row[first + j] = 0.0f;
     __syncwarp();
     griddep_launch_dependents();
     griddep_wait();  // the logits, ids and gradients are complete from here on
-    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
-    long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp;
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps * kTokens;
+    long long t = (static_cast<long long>(blockIdx.x) * kRouteWarps + threadIdx.x / kWarp) * kTokens + sub;
     auto load = [&](long long token, float (&l)[N]) {
         if (kVec) {
             if (has(0)) load_lane<kBf16, N>(p.logits, token * p.E, first, p.E, true, l);
@@ -1036,8 +1037,8 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
     constexpr int kAhead = 3;
     auto prefetch_row = [&](long long token) {
         constexpr int kLine = kBf16 ? 64 : 32;  // logits of 128 bytes
-        if (lane * kLine < p.E)
-            prefetch_l2(static_cast<const char*>(p.logits) + (token * p.E + lane * kLine) * (kBf16 ? 2 : 4));
+        if (at * kLine < p.E)
+            prefetch_l2(static_cast<const char*>(p.logits) + (token * p.E + at * kLine) * (kBf16 ? 2 : 4));
     };
     float next[N];
 #pragma unroll
@@ -1045,13 +1046,14 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
     Slot ahead = {-1, 0.0f};
     if (t < p.tokens) {
         load(t, next);
-        ahead = load_slot(p, t, lane);
+        ahead = load_slot(p, t, at);
     }
-    for (; t < p.tokens; t += step) {
+    for (; t - sub < p.tokens; t += step) {
         const Slot slot = ahead;
         const int idx = slot_expert(p, slot);
         const float l = idx >= 0 ? load_logit<kBf16>(p.logits, t * p.E + idx) : -INFINITY;
-        if (t + step < p.tokens) ahead = load_slot(p, t + step, lane);
+        if (W < kWarp) ahead = Slot{-1, 0.0f};
+        if (t + step < p.tokens) ahead = load_slot(p, t + step, at);
         if (idx >= 0) row[idx] = __int_as_float(lane);  // of two slots with one expert, one keeps its mark
         float d[N];
         float m = -FLT_MAX, sum = 0.0f;
@@ -1062,7 +1064,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         }
         if (t + step < p.tokens) load(t + step, next);
         if (t + kAhead * step < p.tokens) prefetch_row(t + kAhead * step);
-        m = redux_max(m);
+        m = W == kWarp ? redux_max(m) : warp_max<W>(m);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             d[j] = has(j) ? __expf(d[j] - m) : 0.0f;
@@ -1072,17 +1074,32 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         const float g = l > -hi ? slot.g * p.rc.scale : 0.0f;  // a masked expert's score is 0 and stays 0
         const float e = l > -hi ? expf(l - m) : 0.0f;
         float dot = e * g;
-        warp_sum2(sum, dot, lane);
+        if (W == kWarp) {
+            warp_sum2(sum, dot, lane);
+        } else {
+            sum = warp_sum<W>(sum);
+            dot = warp_sum<W>(dot);
+        }
         const float inv = 1.0f / sum;
         // masked logits came out as 0; infinite or NaN ones as NaN, and with all masked m tells
         const bool odd = !(sum > 0.0f) || m <= -hi;
         __syncwarp();
         const bool twice = idx >= 0 && __float_as_int(row[idx]) != lane;
-        if (__any_sync(kFull, odd || twice)) {
-            backward_token<kBf16>(p, t, lane);
-            if (idx >= 0) row[idx] = 0.0f;
-            __syncwarp();
-            continue;
+        bool done = false;  // nothing left to store
+        if (W == kWarp) {
+            if (__any_sync(kFull, odd || twice)) {
+                backward_token<kBf16>(p, t, lane);
+                if (idx >= 0) row[idx] = 0.0f;
+                __syncwarp();
+                continue;
+            }
+        } else {
+            const bool on = t < p.tokens;
+            const uint32_t slow = __ballot_sync(kFull, on && (odd || twice));
+            const uint32_t mine = ((1u << (W % kWarp)) - 1u) << (sub * W);  // the token's lanes
+            done = !on || (slow & mine) != 0u;
+            for (int k = 0; slow != 0u && k < kTokens; ++k)
+                if (__shfl_sync(kFull, slow & mine, k * W) != 0u) backward_token<kBf16>(p, t - sub + k, lane);
         }
         if (idx >= 0) row[idx] = e * g * inv;
         __syncwarp();
@@ -1092,6 +1109,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         __syncwarp();
         if (idx >= 0) row[idx] = 0.0f;
         __syncwarp();
+        if (done) continue;
         if (!kVec) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -1173,15 +1191,21 @@ cudaError_t launch_backward(const RouteBwdArgs& p, int sms, cudaStream_t stream)
     constexpr int kFewest = kBf16 ? 8 : 4;  // a 16-byte vector
     const bool vec = p.E % kFewest == 0;
     if (p.E <= kFewest * kWarp) {
-        if (vec) return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, true>, p, sms, stream);
-        if (p.E <= 2 * kWarp) return launch_tokens(route_backward_lanes_kernel<kBf16, 2, false>, p, sms, stream);
-        return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, false>, p, sms, stream);
+        // short rows: as few lanes to a token as hold them and its slots, and the warp has several tokens (131072
+        // tokens x 64 bf16, K = 8: 15 us, 43 us with a warp to each; x 72, K = 12: 29 and 44 us)
+        if (vec && p.E <= kFewest * 8 && p.K <= 8)
+            return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, true, 8>, p, sms, stream);
+        if (vec && p.E <= kFewest * 16 && p.K <= 16)
+            return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, true, 16>, p, sms, stream);
+        if (vec) return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, true, 32>, p, sms, stream);
+        if (p.E <= 2 * kWarp) return launch_tokens(route_backward_lanes_kernel<kBf16, 2, false, 32>, p, sms, stream);
+        return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, false, 32>, p, sms, stream);
     }
     if (p.E <= 8 * kWarp)
-        return p.E % 8 == 0 ? launch_tokens(route_backward_lanes_kernel<kBf16, 8, true>, p, sms, stream)
-                            : launch_tokens(route_backward_lanes_kernel<kBf16, 8, false>, p, sms, stream);
-    return p.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<kBf16, 16, true>, p, sms, stream)
-                         : launch_tokens(route_backward_lanes_kernel<kBf16, 16, false>, p, sms, stream);
+        return p.E % 8 == 0 ? launch_tokens(route_backward_lanes_kernel<kBf16, 8, true, 32>, p, sms, stream)
+                            : launch_tokens(route_backward_lanes_kernel<kBf16, 8, false, 32>, p, sms, stream);
+    return p.E % 16 == 0 ? launch_tokens(route_backward_lanes_kernel<kBf16, 16, true, 32>, p, sms, stream)
+                         : launch_tokens(route_backward_lanes_kernel<kBf16, 16, false, 32>, p, sms, stream);
 }
 
 }  // namespace

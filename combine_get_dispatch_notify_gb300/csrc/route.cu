@@ -11,8 +11,9 @@
 // keys in 8 groups 27 us with lists, 63 us in shared memory; 524288 x 256 bf16 logits
 // 148 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 617 us in
 // shared memory; 131072 x 256 bf16, sigmoid without a bias, 47 and 89 us.  The bytes
-// alone would take 5 and 48 us of the first two: selection is bound by the integer pipe, which minima, maxima, compares and selects share at half rate (70 %
-// busy in route_bf16_kernel, 57 % in route_lists_kernel, 260 instructions a token).
+// alone would take 5 and 48 us of the first two: selection is bound by the integer
+// pipe, which minima, maxima, compares and selects share at half rate (70 % busy in
+// route_bf16_kernel, 57 % in route_lists_kernel, 260 instructions a token).
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>

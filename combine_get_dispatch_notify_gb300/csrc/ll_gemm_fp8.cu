@@ -118,7 +118,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and scales are complete from here on
-    griddep_launch_dependents();  // after the wait: the few-rows kernel starts on these inputs beside this one
+    griddep_launch_dependents();
     if (warp == 1) count_tiles<false>(s->first, p, lane);
     tc_fence_before();
     __syncthreads();
@@ -417,14 +417,13 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
 }  // namespace gemm
 
 cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream) {
-    // With up to 128 rows an expert there is nothing for the pairs.  Otherwise the few-rows kernel follows them and
-    // takes over SMs as they run dry: it starts on the inputs the pairs started on and waits for the pairs at its end.
-    const bool pairs = g.cap > gemm::kFewRows;
-    if (pairs) {
+    // With up to 128 rows an expert there is nothing for the pairs.  Otherwise the few-rows kernel follows them: its
+    // CTAs take over SMs as they run dry and wait there for the pairs' end.
+    if (g.cap > gemm::kFewRows) {
         const cudaError_t e = g.y_scales != nullptr ? gemm::launch<true>(g, stream) : gemm::launch<false>(g, stream);
         if (e != cudaSuccess) return e;
     }
-    return gemm::launch_few(g, !pairs, stream);
+    return gemm::launch_few(g, stream);
 }
 
 }  // namespace ep

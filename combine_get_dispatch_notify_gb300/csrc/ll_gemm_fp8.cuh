@@ -181,7 +181,7 @@ inline bool make_map_bf16(CUtensorMap* map, const void* base, int n, int rows, i
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, n, rows, outer, box_rows);
 }
 
-cudaError_t launch_few(const GemmArgs& g, bool wait_first, cudaStream_t stream);
+cudaError_t launch_few(const GemmArgs& g, cudaStream_t stream);
 
 }  // namespace gemm
 }  // namespace ep

@@ -1,0 +1,87 @@
+"""Order between the experts' products and what stands around them: inputs written by the kernel
+just before, results read by the one just after, and the hand-overs between a kernel's own warps.
+
+Every comparison is bit for bit: the products add in a fixed order, so a call on inputs that
+lie ready gives the bits that a call in any company has to give.  Those calls themselves are
+held to float64 with the bounds of test_gpu_ll_fp8."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from combine_get_dispatch_notify_gb300 import ep
+from test_gpu_ll_fp8 import check_gemm, gemm_inputs, status_word
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ep.lib()
+
+
+# rows that both kernels share: whole tiles of 256, last ones of 129 to 255, rests of up to 128
+COUNTS = [[300, 256, 384, 1, 0, 513], [1, 640, 128, 129, 385, 0], [520, 0, 257, 640, 255, 31]]
+
+
+@pytest.mark.parametrize("n,k", [(264, 128), (520, 1040)], ids=str)
+def test_product_reads_what_the_kernel_before_it_wrote(n, k):
+    """Counts, rows and scales arrive by copies right before the call, other ones each time and
+    without a pause between the calls; the output is taken away by a copy right behind it."""
+    E, cap = 6, 640
+    sets = [gemm_inputs(E, cap, n, k, 20 + i, counts=c) for i, c in enumerate(COUNTS)]
+    status = status_word()
+    dev = [[t.cuda() for t in s] for s in sets]
+    y = torch.empty(E, cap, n, dtype=torch.bfloat16, device="cuda")
+    want = []
+    for d, s in zip(dev, sets):
+        y.fill_(-7.0)
+        torch.cuda.synchronize()
+        ep.ep_ll_gemm_fp8(*d, y, status)
+        torch.cuda.synchronize()
+        want.append(y.clone())
+        check_gemm(s, y.cpu(), n)
+    a, a_s, w, w_s, count = (torch.empty_like(t) for t in dev[0])
+    got = []
+    for i in range(60):
+        for to, t in zip((a, a_s, w, w_s, count), dev[i % 3]):
+            to.copy_(t)
+        y.fill_(-7.0)
+        ep.ep_ll_gemm_fp8(a, a_s, w, w_s, count, y, status)
+        got.append(y.clone())
+    assert ep.ep_sync_status(status) == ep.EP_OK
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 3]), i
+
+
+def test_product_behind_the_casting_dispatch():
+    """The dispatch lets the product start early; its rows and scales still are the ones multiplied."""
+    R, T, K, E, H, n, cap = 2, 400, 2, 4, 1024, 272, 800
+    sh = ep.EpShape.make(R, T, K, E, H, 1)
+    g = torch.Generator().manual_seed(30)
+    status = status_word()
+    _, _, w, w_s, _ = (t.cuda() for t in gemm_inputs(E, 1, n, H, 31))
+    slot, rng, count = (torch.empty(s, dtype=torch.int32, device="cuda") for s in ((R, T, K), (E, R, 2), (E,)))
+    rows = torch.zeros(E, cap, H, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(E, cap, H // 128, device="cuda")
+    y = torch.empty(E, cap, n, dtype=torch.bfloat16, device="cuda")
+    xs = [(torch.randn(R, T, H, generator=g) * s).to(torch.bfloat16).cuda() for s in (1.0, 30.0)]
+    ids = [torch.rand(R, T, E, generator=g).argsort(-1)[..., :K].contiguous().cuda() for _ in xs]
+
+    def step(i, pause):
+        y.fill_(-7.0)
+        for call in (lambda: ep.ep_ll_layout(sh, ids[i], None, cap, slot, rng, count, status),
+                     lambda: ep.ep_ll_dispatch_fp8(sh, xs[i], ids[i], slot, cap, rows, scales, None, status),
+                     lambda: ep.ep_ll_gemm_fp8(rows, scales, w, w_s, count, y, status)):
+            if pause:
+                torch.cuda.synchronize()
+            call()
+        return y.clone()
+
+    want = [step(i, True) for i in (0, 1)]
+    got = [step(i % 2, False) for i in range(60)]
+    assert ep.ep_sync_status(status) == ep.EP_OK
+    for i, v in enumerate(got):
+        assert torch.equal(v, want[i % 2]), i

@@ -80,6 +80,11 @@ __device__ __forceinline__ long long tile_row(const Tile& t, const Params& p, ui
     return static_cast<long long>(t.e) * p.g.cap + t.m0 + static_cast<int>(rank) * kHalf + row;
 }
 
+// Barrier of the four epilogue warps, one of each warpgroup, that have the same 32 rows.
+__device__ __forceinline__ void quarter_sync(int quarter) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+}
+
 template <bool kSwiglu>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ll_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -338,7 +343,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 8; ++j)
                         if (col + 8 * j < p.g.n) st_v4(out + 8 * j, v[j]);
                 }
-            } else if (warp_on) {
+            } else if (!warp_on) {
+                quarter_sync(quarter);
+            } else {
                 // h = gate / (1 + exp(-gate)) * up; columns past n have zero weights, so h = 0 there
                 float h[kGroupCols];
                 float amax = 0.0f;
@@ -349,9 +356,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     h[2 * j + 1] = gated(a.y, u.y);
                     amax = fmaxf(amax, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
                 }
-                // the other warpgroups have the rest of the block's 128 columns
+                // The other warpgroups have the rest of the block's 128 columns.  Every warp of the quarter comes to the
+                // barrier on every tile, with rows or without: passing it for one tile says that the maxima of the tile
+                // before have been read, so two places take turns.
                 s->amax[i & 1][g][row] = amax;
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+                quarter_sync(quarter);
 #pragma unroll
                 for (int k = 0; k < kGroups; ++k) amax = fmaxf(amax, s->amax[i & 1][k][row]);
                 const float scale = block_scale(amax);

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from combine_get_dispatch_notify_gb300 import ep
-from test_gpu_ll_fp8 import check_gemm, gemm_inputs, status_word
+from test_gpu_ll_fp8 import check_gemm, check_swiglu, gemm_inputs, run_swiglu, status_word
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,45 @@ def test_product_behind_the_casting_dispatch():
     assert ep.ep_sync_status(status) == ep.EP_OK
     for i, v in enumerate(got):
         assert torch.equal(v, want[i % 2]), i
+
+
+@pytest.mark.parametrize("k", [128, 512, 640], ids=str)
+def test_gated_tiles_with_and_without_rows_in_a_quarter(k):
+    """Each pair of SMs walks tiles of 256, 160, 129 and 256 rows by turns: most of its epilogue warps
+    have rows on one tile, none on the next and rows again on the one after.  With few k-blocks a
+    tile its warps may be far apart; every row's scale still comes from that row's own block."""
+    E, cap, n = 8, 256, 76 * 128  # as many column tiles as pairs: a pair keeps its column
+    args = gemm_inputs(E, cap, n, k, 32, halves=2, counts=[256, 160, 256, 129, 256, 160, 129, 256])
+    # experts of very different size: a neighbouring tile's maximum would be far off
+    args[3].mul_(10.0 ** (torch.arange(E) % 5 - 2).view(E, 1, 1, 1))
+    y, ys = run_swiglu(args, n)
+    check_swiglu(args, y, ys, n)
+    for _ in range(10):
+        again = run_swiglu(args, n)
+        assert torch.equal(again[0], y) and torch.equal(again[1], ys)
+
+
+@pytest.mark.parametrize("n,k", [(272, 128), (528, 1040)], ids=str)
+def test_gated_product_reads_what_the_kernel_before_it_wrote(n, k):
+    E, cap = 6, 640
+    sets = [gemm_inputs(E, cap, n, k, 40 + i, halves=2, counts=c) for i, c in enumerate(COUNTS)]
+    status = status_word()
+    dev = [[t.cuda() for t in s] for s in sets]
+    want = []
+    for s in sets:
+        y, ys = run_swiglu(s, n)
+        check_swiglu(s, y, ys, n)
+        want.append((y.cuda(), ys.cuda()))
+    y, ys = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+    into = [torch.empty_like(t) for t in dev[0]]
+    got = []
+    for i in range(60):
+        for to, t in zip(into, dev[i % 3]):
+            to.copy_(t)
+        y.fill_(0x55)
+        ys.fill_(-7.0)
+        ep.ep_ll_gemm_swiglu_fp8(*into, y, ys, status)
+        got.append((y.clone(), ys.clone()))
+    assert ep.ep_sync_status(status) == ep.EP_OK
+    for i, (v, s) in enumerate(got):
+        assert torch.equal(v, want[i % 3][0]) and torch.equal(s, want[i % 3][1]), i

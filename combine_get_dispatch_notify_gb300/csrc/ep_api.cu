@@ -205,10 +205,15 @@ bool gemm_shape_ok(const ep_gemm_shape_t* s, int n_multiple) {
            static_cast<long long>(s->n) * s->k < (1LL << 40);
 }
 
+// Where the products' testing hook withholds them, and its limit of every wait.
+struct Stall {
+    int cta, tile, wait_limit_us;
+};
+
 // Checks shared by the two products; `halves` is 2 when w holds a gate and an up matrix.
 ep_status_t ll_gemm(const ep_gemm_shape_t* s, int halves, const uint8_t* a, const float* a_scales, const uint8_t* w,
                     const float* w_scales, const int32_t* count, void* y, float* y_scales, int32_t* status,
-                    cudaStream_t stream) {
+                    cudaStream_t stream, const Stall* stall = nullptr) {
     if (!gemm_shape_ok(s, halves == 2 ? 16 : 8)) return EP_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(s->num_experts) * s->capacity;
     if (!array_ok(a, rows, 16) || !array_ok(a_scales, rows, 16) || !aligned16(w) || !aligned16(w_scales) ||
@@ -218,6 +223,12 @@ ep_status_t ll_gemm(const ep_gemm_shape_t* s, int halves, const uint8_t* a, cons
     if (rows == 0) return EP_OK;
     GemmArgs g = {s->num_experts, s->capacity, s->n, s->k, a, a_scales, w, w_scales, count, y,
                   halves == 2 ? y_scales : nullptr, status};
+    if (stall != nullptr) {
+        g.stall = true;
+        g.wait_limit_us = stall->wait_limit_us;
+        g.stall_cta = stall->cta;
+        g.stall_tile = stall->tile;
+    }
     return from_cuda(launch_ll_gemm_fp8(g, stream));
 }
 
@@ -836,6 +847,17 @@ ep_status_t ep_ll_gemm_swiglu_fp8(const ep_gemm_shape_t* shape, const uint8_t* a
                                   const uint8_t* w, const float* w_scales, const int32_t* count, uint8_t* y,
                                   float* y_scales, int32_t* status, cudaStream_t stream) {
     return ep::ll_gemm(shape, 2, a, a_scales, w, w_scales, count, y, y_scales, status, stream);
+}
+
+ep_status_t ep_debug_ll_gemm_fp8_stall(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales,
+                                       const uint8_t* w, const float* w_scales, const int32_t* count, void* y,
+                                       float* y_scales, int32_t* status, int32_t stall_cta, int32_t stall_tile,
+                                       int32_t wait_limit_us, cudaStream_t stream) {
+    if (stall_cta < -1 || stall_tile < 0 || stall_tile > (1 << 20) || wait_limit_us < 1 || wait_limit_us > 2000000)
+        return EP_ERR_INVALID_ARG;
+    const ep::Stall stall = {stall_cta, stall_tile, wait_limit_us};
+    return ep::ll_gemm(shape, y_scales != nullptr ? 2 : 1, a, a_scales, w, w_scales, count, y, y_scales, status, stream,
+                       &stall);
 }
 
 ep_status_t ep_sync_status(const int32_t* status, cudaStream_t stream) {

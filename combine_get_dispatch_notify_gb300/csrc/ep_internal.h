@@ -177,6 +177,9 @@ struct GemmArgs {
     void* y;
     float* y_scales;
     int32_t* status;
+    // testing hook: a limit for every device wait, and a CTA (or pair) fed no products from that tile of its own on
+    bool stall = false;
+    int wait_limit_us = 0, stall_cta = -1, stall_tile = 0;
 };
 cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream);
 

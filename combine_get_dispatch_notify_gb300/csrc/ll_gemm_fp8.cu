@@ -72,7 +72,7 @@ struct Shared {
     float amax[2][kGroups][kHalf];           // [tile parity][warpgroup][row]
     int first[kMaxGroups + 2];               // tiles before each group of 32 experts
     uint32_t tmem;
-    int abort;
+    Waits waits;
 };
 
 // Row `row` of this CTA's half of the tile, in the packed rows of all experts.
@@ -85,7 +85,7 @@ __device__ __forceinline__ void quarter_sync(int quarter) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
 }
 
-template <bool kSwiglu>
+template <bool kSwiglu, bool kStall>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ll_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_a128, const __grid_constant__ CUtensorMap map_w,
@@ -115,7 +115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&s->bar.scale_full[i], 1);
             mbar_init(&s->bar.scale_empty[i], 4 * kGroups);
         }
-        s->abort = 0;
+        s->waits = Waits{0, p.g.wait_limit_us};
         fence_mbarrier_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_w);
@@ -152,7 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int wz = kSwiglu ? 2 * tl.e + static_cast<int>(rank) : tl.e;
                 const int ay = tl.m0 + static_cast<int>(rank) * kHalf;
                 for (int b = 0; b < p.kb; ++b) {
-                    if (!(ok = wait_for(&s->bar.empty[st], phase, &s->abort))) break;
+                    if (!(ok = wait_for<kStall>(&s->bar.empty[st], phase, &s->waits))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&s->bar.full[st], bytes);
                     const uint32_t bar = full + st * sizeof(uint64_t);
                     const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
@@ -170,7 +170,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // every stage's last read is over before the CTA may leave
             for (int i = 0; i < kStages && ok; ++i) {
-                ok = wait_for(&s->bar.empty[st], phase, &s->abort);
+                ok = wait_for<kStall>(&s->bar.empty[st], phase, &s->waits);
                 if (++st == kStages) {
                     st = 0;
                     phase ^= 1;
@@ -181,16 +181,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // sums cross to its epilogue warps, and its accumulator comes back, while the other half multiplies ----
             constexpr uint32_t idesc = e4m3_idesc(kTileM, kHalfN);
             const uint32_t half = warp - 1;
-            const uint32_t blocks = mine * p.kb;
+            const int fed = kStall && half == 0 && pair == p.g.stall_cta ? min(mine, p.g.stall_tile) : mine;
+            const uint32_t blocks = fed * p.kb;
             uint32_t st = 0, full_phase = 0, buf = 0, empty_phase = 1;
             for (uint32_t it = 0; it < blocks; ++it) {
                 // everything but the accumulator's hand-back is settled before the wait for it: what follows that
                 // wait is on the path of every block
-                bool ok = wait_for(&s->bar.full[st], full_phase, &s->abort);
+                bool ok = wait_for<kStall>(&s->bar.full[st], full_phase, &s->waits);
                 const uint32_t ta = smem_addr(s_tiles) + st * 2 * kTileBytes;
                 uint64_t da = sw128_desc(ta), dw = sw128_desc(ta + kTileBytes + half * (kTileBytes / 2));
                 asm volatile("" : "+l"(da), "+l"(dw));
-                ok = ok && wait_for(&s->bar.acc_empty[half][buf], empty_phase, &s->abort);
+                ok = ok && wait_for<kStall>(&s->bar.acc_empty[half][buf], empty_phase, &s->waits);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -227,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < left);
                     const float4 w = load_scales(ws, b, p.kb, lane < 2);
                     const uint32_t phase = q / kScaleSlots & 1 ^ 1;  // a fresh barrier passes a wait for phase 1
-                    ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_empty[slot], phase, &s->abort));
+                    ok = __all_sync(0xffffffffu, wait_for<kStall>(&s->bar.scale_empty[slot], phase, &s->waits));
                     if (!ok) break;
                     if (b == 0 && lane == 0) s->tile[i % kTileRing] = tl;
 #pragma unroll
@@ -261,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < mine; ++i) {
             // the tile comes with its first scales: walking here would hold up the sums, some 800 cycles a tile
             const uint32_t first = q % kScaleSlots;
-            bool ok = __all_sync(0xffffffffu, wait_for(&s->bar.scale_full[first], q / kScaleSlots & 1, &s->abort));
+            bool ok = __all_sync(0xffffffffu, wait_for<kStall>(&s->bar.scale_full[first], q / kScaleSlots & 1, &s->waits));
             const bool warp_on = quarter * kWarp < s->tile[i % kTileRing].rows - static_cast<int>(rank) * kHalf;
             uint64_t acc[kSums / 2];  // gated: the gates, then the ups
 #pragma unroll
@@ -269,10 +270,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int b = 0; ok && b < p.kb; ++b, ++it) {
                 const uint32_t buf = it & 1, slot = q % kScaleSlots;
-                ok = b == 0 || (b & 3) != 0 || wait_for(&s->bar.scale_full[slot], q / kScaleSlots & 1, &s->abort);
+                ok = b == 0 || (b & 3) != 0 || wait_for<kStall>(&s->bar.scale_full[slot], q / kScaleSlots & 1, &s->waits);
                 const float2 ws = s->w_scale[slot][b & 3];
                 const float as = s->row_scale[slot][b & 3][row];
-                ok = __all_sync(0xffffffffu, ok && wait_for(&full[buf], (it / 2) & 1, &s->abort));
+                ok = __all_sync(0xffffffffu, ok && wait_for<kStall>(&full[buf], (it / 2) & 1, &s->waits));
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_on) {
@@ -300,8 +301,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) {
-                // the quarter's other warps may be waiting for this one's maxima
-                if (kSwiglu) asm volatile("bar.arrive %0, 128;" ::"r"(1 + quarter) : "memory");
+                // the quarter's other warps may still come to the barriers of this tile and the ones after it: each of
+                // their own waits is bounded too, a barrier that this warp stays away from would not be
+                if (kSwiglu)
+                    for (; i < mine; ++i) quarter_sync(quarter);
                 break;
             }
             const Tile tl = s->tile[i % kTileRing];
@@ -385,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (s->abort != 0) {
+    if (s->waits.ran_out != 0) {
         // a wait ran out: let the copies and products still in flight land before shared memory and TMEM go
         const long long start = globaltimer_ns();
         while (globaltimer_ns() - start < 10000000LL) {
@@ -398,8 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-template <bool kSwiglu>
-cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
+template <bool kSwiglu, bool kStall>
+cudaError_t launch_form(const GemmArgs& g, cudaStream_t stream) {
     Params p = {};
     p.g = g;
     p.kb = scale_blocks(g.k);
@@ -418,8 +421,14 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileM - 1) / kTileM) * p.tiles_n;
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
-    return launch_pdl(ll_gemm_fp8_kernel<kSwiglu>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, map_a,
+    return launch_pdl(ll_gemm_fp8_kernel<kSwiglu, kStall>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, map_a,
                       map_a128, map_w, map_y, p);
+}
+
+cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
+    const bool gated = g.y_scales != nullptr;
+    if (g.stall) return gated ? launch_form<true, true>(g, stream) : launch_form<false, true>(g, stream);
+    return gated ? launch_form<true, false>(g, stream) : launch_form<false, false>(g, stream);
 }
 
 }  // namespace
@@ -429,7 +438,7 @@ cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream) {
     // With up to 128 rows an expert there is nothing for the pairs.  Otherwise the few-rows kernel follows them: its
     // CTAs take over SMs as they run dry and wait there for the pairs' end.
     if (g.cap > gemm::kFewRows) {
-        const cudaError_t e = g.y_scales != nullptr ? gemm::launch<true>(g, stream) : gemm::launch<false>(g, stream);
+        const cudaError_t e = gemm::launch(g, stream);
         if (e != cudaSuccess) return e;
     }
     return gemm::launch_few(g, stream);

@@ -40,20 +40,29 @@ struct Params {
     int kb, nb, tiles_n;
 };
 
-// One wait of a role: false when the limit passes; `abort` then tells the others.
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
-    const long long start = globaltimer_ns();
+// The CTA's bounded waits, in shared memory.
+struct Waits {
+    int ran_out;   // 1 once a wait has: the CTA's end then reports it
+    int limit_us;  // with kStall
+};
+// One wait of a role: false when the limit passes.  The role then leaves, and the roles that wait on it do so when
+// their own waits run out.  kStall: for the testing hook, whose limit is the caller's.  It is a form of the kernels of
+// its own because the limit's register in every wait costs the pairs 4 to 20 % in moves and spills.
+template <bool kStall>
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Waits* w) {
+    const long long start = globaltimer_ns(), limit = kStall ? w->limit_us * 1000LL : kWaitLimitNs;
     do {
-        for (int i = 0; i < 1024; ++i)
+        for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-    } while (globaltimer_ns() - start < kWaitLimitNs);
-    *reinterpret_cast<volatile int*>(abort) = 1;
+    } while (globaltimer_ns() - start < limit);
+    *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
     return false;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* abort) {
+template <bool kStall>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-    return wait_slow(bar, parity, abort);
+    return wait_slow<kStall>(bar, parity, w);
 }
 
 // The tiles of a kernel: experts in order, then row tiles, then weight tiles.

@@ -53,11 +53,12 @@ struct Shared {
     alignas(16) float amax[2][2][kPart][4];                 // [warpgroup][in turn][row of a][warp]
     int first[kMaxGroups + 2];
     uint32_t tmem;
-    int abort;
+    Waits waits;
 };
 
 // Barrier of an epilogue warpgroup.
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+
 // Whether `ok` holds in all its threads.
 __device__ __forceinline__ bool group_all(int g, bool ok) {
     uint32_t all;
@@ -71,7 +72,7 @@ __device__ __forceinline__ bool group_all(int g, bool ok) {
     return all != 0;
 }
 
-template <bool kSwiglu>
+template <bool kSwiglu, bool kStall>
 __global__ void __launch_bounds__(kThreads, 1)
     ll_gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                            const Params p) {
@@ -94,15 +95,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s->scale_full[i], 1);
             mbar_init(&s->scale_empty[i], 8);
         }
-        s->abort = 0;
+        s->waits = Waits{0, p.g.wait_limit_us};
         fence_mbarrier_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_w);
     }
     if (warp == 4) tmem_alloc(&s->tmem, kTmemColumns);
-    // Also behind the pairs: only a grid that has waited is promised the memory of the grids before it.  It costs
-    // nothing that shows: 32768 rows of Zipf-distributed experts, 2048 -> 7168, take 450 us, and 452 us with the inputs
-    // read while the pairs run.
+    // Also behind the pairs: only a grid that has waited is promised the memory of the grids before it.  With the
+    // inputs read while the pairs run, 32 experts with 1024 rows each, gated, 7168 -> 2 x 2048, took 884 us, now 900;
+    // 32768 rows of Zipf-distributed experts, 2048 -> 7168, 452 and 450 us.
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 1) count_tiles<true>(s->first, p, lane);
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int y1 = kSwiglu ? tl.n0 : tl.n0 + kBoxRows;
                 const int z0 = kSwiglu ? 2 * tl.e : tl.e, z1 = kSwiglu ? z0 + 1 : z0;
                 for (int b = 0; b < p.kb; ++b) {
-                    if (!(ok = wait_for(&s->empty[st], phase, &s->abort))) break;
+                    if (!(ok = wait_for<kStall>(&s->empty[st], phase, &s->waits))) break;
                     const uint32_t bar = smem_addr(&s->full[st]), to = smem_addr(s_tiles) + st * kStageBytes;
                     mbar_arrive_expect_tx(&s->full[st], bytes);
                     tma_load_3d_alone(to, &map_w, b * kBlockK, tl.n0, z0, bar);
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every stage's last read is over before the CTA may leave
             for (int i = 0; i < kStages && ok; ++i) {
-                ok = wait_for(&s->empty[st], phase, &s->abort);
+                ok = wait_for<kStall>(&s->empty[st], phase, &s->waits);
                 if (++st == kStages) {
                     st = 0;
                     phase ^= 1;
@@ -154,15 +155,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t st = 0, full_phase = 0, buf = 0, empty_phase = 1;
             Walk walk;
             bool ok = true;
-            for (int t = cta; t < tiles && ok; t += ctas) {
+            const int end = kStall && cta == p.g.stall_cta ? min(tiles, cta + p.g.stall_tile * ctas) : tiles;
+            for (int t = cta; t < end && ok; t += ctas) {
                 const int rows = __shfl_sync(0xffffffffu, tile_at<true>(t, walk, s->first, p, kCols).rows, 0);
                 const uint32_t idesc = e4m3_idesc(kBoxRows, (rows + 15) / 16 * 16);
                 for (int b = 0; b < p.kb; ++b) {
-                    ok = wait_for(&s->full[st], full_phase, &s->abort);
+                    ok = wait_for<kStall>(&s->full[st], full_phase, &s->waits);
                     const uint32_t at = smem_addr(s_tiles) + st * kStageBytes;
                     uint64_t dw = sw128_desc(at), da = sw128_desc(at + 2 * kBoxBytes);
                     asm volatile("" : "+l"(da), "+l"(dw));
-                    ok = ok && wait_for(&s->acc_empty[buf], empty_phase, &s->abort);
+                    ok = ok && wait_for<kStall>(&s->acc_empty[buf], empty_phase, &s->waits);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = load_scales(as + j * step, b, p.kb, lane + j * kWarp < tl.rows);
                     const float4 w = load_scales(ws, b, p.kb, lane < 2);
-                    ok = __all_sync(0xffffffffu, wait_for(&s->scale_empty[slot], phase, &s->abort));
+                    ok = __all_sync(0xffffffffu, wait_for<kStall>(&s->scale_empty[slot], phase, &s->waits));
                     if (!ok) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -238,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int b = 0; b < p.kb; ++b, ++it) {
                 const uint32_t buf = it & 1;
-                ok = (b & 3) != 0 || wait_for(&s->scale_full[slot], slot_phase, &s->abort);
+                ok = (b & 3) != 0 || wait_for<kStall>(&s->scale_full[slot], slot_phase, &s->waits);
                 const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s->row_scale[slot][b & 3] + g * kPart);
                 const float2 ws = s->w_scale[slot][b & 3];
-                ok = __all_sync(0xffffffffu, ok && wait_for(&s->acc_full[buf], (it / 2) & 1, &s->abort));
+                ok = __all_sync(0xffffffffu, ok && wait_for<kStall>(&s->acc_full[buf], (it / 2) & 1, &s->waits));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t col = lanes + buf * kAccColumns;
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (s->abort != 0) {
+    if (s->waits.ran_out != 0) {
         // a wait ran out: let the copies and products still in flight land before shared memory and TMEM go
         const long long start = globaltimer_ns();
         while (globaltimer_ns() - start < 10000000LL) {
@@ -339,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_dealloc(tmem, kTmemColumns);
 }
 
-template <bool kSwiglu>
-cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
+template <bool kSwiglu, bool kStall>
+cudaError_t launch_form(const GemmArgs& g, cudaStream_t stream) {
     Params p = {};
     p.g = g;
     p.kb = scale_blocks(g.k);
@@ -355,14 +357,16 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
     const long long most = static_cast<long long>(g.E) * p.tiles_n;  // the counts are on the device
-    return launch_pdl(ll_gemm_fp8_few_kernel<kSwiglu>, dim3(static_cast<unsigned>(most < sms ? most : sms)),
+    return launch_pdl(ll_gemm_fp8_few_kernel<kSwiglu, kStall>, dim3(static_cast<unsigned>(most < sms ? most : sms)),
                       dim3(kThreads), smem, stream, 0, true, map_a, map_w, p);
 }
 
 }  // namespace
 
 cudaError_t launch_few(const GemmArgs& g, cudaStream_t stream) {
-    return g.y_scales != nullptr ? launch<true>(g, stream) : launch<false>(g, stream);
+    const bool gated = g.y_scales != nullptr;
+    if (g.stall) return gated ? launch_form<true, true>(g, stream) : launch_form<false, true>(g, stream);
+    return gated ? launch_form<true, false>(g, stream) : launch_form<false, false>(g, stream);
 }
 
 }  // namespace gemm

@@ -116,6 +116,7 @@ _SIGS = {
     "ep_check_gemm_shape": (_i32, [ctypes.POINTER(EpGemmShape)]),
     "ep_ll_gemm_fp8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 7 + [_vp]),
     "ep_ll_gemm_swiglu_fp8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_vp]),
+    "ep_debug_ll_gemm_fp8_stall": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_i32] * 3 + [_vp]),
     "ep_sync_status": (_i32, [_vp, _vp]),
     "ep_debug_notify_dispatch_stall": (_i32, [ctypes.POINTER(EpShape)] + [_vp] * 16 +
                                        [_sz, _vp, _i32, _i32, _vp]),
@@ -633,6 +634,24 @@ def ep_ll_gemm_swiglu_fp8(a, a_scales, w, w_scales, count, y, y_scales, status, 
         _t(y_scales, torch.float32, (E, cap, scale_blocks(n)), "y_scales"),
         _t(status, torch.int32, (1,), "status"), _stream(stream))
     _check("ep_ll_gemm_swiglu_fp8", rc)
+
+
+def ep_debug_ll_gemm_fp8_stall(a, a_scales, w, w_scales, count, y, y_scales, status, stall_cta: int, stall_tile: int,
+                               wait_limit_us: int, stream=None) -> None:
+    """Testing hook: :func:`ep_ll_gemm_swiglu_fp8` (:func:`ep_ll_gemm_fp8` where ``y_scales`` is None) with
+    one CTA or pair of CTAs fed no products from its tile ``stall_tile`` on and every device wait
+    bounded by ``wait_limit_us``; the status word then reports a timeout and the context stays usable."""
+    gated = y_scales is not None
+    E, cap, n, k = _gemm_dims(a, w, 4 if gated else 3)
+    nb, kb, two = scale_blocks(n), scale_blocks(k), (2,) if gated else ()
+    rc = lib().ep_debug_ll_gemm_fp8_stall(
+        ctypes.byref(EpGemmShape(E, cap, n, k)), _t(a, torch.uint8, (E, cap, k), "a"),
+        _t(a_scales, torch.float32, (E, cap, kb), "a_scales"), _t(w, torch.uint8, (E, *two, n, k), "w"),
+        _t(w_scales, torch.float32, (E, *two, nb, kb), "w_scales"), _t(count, torch.int32, (E,), "count"),
+        _t(y, torch.uint8 if gated else torch.bfloat16, (E, cap, n), "y"),
+        _t(y_scales, torch.float32, (E, cap, nb), "y_scales", nullable=True), _t(status, torch.int32, (1,), "status"),
+        _i32(stall_cta), _i32(stall_tile), _i32(wait_limit_us), _stream(stream))
+    _check("ep_debug_ll_gemm_fp8_stall", rc)
 
 
 def ep_sync_status(status, stream=None) -> int:

@@ -728,6 +728,23 @@ ep_status_t ep_debug_layout_notify_dispatch_stall(
     int32_t* recv_src_info, int32_t* status, uint64_t* sched, int32_t stall_tile, int32_t wait_limit_us,
     cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Testing hook for failure detection in the experts' products.  Runs
+ * ep_ll_gemm_fp8, or ep_ll_gemm_swiglu_fp8 where `y_scales` is given, with
+ * every device wait bounded by `wait_limit_us` microseconds (1 .. 2e6) and the
+ * tensor cores of one place left without products from its tile number
+ * `stall_tile` (0 .. 2^20) on: pair of CTAs `stall_cta` in the kernel that works
+ * in pairs (the first half of its columns), CTA `stall_cta` in the one for few
+ * rows; -1: none.  Whatever waits for those products gives up, sets
+ * EP_DEV_TIMEOUT and exits, so the context stays usable.  A place without that
+ * many tiles finishes normally.  Output contents are undefined after a stalled
+ * run.
+ */
+ep_status_t ep_debug_ll_gemm_fp8_stall(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales,
+                                       const uint8_t* w, const float* w_scales, const int32_t* count, void* y,
+                                       float* y_scales, int32_t* status, int32_t stall_cta, int32_t stall_tile,
+                                       int32_t wait_limit_us, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

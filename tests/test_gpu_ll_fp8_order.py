@@ -127,3 +127,40 @@ def test_gated_product_reads_what_the_kernel_before_it_wrote(n, k):
     assert ep.ep_sync_status(status) == ep.EP_OK
     for i, (v, s) in enumerate(got):
         assert torch.equal(v, want[i % 3][0]) and torch.equal(s, want[i % 3][1]), i
+
+
+# E, capacity, n, k, counts: pairs of SMs with one to four tiles of one and of four k-blocks; few rows; both in one call
+STALLS = [(4, 256, 76 * 128, 128, [256, 160, 256, 256]), (4, 256, 76 * 128, 512, [256, 129, 256, 256]),
+          (40, 40, 1024, 384, [40] * 40), (8, 400, 4096, 256, [400, 20, 300, 128, 64, 256, 257, 1])]
+
+
+@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("case", STALLS, ids=str)
+def test_a_product_without_products_times_out_and_the_context_survives(case, gated, tile):
+    """One place's tensor cores get nothing from one of its tiles on: the call still ends, reports
+    EP_ERR_TIMEOUT, and the next call on the same buffers is bit for bit what it was before."""
+    E, cap, n, k, counts = case
+    a, a_s, w, w_s, count = (t.cuda() for t in gemm_inputs(E, cap, n, k, 50, halves=2 if gated else 1, counts=counts))
+    status = status_word()
+    y = torch.full((E, cap, n), 0x55 if gated else -7, dtype=torch.uint8 if gated else torch.bfloat16, device="cuda")
+    ys = torch.full((E, cap, ep.scale_blocks(n)), -7.0, device="cuda") if gated else None
+
+    def call():
+        if gated:
+            ep.ep_ll_gemm_swiglu_fp8(a, a_s, w, w_s, count, y, ys, status)
+        else:
+            ep.ep_ll_gemm_fp8(a, a_s, w, w_s, count, y, status)
+        assert ep.ep_sync_status(status) == ep.EP_OK
+
+    call()
+    want = y.clone(), None if ys is None else ys.clone()
+    # every place has its first tile; of the others only that the call ends is known here
+    ep.ep_debug_ll_gemm_fp8_stall(a, a_s, w, w_s, count, y, ys, status, 0, tile, 20000)
+    rc = ep.ep_sync_status(status)
+    assert rc == ep.EP_ERR_TIMEOUT if tile == 0 else rc in (ep.EP_OK, ep.EP_ERR_TIMEOUT)
+    status.zero_()
+    call()
+    assert torch.equal(y, want[0]) and (ys is None or torch.equal(ys, want[1]))
+    ep.ep_debug_ll_gemm_fp8_stall(a, a_s, w, w_s, count, y, ys, status, -1, 0, 2000000)  # nothing stalled
+    assert ep.ep_sync_status(status) == ep.EP_OK and torch.equal(y, want[0])

@@ -820,6 +820,7 @@ struct RouteBwdArgs {
 //
 //   ds_k = (scale g_k - sum_j scale g_j v_j) / sum_kept(s), v = s / sum_kept(s)   or   scale g_k
 //   sigmoid:                dl_k = s_k (1 - s_k) ds_k, 0 for the other experts
+//   sigmoid, renormalised:  that is v_k (1 - s_k) (scale g_k - sum_j scale g_j v_j)
 //   softmax, renormalised:  dl_k = v_k (scale g_k - sum_j scale g_j v_j), 0 for the others
 //   softmax over all:       dl_e = [e kept] s_e ds_e - s_e sum_k s_k ds_k: dense
 
@@ -869,16 +870,15 @@ __device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, float l
     } else if (on) {
         s = 1.0f / (1.0f + expf(-l));
     }
-    float ds = g;  // its gradient
+    float v = s, c = g;  // what the slot's weight is of `scale`, and its gradient
     if (p.rc.renorm) {
         const float total = warp_sum<W>(s);
-        const float v = total > 0.0f ? s / total : 0.0f;
-        const float c = g - warp_sum<W>(v * g);
-        ds = softmax ? c : (total > 0.0f ? c / total : 0.0f);
-        if (softmax) s = v;
+        v = total > 0.0f ? s / total : 0.0f;
+        c -= warp_sum<W>(v * g);
     }
+    // v, not c, is divided by the sum: with every kept sigmoid small, c over the sum is no fp32 number
     r.dot = 0.0f;
-    r.own = softmax ? s * ds : s * (1.0f - s) * ds;
+    r.own = softmax ? v * c : v * (1.0f - s) * c;
     return r;
 }
 

@@ -551,6 +551,8 @@ ep_status_t ep_route(const ep_shape_t* shape, const ep_route_t* route, const voi
  *   ds_k = scale * g_k, or scale / S * (g_k - sum_j g_j s_j / S)
  *   softmax: grad l_e = s_e * (ds_e - sum_k s_k ds_k)   (every eligible e)
  *   sigmoid: grad l_e = s_e * (1 - s_e) * ds_e          (0 where not kept)
+ * Sigmoid with renormalize is formed as s_k / S * (1 - s_k) * scale * (g_k -
+ * sum_j g_j s_j / S), finite also where every kept score is small.
  * Softmax with renormalize depends on the kept logits alone: their softmax v
  * gives grad l_k = scale * v_k * (g_k - sum_j v_j g_j), 0 elsewhere.
  *   logits, logits_bf16  in  as for ep_route (score, renormalize and scale of

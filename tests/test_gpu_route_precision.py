@@ -1,0 +1,49 @@
+"""Gradients and weights of the router where a bound relative to the row's largest element, or
+logits of ordinary size, would not show an error.  References and bounds in float64; each
+test derives its own."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import moe_ref
+from combine_get_dispatch_notify_gb300 import ep
+from test_gpu_route import run_backward
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ep.lib()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("E,K,lo,hi,size", [(64, 2, -88.5, -88.0, 2.0), (64, 2, -80.0, -76.0, 65536.0),
+                                            (256, 8, -88.5, -70.0, 3e4), (34, 17, -88.5, -84.0, 1.0),
+                                            (48, 32, -87.0, -20.0, 1e3)], ids=str)
+def test_backward_of_renormalised_sigmoids_that_are_all_small(E, K, lo, hi, size, dtype):
+    """Every kept score far below 1, down to where it is no normal fp32 number, and incoming gradients
+    as a scaled loss has them: the weights s / sum(s) are ordinary numbers, and so is their gradient.
+
+    With d the error of a score (expf 2 ulp, an addition, a division, 2^-22 more where it is
+    subnormal: below 2^-20), a weight v is off by 2 d + 2^-24, a sum of K terms by K 2^-24 more, and
+    what is left are four roundings: below (4 + 1) 2^-20 + (K + 6) 2^-24 < 2^-16.5 of v (|g| + sum v |g|)."""
+    R, T, scale = 2, 40, 2.5
+    gen = torch.Generator().manual_seed(21)
+    l = (torch.rand(R, T, E, generator=gen) * (hi - lo) + lo).mul(2).round().div(2).to(dtype)  # exact in bf16 too
+    idx = torch.rand(R, T, E, generator=gen).argsort(-1)[..., :K].contiguous()
+    g = torch.randn(R, T, K, generator=gen) * size
+    d, rc = run_backward(l, idx, g, "sigmoid", True, scale)
+    assert rc == ep.EP_OK
+    want = moe_ref.route_backward(l, idx, g, "sigmoid", True, scale)
+    s = torch.sigmoid(l.double()).gather(-1, idx)
+    v = s / s.sum(-1, keepdim=True)
+    size_k = v * (g.double().abs() + (v * g.double().abs()).sum(-1, keepdim=True)) * scale
+    bound = torch.zeros(R, T, E, dtype=torch.float64).scatter_(-1, idx, size_k * 2.0 ** -16.5)
+    if dtype == torch.bfloat16:
+        bound = bound + want.abs() * 2.0 ** -8
+    assert torch.isfinite(d).all()
+    assert ((d.double() - want).abs() <= bound).all()

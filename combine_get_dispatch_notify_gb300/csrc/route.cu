@@ -863,12 +863,14 @@ __device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, float l
         r.dot = warp_sum<W>(r.own);
         return r;
     }
-    float s = 0.0f;  // the kept score
+    float s = 0.0f, rest = 1.0f;  // the kept score; sigmoid: 1 - s, as s exp(-l) where the difference would lose digits
     if (softmax) {
         const float top = warp_max<W>(on ? l : -FLT_MAX);
         if (on) s = expf(l - top);
     } else if (on) {
-        s = 1.0f / (1.0f + expf(-l));
+        const float e = expf(-l);
+        s = 1.0f / (1.0f + e);
+        rest = e < 1.0f ? s * e : 1.0f - s;
     }
     float v = s, c = g;  // what the slot's weight is of `scale`, and its gradient
     if (p.rc.renorm) {
@@ -878,7 +880,7 @@ __device__ __forceinline__ SlotGrad slot_gradient(const RouteBwdArgs& p, float l
     }
     // v, not c, is divided by the sum: with every kept sigmoid small, c over the sum is no fp32 number
     r.dot = 0.0f;
-    r.own = softmax ? v * c : v * (1.0f - s) * c;
+    r.own = softmax ? v * c : v * rest * c;
     return r;
 }
 

@@ -47,3 +47,33 @@ def test_backward_of_renormalised_sigmoids_that_are_all_small(E, K, lo, hi, size
         bound = bound + want.abs() * 2.0 ** -8
     assert torch.isfinite(d).all()
     assert ((d.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("E,K", [(64, 8), (40, 16), (256, 1), (64, 32)], ids=str)
+def test_backward_of_sigmoids_near_one(E, K, dtype, renorm):
+    """s (1 - s) keeps its digits where s is near 1 in fp32, or 1: 1 - s is exp(-l) s.
+
+    exp(-l) is within 2^-22, s and s exp(-l) within 2^-20 with their roundings, a weight within 2^-19
+    (its sum of K terms K 2^-24 more), what it multiplies within (K + 4) 2^-24 of |g| + sum v |g|:
+    together below 2^-18 + K 2^-23 < 2^-16.9 of v (1 - s) (|g| + sum v |g|)."""
+    R, T, scale = 2, 40, 2.5
+    gen = torch.Generator().manual_seed(26)
+    l = (torch.rand(R, T, E, generator=gen) * 44 - 4).mul(4).round().div(4).to(dtype)  # exact in bf16 too
+    idx = torch.rand(R, T, E, generator=gen).argsort(-1)[..., :K].contiguous()
+    g = torch.randn(R, T, K, generator=gen)
+    d, rc = run_backward(l, idx, g, "sigmoid", renorm, scale)
+    assert rc == ep.EP_OK
+    k, gd = l.double().gather(-1, idx), g.double() * scale
+    s = 1 / (1 + torch.exp(-k))
+    rest = 1 / (1 + torch.exp(k))  # 1 - s
+    v = s / s.sum(-1, keepdim=True) if renorm else s
+    dot = (v * gd).sum(-1, keepdim=True) if renorm else 0.0
+    mag = (v * gd.abs()).sum(-1, keepdim=True) if renorm else 0.0
+    zeros = torch.zeros(R, T, E, dtype=torch.float64)
+    want = zeros.scatter(-1, idx, v * rest * (gd - dot))
+    bound = zeros.scatter(-1, idx, v * rest * (gd.abs() + mag) * 2.0 ** -16.9)
+    if dtype == torch.bfloat16:
+        bound = bound + want.abs() * 2.0 ** -8
+    assert ((d.double() - want).abs() <= bound).all()

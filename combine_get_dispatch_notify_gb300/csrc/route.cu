@@ -1007,11 +1007,11 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
 // Dense gradients of up to 512 experts.  With kVec rows are whole 16-byte vectors: lane i holds the N
 // experts from i * N on and reads and writes them as vectors; else it holds every
 // 32nd expert from i on.  It finds its slots' parts in a shared row that is zero
-// but for them.  Bound by HBM: the exponentials are ex2.approx (2^-22, and 2^-24 of
-// the exponent), and rows are brought into L2 three tokens ahead, because the warps that fit
-// hold too few bytes in flight (bf16 50 us without).  A token with unusual logits, or
-// with an expert in two slots, goes through backward_token.  W lanes have a token.  131072 tokens x 256:
-// fp32 50 us (5.7 TB/s, 85 % of the copy rate), bf16 46 us; kVec off costs 2 % and 21 %.
+// but for them.  Bound by the instructions of a token, most of them the same for half the bytes.  Rows are brought into L2 three tokens ahead,
+// because the warps that fit hold too few bytes in flight.  The exponentials are expf: __expf takes 49 us for the
+// fp32 rows below, but its product x log2(e) alone is off by 2^-19 at scores of exp(-60).  A token with unusual
+// logits, or with an expert in two slots, goes through backward_token.  W lanes have a token.  131072 tokens x 256:
+// fp32 55 us (5.1 TB/s, 77 % of the copy rate), bf16 51 us; kVec off costs 2 % and 21 %.
 // route_backward_kernel takes 282 us for the fp32 ones.
 template <bool kBf16, int N, bool kVec, int W>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kerne
         m = W == kWarp ? redux_max(m) : warp_max<W>(m);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            d[j] = has(j) ? __expf(d[j] - m) : 0.0f;
+            d[j] = has(j) ? expf(d[j] - m) : 0.0f;
             sum += d[j];
         }
         const float hi = largest<kBf16>();

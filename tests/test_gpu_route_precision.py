@@ -77,3 +77,24 @@ def test_backward_of_sigmoids_near_one(E, K, dtype, renorm):
     if dtype == torch.bfloat16:
         bound = bound + want.abs() * 2.0 ** -8
     assert ((d.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("R,T,E", [(1, 33, 16), (2, 37, 32), (1, 9, 64), (1, 70, 72), (2, 61, 128), (1, 5, 130),
+                                   (4, 65, 256), (1, 21, 300), (1, 17, 384), (2, 33, 512), (1, 5, 1000)], ids=str)
+def test_backward_of_scores_far_below_the_largest(R, T, E):
+    """One expert holds the row and is kept; the others' gradients are -exp(l_e - max) g.  They are as
+    exact as an fp32 exponential: l_e - max is a multiple of 2^-10 (no rounding), the sum is 1 and
+    the largest score is 1, so expf's 2 ulp (2^-22) and at most six roundings (2^-24) remain: 2^-21.
+    A gradient below 2^-126 is a multiple of 2^-149, and so off by up to one of those."""
+    gen = torch.Generator().manual_seed(22)
+    l = -(torch.rand(R, T, E, generator=gen) * 45 + 40).mul(1024).round().div(1024)  # -40 to -85
+    top = torch.randint(0, E, (R, T, 1), generator=gen)
+    l.scatter_(-1, top, torch.randint(-3, 4, (R, T, 1), generator=gen).float() / 4)
+    g = torch.randn(R, T, 1, generator=gen)
+    d, rc = run_backward(l, top, g, "softmax", False, 1.5)
+    assert rc == ep.EP_OK
+    diff = (l - l.gather(-1, top)).double()
+    want = -torch.exp(diff) * (g.double() * 1.5)
+    others = torch.ones(R, T, E, dtype=torch.bool).scatter_(-1, top, False)
+    assert ((d.double() - want).abs() <= want.abs() * 2.0 ** -21 + 2.0 ** -149)[others].all()
+    assert (d.gather(-1, top).abs() <= g.abs() * 1.5 * 2.0 ** -21).all()  # s (1 - s) g with s = 1

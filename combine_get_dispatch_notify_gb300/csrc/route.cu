@@ -238,6 +238,16 @@ __device__ __forceinline__ uint32_t half_signs(uint32_t v) {
     return r;
 }
 
+// a / b for a in [0, 1] and a sum b of 1 to 512: a quotient by an approximate reciprocal, corrected once by its exact
+// remainder (Markstein), which makes it the nearest fp32 number but where a / b is within 2^-44 of halfway between two.  The
+// general division's checks for sizes that do not occur here cost 524288 x 256 tokens 23 of 145 us.
+__device__ __forceinline__ float over_sum(float a, float b) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+    const float q = a * r;
+    return fmaf(fmaf(-q, b, a), r, q);
+}
+
 template <int N, bool kFew, bool kSigmoid>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const RouteArgs p) {
     __shared__ uint32_t s_slots[kRouteWarps][kWarp];
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
                 }
                 total = warp_sum(total);
             }
-            weight = __fdividef(mine, total);
+            weight = over_sum(mine, total);
         }
         if (lane < p.K) out.put(lane, idx, kept ? weight * p.rc.scale : 0.0f);
     }

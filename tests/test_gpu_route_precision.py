@@ -8,7 +8,7 @@ import torch
 
 import moe_ref
 from combine_get_dispatch_notify_gb300 import ep
-from test_gpu_route import run_backward
+from test_gpu_route import run_backward, run_route
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,17 @@ def test_backward_of_scores_far_below_the_largest(R, T, E):
     others = torch.ones(R, T, E, dtype=torch.bool).scatter_(-1, top, False)
     assert ((d.double() - want).abs() <= want.abs() * 2.0 ** -21 + 2.0 ** -149)[others].all()
     assert (d.gather(-1, top).abs() <= g.abs() * 1.5 * 2.0 ** -21).all()  # s (1 - s) g with s = 1
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_weights_of_equal_logits_are_the_nearest_numbers(dtype, renorm):
+    """Equal logits: every exponential is 1 and their sum a whole number n, so the one rounding is the
+    division's, and each weight is the fp32 number nearest to 1 / n."""
+    for E in range(2, 513, 2):
+        K = min(E, 32) if renorm else 1
+        for k in ({K, max(1, K - E // 2 % 32)} if renorm else {1}):
+            idx, w, rc = run_route(torch.full((1, 1, E), 0.75, dtype=dtype), None, k, score="softmax", renorm=renorm)
+            assert rc == ep.EP_OK and idx.flatten().tolist() == list(range(k))
+            n = k if renorm else E
+            assert (w == torch.tensor(1.0) / torch.tensor(float(n))).all(), (E, k)

@@ -19,6 +19,17 @@ __device__ __forceinline__ float block_scale(float amax) {
     return fmaxf(amax, kFloor) / 448.0f;
 }
 
+// x / scale as the division rounds it, by the reciprocal `inv` = 1 / scale, itself rounded by a division: the product is
+// corrected by its exact remainder, which brings it within one ulp, and from there a second time, which gives the nearest
+// number (Markstein).  An infinite scale leaves 0, or NaN of an infinity, as the division does.  Below scales of about
+// 2^-90 the remainders lose bits, and a quotient beside a tie may round to its other side.
+__device__ __forceinline__ float over_scale(float x, float scale, float inv) {
+    const float q = x * inv;
+    float c = fmaf(fmaf(-q, scale, x), inv, q);
+    c = fmaf(fmaf(-c, scale, x), inv, c);
+    return c == c ? c : q;
+}
+
 // Four floats -> four e4m3 bytes, round to nearest even (lowest byte first).
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;

@@ -376,8 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t v[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            v[k] = pack_e4m3x4(h[j * 16 + k * 4] * inv, h[j * 16 + k * 4 + 1] * inv,
-                                               h[j * 16 + k * 4 + 2] * inv, h[j * 16 + k * 4 + 3] * inv);
+                            v[k] = pack_e4m3x4(over_scale(h[j * 16 + k * 4], scale, inv), over_scale(h[j * 16 + k * 4 + 1], scale, inv),
+                                               over_scale(h[j * 16 + k * 4 + 2], scale, inv), over_scale(h[j * 16 + k * 4 + 3], scale, inv));
                         if (col < p.g.n) st_v4(out + col, make_uint4(v[0], v[1], v[2], v[3]));
                     }
                     if (g == 0) p.g.y_scales[r * p.nb + tl.n0 / kScaleBlock] = scale;

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t* out = static_cast<uint8_t*>(p.g.y) + r0 * p.g.n + n;
 #pragma unroll
                     for (int j = 0; j < kPart; ++j) {
-                        const float q = h[j] * __shfl_sync(0xffffffffu, inv, j);
+                        const float q = over_scale(h[j], __shfl_sync(0xffffffffu, scale, j), __shfl_sync(0xffffffffu, inv, j));
                         if (n < p.g.n && j < valid)
                             out[static_cast<long long>(j) * p.g.n] =
                                 static_cast<uint8_t>(pack_e4m3x4(q, 0.0f, 0.0f, 0.0f));

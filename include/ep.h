@@ -630,6 +630,8 @@ ep_status_t ep_ll_gemm_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const
  * gate and up = p for the two halves of w:
  *   h = gate / (1 + exp(-gate)) * up
  *   y, y_scales = h cast by blocks of 128 columns as in ep_ll_dispatch_fp8
+ *                 (below scales of 2^-90 a quotient beside a tie may go to its
+ *                 other side)
  *   w         in  e4m3 bytes [num_experts][2][n][k]  (gate matrix, up matrix)
  *   w_scales  in  fp32 [num_experts][2][ceil(n / 128)][ceil(k / 128)]
  *   y         out e4m3 bytes [num_experts][capacity][n]

@@ -144,9 +144,17 @@ __device__ __forceinline__ float element(const float4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// h = gate / (1 + exp(-gate)) * up.
+// h = gate / (1 + exp(-gate)) * up.  The quotient is made by an approximate reciprocal and corrected by its exact
+// remainder (Markstein), to half an ulp; both sides are taken a quarter as large so that the reciprocal of a divisor near
+// 2^128 is still a normal number.  __expf and __fdividef would be off by 2^-18 at gates of -80 and 0 below -87.3; the
+// general division, 16 to 32 of them in a row, makes a whole product 4 to 14 % longer.
 __device__ __forceinline__ float gated(float gate, float up) {
-    return __fdividef(gate, 1.0f + __expf(-gate)) * up;
+    const float n = 0.25f * gate, d = fmaf(0.25f, expf(-gate), 0.25f);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float q = n * r;
+    const float c = fmaf(fmaf(-q, d, n), r, q);
+    return (c == c ? c : q) * up;  // an infinite side leaves no remainder
 }
 
 // ---- host ----

@@ -51,3 +51,26 @@ def test_gated_rows_are_cast_by_division(rows):
     scale = h.amax(-1) / 448.0
     assert torch.equal(ys[0], scale.expand(rows, blocks))
     assert torch.equal(y[0], e4m3(h / scale.unsqueeze(-1)).view(1, n).expand(rows, n))
+
+
+@pytest.mark.parametrize("rows", [64, 128, 256, 389])
+def test_activation_has_fp32_precision_at_every_gate(rows):
+    """silu(gate) * up over gates from 20 to -88.6, seen through the scale of a block whose other columns
+    are zero: |h| / 448.  gate = -x and up = 2^40 x are exact; expf's 2 ulp (2^-22), an addition, two
+    divisions and a product (2^-24 each) make 2^-21 relative."""
+    x = torch.linspace(-20.0, 88.6, rows)
+    x[x == 0] = 0.5
+    a = torch.zeros(1, rows, 16)
+    a[0, :, 0] = 1.0
+    w = torch.zeros(1, 2, 128, 16)
+    w[0, 0, 5, 0], w[0, 1, 5, 0] = -1.0, 1.0
+    ws = torch.tensor([1.0, 2.0 ** 40]).view(1, 2, 1, 1)
+    args = (e4m3(a), x.view(1, rows, 1), e4m3(w), ws, torch.tensor([rows], dtype=torch.int32))
+    y, ys = run_swiglu(args, 128)
+    xd = x.double()
+    h = -xd / (1 + torch.exp(xd)) * (xd * 2.0 ** 40)
+    want = h.abs() / 448
+    assert (want > 2.0 ** -100).all()
+    assert ((ys[0, :, 0].double() - want).abs() <= want * 2.0 ** -21).all()
+    assert (y[0, :, 5] == e4m3(torch.where(h < 0, -448.0, 448.0))).all()
+    assert (y[0, :, :5] & 0x7f == 0).all() and (y[0, :, 6:] & 0x7f == 0).all()

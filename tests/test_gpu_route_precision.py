@@ -8,7 +8,7 @@ import torch
 
 import moe_ref
 from combine_get_dispatch_notify_gb300 import ep
-from test_gpu_route import run_backward, run_route
+from test_gpu_route import RTOL, SHAPES, logits_of, run_backward, run_route
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,83 @@ def test_weights_of_equal_logits_are_the_nearest_numbers(dtype, renorm):
             assert rc == ep.EP_OK and idx.flatten().tolist() == list(range(k))
             n = k if renorm else E
             assert (w == torch.tensor(1.0) / torch.tensor(float(n))).all(), (E, k)
+
+
+def gradient_and_sizes(logits, idx, g, score, renorm, scale):
+    """(gradient, magnitude of what each element is the sum of) from the formulas, float64 [R, T, E]."""
+    l, ok = moe_ref.masked_logits(logits)
+    l, ok = torch.from_numpy(l), torch.from_numpy(ok)
+    on = (idx >= 0) & ok.gather(-1, idx.clamp(min=0))
+    at = idx.clamp(min=0)
+    k, g = l.gather(-1, at), torch.where(on, g.double() * scale, 0.0)
+    p = torch.softmax(torch.where(ok, l, -1e300), -1)
+    if score == "softmax" and renorm:
+        s, rest = torch.softmax(torch.where(on, k, -1e300), -1) * on, 1.0
+    elif score == "softmax":
+        s, rest = p.gather(-1, at) * on, 1.0
+    else:
+        s, rest = on / (1 + torch.exp(-k)), 1 / (1 + torch.exp(k))
+    dot = mag = 0.0
+    if renorm:
+        total = s.sum(-1, keepdim=True)
+        s = torch.where(total > 0, s / total.clamp(min=1e-300), 0.0)
+        dot, mag = (s * g).sum(-1, keepdim=True), (s * g).abs().sum(-1, keepdim=True)
+    zeros = torch.zeros_like(l)
+    grad = zeros.scatter_add(-1, at, s * rest * (g - dot) * on)
+    size = zeros.scatter_add(-1, at, s * rest * (g.abs() + mag) * on)
+    if score == "softmax" and not renorm:
+        grad = grad - p * (s * g).sum(-1, keepdim=True)
+        size = size + p * (s * g).abs().sum(-1, keepdim=True)
+    return grad, size
+
+
+@pytest.mark.parametrize("pick", ["largest", "any"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shape", SHAPES + [(1, 37, 64, 8), (2, 29, 48, 6), (1, 33, 128, 12), (1, 21, 300, 8)], ids=str)
+def test_every_gradient_element_is_held_to_its_own_size(shape, score, renorm, dtype, pick):
+    """An element's error is bounded by RTOL of the terms that it is the sum of, not of the row's
+    largest: with many experts the dense softmax part is far below that one everywhere."""
+    R, T, E, K = shape
+    l = logits_of(R, T, E, dtype, 23)
+    gen = torch.Generator().manual_seed(24)
+    order = l.float() if pick == "largest" else torch.rand(R, T, E, generator=gen)
+    idx = order.argsort(-1, descending=True)[..., :K].contiguous()
+    if T > 1 and K > 1:
+        idx[:, 1, K // 2:] = -1
+    g = torch.randn(R, T, K, generator=gen)
+    d, rc = run_backward(l, idx, g, score, renorm, 2.5)
+    assert rc == ep.EP_OK
+    want, size = gradient_and_sizes(l, idx, g, score, renorm, 2.5)
+    bound = RTOL * size
+    if dtype == torch.bfloat16:
+        bound = bound + want.abs() * 2.0 ** -8
+    assert ((d.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("E,K", [(24, 6), (64, 8), (130, 3)], ids=str)
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_every_gradient_element_matches_differences_of_the_forward(score, renorm, E, K):
+    """Central differences of the float64 weights with h = 2^-16: h^2 / 6 times third derivatives (below
+    2 for a weight) and roundings of 2^-52 / h are each below 1e-10 per unit of scale * sum |g|."""
+    R, T = 1, 7
+    l = logits_of(R, T, E, torch.float32, 27)
+    gen = torch.Generator().manual_seed(28)
+    idx = l.argsort(-1, descending=True)[..., :K].contiguous()
+    idx[:, 3:] = torch.rand(R, T - 3, E, generator=gen).argsort(-1)[..., :K]
+    g = torch.randn(R, T, K, generator=gen)
+    d, rc = run_backward(l, idx, g, score, renorm, 1.5)
+    assert rc == ep.EP_OK
+    ok = torch.ones(R, T, E, dtype=torch.bool)
+    h, num = 2.0 ** -16, torch.zeros(R, T, E, dtype=torch.float64)
+    for e in range(E):
+        step = torch.zeros(E, dtype=torch.float64)
+        step[e] = h
+        up = (moe_ref.weights_of(l.double() + step, ok, idx, score, renorm, 1.5) * g).sum(-1)
+        dn = (moe_ref.weights_of(l.double() - step, ok, idx, score, renorm, 1.5) * g).sum(-1)
+        num[..., e] = (up - dn) / (2 * h)
+    _, size = gradient_and_sizes(l, idx, g, score, renorm, 1.5)
+    bound = RTOL * size + 2e-10 * 1.5 * g.double().abs().sum(-1, keepdim=True)
+    assert ((d.double() - num).abs() <= bound).all()

@@ -257,7 +257,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                g % 2 * (kSwiglu ? kGroupCols : kHalfN / 2);
         uint64_t* full = s->bar.acc_full[g / 2];
         const uint32_t empty = mapa(smem_addr(s->bar.acc_empty[g / 2]), 0);
-        const uint32_t scale_empty = mapa(smem_addr(s->bar.scale_empty), rank);
         uint32_t it = 0, q = 0;  // blocks and slots so far
         for (int i = 0; i < mine; ++i) {
             // the tile comes with its first scales: walking here would hold up the sums, some 800 cycles a tile
@@ -296,7 +295,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
                 }
                 if ((b & 3) == 3 || b + 1 == p.kb) {
-                    if (lane == 0) mbar_arrive_cluster_relaxed(scale_empty + slot * 8);
+                    __syncwarp();  // every lane has read the slot; the arrival hands it back: a release
+                    if (lane == 0) mbar_arrive(&s->bar.scale_empty[slot]);
                     ++q;
                 }
             }

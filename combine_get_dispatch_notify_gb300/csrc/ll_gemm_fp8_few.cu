@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = (warp - 4) / 4, quarter = warp % 4;
         const int row = quarter * kWarp + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + g * kPart;
-        const uint32_t empty = mapa(smem_addr(s->acc_empty), 0), scale_empty = mapa(smem_addr(s->scale_empty), 0);
+        const uint32_t empty = mapa(smem_addr(s->acc_empty), 0);
         uint32_t it = 0, slot = 0, slot_phase = 0, turn = 0;
         Walk walk;
         bool ok = true;
@@ -263,13 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();  // the block's sums have left TMEM
-                if (lane == 0) {
-                    mbar_arrive_cluster_relaxed(empty + buf * 8);
-                    if ((b & 3) == 3 || b + 1 == p.kb) mbar_arrive_cluster_relaxed(scale_empty + slot * 8);
-                }
-                if (((b & 3) == 3 || b + 1 == p.kb) && ++slot == kScaleSlots) {
-                    slot = 0;
-                    slot_phase ^= 1;
+                if (lane == 0) mbar_arrive_cluster_relaxed(empty + buf * 8);
+                if ((b & 3) == 3 || b + 1 == p.kb) {
+                    __syncwarp();  // every lane has read the slot; the arrival hands it back: a release
+                    if (lane == 0) mbar_arrive(&s->scale_empty[slot]);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        slot_phase ^= 1;
+                    }
                 }
             }
             ok = group_all(g, ok);  // every warp of the group comes here, also when a wait ran out

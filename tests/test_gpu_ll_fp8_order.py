@@ -164,3 +164,23 @@ def test_a_product_without_products_times_out_and_the_context_survives(case, gat
     assert torch.equal(y, want[0]) and (ys is None or torch.equal(ys, want[1]))
     ep.ep_debug_ll_gemm_fp8_stall(a, a_s, w, w_s, count, y, ys, status, -1, 0, 2000000)  # nothing stalled
     assert ep.ep_sync_status(status) == ep.EP_OK and torch.equal(y, want[0])
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("E,cap,n,k", [(3, 128, 640, 7168), (40, 96, 1024, 3328), (2, 300, 784, 7168)], ids=str)
+def test_scales_of_every_block_are_its_own(E, cap, n, k, gated):
+    """Scales handed over four k-blocks at a time, each four 2^6 larger or smaller than the ones before in
+    the same place: a row that read its neighbours' would be far off."""
+    args = gemm_inputs(E, cap, n, k, 60, halves=2 if gated else 1, counts=[cap] * E)
+    step = 2.0 ** (6.0 * ((torch.arange(args[1].shape[-1]) // 4) % 3 - 1))
+    args[1].mul_(step)
+    args[3].mul_(step.flip(0))
+    if gated:
+        y, ys = run_swiglu(args, n)
+        check_swiglu(args, y, ys, n)
+    else:
+        a, a_s, w, w_s, count = (t.cuda() for t in args)
+        y, status = torch.full((E, cap, n), -7.0, dtype=torch.bfloat16, device="cuda"), status_word()
+        ep.ep_ll_gemm_fp8(a, a_s, w, w_s, count, y, status)
+        assert ep.ep_sync_status(status) == ep.EP_OK
+        check_gemm(args, y.cpu(), n)

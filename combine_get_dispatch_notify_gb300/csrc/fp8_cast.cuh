@@ -13,7 +13,8 @@ __host__ __device__ constexpr int scale_blocks(int n) { return (n + kScaleBlock 
 
 // Scale of a block whose largest magnitude is `amax`.  The floor keeps the
 // scale of a zero (or vanishing) block a normal number, so x / scale is never
-// 0 / 0; a finite bf16 or product row does not come near it otherwise.
+// 0 / 0.  A block whose largest magnitude is below 2^-100 (bf16 and fp32 go down
+// to 2^-133 and 2^-149) gets the same scale and fewer of e4m3's digits, or 0.
 __device__ __forceinline__ float block_scale(float amax) {
     constexpr float kFloor = 7.888609052210118e-31f;  // 2^-100
     return fmaxf(amax, kFloor) / 448.0f;

@@ -9,7 +9,7 @@
 // width, 2 H + K (H + H / 32) bytes.  A slice of 1024 columns, not a whole row, goes to
 // a warp so that a few tokens fill the GPU and the slice stays in registers for its
 // K copies; its eight scales are one 32-byte sector.  2048 tokens x 7168 to 8 slots
-// take 27 us (5.6 TB/s, much of it through L2), 32768 tokens 400 us (6.0 TB/s, 90 % of
+// take 26.5 us (5.7 TB/s, much of it through L2), 32768 tokens 410 us (5.9 TB/s, 88 % of
 // the copy rate).
 #include <cstdint>
 #include <cuda_runtime.h>

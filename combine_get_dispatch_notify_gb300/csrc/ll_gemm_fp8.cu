@@ -14,13 +14,15 @@
 // What bounds it: a block's products take the tensor core 512 cycles, its operands
 // (32 KB to each SM; up to 49 bytes a cycle arrive from L2) 669, and the sixteen
 // epilogue warps' instructions about 550 of the four schedulers; together they run at
-// 860 cycles a block.  The tile is as large as TMEM and the registers for its sums
-// allow: with a smaller one the operands would take longer still.  Measured: 32
-// experts with 1024 rows each, gated, 7168 -> 2 x 2048: 800 us, 2405 TFLOP/s (tensor
-// pipe busy 58 %); 32768 rows in 32 experts by Zipf popularity, 2048 -> 7168: 407 us,
-// 2365 TFLOP/s.  One MMA of 256 columns in place of the halves took 791 us for the
-// first and 481 for the second when the halves took 806 and 460; eight epilogue warps
-// take 900 us and more for the first.
+// 860 cycles a block.  None of them is full: which waits of the chain from operands to
+// sums make up the other 190 cycles has not been measured.  The tile is as large as TMEM and the registers for its sums
+// allow: with a smaller one the operands would take longer still.  Measured, with
+// the few-rows kernel's share: 32 experts with 1024 rows each, gated, 7168 -> 2 x 2048:
+// 890 to 930 us over long blocks, from card to card, 2.1 to 2.2 PFLOP/s; 850 us in a burst of 30 calls
+// (tensor pipe busy 54 %); 32768 rows in 32 experts by Zipf popularity, 2048 -> 7168: 440
+// to 467 us, 2.1 to 2.2 PFLOP/s; 430 us in a burst.  One MMA of 256 columns in place of
+// the halves took 791 us for the first and 481 for the second when the halves took 806
+// and 460, bursts all; eight epilogue warps took 900 us and more for the first.
 //
 // Each CTA loads its own 128 rows of a and half of the weight rows with
 // swizzled TMA; the weights cross HBM once per 256 rows, and only the 32-row

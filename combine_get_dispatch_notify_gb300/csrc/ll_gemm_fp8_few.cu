@@ -16,9 +16,9 @@
 // bytes to the registers of a warp each, would else take as long as everything else),
 // and gate and up of one output column meet in one thread.
 //
-// Measured, 7168 -> 2 x 2048 gated: 256 experts with 64 rows each 1.13 to 1.15 ms, 6.7 TB/s
-// (the copy rate is 6.67); eight experts with one row each 43 us, 5.4 TB/s.  2048 ->
-// 7168, 16 experts with 64 rows each: 46 us, 5.4 TB/s.  The short ones pay some 5 us for the
+// Measured, 7168 -> 2 x 2048 gated: 256 experts with 64 rows each 1.14 to 1.17 ms, 6.6 to 6.7 TB/s
+// (the copy rate is 6.67); eight experts with one row each 42 us, 5.6 TB/s.  2048 ->
+// 7168, 16 experts with 64 rows each: 44.5 us, 5.7 TB/s.  The short ones pay some 5 us for the
 // launch, the first stages and a last round of tiles that not every SM has.  Towards
 // 128 rows shared memory bounds it: operands in and out, and the scales' reads.
 #include <cstdint>

@@ -9,7 +9,7 @@
 // (more than 512 experts, softmax scores with a bias or summed for groups).
 // Where two of them could take a case, measured: 32768 tokens x 256 fp32 sigmoid
 // keys in 8 groups 27 us with lists, 63 us in shared memory; 524288 x 256 bf16 logits
-// 148 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 617 us in
+// 144 us in route_bf16_kernel (2.2 TB/s), 316 us in route_lists_kernel, 617 us in
 // shared memory; 131072 x 256 bf16, sigmoid without a bias, 47 and 89 us.  The bytes
 // alone would take 5 and 48 us of the first two: selection is bound by the integer
 // pipe, which minima, maxima, compares and selects share at half rate (70 % busy in
@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_bf16_kernel(const Ro
 // key has to be out of the runner-up's reach (its cut and its approximation), and
 // the last group kept out of reach of the first one dropped.  The winners'
 // own order is settled by their exact keys.  A token that fails (about one in a
-// hundred) takes its rounds over exact keys.
+// hundred) takes its rounds over exact keys.  So does every token with a masked logit, after its
+// first rounds: with eight of 256 fp32 experts masked in every row, 131072 tokens of softmax
+// take 160 us and 32768 of sigmoids in 8 groups 72 us, where they take 70 and 31 without
+// (each call timed alone; bf16 softmax, whose kernel needs no test, 41 with the mask).
 
 __device__ __forceinline__ float approx_error() { return 9.5367431640625e-07f; }  // 2^-20
 
@@ -956,9 +959,10 @@ __device__ __forceinline__ void zero_elements(void* out, long long lo, long long
 // Gradients that are zero but for the slots' experts (sigmoid, and softmax over
 // the kept experts): W >= K lanes to a token, so a warp has 32 / W tokens at
 // once.  Their rows, one after another in memory, are zeroed as vectors and the
-// slots' parts stored on top.  Bound by HBM's writes and the gathered logits: 131072
-// tokens x 256, K = 8, bf16 26 us, fp32 41 us (with a whole warp to each token, and its row put
-// together in shared memory, bf16 took 66 us).
+// slots' parts stored on top.  It waits for the gathered logits: 131072 tokens x 256, K = 8, bf16 25 us,
+// fp32 41 us, where whole sectors of what it moves would take 17 and 27 (DRAM at 44 % of its peak; a
+// warp stalls 8.8 cycles on loads for each instruction).  With a whole warp to each token, and its row
+// put together in shared memory, bf16 took 66 us.
 template <bool kBf16, int W>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_sparse_kernel(const RouteBwdArgs p) {
     constexpr int kTokens = kWarp / W;
@@ -1021,7 +1025,7 @@ __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_kernel(cons
 // because the warps that fit hold too few bytes in flight.  The exponentials are expf: __expf takes 49 us for the
 // fp32 rows below, but its product x log2(e) alone is off by 2^-19 at scores of exp(-60).  A token with unusual
 // logits, or with an expert in two slots, goes through backward_token.  W lanes have a token.  131072 tokens x 256:
-// fp32 55 us (5.1 TB/s, 77 % of the copy rate), bf16 51 us; kVec off costs 2 % and 21 %.
+// fp32 54 us (5.2 TB/s, 78 % of the copy rate), bf16 51 us; kVec off costs 2 % and 16 %.
 // route_backward_kernel takes 282 us for the fp32 ones.
 template <bool kBf16, int N, bool kVec, int W>
 __global__ void __launch_bounds__(kRouteWarps* kWarp) route_backward_lanes_kernel(const RouteBwdArgs p) {
@@ -1205,7 +1209,7 @@ cudaError_t launch_backward(const RouteBwdArgs& p, int sms, cudaStream_t stream)
     const bool vec = p.E % kFewest == 0;
     if (p.E <= kFewest * kWarp) {
         // short rows: as few lanes to a token as hold them and its slots, and the warp has several tokens (131072
-        // tokens x 64 bf16, K = 8: 15 us, 43 us with a warp to each; x 72, K = 12: 29 and 44 us)
+        // tokens x 64 bf16, K = 8: 18 us, 51 us with a warp to each; x 72, K = 12: 35 and 51 us)
         if (vec && p.E <= kFewest * 8 && p.K <= 8)
             return launch_tokens(route_backward_lanes_kernel<kBf16, kFewest, true, 8>, p, sms, stream);
         if (vec && p.E <= kFewest * 16 && p.K <= 16)
@@ -1230,7 +1234,8 @@ cudaError_t launch_route(const Shape& sh, const RouteCfg& rc, const void* logits
     const RouteArgs p = {logits, bias, topk_idx, topk_w, status, static_cast<long long>(sh.R) * sh.T, sh.E, sh.K, rc};
     const bool by_logit = rc.score == 0 && bias == nullptr && (rc.group_top == 1 || rc.topk_groups == rc.G);
     // experts of a lane: twelve up to 384, unless only sixteen divide them into runs (131072 x 384 bf16 softmax: 53 us
-    // with twelve, 84 us with sixteen; fp32 87 and 126 us)
+    // with twelve, 84 us with sixteen; fp32 87 and 126 us).  The strided forms (kAny) of twelve and sixteen spill 40 to
+    // 128 bytes a thread where groups or sigmoids need registers beside the lists.
     const bool twelve = sh.E <= 384 && (sh.E % 12 == 0 || sh.E % 16 != 0);
     const int n = sh.E <= 64 ? 2 : sh.E <= 128 ? 4 : sh.E <= 256 ? 8 : twelve ? 12 : 16;
     if (sh.E <= 512 && (rc.score == 1 || by_logit)) {

@@ -232,6 +232,56 @@ ep_status_t ll_gemm(const ep_gemm_shape_t* s, int halves, const uint8_t* a, cons
     return from_cuda(launch_ll_gemm_fp8(g, stream));
 }
 
+bool gemm_shape_bf16_ok(const ep_gemm_shape_t* s) {
+    if (s == nullptr) return false;
+    const long long most = 1LL << 38, cap = s->capacity, n = s->n, k = s->k;
+    return s->num_experts >= 1 && s->num_experts <= 8192 && cap >= 0 && cap <= (1 << 24) &&
+           s->num_experts * cap < (1LL << 31) && n >= 8 && n % 8 == 0 && n <= (1 << 20) && k >= 8 && k % 8 == 0 &&
+           k <= (1 << 20) && cap * n < most && cap * k < most && n * k < most;
+}
+
+// Checks shared by the bf16 products.  Arrays along the capacity may be NULL where that is 0; a weight gradient is
+// written all the same.
+ep_status_t ll_gemm_bf16(const ep_gemm_shape_t* s, Bf16Form form, const uint16_t* rows, const uint16_t* other,
+                         const uint16_t* gate_up, const int32_t* count, void* out, uint16_t* gate_up_out, bool out_bf16,
+                         int32_t* status, cudaStream_t stream) {
+    if (!gemm_shape_bf16_ok(s)) return EP_ERR_INVALID_ARG;
+    const bool wgrad = form == Bf16Form::kWgrad;
+    const long long cap_rows = static_cast<long long>(s->num_experts) * s->capacity;
+    if (!array_ok(rows, cap_rows, 16) || !array_ok(other, wgrad ? cap_rows : 1, 16) || !aligned4(count) ||
+        !array_ok(out, wgrad ? 1 : cap_rows, 16) || (gate_up_out != nullptr && !aligned16(gate_up_out)) ||
+        (form == Bf16Form::kDswiglu && (!array_ok(gate_up, cap_rows, 16) || (gate_up == out && cap_rows > 0))) ||
+        !aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (cap_rows == 0 && !wgrad) return EP_OK;
+    return from_cuda(launch_ll_gemm_bf16(Bf16GemmArgs{form, s->num_experts, s->capacity, s->n, s->k, rows, other, gate_up,
+                                                      count, out, gate_up_out, out_bf16, status},
+                                         stream));
+}
+
+size_t swiglu_int8_workspace(const ep_gemm_shape_t* s) {
+    return static_cast<size_t>(s->num_experts) * s->capacity * s->n * sizeof(float);
+}
+
+// Checks shared by the two int8 products; `halves` is 2 when w holds a gate and an up matrix.
+ep_status_t ll_gemm_int8(const ep_gemm_shape_t* s, int halves, const int8_t* a, const float* a_scales, const int8_t* w,
+                         const float* w_scales, const int32_t* count, void* y, float* y_scales, void* workspace,
+                         size_t workspace_bytes, int32_t* status, cudaStream_t stream) {
+    if (!gemm_shape_ok(s, halves == 2 ? 16 : 8)) return EP_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(s->num_experts) * s->capacity;
+    if (!array_ok(a, rows, 16) || !array_ok(a_scales, rows, 16) || !aligned16(w) || !aligned16(w_scales) ||
+        !aligned4(count) || !array_ok(y, rows, 16) || !aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (halves == 2 && (!array_ok(y_scales, rows, 16) || !array_ok(workspace, rows, 16) ||
+                        workspace_bytes < swiglu_int8_workspace(s)))
+        return EP_ERR_INVALID_ARG;
+    if (rows == 0) return EP_OK;
+    return from_cuda(launch_ll_gemm_int8(Int8GemmArgs{s->num_experts, s->capacity, s->n, s->k, a, a_scales, w, w_scales,
+                                                      count, y, halves == 2 ? y_scales : nullptr,
+                                                      static_cast<float*>(workspace), status},
+                                         stream));
+}
+
 ep_status_t notify_common(const ep_shape_t* shape, const uint8_t* is_token_in_rank,
                           const int32_t* num_tokens_per_rank, const int32_t* num_tokens_per_rdma_rank,
                           const int32_t* num_tokens_per_expert, int32_t* rank_prefix_matrix,
@@ -858,6 +908,94 @@ ep_status_t ep_debug_ll_gemm_fp8_stall(const ep_gemm_shape_t* shape, const uint8
     const ep::Stall stall = {stall_cta, stall_tile, wait_limit_us};
     return ep::ll_gemm(shape, y_scales != nullptr ? 2 : 1, a, a_scales, w, w_scales, count, y, y_scales, status, stream,
                        &stall);
+}
+
+ep_status_t ep_ll_combine_backward(const ep_shape_t* shape, const uint16_t* grad_combined, const uint16_t* y,
+                                   int32_t expert_capacity, const int64_t* topk_idx, const float* topk_w,
+                                   const int32_t* slot_pos, uint16_t* grad_y, float* grad_topk_w, int32_t* status,
+                                   cudaStream_t stream) {
+    ep::Shape sh;
+    if (!ep::make_shape(shape, &sh) || expert_capacity < 0) return EP_ERR_INVALID_ARG;
+    const long long tokens = static_cast<long long>(sh.R) * sh.T;
+    const long long rows = static_cast<long long>(sh.E) * expert_capacity;
+    if (!ep::array_ok(grad_combined, tokens, 16) || !ep::array_ok(y, rows, 16) || !ep::array_ok(topk_idx, tokens, 8) ||
+        !ep::array_ok(topk_w, tokens, 4) || !ep::array_ok(slot_pos, tokens, 4) || !ep::array_ok(grad_y, rows, 16) ||
+        !ep::array_ok(grad_topk_w, tokens, 4) || !ep::aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (tokens == 0) return EP_OK;
+    return ep::from_cuda(ep::launch_ll_combine_backward(sh, grad_combined, y, expert_capacity, topk_idx, topk_w, slot_pos,
+                                                        grad_y, grad_topk_w, status, stream));
+}
+
+ep_status_t ep_check_gemm_shape_bf16(const ep_gemm_shape_t* shape) {
+    return ep::gemm_shape_bf16_ok(shape) ? EP_OK : EP_ERR_INVALID_ARG;
+}
+
+ep_status_t ep_ll_gemm_bf16(const ep_gemm_shape_t* shape, const uint16_t* a, const uint16_t* w, const int32_t* count,
+                            uint16_t* y, int32_t* status, cudaStream_t stream) {
+    return ep::ll_gemm_bf16(shape, ep::Bf16Form::kPlain, a, w, nullptr, count, y, nullptr, true, status, stream);
+}
+
+ep_status_t ep_ll_gemm_swiglu_bf16(const ep_gemm_shape_t* shape, const uint16_t* a, const uint16_t* w,
+                                   const int32_t* count, uint16_t* y, uint16_t* gate_up, int32_t* status,
+                                   cudaStream_t stream) {
+    return ep::ll_gemm_bf16(shape, ep::Bf16Form::kSwiglu, a, w, nullptr, count, y, gate_up, true, status, stream);
+}
+
+ep_status_t ep_ll_gemm_dgrad_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* w,
+                                  const int32_t* count, uint16_t* grad_a, int32_t* status, cudaStream_t stream) {
+    return ep::ll_gemm_bf16(shape, ep::Bf16Form::kDgrad, grad_y, w, nullptr, count, grad_a, nullptr, true, status,
+                            stream);
+}
+
+ep_status_t ep_ll_gemm_dswiglu_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* w,
+                                    const uint16_t* gate_up, const int32_t* count, uint16_t* grad_gate_up,
+                                    int32_t* status, cudaStream_t stream) {
+    return ep::ll_gemm_bf16(shape, ep::Bf16Form::kDswiglu, grad_y, w, gate_up, count, grad_gate_up, nullptr, true, status,
+                            stream);
+}
+
+ep_status_t ep_ll_gemm_wgrad_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* a,
+                                  const int32_t* count, void* grad_w, int32_t grad_w_bf16, int32_t* status,
+                                  cudaStream_t stream) {
+    if (grad_w_bf16 < 0 || grad_w_bf16 > 1) return EP_ERR_INVALID_ARG;
+    return ep::ll_gemm_bf16(shape, ep::Bf16Form::kWgrad, grad_y, a, nullptr, count, grad_w, nullptr, grad_w_bf16 != 0,
+                            status, stream);
+}
+
+ep_status_t ep_ll_dispatch_int8(const ep_shape_t* shape, const uint16_t* x, const int64_t* topk_idx,
+                                const int32_t* slot_pos, int32_t expert_capacity, int8_t* recv_x,
+                                float* recv_x_scales, int32_t* recv_src_info, int32_t* status,
+                                cudaStream_t stream) {
+    ep::Shape sh;
+    if (!ep::make_shape(shape, &sh) || expert_capacity < 0 || sh.H % 16 != 0) return EP_ERR_INVALID_ARG;
+    const long long tokens = static_cast<long long>(sh.R) * sh.T;
+    const long long rows = static_cast<long long>(sh.E) * expert_capacity;
+    if (!ep::array_ok(x, tokens, 16) || !ep::array_ok(topk_idx, tokens, 8) || !ep::array_ok(slot_pos, tokens, 4) ||
+        !ep::array_ok(recv_x, rows, 16) || !ep::array_ok(recv_x_scales, rows, 4) ||
+        (recv_src_info != nullptr && !ep::aligned8(recv_src_info)) || !ep::aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (tokens == 0 || rows == 0) return EP_OK;
+    return ep::from_cuda(ep::launch_ll_dispatch_int8(sh, x, topk_idx, slot_pos, expert_capacity, recv_x, recv_x_scales,
+                                                     recv_src_info, status, stream));
+}
+
+ep_status_t ep_ll_gemm_int8(const ep_gemm_shape_t* shape, const int8_t* a, const float* a_scales, const int8_t* w,
+                            const float* w_scales, const int32_t* count, uint16_t* y, int32_t* status,
+                            cudaStream_t stream) {
+    return ep::ll_gemm_int8(shape, 1, a, a_scales, w, w_scales, count, y, nullptr, nullptr, 0, status, stream);
+}
+
+size_t ep_ll_gemm_swiglu_int8_workspace_bytes(const ep_gemm_shape_t* shape) {
+    return ep::gemm_shape_ok(shape, 16) ? ep::swiglu_int8_workspace(shape) : 0;
+}
+
+ep_status_t ep_ll_gemm_swiglu_int8(const ep_gemm_shape_t* shape, const int8_t* a, const float* a_scales,
+                                   const int8_t* w, const float* w_scales, const int32_t* count, int8_t* y,
+                                   float* y_scales, void* workspace, size_t workspace_bytes, int32_t* status,
+                                   cudaStream_t stream) {
+    return ep::ll_gemm_int8(shape, 2, a, a_scales, w, w_scales, count, y, y_scales, workspace, workspace_bytes, status,
+                            stream);
 }
 
 ep_status_t ep_sync_status(const int32_t* status, cudaStream_t stream) {

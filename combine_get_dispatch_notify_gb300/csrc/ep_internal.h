@@ -183,4 +183,46 @@ struct GemmArgs {
 };
 cudaError_t launch_ll_gemm_fp8(const GemmArgs& g, cudaStream_t stream);
 
+// Gradient of the weighted combine (see ep_ll_combine_backward).
+cudaError_t launch_ll_combine_backward(const Shape& sh, const uint16_t* grad, const uint16_t* y, int cap,
+                                       const int64_t* topk_idx, const float* topk_w, const int32_t* slot_pos,
+                                       uint16_t* grad_y, float* grad_topk_w, int32_t* status, cudaStream_t stream);
+
+// LL dispatch with the rows cast to int8 on the way (H % 16 == 0).
+cudaError_t launch_ll_dispatch_int8(const Shape& sh, const uint16_t* x, const int64_t* topk_idx,
+                                    const int32_t* slot_pos, int cap, int8_t* recv_x, float* recv_x_scales,
+                                    int32_t* recv_src_info, int32_t* status, cudaStream_t stream);
+
+// Experts' bf16 products (see ep_ll_gemm_bf16 and its neighbours for the forms).
+enum class Bf16Form { kPlain, kSwiglu, kDgrad, kDswiglu, kWgrad };
+struct Bf16GemmArgs {
+    Bf16Form form;
+    int E, cap, n, k;
+    const uint16_t* rows;   // a; the gradients: grad_y
+    const uint16_t* other;  // w; kWgrad: a
+    const uint16_t* gate_up;
+    const int32_t* count;
+    void* out;          // y, grad_a, grad_gate_up or grad_w
+    uint16_t* gate_up_out;  // kSwiglu, may be NULL
+    bool out_bf16;      // kWgrad
+    int32_t* status;
+};
+cudaError_t launch_ll_gemm_bf16(const Bf16GemmArgs& g, cudaStream_t stream);
+
+// Experts' int8 products.  y_scales == NULL: y is bf16 [E][cap][n]; else w holds
+// the gate and the up matrix, h is fp32 [E][cap][n] scratch and y int8.
+struct Int8GemmArgs {
+    int E, cap, n, k;
+    const int8_t* a;
+    const float* a_scales;
+    const int8_t* w;
+    const float* w_scales;
+    const int32_t* count;
+    void* y;
+    float* y_scales;
+    float* h;
+    int32_t* status;
+};
+cudaError_t launch_ll_gemm_int8(const Int8GemmArgs& g, cudaStream_t stream);
+
 }  // namespace ep

@@ -117,6 +117,17 @@ _SIGS = {
     "ep_ll_gemm_fp8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 7 + [_vp]),
     "ep_ll_gemm_swiglu_fp8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_vp]),
     "ep_debug_ll_gemm_fp8_stall": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_i32] * 3 + [_vp]),
+    "ep_ll_combine_backward": (_i32, [ctypes.POINTER(EpShape), _vp, _vp, _i32] + [_vp] * 6 + [_vp]),
+    "ep_check_gemm_shape_bf16": (_i32, [ctypes.POINTER(EpGemmShape)]),
+    "ep_ll_gemm_bf16": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 5 + [_vp]),
+    "ep_ll_gemm_swiglu_bf16": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 6 + [_vp]),
+    "ep_ll_gemm_dgrad_bf16": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 5 + [_vp]),
+    "ep_ll_gemm_dswiglu_bf16": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 6 + [_vp]),
+    "ep_ll_gemm_wgrad_bf16": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 4 + [_i32, _vp, _vp]),
+    "ep_ll_dispatch_int8": (_i32, [ctypes.POINTER(EpShape), _vp, _vp, _vp, _i32] + [_vp] * 4 + [_vp]),
+    "ep_ll_gemm_int8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 7 + [_vp]),
+    "ep_ll_gemm_swiglu_int8_workspace_bytes": (_sz, [ctypes.POINTER(EpGemmShape)]),
+    "ep_ll_gemm_swiglu_int8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_sz, _vp, _vp]),
     "ep_sync_status": (_i32, [_vp, _vp]),
     "ep_debug_notify_dispatch_stall": (_i32, [ctypes.POINTER(EpShape)] + [_vp] * 16 +
                                        [_sz, _vp, _i32, _i32, _vp]),
@@ -654,6 +665,153 @@ def ep_debug_ll_gemm_fp8_stall(a, a_scales, w, w_scales, count, y, y_scales, sta
     _check("ep_debug_ll_gemm_fp8_stall", rc)
 
 
+def _here(status, *tensors) -> None:
+    """Refuses tensors of another device than the current one, whose stream the call runs on."""
+    device = torch.cuda.current_device()
+    for t in (status, *tensors):
+        if t is not None and t.is_cuda and t.get_device() != device:
+            raise ValueError(f"tensors must be on the current device (cuda:{device}), got {t.device}")
+
+
+def ep_ll_combine_backward(shape: EpShape, grad_combined, y, expert_capacity: int, topk_idx, topk_w, slot_pos, grad_y,
+                           grad_topk_w, status, stream=None) -> None:
+    """Gradient of :func:`ep_ll_combine`: ``grad_combined`` [R, T, H] bf16 and the expert outputs
+    ``y`` -> ``grad_y`` [E, capacity, H] bf16 (rows without a slot are left as they are) and
+    ``grad_topk_w`` [R, T, K] fp32 (every element written)."""
+    R, T, K, E, H = shape.num_ranks, shape.num_tokens, shape.num_topk, shape.num_experts, shape.hidden
+    cap = expert_capacity
+    args = (_t(grad_combined, torch.bfloat16, (R, T, H), "grad_combined"), _t(y, torch.bfloat16, (E, cap, H), "y"),
+            _i32(cap), _t(topk_idx, torch.int64, (R, T, K), "topk_idx"), _t(topk_w, torch.float32, (R, T, K), "topk_w"),
+            _t(slot_pos, torch.int32, (R, T, K), "slot_pos"), _t(grad_y, torch.bfloat16, (E, cap, H), "grad_y"),
+            _t(grad_topk_w, torch.float32, (R, T, K), "grad_topk_w"), _t(status, torch.int32, (1,), "status"))
+    _here(status, grad_combined, y, topk_idx, topk_w, slot_pos, grad_y, grad_topk_w)
+    _check("ep_ll_combine_backward", lib().ep_ll_combine_backward(ctypes.byref(shape), *args, _stream(stream)))
+
+
+def ep_check_gemm_shape_bf16(shape: EpGemmShape) -> int:
+    return lib().ep_check_gemm_shape_bf16(ctypes.byref(shape))
+
+
+def ep_ll_gemm_bf16(a, w, count, y, status, stream=None) -> None:
+    """Experts' product in bf16: ``a`` [E, capacity, k] and ``w`` [E, n, k] with ``count`` [E]
+    rows per expert -> ``y`` [E, capacity, n]."""
+    E, cap, n, k = _gemm_dims(a, w, 3)
+    bf16 = torch.bfloat16
+    args = (_t(a, bf16, (E, cap, k), "a"), _t(w, bf16, (E, n, k), "w"), _t(count, torch.int32, (E,), "count"),
+            _t(y, bf16, (E, cap, n), "y"), _t(status, torch.int32, (1,), "status"))
+    _here(status, a, w, count, y)
+    _check("ep_ll_gemm_bf16", lib().ep_ll_gemm_bf16(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def ep_ll_gemm_swiglu_bf16(a, w, count, y, gate_up, status, stream=None) -> None:
+    """Gate and up products and silu(gate) * up in one launch: ``w`` [E, 2, n, k] (gate, up) ->
+    ``y`` [E, capacity, n] bf16, and where ``gate_up`` [E, capacity, 2, n] is given (not None)
+    both products, which the gradient starts from."""
+    E, cap, n, k = _gemm_dims(a, w, 4)
+    bf16 = torch.bfloat16
+    args = (_t(a, bf16, (E, cap, k), "a"), _t(w, bf16, (E, 2, n, k), "w"), _t(count, torch.int32, (E,), "count"),
+            _t(y, bf16, (E, cap, n), "y"), _t(gate_up, bf16, (E, cap, 2, n), "gate_up", nullable=True),
+            _t(status, torch.int32, (1,), "status"))
+    _here(status, a, w, count, y, gate_up)
+    _check("ep_ll_gemm_swiglu_bf16",
+           lib().ep_ll_gemm_swiglu_bf16(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def _grad_dims(grad_y, w):
+    for t, name in ((grad_y, "grad_y"), (w, "w")):
+        if t is None or t.dim() != 3:
+            raise ValueError(f"{name} must have 3 dimensions")
+    return grad_y.shape[0], grad_y.shape[1], grad_y.shape[2], w.shape[2]
+
+
+def ep_ll_gemm_dgrad_bf16(grad_y, w, count, grad_a, status, stream=None) -> None:
+    """Gradient of a product's rows: ``grad_y`` [E, capacity, n] and ``w`` [E, n, k] ->
+    ``grad_a`` [E, capacity, k] (the gated product's: ``grad_gate_up`` and ``w`` viewed with 2 n)."""
+    E, cap, n, k = _grad_dims(grad_y, w)
+    bf16 = torch.bfloat16
+    args = (_t(grad_y, bf16, (E, cap, n), "grad_y"), _t(w, bf16, (E, n, k), "w"), _t(count, torch.int32, (E,), "count"),
+            _t(grad_a, bf16, (E, cap, k), "grad_a"), _t(status, torch.int32, (1,), "status"))
+    _here(status, grad_y, w, count, grad_a)
+    _check("ep_ll_gemm_dgrad_bf16",
+           lib().ep_ll_gemm_dgrad_bf16(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def ep_ll_gemm_dswiglu_bf16(grad_y, w, gate_up, count, grad_gate_up, status, stream=None) -> None:
+    """Gradient of the last product's rows carried through the gated activation: ``grad_y``
+    [E, capacity, n], ``w`` [E, n, k] and the kept ``gate_up`` [E, capacity, 2, k] ->
+    ``grad_gate_up`` [E, capacity, 2, k]."""
+    E, cap, n, k = _grad_dims(grad_y, w)
+    bf16 = torch.bfloat16
+    args = (_t(grad_y, bf16, (E, cap, n), "grad_y"), _t(w, bf16, (E, n, k), "w"),
+            _t(gate_up, bf16, (E, cap, 2, k), "gate_up"), _t(count, torch.int32, (E,), "count"),
+            _t(grad_gate_up, bf16, (E, cap, 2, k), "grad_gate_up"), _t(status, torch.int32, (1,), "status"))
+    _here(status, grad_y, w, gate_up, count, grad_gate_up)
+    _check("ep_ll_gemm_dswiglu_bf16",
+           lib().ep_ll_gemm_dswiglu_bf16(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def ep_ll_gemm_wgrad_bf16(grad_y, a, count, grad_w, status, stream=None) -> None:
+    """Gradient of a product's weights: ``grad_y`` [E, capacity, n] and ``a`` [E, capacity, k] ->
+    ``grad_w`` [E, n, k], fp32 or bf16, every element written."""
+    E, cap, n, k = _grad_dims(grad_y, a)
+    if grad_w is not None and grad_w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"grad_w must be torch.float32 or torch.bfloat16, got {grad_w.dtype}")
+    gt = torch.float32 if grad_w is None else grad_w.dtype
+    args = (_t(grad_y, torch.bfloat16, (E, cap, n), "grad_y"), _t(a, torch.bfloat16, (E, cap, k), "a"),
+            _t(count, torch.int32, (E,), "count"), _t(grad_w, gt, (E, n, k), "grad_w"), _i32(int(gt == torch.bfloat16)),
+            _t(status, torch.int32, (1,), "status"))
+    _here(status, grad_y, a, count, grad_w)
+    _check("ep_ll_gemm_wgrad_bf16",
+           lib().ep_ll_gemm_wgrad_bf16(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def ep_ll_dispatch_int8(shape: EpShape, x, topk_idx, slot_pos, expert_capacity: int, recv_x, recv_x_scales,
+                        recv_src_info, status, stream=None) -> None:
+    """:func:`ep_ll_dispatch` with the rows cast to int8, one fp32 scale per row ([E, capacity])."""
+    R, T, K, E, H = shape.num_ranks, shape.num_tokens, shape.num_topk, shape.num_experts, shape.hidden
+    cap = expert_capacity
+    args = (_t(x, torch.bfloat16, (R, T, H), "x"), _t(topk_idx, torch.int64, (R, T, K), "topk_idx"),
+            _t(slot_pos, torch.int32, (R, T, K), "slot_pos"), _i32(cap), _t(recv_x, torch.int8, (E, cap, H), "recv_x"),
+            _t(recv_x_scales, torch.float32, (E, cap), "recv_x_scales"),
+            _t(recv_src_info, torch.int32, (E, cap, 2), "recv_src_info", nullable=True),
+            _t(status, torch.int32, (1,), "status"))
+    _here(status, x, topk_idx, slot_pos, recv_x, recv_x_scales, recv_src_info)
+    _check("ep_ll_dispatch_int8", lib().ep_ll_dispatch_int8(ctypes.byref(shape), *args, _stream(stream)))
+
+
+def ep_ll_gemm_int8(a, a_scales, w, w_scales, count, y, status, stream=None) -> None:
+    """Experts' product in int8: ``a`` [E, capacity, k] with a scale per row ([E, capacity]), ``w``
+    [E, n, k] with a scale per output column ([E, n]), ``count`` [E] -> ``y`` [E, capacity, n] bf16."""
+    E, cap, n, k = _gemm_dims(a, w, 3)
+    args = (_t(a, torch.int8, (E, cap, k), "a"), _t(a_scales, torch.float32, (E, cap), "a_scales"),
+            _t(w, torch.int8, (E, n, k), "w"), _t(w_scales, torch.float32, (E, n), "w_scales"),
+            _t(count, torch.int32, (E,), "count"), _t(y, torch.bfloat16, (E, cap, n), "y"),
+            _t(status, torch.int32, (1,), "status"))
+    _here(status, a, a_scales, w, w_scales, count, y)
+    _check("ep_ll_gemm_int8", lib().ep_ll_gemm_int8(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def ep_ll_gemm_swiglu_int8_workspace_bytes(shape: EpGemmShape) -> int:
+    return int(lib().ep_ll_gemm_swiglu_int8_workspace_bytes(ctypes.byref(shape)))
+
+
+def ep_ll_gemm_swiglu_int8(a, a_scales, w, w_scales, count, y, y_scales, workspace, status, stream=None) -> None:
+    """Gate and up products in int8, silu(gate) * up and its cast by rows: ``w`` [E, 2, n, k] with
+    ``w_scales`` [E, 2, n] -> ``y`` [E, capacity, n] int8, ``y_scales`` [E, capacity]; ``workspace``
+    of :func:`ep_ll_gemm_swiglu_int8_workspace_bytes` bytes."""
+    E, cap, n, k = _gemm_dims(a, w, 4)
+    shape = EpGemmShape(E, cap, n, k)
+    args = (_t(a, torch.int8, (E, cap, k), "a"), _t(a_scales, torch.float32, (E, cap), "a_scales"),
+            _t(w, torch.int8, (E, 2, n, k), "w"), _t(w_scales, torch.float32, (E, 2, n), "w_scales"),
+            _t(count, torch.int32, (E,), "count"), _t(y, torch.int8, (E, cap, n), "y"),
+            _t(y_scales, torch.float32, (E, cap), "y_scales"))
+    ws, nws = _workspace(workspace, ep_ll_gemm_swiglu_int8_workspace_bytes(shape))
+    _here(status, a, a_scales, w, w_scales, count, y, y_scales, workspace)
+    _check("ep_ll_gemm_swiglu_int8",
+           lib().ep_ll_gemm_swiglu_int8(ctypes.byref(shape), *args, ws, nws, _t(status, torch.int32, (1,), "status"),
+                                        _stream(stream)))
+
+
 def ep_sync_status(status, stream=None) -> int:
     """Wait for the stream and return the status code the device word maps to."""
     return int(lib().ep_sync_status(_t(status, torch.int32, (1,), "status"), _stream(stream)))
@@ -752,14 +910,102 @@ def cast_weight_blocks(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     return q.view(torch.uint8).flatten(-4, -3).flatten(-2)[..., :n, :k].contiguous(), scales
 
 
+def cast_weight_channels(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Weights [..., n, k] as the experts' int8 products take them: int8 and one fp32 scale per
+    output column ([..., n]), the row's largest magnitude by 1 / 127.  Plain torch, for use once
+    when weights are loaded."""
+    w = w.float()
+    scales = (w.abs().amax(-1).clamp(min=2.0 ** -100) * (1.0 / 127.0)).contiguous()
+    return torch.round(w / scales.unsqueeze(-1)).to(torch.int8).contiguous(), scales
+
+
+def _route_and_place(layer, logits, bias, stream) -> None:
+    """Router and low-latency layout of a layer: fills its topk_idx, topk_w, slot_pos,
+    layout_range and count."""
+    sh = layer.shape
+    ep_route(sh, layer.route, logits, bias, layer.topk_idx, layer.topk_w, layer.status, stream)
+    counts = None
+    if layer.layout is not None:
+        L = layer.layout
+        ep_get_dispatch_layout(sh, layer.topk_idx, L["num_tokens_per_rank"], L["num_tokens_per_rdma_rank"],
+                               L["num_tokens_per_expert"], L["is_token_in_rank"], layer.status, stream)
+        counts = L["num_tokens_per_expert"]
+    ep_ll_layout(sh, layer.topk_idx, counts, layer.expert_capacity, layer.slot_pos, layer.layout_range, layer.count,
+                 layer.status, stream)
+
+
 @dataclass
 class MoELayer:
     """A mixture-of-experts layer on the low-latency layout: router, layout, casting
-    dispatch, gated e4m3 experts, weighted combine.  Owns every buffer; :meth:`run`
+    dispatch, gated e4m3 or int8 experts, weighted combine.  Owns every buffer; :meth:`run`
     launches the calls on the current stream without synchronising.
 
     ``ffn`` is the experts' inner size; ``expert_capacity`` bounds the rows of an expert
-    (slots beyond it are dropped and reported as EP_ERR_CAPACITY)."""
+    (slots beyond it are dropped and reported as EP_ERR_CAPACITY).  ``weights`` is "fp8" (e4m3
+    with 128 x 128 block scales) or "int8" (a scale for each token and output column)."""
+
+    shape: EpShape
+    route: EpRoute
+    ffn: int
+    expert_capacity: int
+    device: str = "cuda"
+    weights: str = "fp8"
+
+    def __post_init__(self):
+        if self.weights not in ("fp8", "int8"):
+            raise ValueError(f"weights must be 'fp8' or 'int8', got {self.weights!r}")
+        sh, cap, F, dev = self.shape, self.expert_capacity, self.ffn, self.device
+        R, T, K, E, H = sh.num_ranks, sh.num_tokens, sh.num_topk, sh.num_experts, sh.hidden
+        z = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.topk_idx, self.topk_w = z(R, T, K, dt=torch.int64), z(R, T, K, dt=torch.float32)
+        # the layout counts for itself where one cluster of R CTAs can; else the counts come from the layout step
+        self.layout = None if R <= 16 and R * E <= 16384 else alloc_layout(sh, dev)
+        self.slot_pos, self.layout_range, self.count = z(R, T, K), z(E, R, 2), z(E)
+        if self.weights == "int8":
+            self.rows, self.row_scales = z(E, cap, H, dt=torch.int8), z(E, cap, dt=torch.float32)
+            self.inner, self.inner_scales = z(E, cap, F, dt=torch.int8), z(E, cap, dt=torch.float32)
+            self.workspace = z(ep_ll_gemm_swiglu_int8_workspace_bytes(EpGemmShape(E, cap, F, H)), dt=torch.uint8)
+        else:
+            self.rows = z(E, cap, H, dt=torch.uint8)
+            self.row_scales = z(E, cap, scale_blocks(H), dt=torch.float32)
+            self.inner = z(E, cap, F, dt=torch.uint8)
+            self.inner_scales = z(E, cap, scale_blocks(F), dt=torch.float32)
+        self.y = z(E, cap, H, dt=torch.bfloat16)
+        self.combined_x = z(R, T, H, dt=torch.bfloat16)
+
+    def run(self, x, logits, bias, w13, w13_scales, w2, w2_scales, stream=None):
+        """``x`` [R, T, H] bf16 and router ``logits`` [R, T, E] -> combined_x [R, T, H] bf16.
+        Weights as :func:`cast_weight_blocks` (int8: :func:`cast_weight_channels`) makes them:
+        ``w13`` [E, 2, ffn, H] (gate, up) and ``w2`` [E, H, ffn]; ``bias`` [E] of the selection, or None."""
+        sh, cap = self.shape, self.expert_capacity
+        _route_and_place(self, logits, bias, stream)
+        if self.weights == "int8":
+            ep_ll_dispatch_int8(sh, x, self.topk_idx, self.slot_pos, cap, self.rows, self.row_scales, None, self.status,
+                                stream)
+            ep_ll_gemm_swiglu_int8(self.rows, self.row_scales, w13, w13_scales, self.count, self.inner,
+                                   self.inner_scales, self.workspace, self.status, stream)
+            ep_ll_gemm_int8(self.inner, self.inner_scales, w2, w2_scales, self.count, self.y, self.status, stream)
+        else:
+            ep_ll_dispatch_fp8(sh, x, self.topk_idx, self.slot_pos, cap, self.rows, self.row_scales, None, self.status,
+                               stream)
+            ep_ll_gemm_swiglu_fp8(self.rows, self.row_scales, w13, w13_scales, self.count, self.inner,
+                                  self.inner_scales, self.status, stream)
+            ep_ll_gemm_fp8(self.inner, self.inner_scales, w2, w2_scales, self.count, self.y, self.status, stream)
+        ep_ll_combine(sh, self.y, cap, self.topk_idx, self.topk_w, self.slot_pos, self.combined_x, self.status, stream)
+        return self.combined_x
+
+
+@dataclass
+class MoETrainLayer:
+    """A mixture-of-experts layer that trains, on the low-latency layout in bf16: router, layout,
+    dispatch, gated experts, weighted combine, and in :meth:`backward` all of their gradients.
+    Owns every buffer; both methods launch their calls on the current stream without
+    synchronising, and either can be captured in a CUDA graph.
+
+    ``ffn`` is the experts' inner size; ``expert_capacity`` bounds the rows of an expert
+    (slots beyond it are dropped and reported as EP_ERR_CAPACITY; they have no gradient).
+    :meth:`backward` reads what the last :meth:`run` left in the buffers."""
 
     shape: EpShape
     route: EpRoute
@@ -770,36 +1016,46 @@ class MoELayer:
     def __post_init__(self):
         sh, cap, F, dev = self.shape, self.expert_capacity, self.ffn, self.device
         R, T, K, E, H = sh.num_ranks, sh.num_tokens, sh.num_topk, sh.num_experts, sh.hidden
-        z = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+        z = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        # dispatch's unit counter: zeroed once here, every call leaves it zero
+        self.sched = torch.zeros(1, dtype=torch.int64, device=dev)
         self.topk_idx, self.topk_w = z(R, T, K, dt=torch.int64), z(R, T, K, dt=torch.float32)
         # the layout counts for itself where one cluster of R CTAs can; else the counts come from the layout step
         self.layout = None if R <= 16 and R * E <= 16384 else alloc_layout(sh, dev)
-        self.slot_pos, self.layout_range, self.count = z(R, T, K), z(E, R, 2), z(E)
-        self.rows = z(E, cap, H, dt=torch.uint8)
-        self.row_scales = z(E, cap, scale_blocks(H), dt=torch.float32)
-        self.inner = z(E, cap, F, dt=torch.uint8)
-        self.inner_scales = z(E, cap, scale_blocks(F), dt=torch.float32)
-        self.y = z(E, cap, H, dt=torch.bfloat16)
-        self.combined_x = z(R, T, H, dt=torch.bfloat16)
+        self.slot_pos, self.layout_range = z(R, T, K, dt=torch.int32), z(E, R, 2, dt=torch.int32)
+        self.count = z(E, dt=torch.int32)
+        self.rows, self.gate_up, self.inner = z(E, cap, H), z(E, cap, 2, F), z(E, cap, F)
+        self.y, self.combined_x = z(E, cap, H), z(R, T, H)
+        self.grad_y, self.grad_topk_w = z(E, cap, H), z(R, T, K, dt=torch.float32)
+        self.grad_gate_up, self.grad_rows, self.grad_x = z(E, cap, 2, F), z(E, cap, H), z(R, T, H)
+        self.ones = torch.ones(R, T, K, device=dev)  # the dispatch's gradient is a combine with these weights
 
-    def run(self, x, logits, bias, w13, w13_scales, w2, w2_scales, stream=None):
-        """``x`` [R, T, H] bf16 and router ``logits`` [R, T, E] -> combined_x [R, T, H] bf16.
-        Weights as :func:`cast_weight_blocks` makes them: ``w13`` [E, 2, ffn, H] (gate, up) and
-        ``w2`` [E, H, ffn]; ``bias`` [E] of the selection, or None."""
+    def run(self, x, logits, bias, w13, w2, stream=None):
+        """``x`` [R, T, H] bf16 and router ``logits`` [R, T, E] -> combined_x [R, T, H] bf16, with
+        ``w13`` [E, 2, ffn, H] (gate, up) and ``w2`` [E, H, ffn] bf16; ``bias`` [E] of the
+        selection, or None."""
         sh, cap = self.shape, self.expert_capacity
-        ep_route(sh, self.route, logits, bias, self.topk_idx, self.topk_w, self.status, stream)
-        counts = None
-        if self.layout is not None:
-            L = self.layout
-            ep_get_dispatch_layout(sh, self.topk_idx, L["num_tokens_per_rank"], L["num_tokens_per_rdma_rank"],
-                                   L["num_tokens_per_expert"], L["is_token_in_rank"], self.status, stream)
-            counts = L["num_tokens_per_expert"]
-        ep_ll_layout(sh, self.topk_idx, counts, cap, self.slot_pos, self.layout_range, self.count, self.status, stream)
-        ep_ll_dispatch_fp8(sh, x, self.topk_idx, self.slot_pos, cap, self.rows, self.row_scales, None, self.status,
-                           stream)
-        ep_ll_gemm_swiglu_fp8(self.rows, self.row_scales, w13, w13_scales, self.count, self.inner, self.inner_scales,
-                              self.status, stream)
-        ep_ll_gemm_fp8(self.inner, self.inner_scales, w2, w2_scales, self.count, self.y, self.status, stream)
+        _route_and_place(self, logits, bias, stream)
+        ep_ll_dispatch(sh, x, self.topk_idx, self.slot_pos, cap, self.rows, None, self.status, stream, self.sched)
+        ep_ll_gemm_swiglu_bf16(self.rows, w13, self.count, self.inner, self.gate_up, self.status, stream)
+        ep_ll_gemm_bf16(self.inner, w2, self.count, self.y, self.status, stream)
         ep_ll_combine(sh, self.y, cap, self.topk_idx, self.topk_w, self.slot_pos, self.combined_x, self.status, stream)
         return self.combined_x
+
+    def backward(self, grad_out, logits, w13, w2, grad_logits, grad_w13, grad_w2, stream=None):
+        """``grad_out`` [R, T, H] bf16, and the last run's ``logits`` and weights -> grad_x
+        [R, T, H] bf16; writes ``grad_logits`` (the logits' type), ``grad_w13`` and ``grad_w2``
+        (fp32 or bf16, the weights' shapes), every element of them."""
+        sh, cap, F = self.shape, self.expert_capacity, self.ffn
+        E, H = sh.num_experts, sh.hidden
+        ep_ll_combine_backward(sh, grad_out, self.y, cap, self.topk_idx, self.topk_w, self.slot_pos, self.grad_y,
+                               self.grad_topk_w, self.status, stream)
+        ep_route_backward(sh, self.route, logits, self.topk_idx, self.grad_topk_w, grad_logits, self.status, stream)
+        ep_ll_gemm_dswiglu_bf16(self.grad_y, w2, self.gate_up, self.count, self.grad_gate_up, self.status, stream)
+        flat = self.grad_gate_up.view(E, cap, 2 * F)
+        ep_ll_gemm_dgrad_bf16(flat, w13.view(E, 2 * F, H), self.count, self.grad_rows, self.status, stream)
+        ep_ll_combine(sh, self.grad_rows, cap, self.topk_idx, self.ones, self.slot_pos, self.grad_x, self.status, stream)
+        ep_ll_gemm_wgrad_bf16(flat, self.rows, self.count, grad_w13.view(E, 2 * F, H), self.status, stream)
+        ep_ll_gemm_wgrad_bf16(self.grad_y, self.inner, self.count, grad_w2, self.status, stream)
+        return self.grad_x

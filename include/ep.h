@@ -18,6 +18,15 @@
  *   ep_ll_dispatch_fp8            rows cast to e4m3 as they are packed
  *   ep_ll_gemm_swiglu_fp8,        the experts' block-scaled products, with the
  *   ep_ll_gemm_fp8                gated activation and without
+ *   ep_ll_gemm_swiglu_bf16,       the experts' products in bf16, and what their
+ *   ep_ll_gemm_bf16,              gradients need: the products with the
+ *   ep_ll_gemm_dgrad_bf16,        transposed weights (with the gated
+ *   ep_ll_gemm_dswiglu_bf16,      activation's gradient and without) and the
+ *   ep_ll_gemm_wgrad_bf16         weights' gradients
+ *   ep_ll_combine_backward        gradient of the weighted combine
+ *   ep_ll_dispatch_int8,          rows cast to int8 as they are packed, and the
+ *   ep_ll_gemm_swiglu_int8,       experts' int8 products with a scale for each
+ *   ep_ll_gemm_int8               row and each output column
  *
  * Pages the operations come from (cited by title and section):
  *   [IN] "notify_dispatch (internode.cu)" notes on DeepEP: sm0 stages 3-6 and
@@ -641,6 +650,158 @@ ep_status_t ep_ll_gemm_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const
 ep_status_t ep_ll_gemm_swiglu_fp8(const ep_gemm_shape_t* shape, const uint8_t* a, const float* a_scales,
                                   const uint8_t* w, const float* w_scales, const int32_t* count, uint8_t* y,
                                   float* y_scales, int32_t* status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gradient of ep_ll_combine, combined_x[t] = sum_k topk_w[t][k] *
+ * y[row of slot (t, k)], with g = grad_combined:
+ *   grad_y[row of (t, k)] = bf16(topk_w[t][k] * g[t])
+ *   grad_topk_w[t][k]     = sum_h g[t][h] * y[row of (t, k)][h]   (fp32)
+ * so a slot is read once, used for both and written once.  (The dispatch's
+ * own gradient is ep_ll_combine with weights of 1.)
+ *   grad_combined    in  bf16 bits [R][T][H]
+ *   y                in  bf16 bits [E][expert_capacity][H]  as ep_ll_combine read it
+ *   topk_idx, topk_w, slot_pos  as for ep_ll_combine
+ *   grad_y           out bf16 bits [E][expert_capacity][H]; rows without a slot are left as they are
+ *   grad_topk_w      out fp32 [R][T][K], every element written (0 for a slot without a row)
+ * A slot with an id or position past its range sets EP_DEV_INCONSISTENT and
+ * counts as one without a row.  Slots hold rows of their own (ep_ll_layout's do).
+ */
+ep_status_t ep_ll_combine_backward(const ep_shape_t* shape, const uint16_t* grad_combined, const uint16_t* y,
+                                   int32_t expert_capacity, const int64_t* topk_idx, const float* topk_w,
+                                   const int32_t* slot_pos, uint16_t* grad_y, float* grad_topk_w, int32_t* status,
+                                   cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Experts' products in bf16 on the per-expert packed layout, and their
+ * gradients: a gated feed-forward block that can be trained.  Sums are fp32 and
+ * each output element is rounded once.  Only rows m < min(count[e], capacity)
+ * are read and written; other output rows are left as they are, whatever the
+ * buffers hold there.  An expert without rows costs nothing but its weight
+ * gradient, which is 0.
+ *
+ * Shapes are ep_gemm_shape_t with n and k multiples of 8, from 8 to 2^20,
+ * num_experts * capacity below 2^31, and capacity * n, capacity * k and n * k
+ * below 2^38.  A device wait that runs out sets EP_DEV_TIMEOUT (the outputs are
+ * then unspecified).
+ */
+
+/* EP_OK when `shape` obeys the rules above, else EP_ERR_INVALID_ARG. */
+ep_status_t ep_check_gemm_shape_bf16(const ep_gemm_shape_t* shape);
+
+/* ep_ll_gemm_bf16: y[m][j] = sum_k a[m][k] w[j][k], the product that ends a block.
+ *   a      in  bf16 bits [num_experts][capacity][k]
+ *   w      in  bf16 bits [num_experts][n][k]
+ *   count  in  int32 [num_experts]  rows of each expert (ep_ll_layout's count)
+ *   y      out bf16 bits [num_experts][capacity][n]
+ */
+ep_status_t ep_ll_gemm_bf16(const ep_gemm_shape_t* shape, const uint16_t* a, const uint16_t* w, const int32_t* count,
+                            uint16_t* y, int32_t* status, cudaStream_t stream);
+
+/* ep_ll_gemm_swiglu_bf16: the two products that begin a block and their
+ * activation, gate and up = a w^T for the two halves of w:
+ *   y = gate / (1 + exp(-gate)) * up     (gate and up unrounded)
+ *   w        in  bf16 bits [num_experts][2][n][k]  (gate matrix, up matrix)
+ *   y        out bf16 bits [num_experts][capacity][n]
+ *   gate_up  out bf16 bits [num_experts][capacity][2][n]  gate and up, which the
+ *                gradient starts from; NULL where none is wanted
+ */
+ep_status_t ep_ll_gemm_swiglu_bf16(const ep_gemm_shape_t* shape, const uint16_t* a, const uint16_t* w,
+                                   const int32_t* count, uint16_t* y, uint16_t* gate_up, int32_t* status,
+                                   cudaStream_t stream);
+
+/* ep_ll_gemm_dgrad_bf16: gradient of a product's rows,
+ *   grad_a[m][k] = sum_j grad_y[m][j] w[j][k]
+ * (for the gated product's rows: grad_y = grad_gate_up and w, both of 2 n).
+ *   grad_y  in  bf16 bits [num_experts][capacity][n]
+ *   w       in  bf16 bits [num_experts][n][k]
+ *   grad_a  out bf16 bits [num_experts][capacity][k]
+ */
+ep_status_t ep_ll_gemm_dgrad_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* w,
+                                  const int32_t* count, uint16_t* grad_a, int32_t* status, cudaStream_t stream);
+
+/* ep_ll_gemm_dswiglu_bf16: gradient of the last product's rows carried through
+ * the activation, gh = grad_y w as above and s = 1 / (1 + exp(-gate)):
+ *   grad_gate = gh * up * s * (1 + gate * (1 - s)),  grad_up = gh * gate * s
+ *   grad_y        in  bf16 bits [num_experts][capacity][n]
+ *   w             in  bf16 bits [num_experts][n][k]  (the block's last matrix)
+ *   gate_up       in  bf16 bits [num_experts][capacity][2][k]  of ep_ll_gemm_swiglu_bf16
+ *   grad_gate_up  out bf16 bits [num_experts][capacity][2][k]; may not be gate_up
+ */
+ep_status_t ep_ll_gemm_dswiglu_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* w,
+                                    const uint16_t* gate_up, const int32_t* count, uint16_t* grad_gate_up,
+                                    int32_t* status, cudaStream_t stream);
+
+/* ep_ll_gemm_wgrad_bf16: gradient of a product's weights,
+ *   grad_w[j][k] = sum_{m < count} grad_y[m][j] a[m][k]
+ *   grad_y       in  bf16 bits [num_experts][capacity][n]
+ *   a            in  bf16 bits [num_experts][capacity][k]
+ *   grad_w       out [num_experts][n][k] fp32, or bf16 bits when grad_w_bf16 is 1;
+ *                    every element written (0 for an expert without rows)
+ *   grad_w_bf16  0 or 1
+ */
+ep_status_t ep_ll_gemm_wgrad_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* a,
+                                  const int32_t* count, void* grad_w, int32_t grad_w_bf16, int32_t* status,
+                                  cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Low-latency dispatch that casts to int8: ep_ll_dispatch with every row cast
+ * on the way, one fp32 scale for each row.  For a token with largest magnitude m:
+ *   scale = max(m, 2^-100) * r,  q = round(x / scale)   (ties to even)
+ * (r the fp32 number next to 1 / 127, fp32 division; the floor keeps the scale of a zero row a normal number).  A
+ * row that holds an infinity gets an infinite scale and one that holds a NaN
+ * the scale NaN, with zeros for elements: int8 has no value for either, and
+ * so the row reads back as NaN and not as a wrong number.
+ *   x              in  bf16 bits [R][T][H], H % 16 == 0
+ *   topk_idx       in  int64 [R][T][K]
+ *   slot_pos       in  int32 [R][T][K]  from ep_ll_layout
+ *   recv_x         out int8 [E][expert_capacity][H]
+ *   recv_x_scales  out fp32 [E][expert_capacity]
+ *   recv_src_info  out int32 [E][expert_capacity][2] (source rank, token), or NULL
+ * A slot whose id is outside [0, E) or whose position is outside [0,
+ * expert_capacity) is skipped; rows not written are left as they are.
+ */
+ep_status_t ep_ll_dispatch_int8(const ep_shape_t* shape, const uint16_t* x, const int64_t* topk_idx,
+                                const int32_t* slot_pos, int32_t expert_capacity, int8_t* recv_x,
+                                float* recv_x_scales, int32_t* recv_src_info, int32_t* status,
+                                cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Experts' products in int8 with a scale for each row and each output column:
+ *   p[e][m][j] = a_scales[e][m] * w_scales[e][j] * sum_k a[e][m][k] * w[e][j][k]
+ * The sum is held in fp32, which is exact while it stays within 2^24 (so for k
+ * <= 1024 always), and rounds like any fp32 sum beyond.  Rows behind an
+ * expert's count and experts without rows as for ep_ll_gemm_fp8; shapes obey
+ * ep_check_gemm_shape.
+ *
+ * ep_ll_gemm_int8: y = bf16(p)
+ *   a         in  int8 [num_experts][capacity][k]
+ *   a_scales  in  fp32 [num_experts][capacity]
+ *   w         in  int8 [num_experts][n][k]
+ *   w_scales  in  fp32 [num_experts][n]
+ *   count     in  int32 [num_experts]
+ *   y         out bf16 bits [num_experts][capacity][n]
+ */
+ep_status_t ep_ll_gemm_int8(const ep_gemm_shape_t* shape, const int8_t* a, const float* a_scales, const int8_t* w,
+                            const float* w_scales, const int32_t* count, uint16_t* y, int32_t* status,
+                            cudaStream_t stream);
+
+/* Bytes that ep_ll_gemm_swiglu_int8 wants as workspace (0 for an invalid shape): the activations in fp32, since a
+ * row's scale is known once all of its columns are. */
+size_t ep_ll_gemm_swiglu_int8_workspace_bytes(const ep_gemm_shape_t* shape);
+
+/* ep_ll_gemm_swiglu_int8: gate and up, the activation and its cast (n % 16 == 0):
+ *   h = gate / (1 + exp(-gate)) * up;  y, y_scales = h cast by rows as in ep_ll_dispatch_int8
+ *   w          in  int8 [num_experts][2][n][k]  (gate matrix, up matrix)
+ *   w_scales   in  fp32 [num_experts][2][n]
+ *   y          out int8 [num_experts][capacity][n]
+ *   y_scales   out fp32 [num_experts][capacity]
+ *   workspace  at least ep_ll_gemm_swiglu_int8_workspace_bytes(shape) bytes, 16-byte
+ *              aligned; holds nothing between calls, calls that may overlap need one each
+ */
+ep_status_t ep_ll_gemm_swiglu_int8(const ep_gemm_shape_t* shape, const int8_t* a, const float* a_scales,
+                                   const int8_t* w, const float* w_scales, const int32_t* count, int8_t* y,
+                                   float* y_scales, void* workspace, size_t workspace_bytes, int32_t* status,
+                                   cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Waits for `stream`, reads the device status word (a 4-byte copy into host

@@ -29,6 +29,23 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Arrival that publishes this thread's writes, and what it has waited for, to the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Its wait's counterpart.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // ---- TMA: one box of a 3-D tensor map into this CTA's shared memory, its
 // bytes counted on an mbarrier of this CTA or of its pair's leader ----
 __device__ __forceinline__ void tma_load_3d(uint32_t smem, const CUtensorMap* map, int x, int y, int z,
@@ -182,6 +199,27 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t a, uint64_t b
         "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
+// ---- tcgen05.mma, 16-bit operands -> fp32 in TMEM ----
+// Descriptor of an operand whose rows of shared memory run along m or n (64 values, 128 bytes, swizzled) and follow one
+// another along k: 8-row groups 1024 bytes apart, the next 64 values of m or n `next` bytes further.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem, uint32_t next) {
+    return (static_cast<uint64_t>((smem & 0x3ffffu) >> 4)) | (static_cast<uint64_t>(next >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+// Instruction descriptor: fp32 accumulators, both operands bf16; a, b: rows along k (false) or along m, n (true).
+__host__ __device__ constexpr uint32_t bf16_idesc(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
 // Arrives on the mbarrier at this offset in both CTAs once every MMA issued
 // so far has completed.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {

@@ -1,22 +1,26 @@
 // Experts' bf16 products and their gradients on the tensor cores
 // (ep_ll_gemm_bf16 and its neighbours).
 //
-//   rows forms   D[m][j] = sum_c r[m][c] w[j][c]    (kPlain, kSwiglu)
-//                D[m][j] = sum_c r[m][c] w[c][j]    (kDgrad, kDswiglu)
-//   kWgrad       D[i][j] = sum_m r[m][i] a[m][j]    over an expert's rows
+//   kPlain, kSwiglu    D[j][m] = sum_c w[j][c] r[m][c]
+//   kDgrad, kDswiglu   D[j][m] = sum_c w[c][j] r[m][c]
+//   kWgrad             D[i][j] = sum_m r[m][i] a[m][j]    over an expert's rows
 //
-// A pair of CTAs (one cluster, two SMs) owns a tile of 256 x 256 and walks the
-// contraction in blocks of 64: each CTA loads its own 128 rows of the first operand
-// and half of the second with swizzled TMA, one thread feeds the pair's tensor cores
-// (tcgen05.mma, K = 16), and the sums stay in TMEM until the tile is done, in two
-// accumulators that take turns so that one is read while the other is summed.
-// Whether an operand's rows of memory run along the contraction or across it is
-// settled by its descriptor: nothing is transposed in memory.  For the gated product
-// the second operand is 128 rows of the gate matrix and the same 128 of the up matrix, so both
-// projections of one column meet in one thread.
+// A pair of CTAs (one cluster, two SMs) owns a tile of two blocks of 256 rows of the first
+// operand x up to 256 rows of the second and walks the contraction in steps of 64: each
+// CTA loads its own half of every block with swizzled TMA, two warps feed the pair's
+// tensor cores (tcgen05.mma, K = 16), one for each block of 256, and the sums stay in TMEM
+// until the tile is done.  Whether an operand's rows of memory run along the contraction
+// or across it is settled by its descriptor: nothing is transposed in memory.
+//
+// In the forms over rows the weights are the first operand and an expert's rows the
+// second, because that one's size goes in steps of 32: an expert's last rows cost
+// the tensor cores what they are, not a whole tile.  The sums then lie transposed in
+// TMEM (lane = output column) and go through 8 x 8 matrix stores into rows again.  For
+// the gated product the two blocks are the gate and the up matrix, so both projections
+// of an output meet in one thread.
 //
 // An expert's rows are the contraction of a weight gradient and may end inside a
-// block: the block's last step of 16 is then zeroed behind them in shared memory, in both
+// step of 64: its last 16 rows are then zeroed behind them in shared memory, in both
 // operands, because what lies there may be a NaN.
 #include <cstdint>
 #include <cuda.h>
@@ -37,42 +41,51 @@ namespace {
 
 using gemm::Waits;
 
-constexpr int kTileM = 256;                        // of a pair; each CTA has half
-constexpr int kTileN = 256;
+constexpr int kBlock = 256;                    // rows of a block of the first operand; each CTA has half
+constexpr int kTileRows = 256;                 // most rows of the second operand
 constexpr int kHalf = 128;
-constexpr int kBlockK = 64;                        // bf16: one 128-byte swizzled row
-constexpr int kOperand = kHalf * kBlockK * 2;      // one operand of a CTA's stage, 16 KB
-constexpr int kBox = kBlockK * 128;                // 64 rows x 128 bytes of an operand that runs across the contraction
-constexpr int kChunk = 32;                         // rows of the smaller box of the rows operand
-constexpr int kStages = 6;
+constexpr int kBlockK = 64;                    // bf16: one 128-byte swizzled row
+constexpr int kBox = kBlockK * 128;            // 64 rows x 128 bytes, 8 KB
+constexpr int kOperand = 2 * kBox;             // 128 rows of an operand
+constexpr int kStageBytes = 3 * kOperand;      // two blocks of the first operand, one of the second
+constexpr int kChunk = 16;                     // rows of the smaller box of the rows operand
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = 128 + kEpilogueWarps * kWarp;  // producer, MMA, relay, spare | epilogue
-constexpr int kOutRow = 128;                       // bytes of one epilogue thread's results
-constexpr int kOutBytes = kWarp * kOutRow;         // of a warp's
+constexpr int kThreads = 128 + kEpilogueWarps * kWarp;  // producer, two MMA warps, relay | epilogue
 constexpr int kTmemColumns = 512;
+constexpr int kOutCols = 32, kOutRows = 32;    // of a warp's box of output
+constexpr int kOutBytes = kOutCols * kOutRows * 2;
+
+// Stages and bytes of an epilogue warp's buffers: where sums are widened (fp32 output) or gate and up come in on the way
+// out, a stage is given up for twice the buffers.
+template <Bf16Form kForm, bool kOut16>
+constexpr bool kWide = kForm == Bf16Form::kDswiglu || (kForm == Bf16Form::kWgrad && !kOut16);
+constexpr int kMostStages = 4;
 
 struct Params {
     Bf16GemmArgs g;
-    int kb;                // blocks of the contraction (rows forms)
-    int tiles_m, tiles_n;  // tiles_m: kWgrad
+    int kb;                // steps of the contraction (forms over rows)
     int out_n;             // columns of the output (of each half of it)
+    int tiles_m, tiles_n;  // kWgrad: tiles of output rows and columns
+    int blocks;            // kWgrad: blocks of a tile
 };
 
 struct Shared {
-    uint64_t full[kStages];      // bytes have landed: leader's, of both CTAs (rows forms); each CTA's own (kWgrad)
-    uint64_t ready[kStages];     // leader's, kWgrad: both CTAs' blocks are complete and zeroed behind the last row
-    uint64_t empty[kStages];     // both: the MMAs that read the stage are done
-    uint64_t acc_full[2];        // both: a tile's sums are in TMEM
-    uint64_t acc_empty[2];       // leader's: the epilogue warps of the pair have read them
-    int first[kRowGroups + 2];   // tiles before each group of 32 experts
+    uint64_t full[kMostStages];    // leader's: both CTAs' bytes have landed
+    uint64_t landed[kMostStages];  // kWgrad, each CTA's own: the bytes of a step that ends an expert's rows
+    uint64_t empty[kMostStages];   // both: the MMAs that read the stage are done
+    uint64_t acc_full[2];          // both: a block's sums are in TMEM
+    uint64_t acc_empty[2];         // leader's: the pair's epilogue warps have read them
+    uint64_t loaded[kEpilogueWarps][2];  // kDswiglu: gate and up are in the warp's buffers
+    int first[kRowGroups + 2];     // tiles before each group of 32 experts
     uint32_t tmem;
     Waits waits;
 };
 
-// Bounded waits, as gemm::wait_for, at cluster scope.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
+    return gemm::wait_for<false>(bar, parity, w);
+}
+// At cluster scope: what another CTA's threads wrote before they arrived is visible.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Waits* w) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait_cluster(bar, parity)) return true;
     const long long start = globaltimer_ns();
     do {
         for (int i = 0; i < 64; ++i)
@@ -81,64 +94,117 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Wai
     *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
     return false;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
-    return gemm::wait_for<false>(bar, parity, w);
-}
 
-// A place in a ring of barriers.
-template <int kSize>
+// A place in the ring of stages.
+template <int kStages>
 struct Ring {
     uint32_t at = 0, phase;
     __device__ __forceinline__ explicit Ring(uint32_t first_phase) : phase(first_phase) {}
     __device__ __forceinline__ void next() {
-        if (++at == kSize) {
+        if (++at == kStages) {
             at = 0;
             phase ^= 1;
         }
     }
+    __device__ __forceinline__ void skip(uint32_t steps) {
+        const uint32_t to = at + steps;
+        phase ^= to / kStages & 1;
+        at = to % kStages;
+    }
 };
 
-// Tile t of a weight gradient: expert, tile of rows, tile of columns.
-struct WgradTile {
-    int e, m, n, rows;
+// One tile of either kind.
+struct Tile {
+    int e;
+    int a0;      // first row of the first operand's first block (an output column; kWgrad: an output row)
+    int blocks;  // that hold any
+    int b0;      // kWgrad: first output column
+    int m0;      // forms over rows: first row of the expert
+    int rows;    // valid rows: of the tile; kWgrad: of the expert
 };
-__device__ __forceinline__ WgradTile wgrad_tile(int t, const Params& p) {
-    const int per = p.tiles_m * p.tiles_n, e = t / per, local = t - e * per;
-    return WgradTile{e, local / p.tiles_n, local % p.tiles_n, min(max(__ldg(p.g.count + e), 0), p.g.cap)};
+
+// The tiles of this pair in turn.
+template <Bf16Form kForm>
+struct Tiles {
+    static constexpr bool kWgrad = kForm == Bf16Form::kWgrad;
+    const Params& p;
+    RowTiles<kTileRows> walk;
+    int blocks;  // of a tile (1: a tile is one block, the two accumulators take turns)
+
+    __device__ __forceinline__ Tile at(int t) {
+        Tile r;
+        if (kWgrad) {
+            const int per = p.tiles_m * p.tiles_n, local = t - t / per * per;
+            r.e = t / per;
+            r.a0 = local / p.tiles_n * blocks * kBlock;
+            r.b0 = local % p.tiles_n * kTileRows;
+            r.rows = walk.rows_of(r.e);
+            r.m0 = 0;
+            r.blocks = min(blocks, (p.g.n - r.a0 + kBlock - 1) / kBlock);
+        } else {
+            const RowTile w = walk.at(t);
+            r.e = w.e;
+            r.m0 = w.m0;
+            r.rows = min(w.rows, kTileRows);
+            r.b0 = 0;
+            if (kForm == Bf16Form::kSwiglu) {
+                r.a0 = w.col * kBlock;
+                r.blocks = 2;
+            } else {
+                r.a0 = w.col * blocks * kBlock;
+                r.blocks = min(blocks, (p.out_n - r.a0 + kBlock - 1) / kBlock);
+            }
+        }
+        return r;
+    }
+    // Steps of 64 of the contraction.
+    __device__ __forceinline__ int steps(const Tile& t) const { return kWgrad ? (t.rows + kBlockK - 1) / kBlockK : p.kb; }
+};
+// The block that accumulator `half` has of the pair's tile number `i`, or -1.
+__device__ __forceinline__ int block_of(const Tile& t, int blocks, int i, int half) {
+    if (blocks == 2) return half < t.blocks ? half : -1;
+    return (i & 1) == half ? 0 : -1;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 template <Bf16Form kForm, bool kOut16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ll_gemm_bf16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a32,
-                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out,
+    ll_gemm_bf16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ CUtensorMap map_b16, const __grid_constant__ CUtensorMap map_out,
                         const __grid_constant__ CUtensorMap map_gate_up, const Params p) {
     constexpr bool kWgrad = kForm == Bf16Form::kWgrad;
     constexpr bool kSwiglu = kForm == Bf16Form::kSwiglu, kDswiglu = kForm == Bf16Form::kDswiglu;
-    constexpr bool kAcrossB = kWgrad || kForm == Bf16Form::kDgrad || kDswiglu;  // b's rows run across the contraction
+    constexpr bool kAcrossA = kWgrad || kForm == Bf16Form::kDgrad || kDswiglu;  // its rows of memory run across the contraction
+    constexpr int kStages = kWide<kForm, kOut16> ? 3 : 4;
+    constexpr int kBufBytes = kWide<kForm, kOut16> ? 4 * kOutBytes : 2 * kOutBytes;  // of an epilogue warp
     extern __shared__ uint8_t s_raw[];
     // stages first, on a 1024-byte boundary as the swizzle needs, at the same offset in both CTAs
     uint8_t* s_tiles = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
-    uint8_t* s_out = s_tiles + kStages * 2 * kOperand;
-    Shared* s = reinterpret_cast<Shared*>(s_out + kEpilogueWarps * kOutBytes);
+    uint8_t* s_out = s_tiles + kStages * kStageBytes;
+    Shared* s = reinterpret_cast<Shared*>(s_out + kEpilogueWarps * kBufBytes);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s->full[i], 1);
-            mbar_init(&s->ready[i], 2);
-            mbar_init(&s->empty[i], 1);
+            mbar_init(&s->full[i], kWgrad ? 2 : 1);
+            mbar_init(&s->landed[i], 1);
+            mbar_init(&s->empty[i], 2);  // both blocks' MMAs
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 2 * kEpilogueWarps);
+            mbar_init(&s->acc_empty[i], kSwiglu ? 2 * kEpilogueWarps : kEpilogueWarps);  // of the pair
         }
+        for (int i = 0; i < kEpilogueWarps; ++i)
+            for (int j = 0; j < 2; ++j) mbar_init(&s->loaded[i][j], 1);
         s->waits = Waits{0, 0};
         fence_mbarrier_init();
         prefetch_tensormap(&map_a);
@@ -148,319 +214,386 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and weights are complete from here on
     griddep_launch_dependents();
-    RowTiles<kTileM> walk{p.g.count, s->first, p.g.E, p.g.cap, p.tiles_n};
-    if (!kWgrad && warp == 1) walk.fill(s->first, lane);
+    Tiles<kForm> list{p, RowTiles<kTileRows>{p.g.count, s->first, p.g.E, p.g.cap, p.tiles_n}, kWgrad ? p.blocks : 2};
+    if (!kWgrad && warp == 1) list.walk.fill(s->first, lane);
     tc_fence_before();
     __syncthreads();
     cluster_arrive_release();
     cluster_wait_acquire();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
-    const int tiles = kWgrad ? p.g.E * p.tiles_m * p.tiles_n : walk.total();
+    const int tiles = kWgrad ? p.g.E * p.tiles_m * p.tiles_n : list.walk.total();
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        regs_down<64>();
+        if (warp == 0 && lane == 0) {
             // ---- producer ----
             Ring<kStages> st(1);  // a fresh barrier passes a wait for phase 1
             bool ok = true;
-            const uint32_t full = mapa(smem_addr(&s->full[0]), kWgrad ? rank : 0);
+            const uint32_t full = mapa(smem_addr(&s->full[0]), 0);
             for (int t = pair; t < tiles && ok; t += pairs) {
-                int e, ax, ay, bx, kb = p.kb, chunks0 = 4, chunks1 = 4;
-                if (kWgrad) {
-                    const WgradTile tl = wgrad_tile(t, p);
-                    e = tl.e;
-                    ax = tl.m * kTileM + static_cast<int>(rank) * kHalf;
-                    ay = 0;
-                    bx = tl.n * kTileN;
-                    kb = (tl.rows + kBlockK - 1) / kBlockK;
-                } else {
-                    const RowTile tl = walk.at(t);
-                    e = tl.e;
-                    ax = 0;
-                    ay = tl.m0 + static_cast<int>(rank) * kHalf;
-                    bx = tl.col * (kSwiglu ? kHalf : kTileN);
-                    chunks0 = (min(tl.rows, kHalf) + kChunk - 1) / kChunk;
-                    chunks1 = (min(max(tl.rows - kHalf, 0), kHalf) + kChunk - 1) / kChunk;
-                }
-                if (!kSwiglu) bx += static_cast<int>(rank) * kHalf;
-                const int chunks = rank == 0 ? chunks0 : chunks1;
-                const uint32_t bytes = kWgrad ? 2 * kOperand : 2 * kOperand + (chunks0 + chunks1) * kChunk * 128;
-                for (int b = 0; b < kb; ++b) {
+                const Tile tl = list.at(t);
+                const int steps = list.steps(tl);
+                const int n = kWgrad ? kTileRows : (tl.rows + 31) / 32 * 32;  // rows of the second operand
+                const int a0 = tl.a0 + static_cast<int>(rank) * kHalf;
+                const int b0 = (kWgrad ? tl.b0 : tl.m0) + static_cast<int>(rank) * (n / 2);
+                const uint32_t bytes = tl.blocks * kOperand + n / 2 * 128;  // of each CTA
+                for (int b = 0; b < steps; ++b) {
                     if (!(ok = wait_for(&s->empty[st.at], st.phase, &s->waits))) break;
-                    if (kWgrad || rank == 0) mbar_arrive_expect_tx(&s->full[st.at], bytes);
-                    const uint32_t bar = full + st.at * sizeof(uint64_t);
-                    const uint32_t ta = smem_addr(s_tiles) + st.at * 2 * kOperand, tb = ta + kOperand;
+                    uint32_t bar = full + st.at * sizeof(uint64_t);
+                    if (kWgrad && (tl.rows - b * kBlockK < kBlockK) && tl.rows % 16 != 0) {
+                        bar = mapa(smem_addr(&s->landed[st.at]), rank);
+                        mbar_arrive_expect_tx(&s->landed[st.at], bytes);
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(&s->full[st.at], 2 * bytes);
+                        if (kWgrad) mbar_arrive(&s->full[st.at]);
+                    }
+                    const uint32_t to = smem_addr(s_tiles) + st.at * kStageBytes, tb = to + 2 * kOperand;
                     const int c = b * kBlockK;
-                    if (kAcrossB) {
-                        for (int i = 0; i < 2; ++i) tma_load_3d(tb + i * kBox, &map_b, bx + i * 64, c, e, bar);
-                    } else {
-                        tma_load_3d(tb, &map_b, c, bx, kSwiglu ? 2 * e + static_cast<int>(rank) : e, bar);
+                    for (int i = 0; i < tl.blocks; ++i) {
+                        const uint32_t ta = to + i * kOperand;
+                        if (kSwiglu) {
+                            tma_load_3d(ta, &map_a, c, a0, 2 * tl.e + i, bar);
+                        } else if (kAcrossA) {
+                            for (int j = 0; j < 2; ++j) tma_load_3d(ta + j * kBox, &map_a, a0 + i * kBlock + j * 64, c, tl.e, bar);
+                        } else {
+                            tma_load_3d(ta, &map_a, c, a0 + i * kBlock, tl.e, bar);
+                        }
                     }
                     if (kWgrad) {
-                        for (int i = 0; i < 2; ++i) tma_load_3d(ta + i * kBox, &map_a, ax + i * 64, c, e, bar);
-                    } else if (chunks == kHalf / kChunk) {
-                        tma_load_3d(ta, &map_a, c, ay, e, bar);
+                        for (int j = 0; j < 2; ++j) tma_load_3d(tb + j * kBox, &map_b, b0 + j * 64, c, tl.e, bar);
+                    } else if (n == kTileRows) {
+                        tma_load_3d(tb, &map_b, c, b0, tl.e, bar);
                     } else {
-                        for (int i = 0; i < chunks; ++i)
-                            tma_load_3d(ta + i * kChunk * 128, &map_a32, c, ay + i * kChunk, e, bar);
+                        for (int i = 0; i < n / 2; i += kChunk) tma_load_3d(tb + i * 128, &map_b16, c, b0 + i, tl.e, bar);
                     }
                     st.next();
                 }
             }
             // every stage's last read is over before the CTA may leave
             for (int i = 0; i < kStages && ok; ++i, st.next()) ok = wait_for(&s->empty[st.at], st.phase, &s->waits);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0) {
-            // ---- MMA ----
-            constexpr uint32_t idesc = bf16_idesc(kTileM, kTileN, kWgrad, kAcrossB);
+        } else if ((warp == 1 || warp == 2) && rank == 0) {
+            // ---- MMA: two warps feed the pair's tensor cores, one for each accumulator.  One accumulator's sums cross to
+            // their epilogue warps, and it comes back, while the other one multiplies ----
+            const int half = warp - 1;
             Ring<kStages> st(0);
-            Ring<2> acc(1);
+            uint32_t acc_phase = 1;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                int kb = p.kb, last = kBlockK / 16;  // steps of the last block
-                if (kWgrad) {
-                    const int rows = __shfl_sync(0xffffffffu, wgrad_tile(t, p).rows, 0);
-                    if (rows == 0) continue;
-                    kb = (rows + kBlockK - 1) / kBlockK;
-                    last = (rows - (kb - 1) * kBlockK + 15) / 16;
+            for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
+                const Tile tl = list.at(t);
+                const int steps = __shfl_sync(0xffffffffu, list.steps(tl), 0);
+                if (steps == 0) continue;
+                const int block = __shfl_sync(0xffffffffu, block_of(tl, list.blocks, i, half), 0);
+                if (block < 0) {
+                    // the other warp's tile: only this one's arrivals (a barrier tells phases apart by one bit, so a wait
+                    // may not be left out)
+                    for (int b = 0; b < steps && ok; ++b, st.next()) {
+                        ok = __all_sync(0xffffffffu, wait_for(&s->full[st.at], st.phase, &s->waits));
+                        if (ok && elect_one()) mma_commit_pair(smem_addr(&s->empty[st.at]));
+                        __syncwarp();
+                    }
+                    continue;
                 }
-                ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[acc.at], acc.phase, &s->waits));
-                const uint32_t d = tmem + acc.at * kTileN;
-                for (int b = 0; b < kb && ok; ++b) {
-                    const bool landed = kWgrad ? wait_cluster(&s->ready[st.at], st.phase, &s->waits)
-                                               : wait_for(&s->full[st.at], st.phase, &s->waits);
-                    ok = __all_sync(0xffffffffu, landed);
+                const int rows = __shfl_sync(0xffffffffu, tl.rows, 0);
+                const uint32_t idesc = bf16_idesc(kBlock, kWgrad ? kTileRows : (rows + 31) / 32 * 32, kAcrossA, kWgrad);
+                const bool ragged = kWgrad && rows % 16 != 0;
+                const int last = kWgrad ? (rows - (steps - 1) * kBlockK + 15) / 16 : kBlockK / 16;  // MMAs of the last step
+                ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
+                acc_phase ^= 1;
+                const uint32_t d = tmem + half * kTileRows;
+                for (int b = 0; b < steps && ok; ++b) {
+                    const bool end = b + 1 == steps;
+                    const bool there = ragged && end ? wait_cluster(&s->full[st.at], st.phase, &s->waits)
+                                                     : wait_for(&s->full[st.at], st.phase, &s->waits);
+                    ok = __all_sync(0xffffffffu, there);
                     if (!ok) break;
-                    const uint32_t ta = smem_addr(s_tiles) + st.at * 2 * kOperand, tb = ta + kOperand;
-                    uint64_t da = kWgrad ? sw128_desc_mn(ta, kBox) : sw128_desc(ta);
-                    uint64_t db = kAcrossB ? sw128_desc_mn(tb, kBox) : sw128_desc(tb);
+                    const uint32_t to = smem_addr(s_tiles) + st.at * kStageBytes;
+                    const uint32_t ta = to + block * kOperand, tb = to + 2 * kOperand;
+                    uint64_t da = kAcrossA ? sw128_desc_mn(ta, kBox) : sw128_desc(ta);
+                    uint64_t db = kWgrad ? sw128_desc_mn(tb, kBox) : sw128_desc(tb);
                     asm volatile("" : "+l"(da), "+l"(db));
                     tc_fence_after();
                     if (elect_one()) {
-                        // a step of 16: 32 bytes further inside the swizzled row, or 16 rows further
+                        // 16 of the contraction: 32 bytes further inside the swizzled row, or 16 rows further
 #pragma unroll
                         for (int k = 0; k < kBlockK / 16; ++k)
-                            if (!kWgrad || b + 1 < kb || k < last)
-                                mma_f16_pair(d, da + k * (kWgrad ? 128 : 2), db + k * (kAcrossB ? 128 : 2), idesc,
-                                             b > 0 || k > 0);
+                            if (!kWgrad || !end || k < last)
+                                mma_f16_pair(d, da + k * (kAcrossA ? 128 : 2), db + k * (kWgrad ? 128 : 2), idesc, b > 0 || k > 0);
                         mma_commit_pair(smem_addr(&s->empty[st.at]));
-                        if (b + 1 == kb) mma_commit_pair(smem_addr(&s->acc_full[acc.at]));
+                        if (end) mma_commit_pair(smem_addr(&s->acc_full[half]));
                     }
                     __syncwarp();
                     st.next();
                 }
-                acc.next();
             }
-        }
-    } else if (warp == 2) {
-        if (kWgrad) {
-            // ---- relay: each block as it lands, zeroed behind the expert's last row ----
+        } else if (warp == 3 && kWgrad) {
+            // ---- relay: the step that ends an expert's rows, zeroed behind the last of them ----
             Ring<kStages> st(0);
+            uint32_t phases = 0;  // of the landed barriers, a bit each
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const int rows = wgrad_tile(t, p).rows, kb = (rows + kBlockK - 1) / kBlockK;
-                for (int b = 0; b < kb; ++b) {
-                    ok = __all_sync(0xffffffffu, wait_for(&s->full[st.at], st.phase, &s->waits));
+                const Tile tl = list.at(t);
+                const int steps = list.steps(tl), left = tl.rows - (steps - 1) * kBlockK;
+                if (tl.rows % 16 != 0) {
+                    st.skip(steps - 1);
+                    ok = __all_sync(0xffffffffu, wait_for(&s->landed[st.at], phases >> st.at & 1, &s->waits));
                     if (!ok) break;
-                    const int left = rows - b * kBlockK;
-                    if (left < kBlockK && left % 16 != 0) {
-                        const int end = (left + 15) / 16 * 16;
-                        uint8_t* to = s_tiles + st.at * 2 * kOperand;
-                        // whole rows of 128 bytes in each of the four boxes, so the swizzle does not matter
-                        for (int i = lane; i < (end - left) * 32; i += kWarp) {
-                            const int box = i / 8 % 4, row = left + i / 32;
-                            *reinterpret_cast<uint4*>(to + box * kBox + row * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->ready[st.at]), 0));
+                    phases ^= 1u << st.at;
+                    uint8_t* to = s_tiles + st.at * kStageBytes;
+                    const int more = (left + 15) / 16 * 16 - left;
+                    // whole rows of 128 bytes in each of the six boxes, so the swizzle does not matter
+                    for (int i = lane; i < more * 48; i += kWarp)
+                        *reinterpret_cast<uint4*>(to + i / 8 % 6 * kBox + (left + i / 48) * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->full[st.at]), 0));
                     st.next();
+                } else {
+                    st.skip(steps);
                 }
             }
         }
-    } else if (warp >= 4) {
-        // ---- epilogue: thread = one row; four warps have one half of the tile's columns, four the other ----
+        __syncwarp();
+    } else {
+        // ---- epilogue: four warps to an accumulator, a quarter of its 128 lanes each; gated: all of them read both ----
+        regs_up<208>();
         const int half = (warp - 4) / 4, quarter = warp % 4;
-        const int row = static_cast<int>(rank) * kHalf + quarter * kWarp + lane;  // of the tile
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
         const uint32_t empty = mapa(smem_addr(&s->acc_empty[0]), 0);
-        uint8_t* to = s_out + (warp - 4) * kOutBytes;
-        const uint32_t to_addr = smem_addr(to);
-        Ring<2> acc(0);
-        // 128 bytes of this thread's row into the warp's box of shared memory, in swizzled rows
-        const auto stage = [&](const uint4 (&v)[8]) {
-            if (lane == 0) bulk_wait_read<0>();  // the last store has left the buffer
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(to + lane * kOutRow + ((j ^ (lane & 7)) << 4)) = v[j];
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
+        const uint32_t buf = smem_addr(s_out + (warp - 4) * kBufBytes);
+        uint32_t acc_phase = 0;
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
-            if (kWgrad) {
-                const WgradTile tl = wgrad_tile(t, p);
-                if (tl.rows > 0) {
-                    ok = __all_sync(0xffffffffu, wait_for(&s->acc_full[acc.at], acc.phase, &s->waits));
+        const auto hand_back = [&](int h) {
+            tc_fence_before();
+            if (lane == 0) mbar_arrive_cluster_relaxed(empty + h * 8);
+        };
+        if (kWgrad) {
+            // thread = one output row
+            constexpr int kCols = kOut16 ? 64 : 32;  // of one store: 128 bytes a row
+            constexpr int kBoxes = kWide<kForm, kOut16> ? 2 : 1;
+            uint32_t turn = 0;
+            const auto store = [&](const uint4 (&v)[8], int x, int y, int e) {
+                if (x >= p.g.k || y >= p.g.n) return;
+                const uint32_t to = buf + turn % kBoxes * (2 * kOutBytes);
+                ++turn;
+                if (lane == 0) bulk_wait_read<kBoxes - 1>();  // the store before has left this buffer
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                                 "r"(v[j].x), "r"(v[j].y), "r"(v[j].z), "r"(v[j].w)
+                                 : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&map_out, to, x, y, e);
+                    bulk_commit();
+                }
+            };
+            for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
+                const Tile tl = list.at(t);
+                const int block = block_of(tl, list.blocks, i, half);
+                if (block < 0) continue;
+                const bool any = tl.rows > 0;  // without rows the gradient is 0 and the tensor cores have nothing
+                if (any) {
+                    ok = __all_sync(0xffffffffu, wait_for(&s->acc_full[half], acc_phase, &s->waits));
                     if (!ok) break;
+                    acc_phase ^= 1;
                     tc_fence_after();
                 }
-                const int y = tl.m * kTileM + static_cast<int>(rank) * kHalf + quarter * kWarp;
-                constexpr int kCols = kOut16 ? 64 : 32;  // of one store
-#pragma unroll 1
-                for (int c = 0; c < kHalf; c += kCols) {
-                    uint4 v[8];
-                    uint32_t* w = reinterpret_cast<uint32_t*>(v);
+                const int y = tl.a0 + block * kBlock + static_cast<int>(rank) * kHalf + quarter * kWarp;
+                const uint32_t d = lanes + half * kTileRows;
+                if (kOut16) {
+                    // all columns into registers, so that the accumulator is free while they are stored
+                    uint4 v[kTileRows / kCols][8];
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 32) {
+                    for (int c = 0; c < kTileRows; c += 32) {
                         uint64_t x[16];
-                        if (tl.rows > 0) {
-                            tmem_read(lanes + acc.at * kTileN + half * kHalf + c + i, x);
-                        } else {
+                        if (any) tmem_read(d + c, x);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) x[j] = 0;
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            reinterpret_cast<uint32_t*>(v)[c / 2 + j] = any ? pack_bf16(unpack2(x[j])) : 0u;
+                    }
+                    if (any) hand_back(half);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 f = unpack2(x[j]);
-                            if (kOut16) {
-                                w[i / 2 + j] = pack_bf16(f.x, f.y);
-                            } else {
-                                w[2 * j] = __float_as_uint(f.x);
-                                w[2 * j + 1] = __float_as_uint(f.y);
-                            }
-                        }
-                    }
-                    if (c + kCols == kHalf && tl.rows > 0) {
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(empty + acc.at * 8);
-                    }
-                    const int x0 = tl.n * kTileN + half * kHalf + c;
-                    if (x0 >= p.g.k || y >= p.g.n) continue;
-                    stage(v);
-                    if (lane == 0) {
-                        tma_store_3d(&map_out, to_addr, x0, y, tl.e);
-                        bulk_commit();
-                    }
-                }
-                if (tl.rows > 0) acc.next();
-                continue;
-            }
-            const RowTile tl = walk.at(t);
-            ok = __all_sync(0xffffffffu, wait_for(&s->acc_full[acc.at], acc.phase, &s->waits));
-            if (!ok) break;
-            tc_fence_after();
-            const int y = tl.m0 + static_cast<int>(rank) * kHalf + quarter * kWarp;  // the warp's first row
-            const bool whole = row - lane + kWarp <= tl.rows, valid = row < tl.rows;
-            const long long r = static_cast<long long>(tl.e) * p.g.cap + y + lane;
-            const uint32_t d = lanes + acc.at * kTileN;
-            const auto hand_back = [&] {
-                tc_fence_before();
-                if (lane == 0) mbar_arrive_cluster_relaxed(empty + acc.at * 8);
-            };
-            if (row - lane >= tl.rows) {
-                hand_back();
-                acc.next();
-                continue;
-            }
-            // 64 columns from `col` on of the output, or of half `which` of an output of two halves
-            const auto put = [&](const uint4 (&v)[8], int col, bool halves, int which, const CUtensorMap* map, void* out) {
-                if (col >= p.out_n) return;
-                if (whole) {
-                    stage(v);
-                    if (lane == 0) {
-                        if (halves)
-                            tma_store_3d(map, to_addr, col, which, static_cast<int>(r));
-                        else
-                            tma_store_3d(map, to_addr, col, y, tl.e);
-                        bulk_commit();
-                    }
-                } else if (valid) {
-                    uint16_t* o = static_cast<uint16_t*>(out) + (halves ? 2 * r + which : r) * p.out_n + col;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + 8 * j < p.out_n) st_v4(o + 8 * j, v[j]);
-                }
-            };
-            if (kSwiglu) {
-                const int col = tl.col * kHalf + half * 64;
-                uint4 vg[8], vu[8], vh[8];
-#pragma unroll
-                for (int i = 0; i < 64; i += 16) {
-                    uint64_t g[8], u[8];
-                    tmem_read16x2(d + half * 64 + i, d + kHalf + half * 64 + i, g, u);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 a = unpack2(g[j]), b = unpack2(u[j]);
-                        reinterpret_cast<uint32_t*>(vg)[i / 2 + j] = pack_bf16(a.x, a.y);
-                        reinterpret_cast<uint32_t*>(vu)[i / 2 + j] = pack_bf16(b.x, b.y);
-                        reinterpret_cast<uint32_t*>(vh)[i / 2 + j] = pack_bf16(gated_unit(a.x, b.x), gated_unit(a.y, b.y));
-                    }
-                }
-                hand_back();
-                put(vh, col, false, 0, &map_out, p.g.out);
-                if (p.g.gate_up_out != nullptr) {
-                    put(vg, col, true, 0, &map_gate_up, p.g.gate_up_out);
-                    put(vu, col, true, 1, &map_gate_up, p.g.gate_up_out);
-                }
-            } else {
+                    for (int c = 0; c < kTileRows / kCols; ++c) store(v[c], tl.b0 + c * kCols, y, tl.e);
+                } else {
 #pragma unroll 1
-                for (int c = 0; c < kHalf; c += 64) {
-                    const int col = tl.col * kTileN + half * kHalf + c;
-                    if (kDswiglu) {
-                        uint4 vg[8], vu[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            vg[j] = vu[j] = make_uint4(0, 0, 0, 0);
-                            if (valid && col + 8 * j < p.out_n) {
-                                vg[j] = ld_nc_v4(p.g.gate_up + 2 * r * p.out_n + col + 8 * j);
-                                vu[j] = ld_nc_v4(p.g.gate_up + (2 * r + 1) * p.out_n + col + 8 * j);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 64; i += 32) {
-                            uint64_t x[16];
-                            tmem_read(d + half * kHalf + c + i, x);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                uint32_t& wg = reinterpret_cast<uint32_t*>(vg)[i / 2 + j];
-                                uint32_t& wu = reinterpret_cast<uint32_t*>(vu)[i / 2 + j];
-                                const float2 f = unpack2(x[j]);
-                                const float2 lo = gated_unit_gradient(f.x, __uint_as_float(wg << 16), __uint_as_float(wu << 16));
-                                const float2 hi = gated_unit_gradient(f.y, __uint_as_float(wg & 0xffff0000u),
-                                                                      __uint_as_float(wu & 0xffff0000u));
-                                wg = pack_bf16(lo.x, hi.x);
-                                wu = pack_bf16(lo.y, hi.y);
-                            }
-                        }
-                        if (c + 64 == kHalf) hand_back();
-                        put(vg, col, true, 0, &map_out, p.g.out);
-                        put(vu, col, true, 1, &map_out, p.g.out);
-                    } else {
+                    for (int c = 0; c < kTileRows; c += kCols) {
+                        uint64_t x[16];
+                        if (any) tmem_read(d + c, x);
                         uint4 v[8];
 #pragma unroll
-                        for (int i = 0; i < 64; i += 32) {
-                            uint64_t x[16];
-                            tmem_read(d + half * kHalf + c + i, x);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float2 f = unpack2(x[j]);
-                                reinterpret_cast<uint32_t*>(v)[i / 2 + j] = pack_bf16(f.x, f.y);
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 f = any ? unpack2(x[j]) : make_float2(0.0f, 0.0f);
+                            reinterpret_cast<uint32_t*>(v)[2 * j] = __float_as_uint(f.x);
+                            reinterpret_cast<uint32_t*>(v)[2 * j + 1] = __float_as_uint(f.y);
                         }
-                        if (c + 64 == kHalf) hand_back();
-                        put(v, col, false, 0, &map_out, p.g.out);
+                        if (any && c + kCols == kTileRows) hand_back(half);
+                        store(v, tl.b0 + c, y, tl.e);
                     }
                 }
             }
-            acc.next();
+        } else {
+            // Boxes of 32 rows x 32 output columns in rows of 64 swizzled bytes.  This lane's address for the 8 x 8
+            // matrices of eight rows: matrix lane / 8 is 8 columns, 16 bytes.
+            const auto address = [&](uint32_t box, int rows8) {
+                const int r = rows8 * 8 + lane % 8;
+                return box + r * 64 + ((lane / 8 ^ (r >> 1 & 3)) << 4);
+            };
+            // A box out to rows r0.. of the output: `which` of its halves where it has two (0 and 1, else -1).
+            const auto send = [&](uint32_t box, const CUtensorMap* map, void* out, int which, int e, int row, int rows, int col) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                const long long r0 = static_cast<long long>(e) * p.g.cap + row;
+                if (rows >= kOutRows) {
+                    if (lane == 0) {
+                        if (which >= 0)
+                            tma_store_3d(map, box, col, which, static_cast<int>(r0));
+                        else
+                            tma_store_3d(map, box, col, row, e);
+                        bulk_commit();
+                    }
+                } else {
+                    // the expert's last rows, one by one: what lies behind them stays as it is
+#pragma unroll
+                    for (int i = 0; i < kOutRows; i += 8) {
+                        const int r = i + lane / 4, c = col + lane % 4 * 8;
+                        if (r < rows && c < p.out_n) {
+                            uint4 v;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                         : "r"(box + r * 64 + ((lane % 4 ^ (r >> 1 & 3)) << 4)));
+                            const long long at = which >= 0 ? 2 * (r0 + r) + which : r0 + r;
+                            st_v4(static_cast<uint16_t*>(out) + at * p.out_n + c, v);
+                        }
+                    }
+                    fence_proxy_async_smem();  // before a copy may fill the box again
+                    __syncwarp();
+                    if (lane == 0) bulk_commit();  // an empty group: the waits count boxes
+                }
+            };
+            uint32_t turn = 0;
+            // The buffer that takes turns with the other one, once its last store has left it.
+            const auto next_box = [&] {
+                if (lane == 0) bulk_wait_read<1>();
+                __syncwarp();
+                return buf + (turn++ & 1) * kOutBytes;
+            };
+            // 32 rows x 32 columns packed as matrices, out.
+            const auto put = [&](const uint32_t (&v)[16], const CUtensorMap* map, void* out, int which, const Tile& tl, int c,
+                                 int col) {
+                const uint32_t box = next_box();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) store_matrices_trans(address(box, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                send(box, map, out, which, tl.e, tl.m0 + c, tl.rows - c, col);
+            };
+            uint32_t loads = 0;  // kDswiglu: boxes of gate and up asked for
+            for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
+                const Tile tl = list.at(t);
+                const int block = kSwiglu ? 0 : block_of(tl, list.blocks, i, half);
+                if (block < 0) continue;
+                const int col = tl.a0 + block * kBlock + static_cast<int>(rank) * kHalf + quarter * kWarp;
+                const bool on = col < p.out_n;
+                const auto load = [&](int c) {  // kDswiglu: gate and up of the rows from c on, into the next set of buffers
+                    const int set = loads & 1;
+                    ++loads;
+                    if (lane == 0) {
+                        bulk_wait_read<0>();  // what was stored from there has left
+                        mbar_arrive_expect_tx(&s->loaded[warp - 4][set], 2 * kOutBytes);
+                        const int r0 = static_cast<int>(static_cast<long long>(tl.e) * p.g.cap + tl.m0 + c);
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_3d_alone(buf + set * 2 * kOutBytes + j * kOutBytes, &map_gate_up, col, j, r0,
+                                              smem_addr(&s->loaded[warp - 4][set]));
+                    }
+                };
+                if (kDswiglu && on) load(0);
+                ok = wait_for(&s->acc_full[half], acc_phase, &s->waits);
+                if (kSwiglu) ok = ok && wait_for(&s->acc_full[half ^ 1], acc_phase, &s->waits);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                acc_phase ^= 1;
+                tc_fence_after();
+                if (!on) {
+                    hand_back(half);
+                    if (kSwiglu) hand_back(half ^ 1);
+                    continue;
+                }
+                if (kSwiglu) {
+                    // boxes of 32 rows in turn for the two warps of a quarter
+#pragma unroll 1
+                    for (int c = half * kOutRows; c < tl.rows; c += 2 * kOutRows) {
+                        uint32_t g[16], u[16], h[16];
+                        uint64_t x[16], y[16];
+                        tmem_read_matrices(lanes + c, x);
+                        tmem_read_matrices(lanes + kTileRows + c, y);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 a = unpack2(x[j]), b = unpack2(y[j]);
+                            h[j] = pack_bf16(make_float2(gated_unit(a.x, b.x), gated_unit(a.y, b.y)));
+                            g[j] = pack_bf16(a);
+                            u[j] = pack_bf16(b);
+                        }
+                        put(h, &map_out, p.g.out, -1, tl, c, col);
+                        if (p.g.gate_up_out != nullptr) {
+                            put(g, &map_gate_up, p.g.gate_up_out, 0, tl, c, col);
+                            put(u, &map_gate_up, p.g.gate_up_out, 1, tl, c, col);
+                        }
+                    }
+                    hand_back(0);
+                    hand_back(1);
+                } else if (kDswiglu) {
+#pragma unroll 1
+                    for (int c = 0; c < tl.rows; c += kOutRows) {
+                        const uint32_t now = loads - 1;  // this box's number
+                        if (c + kOutRows < tl.rows) load(c + kOutRows);
+                        const uint32_t box = buf + (now & 1) * 2 * kOutBytes;
+                        uint64_t x[16];
+                        tmem_read_matrices(lanes + half * kTileRows + c, x);
+                        if (c + kOutRows >= tl.rows) hand_back(half);
+                        ok = __all_sync(0xffffffffu, wait_for(&s->loaded[warp - 4][now & 1], now >> 1 & 1, &s->waits));
+                        if (!ok) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t g[4], u[4];
+                            load_matrices_trans(address(box, j), g);
+                            load_matrices_trans(address(box + kOutBytes, j), u);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const float2 f = unpack2(x[4 * j + m]), a = unpack_bf16(g[m]), b = unpack_bf16(u[m]);
+                                const float2 lo = gated_unit_gradient(f.x, a.x, b.x), hi = gated_unit_gradient(f.y, a.y, b.y);
+                                g[m] = pack_bf16(make_float2(lo.x, hi.x));
+                                u[m] = pack_bf16(make_float2(lo.y, hi.y));
+                            }
+                            __syncwarp();  // every lane has its values before they are overwritten
+                            store_matrices_trans(address(box, j), g[0], g[1], g[2], g[3]);
+                            store_matrices_trans(address(box + kOutBytes, j), u[0], u[1], u[2], u[3]);
+                        }
+                        for (int j = 0; j < 2; ++j)
+                            send(box + j * kOutBytes, &map_out, p.g.out, j, tl.e, tl.m0 + c, tl.rows - c, col);
+                    }
+                    if (!ok) break;
+                } else {
+                    // all rows into registers, so that the accumulator is free while they are stored
+                    uint32_t v[kTileRows / kOutRows][16];
+#pragma unroll
+                    for (int c = 0; c < kTileRows / kOutRows; ++c)
+                        if (c * kOutRows < tl.rows) {
+                            uint64_t x[16];
+                            tmem_read_matrices(lanes + half * kTileRows + c * kOutRows, x);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[c][j] = pack_bf16(unpack2(x[j]));
+                        }
+                    hand_back(half);
+#pragma unroll
+                    for (int c = 0; c < kTileRows / kOutRows; ++c)
+                        if (c * kOutRows < tl.rows) put(v[c], &map_out, p.g.out, -1, tl, c * kOutRows, col);
+                }
+            }
         }
         if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
-    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (s->waits.ran_out != 0) {
@@ -476,15 +609,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-// Map of [rows][2][cols] bf16, boxes of 64 columns of one half x 32 rows.
-bool make_map_halves(CUtensorMap* map, const void* base, int cols, long long rows) {
+// Map of the outputs of the forms over rows, boxes of 32 columns x 32 rows in 64 swizzled bytes a row: of
+// [outer][rows][cols] bf16, or of [rows][2][cols].
+bool make_out_map(CUtensorMap* map, const void* base, int cols, long long rows, int outer, bool halves) {
     const auto encode = gemm::encode_tiled();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), 2, static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * 4};
-    const cuuint32_t box[3] = {64, 1, kWarp}, step[3] = {1, 1, 1};
+    const cuuint64_t row = static_cast<cuuint64_t>(cols) * 2, all = static_cast<cuuint64_t>(rows);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), halves ? 2 : all, halves ? all : static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[2] = {row, halves ? 2 * row : row * all};
+    const cuuint32_t box[3] = {kOutCols, halves ? 1u : kOutRows, halves ? kOutRows : 1u}, step[3] = {1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -492,40 +627,43 @@ template <Bf16Form kForm, bool kOut16>
 cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
     using gemm::make_map_bf16;
     constexpr bool kWgrad = kForm == Bf16Form::kWgrad, kSwiglu = kForm == Bf16Form::kSwiglu;
-    constexpr bool kTransposed = kForm == Bf16Form::kDgrad || kForm == Bf16Form::kDswiglu;
+    constexpr bool kDswiglu = kForm == Bf16Form::kDswiglu;
+    constexpr bool kTransposed = kForm == Bf16Form::kDgrad || kDswiglu;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const auto over = [](int v, int by) { return (v + by - 1) / by; };
     Params p = {};
     p.g = g;
-    const int inner = kTransposed ? g.n : g.k;  // rows forms: the contraction
+    const int inner = kTransposed ? g.n : g.k;  // forms over rows: the contraction
     p.out_n = kWgrad || kTransposed ? g.k : g.n;
     p.kb = over(inner, kBlockK);
-    p.tiles_m = over(g.n, kTileM);
-    p.tiles_n = over(p.out_n, kSwiglu ? kHalf : kTileN);
-    CUtensorMap a = {}, a32 = {}, b = {}, out = {}, gate_up = {};
+    p.blocks = 2;
+    p.tiles_m = over(g.n, p.blocks * kBlock);
+    p.tiles_n = kWgrad ? over(g.k, kTileRows) : over(p.out_n, kSwiglu ? kBlock : p.blocks * kBlock);
+    CUtensorMap a = {}, b = {}, b16 = {}, out = {}, gate_up = {};
     bool ok;
     if (kWgrad) {
-        if (g.cap > 0)  // without a capacity nothing is loaded
-            ok = make_map_bf16(&a, g.rows, g.n, g.cap, g.E, kBlockK) && make_map_bf16(&b, g.other, g.k, g.cap, g.E, kBlockK);
-        else
-            ok = make_map_bf16(&a, g.out, g.k, g.n, g.E, kBlockK) && make_map_bf16(&b, g.out, g.k, g.n, g.E, kBlockK);
-        ok = ok && (kOut16 ? make_map_bf16(&out, g.out, g.k, g.n, g.E, kWarp)
-                           : gemm::make_map(&out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.out, g.k, g.n, g.E, kWarp));
+        // without a capacity nothing is loaded, but a map needs an array
+        const bool none = g.cap == 0;
+        ok = make_map_bf16(&a, none ? g.out : g.rows, g.n, none ? 1 : g.cap, none ? 1 : g.E, kBlockK) &&
+             make_map_bf16(&b, none ? g.out : g.other, g.k, none ? 1 : g.cap, none ? 1 : g.E, kBlockK) &&
+             (kOut16 ? make_map_bf16(&out, g.out, g.k, g.n, g.E, kWarp)
+                     : gemm::make_map(&out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.out, g.k, g.n, g.E, kWarp));
     } else {
-        ok = make_map_bf16(&a, g.rows, inner, g.cap, g.E, kHalf) && make_map_bf16(&a32, g.rows, inner, g.cap, g.E, kChunk) &&
-             make_map_bf16(&b, g.other, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kTransposed ? kBlockK : kHalf);
         const long long rows = static_cast<long long>(g.E) * g.cap;
-        ok = ok && (kForm == Bf16Form::kDswiglu ? make_map_halves(&out, g.out, p.out_n, rows)
-                                                : make_map_bf16(&out, g.out, p.out_n, g.cap, g.E, kWarp));
-        if (g.gate_up_out != nullptr) ok = ok && make_map_halves(&gate_up, g.gate_up_out, p.out_n, rows);
+        ok = make_map_bf16(&a, g.other, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kTransposed ? kBlockK : kHalf) &&
+             make_map_bf16(&b, g.rows, inner, g.cap, g.E, kHalf) && make_map_bf16(&b16, g.rows, inner, g.cap, g.E, kChunk) &&
+             (kDswiglu ? make_out_map(&out, g.out, p.out_n, rows, 1, true) : make_out_map(&out, g.out, p.out_n, g.cap, g.E, false));
+        const void* halves = kDswiglu ? static_cast<const void*>(g.gate_up) : g.gate_up_out;
+        if (halves != nullptr) ok = ok && make_out_map(&gate_up, halves, p.out_n, rows, 1, true);
     }
     if (!ok) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + kStages * 2 * kOperand + kEpilogueWarps * kOutBytes + sizeof(Shared);
+    constexpr bool wide = kWide<kForm, kOut16>;
+    const size_t smem = 1024 + (wide ? 3 : 4) * kStageBytes + kEpilogueWarps * (wide ? 4 : 2) * kOutBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
-    const long long most = static_cast<long long>(g.E) * (kWgrad ? p.tiles_m : over(g.cap, kTileM)) * p.tiles_n;
+    const long long most = static_cast<long long>(g.E) * (kWgrad ? p.tiles_m : over(g.cap, kTileRows)) * p.tiles_n;
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
-    return launch_pdl(ll_gemm_bf16_kernel<kForm, kOut16>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, a, a32, b,
+    return launch_pdl(ll_gemm_bf16_kernel<kForm, kOut16>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, a, b, b16,
                       out, gate_up, p);
 }
 

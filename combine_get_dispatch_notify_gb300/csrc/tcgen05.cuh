@@ -158,6 +158,41 @@ __device__ __forceinline__ void tmem_read16x2(uint32_t addr0, uint32_t addr1, ui
         : "memory");
 }
 
+// 32 columns of this warp's 32 lanes in the order of 8 x 8 matrices: x[4 i + m], i = 0..3, is the element pair that lane T
+// has of matrix m, rows (lanes of TMEM) 8 m + T / 4, columns 8 i + 2 (T % 4) and the next.
+__device__ __forceinline__ void tmem_read_matrices(uint32_t addr, uint64_t (&x)[16]) {
+    asm volatile(
+        "{\n\t.reg .b32 r<32>;\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{r16, r17, r18, r19, r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {r0, r1}; mov.b64 %1, {r2, r3}; mov.b64 %2, {r16, r17}; mov.b64 %3, {r18, r19};\n\t"
+        "mov.b64 %4, {r4, r5}; mov.b64 %5, {r6, r7}; mov.b64 %6, {r20, r21}; mov.b64 %7, {r22, r23};\n\t"
+        "mov.b64 %8, {r8, r9}; mov.b64 %9, {r10, r11}; mov.b64 %10, {r24, r25}; mov.b64 %11, {r26, r27};\n\t"
+        "mov.b64 %12, {r12, r13}; mov.b64 %13, {r14, r15}; mov.b64 %14, {r28, r29}; mov.b64 %15, {r30, r31};\n\t"
+        "}"
+        : "=l"(x[0]), "=l"(x[1]), "=l"(x[2]), "=l"(x[3]), "=l"(x[4]), "=l"(x[5]), "=l"(x[6]), "=l"(x[7]),
+          "=l"(x[8]), "=l"(x[9]), "=l"(x[10]), "=l"(x[11]), "=l"(x[12]), "=l"(x[13]), "=l"(x[14]), "=l"(x[15])
+        : "r"(addr), "r"(addr + (16u << 16))
+        : "memory");
+}
+
+// ---- 8 x 8 matrices of 16-bit values, transposed on their way to or from shared memory: lane l gives the address of
+// row l % 8 (16 bytes) of matrix l / 8, which is that matrix's column l % 8 in the registers ----
+__device__ __forceinline__ void store_matrices_trans(uint32_t smem, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrices_trans(uint32_t smem, uint32_t (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(smem)
+                 : "memory");
+}
+
 // ---- packed fp32 pairs ----
 // acc += x * s, each half rounded once.  The packed form runs at the scalar
 // form's rate (fma pipe) but takes half the issue slots.

@@ -65,8 +65,7 @@ struct Params {
     Bf16GemmArgs g;
     int kb;                // steps of the contraction (forms over rows)
     int out_n;             // columns of the output (of each half of it)
-    int tiles_m, tiles_n;  // kWgrad: tiles of output rows and columns
-    int blocks;            // kWgrad: blocks of a tile
+    int blocks, tiles_m, tiles_n;  // kWgrad: blocks of a tile, tiles of output rows and columns
 };
 
 struct Shared {
@@ -214,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and weights are complete from here on
     griddep_launch_dependents();
-    Tiles<kForm> list{p, RowTiles<kTileRows>{p.g.count, s->first, p.g.E, p.g.cap, p.tiles_n}, kWgrad ? p.blocks : 2};
+    Tiles<kForm> list{p, RowTiles<kTileRows>{p.g.count, s->first, p.g.E, p.g.cap}, kWgrad ? p.blocks : 2};
     if (!kWgrad && warp == 1) list.walk.fill(s->first, lane);
     tc_fence_before();
     __syncthreads();
@@ -222,7 +221,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_wait_acquire();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
-    const int tiles = kWgrad ? p.g.E * p.tiles_m * p.tiles_n : list.walk.total();
+    int tiles = p.g.E * p.tiles_m * p.tiles_n;
+    if (!kWgrad) {
+        const int row_tiles = list.walk.row_tiles(), columns = (p.out_n + kBlock - 1) / kBlock;
+        if (!kSwiglu) list.blocks = blocks_of_tiles(row_tiles, columns, pairs);
+        list.walk.tiles_n = kSwiglu ? columns : (columns + list.blocks - 1) / list.blocks;
+        tiles = row_tiles * list.walk.tiles_n;
+    }
 
     if (warp < 4) {
         regs_down<64>();
@@ -639,7 +644,7 @@ cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
     p.kb = over(inner, kBlockK);
     p.blocks = 2;
     p.tiles_m = over(g.n, p.blocks * kBlock);
-    p.tiles_n = kWgrad ? over(g.k, kTileRows) : over(p.out_n, kSwiglu ? kBlock : p.blocks * kBlock);
+    p.tiles_n = over(g.k, kTileRows);
     CUtensorMap a = {}, b = {}, b16 = {}, out = {}, gate_up = {};
     bool ok;
     if (kWgrad) {
@@ -661,7 +666,8 @@ cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
     constexpr bool wide = kWide<kForm, kOut16>;
     const size_t smem = 1024 + (wide ? 3 : 4) * kStageBytes + kEpilogueWarps * (wide ? 4 : 2) * kOutBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
-    const long long most = static_cast<long long>(g.E) * (kWgrad ? p.tiles_m : over(g.cap, kTileRows)) * p.tiles_n;
+    const long long most = static_cast<long long>(g.E) *
+                           (kWgrad ? p.tiles_m * p.tiles_n : over(g.cap, kTileRows) * over(p.out_n, kBlock));
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
     return launch_pdl(ll_gemm_bf16_kernel<kForm, kOut16>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, a, b, b16,
                       out, gate_up, p);

@@ -1,58 +1,394 @@
-// Experts' int8 products (ep_ll_gemm_int8, ep_ll_gemm_swiglu_int8): 16 x 16 tiles
-// in shared memory, then for the gated product a cast by rows.
+// Experts' int8 products on the tensor cores (ep_ll_gemm_int8,
+// ep_ll_gemm_swiglu_int8).
+//
+//   D[j][m] = sum_k w[j][k] a[m][k];  p[m][j] = as[m] ws[j] D[j][m]
+//
+// sm_103a's tensor cores take no int8, but every int8 value is an fp16 value, so the
+// bytes cross memory as int8 and become fp16 on the SM: weights in registers on their way
+// into TMEM, from where they are the tensor cores' first operand, an expert's rows on
+// their way from one place of shared memory to another.  Products are exact and sums are
+// fp32: exact too as long as they stay within 2^24.  A byte b becomes a number without a
+// conversion instruction: b + 128 in the low bits of 1024 makes the fp16 number 1152 + b.
+//
+// A pair of CTAs (one cluster, two SMs) owns a tile of two blocks of 256 weight
+// rows x up to 128 rows of an expert, in steps of 32, and walks k in steps of 128.  Per CTA:
+// a producer (TMA), four warps that convert each block's weights, two that
+// convert the rows, on the pair's first CTA two that feed the tensor cores (a block
+// each), eight that scale the sums and write them out.  For the gated product the blocks
+// are the gate and the up matrix.  Its activations leave as fp32, because the scale of a row
+// is known once the row is complete; a second kernel casts them.
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "ep.h"
 #include "ep_device.cuh"
 #include "ep_internal.h"
-#include "int8_cast.cuh"
 #include "gated.cuh"
+#include "int8_cast.cuh"
+#include "ll_gemm_fp8.cuh"
+#include "row_tiles.cuh"
+#include "tcgen05.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kTile = 16;
+using gemm::Waits;
+
+constexpr int kBlock = 256;               // weight rows of a block; each CTA has half
+constexpr int kHalf = 128;
+constexpr int kTileRows = 128;            // most rows of an expert in a tile
+constexpr int kBlockK = 128;              // int8: one 128-byte swizzled row
+constexpr int kWeightBytes = kHalf * kBlockK;          // a CTA's part of a block, 16 KB
+constexpr int kRowBytes = kTileRows / 2 * kBlockK;     // a CTA's part of the rows, 8 KB
+constexpr int kStageBytes = 2 * kWeightBytes + kRowBytes;
+constexpr int kStages = 4;
+constexpr int kHalfRows = kTileRows / 2 * 128;         // half a step of rows in fp16: 64 rows x 64 values
+constexpr int kRowsBytes = 2 * kHalfRows;              // a step of rows in fp16, 16 KB
+constexpr int kSlots = 2;                 // of converted steps: weights in TMEM, rows in shared memory
+constexpr int kChunk = 16;                // rows of the smaller box of a
+constexpr int kWeightWarps = 8, kRowWarps = 2, kEpilogueWarps = 8;
+constexpr int kThreads = (4 + kWeightWarps + kEpilogueWarps + kRowWarps) * kWarp;
+constexpr int kTmemColumns = 512;
+constexpr int kSlotColumns = kBlockK / 2;              // TMEM columns of a step of weights
+constexpr int kWeightColumns = 2 * kTileRows;          // where they begin, behind both accumulators
+
+struct Params {
+    Int8GemmArgs g;
+    int kb;
+};
+
+struct Shared {
+    uint64_t raw_full[kStages];       // this CTA's bytes have landed
+    uint64_t raw_empty[kStages];      // its converting warps have read them
+    uint64_t w_full[2][kSlots];       // leader's: a block's step is in both CTAs' TMEM
+    uint64_t w_empty[2][kSlots];      // both: the MMAs that read it are done
+    uint64_t rows_full[kSlots];       // leader's: a step of rows is in both CTAs' shared memory
+    uint64_t rows_empty[kSlots];      // both: both blocks' MMAs that read it are done
+    uint64_t acc_full[2];             // both: a block's sums are in TMEM
+    uint64_t acc_empty[2];            // leader's: the pair's epilogue warps have read them
+    int first[kRowGroups + 2];        // tiles of rows before each group of 32 experts
+    uint32_t tmem;
+    Waits waits;
+};
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
+    return gemm::wait_for<false>(bar, parity, w);
+}
+// At cluster scope: what another CTA's threads wrote before they arrived is visible.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Waits* w) {
+    const long long start = globaltimer_ns();
+    do {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return true;
+    } while (globaltimer_ns() - start < gemm::kWaitLimitNs);
+    *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
+    return false;
+}
+
+// Four int8 values (lowest byte first) -> two pairs of fp16.
+__device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = v ^ 0x80808080u;  // + 128
+    const __half2 back = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);  // 1024 + u
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), back);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), back);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+// 16 bytes of a swizzled row of shared memory.
+__device__ __forceinline__ uint4 row_piece(uint32_t tile, int row, int piece) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(tile + row * 128 + ((piece ^ (row & 7)) << 4)));
+    return v;
+}
+
+// The block that accumulator `half` has of the pair's tile number `i`, or -1.
+__device__ __forceinline__ int block_of(int live, int blocks, int i, int half) {
+    if (blocks == 2) return half < live ? half : -1;
+    return (i & 1) == half ? 0 : -1;
+}
 
 template <bool kSwiglu>
-__global__ void ll_gemm_int8_kernel(const Int8GemmArgs p) {
-    __shared__ float s_a[kTile][kTile + 1], s_b[2][kTile][kTile + 1];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int tx = threadIdx.x, ty = threadIdx.y;
-    for (int e = blockIdx.z; e < p.E; e += gridDim.z) {
-        const int M = min(max(__ldg(p.count + e), 0), p.cap);
-        for (int m0 = blockIdx.y * kTile; m0 < M; m0 += gridDim.y * kTile)
-            for (int n0 = blockIdx.x * kTile; n0 < p.n; n0 += gridDim.x * kTile) {
-                float acc[2] = {0.0f, 0.0f};
-                for (int k0 = 0; k0 < p.k; k0 += kTile) {
-                    const int m = m0 + ty, j = n0 + ty, c = k0 + tx;
-                    const long long w0 = (static_cast<long long>(kSwiglu ? 2 : 1) * e * p.n + j) * p.k + c;
-                    const bool in = j < p.n && c < p.k;
-                    s_a[ty][tx] = m < M && c < p.k ? p.a[(static_cast<long long>(e) * p.cap + m) * p.k + c] : 0;
-                    s_b[0][ty][tx] = in ? p.w[w0] : 0;
-                    s_b[1][ty][tx] = in && kSwiglu ? p.w[w0 + static_cast<long long>(p.n) * p.k] : 0;
-                    __syncthreads();
-#pragma unroll
-                    for (int i = 0; i < kTile; ++i) {
-                        acc[0] = fmaf(s_a[ty][i], s_b[0][tx][i], acc[0]);
-                        acc[1] = fmaf(s_a[ty][i], s_b[1][tx][i], acc[1]);
-                    }
-                    __syncthreads();
-                }
-                const int m = m0 + ty, j = n0 + tx;
-                if (m >= M || j >= p.n) continue;
-                const long long row = static_cast<long long>(e) * p.cap + m;
-                const float as = __ldg(p.a_scales + row);
-                const float* ws = p.w_scales + static_cast<long long>(kSwiglu ? 2 : 1) * e * p.n + j;
-                if (kSwiglu)
-                    p.h[row * p.n + j] = gated_unit(acc[0] * (as * __ldg(ws)), acc[1] * (as * __ldg(ws + p.n)));
-                else
-                    static_cast<__nv_bfloat16*>(p.y)[row * p.n + j] = __float2bfloat16_rn(acc[0] * (as * __ldg(ws)));
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ll_gemm_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ CUtensorMap map_a16, const Params p) {
+    extern __shared__ uint8_t s_raw[];
+    // swizzled tiles first, on a 1024-byte boundary, at the same offset in both CTAs
+    uint8_t* s_stages = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
+    uint8_t* s_rows = s_stages + kStages * kStageBytes;
+    Shared* s = reinterpret_cast<Shared*>(s_rows + kSlots * kRowsBytes);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s->raw_full[i], 1);
+            mbar_init(&s->raw_empty[i], kWeightWarps + kRowWarps);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&s->w_full[h][i], kWeightWarps);  // half of them, in both CTAs
+                mbar_init(&s->w_empty[h][i], 1);
             }
+            mbar_init(&s->rows_full[i], 2 * kRowWarps);
+            mbar_init(&s->rows_empty[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], kSwiglu ? 2 * kEpilogueWarps : kEpilogueWarps);  // of the pair
+        }
+        s->waits = Waits{0, 0};
+        fence_mbarrier_init();
+        prefetch_tensormap(&map_w);
+        prefetch_tensormap(&map_a);
     }
+    if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
+    griddep_wait();  // counts, rows and scales are complete from here on
+    griddep_launch_dependents();
+    RowTiles<kTileRows> walk{p.g.count, s->first, p.g.E, p.g.cap};
+    if (warp == 1) walk.fill(s->first, lane);
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    const uint32_t tmem = s->tmem;
+    const int columns = (p.g.n + kBlock - 1) / kBlock, row_tiles = walk.row_tiles();
+    const int blocks = kSwiglu ? 2 : blocks_of_tiles(row_tiles, columns, pairs);
+    walk.tiles_n = kSwiglu ? columns : (columns + blocks - 1) / blocks;
+    const int tiles = row_tiles * walk.tiles_n;
+    // first output column of a tile, and its blocks that hold any
+    const auto first_column = [&](const RowTile& t) { return t.col * (kSwiglu ? 1 : blocks) * kBlock; };
+    const auto live_blocks = [&](const RowTile& t) {
+        return kSwiglu ? 2 : min(blocks, (p.g.n - first_column(t) + kBlock - 1) / kBlock);
+    };
+    // rows of a tile as the tensor cores take them
+    const auto width = [&](const RowTile& t) { return (min(t.rows, kTileRows) + 31) / 32 * 32; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- producer: this CTA's half of the weights and of the rows ----
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const RowTile tl = walk.at(t);
+                const int n = width(tl), live = live_blocks(tl);
+                const int w0 = first_column(tl) + static_cast<int>(rank) * kHalf, a0 = tl.m0 + static_cast<int>(rank) * (n / 2);
+                for (int b = 0; b < p.kb; ++b, ++it) {
+                    const uint32_t st = it % kStages;
+                    if (!(ok = wait_for(&s->raw_empty[st], it / kStages & 1 ^ 1, &s->waits))) break;
+                    const uint32_t bar = smem_addr(&s->raw_full[st]), to = smem_addr(s_stages) + st * kStageBytes;
+                    mbar_arrive_expect_tx(&s->raw_full[st], live * kWeightBytes + n / 2 * kBlockK);
+                    for (int i = 0; i < live; ++i)
+                        tma_load_3d_alone(to + i * kWeightBytes, &map_w, b * kBlockK, kSwiglu ? w0 : w0 + i * kBlock,
+                                          kSwiglu ? 2 * tl.e + i : tl.e, bar);
+                    if (n == kTileRows)
+                        tma_load_3d_alone(to + 2 * kWeightBytes, &map_a, b * kBlockK, a0, tl.e, bar);
+                    else
+                        for (int i = 0; i < n / 2; i += kChunk)
+                            tma_load_3d_alone(to + 2 * kWeightBytes + i * kBlockK, &map_a16, b * kBlockK, a0 + i, tl.e, bar);
+                }
+            }
+            // every stage has been read before the CTA may leave
+            for (int i = 0; i < kStages && ok; ++i, ++it)
+                ok = wait_for(&s->raw_empty[it % kStages], it / kStages & 1 ^ 1, &s->waits);
+        }
+    } else if (warp == 1 || warp == 2) {
+        if (rank == 0) {
+            // ---- MMA: a warp for each block ----
+            const int half = warp - 1;
+            uint32_t it = 0, mine = 0, acc_phase = 1;  // steps so far: all, and this block's
+            bool ok = true;
+            for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
+                const RowTile tl = walk.at(t);
+                const int block = __shfl_sync(0xffffffffu, block_of(live_blocks(tl), blocks, i, half), 0);
+                const uint32_t idesc = f16_idesc(kBlock, __shfl_sync(0xffffffffu, width(tl), 0));
+                if (block >= 0) {
+                    ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
+                    acc_phase ^= 1;
+                }
+                for (int b = 0; b < p.kb && ok; ++b, ++it) {
+                    const uint32_t rs = it % kSlots, ws = mine % kSlots;
+                    ok = wait_cluster(&s->rows_full[rs], it / kSlots & 1, &s->waits);
+                    if (block >= 0) ok = ok && wait_cluster(&s->w_full[half][ws], mine / kSlots & 1, &s->waits);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint64_t db = sw128_desc(smem_addr(s_rows) + rs * kRowsBytes);
+                    asm volatile("" : "+l"(db));
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (block >= 0) {
+                            const uint32_t a = tmem + kWeightColumns + (half * kSlots + ws) * kSlotColumns;
+#pragma unroll
+                            for (int k = 0; k < kBlockK / 16; ++k)
+                                mma_f16_pair_tmem(tmem + half * kTileRows, a + k * 8, db + k / 4 * (kHalfRows >> 4) + k % 4 * 2,
+                                                  idesc, b > 0 || k > 0);
+                            mma_commit_pair(smem_addr(&s->w_empty[half][ws]));
+                            if (b + 1 == p.kb) mma_commit_pair(smem_addr(&s->acc_full[half]));
+                        }
+                        mma_commit_pair(smem_addr(&s->rows_empty[rs]));
+                    }
+                    __syncwarp();
+                    if (block >= 0) ++mine;
+                }
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + kWeightWarps) {
+        // ---- weights: thread = one weight row, 128 bytes a step -> 64 columns of TMEM ----
+        const int half = (warp - 4) / 4, quarter = warp % 4, row = quarter * kWarp + lane;
+        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + kWeightColumns + half * kSlots * kSlotColumns;
+        const uint32_t full = mapa(smem_addr(&s->w_full[half][0]), 0);
+        uint32_t it = 0, mine = 0;
+        bool ok = true;
+        for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
+            const int block = block_of(live_blocks(walk.at(t)), blocks, i, half);
+            for (int b = 0; b < p.kb; ++b, ++it) {
+                const uint32_t st = it % kStages, ws = mine % kSlots;
+                ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits);
+                if (block >= 0) ok = ok && wait_for(&s->w_empty[half][ws], mine / kSlots & 1 ^ 1, &s->waits);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (block >= 0) {
+                    tc_fence_after();
+                    const uint32_t from = smem_addr(s_stages) + st * kStageBytes + block * kWeightBytes;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 x = row_piece(from, row, 4 * h + j);
+                            widen(x.x, v[8 * j], v[8 * j + 1]);
+                            widen(x.y, v[8 * j + 2], v[8 * j + 3]);
+                            widen(x.z, v[8 * j + 4], v[8 * j + 5]);
+                            widen(x.w, v[8 * j + 6], v[8 * j + 7]);
+                        }
+                        tmem_write(to + ws * kSlotColumns + h * 32, v);
+                    }
+                    tmem_write_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(full + ws * 8);
+                    ++mine;
+                }
+                if (lane == 0) mbar_arrive(&s->raw_empty[st]);
+            }
+        }
+    } else if (warp >= 4 + kWeightWarps + kEpilogueWarps) {
+        // ---- rows: thread = one row, 128 bytes a step -> two halves of 64 fp16 in swizzled rows ----
+        const int row = (warp - (4 + kWeightWarps + kEpilogueWarps)) * kWarp + lane;  // of this CTA's 64
+        const uint32_t full = mapa(smem_addr(&s->rows_full[0]), 0);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            const bool on = row < width(walk.at(t)) / 2;
+            for (int b = 0; b < p.kb; ++b, ++it) {
+                const uint32_t st = it % kStages, rs = it % kSlots;
+                ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits) &&
+                     wait_for(&s->rows_empty[rs], it / kSlots & 1 ^ 1, &s->waits);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (on) {
+                    const uint32_t from = smem_addr(s_stages) + st * kStageBytes + 2 * kWeightBytes;
+                    const uint32_t to = smem_addr(s_rows) + rs * kRowsBytes + row * 128;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {  // 16 values
+                        const uint4 x = row_piece(from, row, j);
+                        uint32_t v[8];
+                        widen(x.x, v[0], v[1]);
+                        widen(x.y, v[2], v[3]);
+                        widen(x.z, v[4], v[5]);
+                        widen(x.w, v[6], v[7]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             to + j / 4 * kHalfRows + (((j % 4 * 2 + h) ^ (row & 7)) << 4)),
+                                         "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3])
+                                         : "memory");
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s->raw_empty[st]);
+                    mbar_arrive_cluster(full + rs * 8);
+                }
+            }
+        }
+    } else if (warp >= 4 + kWeightWarps) {
+        // ---- epilogue: lane = one output column, a quarter of a block's 128 to a warp ----
+        const int half = (warp - 4 - kWeightWarps) / 4, quarter = warp % 4;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
+        const uint32_t empty = mapa(smem_addr(&s->acc_empty[0]), 0);
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        const auto hand_back = [&](int h) {
+            tc_fence_before();
+            if (lane == 0) mbar_arrive_cluster_relaxed(empty + h * 8);
+        };
+        for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
+            const RowTile tl = walk.at(t);
+            const int block = kSwiglu ? 0 : block_of(live_blocks(tl), blocks, i, half);
+            if (block < 0) continue;
+            const int col = first_column(tl) + block * kBlock + static_cast<int>(rank) * kHalf + quarter * kWarp + lane;
+            const bool on = col < p.g.n;
+            const long long r0 = static_cast<long long>(tl.e) * p.g.cap + tl.m0;
+            const float* ws = p.g.w_scales + static_cast<long long>(tl.e) * (kSwiglu ? 2 : 1) * p.g.n + col;
+            const float s0 = on ? __ldg(ws) : 0.0f, s1 = on && kSwiglu ? __ldg(ws + p.g.n) : 0.0f;
+            const int rows = min(tl.rows, kTileRows);
+            ok = wait_for(&s->acc_full[half], acc_phase, &s->waits);
+            if (kSwiglu) ok = ok && wait_for(&s->acc_full[half ^ 1], acc_phase, &s->waits);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            acc_phase ^= 1;
+            tc_fence_after();
+            // 16 rows at a time; gated: in turn for the two warps of a quarter
+#pragma unroll 1
+            for (int c = kSwiglu ? half * 16 : 0; c < rows; c += kSwiglu ? 32 : 16) {
+                const float mine = lane < 16 && c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
+                uint64_t x[8], y[8];
+                if (kSwiglu)
+                    tmem_read16x2(lanes + c, lanes + kTileRows + c, x, y);
+                else
+                    tmem_read(lanes + half * kTileRows + c, x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float as = __shfl_sync(0xffffffffu, mine, j);
+                    const float2 a = unpack2(x[j / 2]);
+                    const float d = (j & 1 ? a.y : a.x) * (as * s0);
+                    if (kSwiglu) {
+                        const float2 b = unpack2(y[j / 2]);
+                        const float u = (j & 1 ? b.y : b.x) * (as * s1);
+                        if (on && c + j < rows) p.g.h[(r0 + c + j) * p.g.n + col] = gated_unit(d, u);
+                    } else if (on && c + j < rows) {
+                        static_cast<__nv_bfloat16*>(p.g.y)[(r0 + c + j) * p.g.n + col] = __float2bfloat16_rn(d);
+                    }
+                }
+            }
+            hand_back(kSwiglu ? 0 : half);
+            if (kSwiglu) hand_back(1);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (s->waits.ran_out != 0) {
+        // a wait ran out: let the copies and products still in flight land before shared memory and TMEM go
+        const long long start = globaltimer_ns();
+        while (globaltimer_ns() - start < 10000000LL) {
+        }
+        if (threadIdx.x == 0) flag_error(p.g.status, EP_DEV_TIMEOUT);
+    }
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
 // ---- the gated product's rows, cast ----
@@ -90,13 +426,27 @@ __global__ void __launch_bounds__(kCastThreads) cast_rows_kernel(const Int8GemmA
     }
 }
 
+template <bool kSwiglu>
+cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const Params p = {g, (g.k + kBlockK - 1) / kBlockK};
+    CUtensorMap w, a, a16;
+    if (!gemm::make_map(&w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf) ||
+        !gemm::make_map(&a, g.a, g.k, g.cap, g.E, kTileRows / 2) || !gemm::make_map(&a16, g.a, g.k, g.cap, g.E, kChunk))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + kStages * kStageBytes + kSlots * kRowsBytes + sizeof(Shared);
+    // an upper bound of the tiles: the counts are on the device
+    const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows - 1) / kTileRows) * ((g.n + kBlock - 1) / kBlock);
+    const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
+    return launch_pdl(ll_gemm_int8_kernel<kSwiglu>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, w, a, a16, p);
+}
+
 }  // namespace
 
 cudaError_t launch_ll_gemm_int8(const Int8GemmArgs& g, cudaStream_t stream) {
-    const auto tiles = [](int v) { return static_cast<unsigned>(v < kTile * 1024 ? (v + kTile - 1) / kTile : 1024); };
-    const dim3 grid(tiles(g.n), tiles(g.cap), static_cast<unsigned>(g.E)), block(kTile, kTile);
-    if (g.y_scales == nullptr) return launch_pdl(ll_gemm_int8_kernel<false>, grid, block, 0, stream, 0, false, g);
-    const cudaError_t e = launch_pdl(ll_gemm_int8_kernel<true>, grid, block, 0, stream, 0, false, g);
+    if (g.y_scales == nullptr) return launch<false>(g, stream);
+    const cudaError_t e = launch<true>(g, stream);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(g.E) * g.cap;
     return launch_pdl(cast_rows_kernel, dim3(static_cast<unsigned>(rows < 4096 ? rows : 4096)), dim3(kCastThreads), 0,

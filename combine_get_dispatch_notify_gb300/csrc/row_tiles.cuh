@@ -15,19 +15,19 @@ struct RowTile {
     int e, m0, col, rows;  // expert, first row, tile of columns, valid rows of the expert from m0 on
 };
 
-// `first` (shared memory, kRowGroups + 2 words) holds the tiles before each group of 32 experts; a walk goes on from the
-// expert of its last tile.
+// `first` (shared memory, kRowGroups + 2 words) holds the tiles of rows before each group of 32 experts; a walk goes on
+// from the expert of its last tile.
 template <int kTileM>
 struct RowTiles {
     const int32_t* count;
     const int* first;
-    int E, cap, tiles_n;
-    int e = 0, before = 0;  // an expert, and the tiles before it
+    int E, cap;
+    int tiles_n = 1;        // tiles of columns
+    int e = 0, before = 0;  // an expert, and the tiles of rows before it
 
     __device__ __forceinline__ int rows_of(int i) const { return min(max(__ldg(count + i), 0), cap); }
-    __device__ __forceinline__ int tiles_of(int i) const { return (rows_of(i) + kTileM - 1) / kTileM * tiles_n; }
 
-    __device__ __forceinline__ int total() const { return first[(E + kWarp - 1) / kWarp]; }
+    __device__ __forceinline__ int row_tiles() const { return first[(E + kWarp - 1) / kWarp]; }
 
     // Fills `to` (one warp).
     __device__ __forceinline__ void fill(int* to, int lane) const {
@@ -36,30 +36,41 @@ struct RowTiles {
         for (int i = 0; i < groups; ++i) {
             if (lane == 0) to[i] = base;
             const int at = i * kWarp + lane;
-            base += static_cast<int>(__reduce_add_sync(0xffffffffu, at < E ? tiles_of(at) : 0));
+            base += static_cast<int>(__reduce_add_sync(0xffffffffu, at < E ? (rows_of(at) + kTileM - 1) / kTileM : 0));
         }
         if (lane == 0) to[groups] = base;
     }
 
-    // Tile t, which is below total() and not before the last one asked for.
+    // Tile t, which is below row_tiles() * tiles_n and not before the last one asked for.
     __device__ __forceinline__ RowTile at(int t) {
-        if (first[e / kWarp + 1] <= t) {
+        const int want = t / tiles_n;
+        if (first[e / kWarp + 1] <= want) {
             int group = e / kWarp + 1;
-            while (first[group + 1] <= t) ++group;
+            while (first[group + 1] <= want) ++group;
             e = group * kWarp;
             before = first[group];
         }
-        int rows, n;
+        int rows;
         for (;;) {
             rows = rows_of(e);
-            n = (rows + kTileM - 1) / kTileM * tiles_n;
-            if (before + n > t) break;
+            const int n = (rows + kTileM - 1) / kTileM;
+            if (before + n > want) break;
             before += n;
             ++e;
         }
-        const int local = t - before, m0 = local / tiles_n * kTileM;
-        return RowTile{e, m0, local % tiles_n, rows - m0};
+        const int m0 = (want - before) * kTileM;
+        return RowTile{e, m0, t - want * tiles_n, rows - m0};
     }
 };
+
+// Blocks of a tile for products whose tiles may have two blocks of output columns or one: two, which read the rows half
+// as often, unless single ones leave a call's last round of tiles so much fuller that an eighth of the rounds is saved
+// (few tiles: one row to each of eight experts, 28 blocks of columns, 76 pairs: 3 rounds of single blocks against
+// 2 of double ones).
+__device__ __forceinline__ int blocks_of_tiles(int row_tiles, int column_blocks, int pairs) {
+    const int one = (row_tiles * column_blocks + pairs - 1) / pairs;
+    const int two = (row_tiles * ((column_blocks + 1) / 2) + pairs - 1) / pairs;
+    return 8 * one <= 7 * 2 * two ? 1 : 2;
+}
 
 }  // namespace ep

@@ -158,6 +158,20 @@ __device__ __forceinline__ void tmem_read16x2(uint32_t addr0, uint32_t addr1, ui
         : "memory");
 }
 
+// 32 columns of this warp's 32 lanes, written (tmem_write_wait before another thread may read them).
+__device__ __forceinline__ void tmem_write(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_write_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // 32 columns of this warp's 32 lanes in the order of 8 x 8 matrices: x[4 i + m], i = 0..3, is the element pair that lane T
 // has of matrix m, rows (lanes of TMEM) 8 m + T / 4, columns 8 i + 2 (T % 4) and the next.
 __device__ __forceinline__ void tmem_read_matrices(uint32_t addr, uint64_t (&x)[16]) {
@@ -241,6 +255,18 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem, uint32_t next) 
     return (static_cast<uint64_t>((smem & 0x3ffffu) >> 4)) | (static_cast<uint64_t>(next >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(2) << 61);
+}
+// Both operands fp16, rows along k.
+__host__ __device__ constexpr uint32_t f16_idesc(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// The first operand from TMEM: lane = row, a column = two values along k.
+__device__ __forceinline__ void mma_f16_pair_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
 }
 // Instruction descriptor: fp32 accumulators, both operands bf16; a, b: rows along k (false) or along m, n (true).
 __host__ __device__ constexpr uint32_t bf16_idesc(int m, int n, bool a_mn, bool b_mn) {

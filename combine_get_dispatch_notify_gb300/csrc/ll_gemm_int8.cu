@@ -48,9 +48,10 @@ constexpr int kStageBytes = 2 * kWeightBytes + kRowBytes;
 constexpr int kStages = 4;
 constexpr int kHalfRows = kTileRows / 2 * 128;         // half a step of rows in fp16: 64 rows x 64 values
 constexpr int kRowsBytes = 2 * kHalfRows;              // a step of rows in fp16, 16 KB
-constexpr int kSlots = 2;                 // of converted steps: weights in TMEM, rows in shared memory
+constexpr int kSlots = 2;                 // of converted steps of weights, in TMEM
+constexpr int kRowSlots = 4;              // of converted steps of rows, in shared memory
 constexpr int kChunk = 16;                // rows of the smaller box of a
-constexpr int kWeightWarps = 8, kRowWarps = 2, kEpilogueWarps = 8;
+constexpr int kWeightWarps = 8, kEpilogueWarps = 8, kRowWarps = kRowSlots;
 constexpr int kThreads = (4 + kWeightWarps + kEpilogueWarps + kRowWarps) * kWarp;
 constexpr int kTmemColumns = 512;
 constexpr int kSlotColumns = kBlockK / 2;              // TMEM columns of a step of weights
@@ -66,8 +67,8 @@ struct Shared {
     uint64_t raw_empty[kStages];      // its converting warps have read them
     uint64_t w_full[2][kSlots];       // leader's: a block's step is in both CTAs' TMEM
     uint64_t w_empty[2][kSlots];      // both: the MMAs that read it are done
-    uint64_t rows_full[kSlots];       // leader's: a step of rows is in both CTAs' shared memory
-    uint64_t rows_empty[kSlots];      // both: both blocks' MMAs that read it are done
+    uint64_t rows_full[kRowSlots];    // leader's: a step of rows is in both CTAs' shared memory
+    uint64_t rows_empty[kRowSlots];   // both: both blocks' MMAs that read it are done
     uint64_t acc_full[2];             // both: a block's sums are in TMEM
     uint64_t acc_empty[2];            // leader's: the pair's epilogue warps have read them
     int first[kRowGroups + 2];        // tiles of rows before each group of 32 experts
@@ -122,7 +123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // swizzled tiles first, on a 1024-byte boundary, at the same offset in both CTAs
     uint8_t* s_stages = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
     uint8_t* s_rows = s_stages + kStages * kStageBytes;
-    Shared* s = reinterpret_cast<Shared*>(s_rows + kSlots * kRowsBytes);
+    Shared* s = reinterpret_cast<Shared*>(s_rows + kRowSlots * kRowsBytes);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -130,14 +131,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s->raw_full[i], 1);
-            mbar_init(&s->raw_empty[i], kWeightWarps + kRowWarps);
+            mbar_init(&s->raw_empty[i], kWeightWarps + 1);
         }
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kSlots; ++i)
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&s->w_full[h][i], kWeightWarps);  // half of them, in both CTAs
                 mbar_init(&s->w_empty[h][i], 1);
             }
-            mbar_init(&s->rows_full[i], 2 * kRowWarps);
+        for (int i = 0; i < kRowSlots; ++i) {
+            mbar_init(&s->rows_full[i], 2);
             mbar_init(&s->rows_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -172,6 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // rows of a tile as the tensor cores take them
     const auto width = [&](const RowTile& t) { return (min(t.rows, kTileRows) + 31) / 32 * 32; };
 
+    if (warp < 4) regs_down<40>();
     if (warp == 0) {
         if (lane == 0) {
             // ---- producer: this CTA's half of the weights and of the rows ----
@@ -215,9 +218,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     acc_phase ^= 1;
                 }
                 for (int b = 0; b < p.kb && ok; ++b, ++it) {
-                    const uint32_t rs = it % kSlots, ws = mine % kSlots;
-                    ok = wait_cluster(&s->rows_full[rs], it / kSlots & 1, &s->waits);
-                    if (block >= 0) ok = ok && wait_cluster(&s->w_full[half][ws], mine / kSlots & 1, &s->waits);
+                    const uint32_t rs = it % kRowSlots, ws = mine % kSlots;
+                    ok = wait_cluster(&s->rows_full[rs], it / kRowSlots & 1, &s->waits);
+                    if (block >= 0) ok = ok && wait_for(&s->w_full[half][ws], mine / kSlots & 1, &s->waits);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     uint64_t db = sw128_desc(smem_addr(s_rows) + rs * kRowsBytes);
@@ -241,7 +244,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp >= 4 && warp < 4 + kWeightWarps) {
-        // ---- weights: thread = one weight row, 128 bytes a step -> 64 columns of TMEM ----
+        // ---- weights: thread = one weight row, 128 bytes a step -> 64 columns of TMEM.  Arrivals are relaxed: what they
+        // announce is in TMEM, which the tcgen05 waits and fences on both sides put in order ----
+        regs_down<72>();
         const int half = (warp - 4) / 4, quarter = warp % 4, row = quarter * kWarp + lane;
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + kWeightColumns + half * kSlots * kSlotColumns;
         const uint32_t full = mapa(smem_addr(&s->w_full[half][0]), 0);
@@ -274,28 +279,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_write_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full + ws * 8);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(full + ws * 8);
                     ++mine;
                 }
                 if (lane == 0) mbar_arrive(&s->raw_empty[st]);
             }
         }
     } else if (warp >= 4 + kWeightWarps + kEpilogueWarps) {
-        // ---- rows: thread = one row, 128 bytes a step -> two halves of 64 fp16 in swizzled rows ----
-        const int row = (warp - (4 + kWeightWarps + kEpilogueWarps)) * kWarp + lane;  // of this CTA's 64
-        const uint32_t full = mapa(smem_addr(&s->rows_full[0]), 0);
+        // ---- rows: a step to each of four warps in turn, 128 bytes of a row -> two halves of 64 fp16 in swizzled rows.
+        // Their arrival releases shared memory to the cluster, which takes longer than a step of the tensor cores
+        // (1000 cycles and more: two warps that shared every step made each of them as long), hence the turns ----
+        regs_down<72>();
+        const uint32_t rs = warp - (4 + kWeightWarps + kEpilogueWarps);  // warp and slot
+        const uint32_t full = mapa(smem_addr(&s->rows_full[rs]), 0);
         uint32_t it = 0;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
-            const bool on = row < width(walk.at(t)) / 2;
+            const int mine = width(walk.at(t)) / 2;  // rows of this CTA
             for (int b = 0; b < p.kb; ++b, ++it) {
-                const uint32_t st = it % kStages, rs = it % kSlots;
+                if (it % kRowSlots != rs) continue;
+                const uint32_t st = it % kStages;
                 ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits) &&
-                     wait_for(&s->rows_empty[rs], it / kSlots & 1 ^ 1, &s->waits);
+                     wait_for(&s->rows_empty[rs], it / kRowSlots & 1 ^ 1, &s->waits);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (on) {
-                    const uint32_t from = smem_addr(s_stages) + st * kStageBytes + 2 * kWeightBytes;
+                const uint32_t from = smem_addr(s_stages) + st * kStageBytes + 2 * kWeightBytes;
+#pragma unroll 1
+                for (int row = lane; row < mine; row += kWarp) {
                     const uint32_t to = smem_addr(s_rows) + rs * kRowsBytes + row * 128;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {  // 16 values
@@ -312,17 +322,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                          "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3])
                                          : "memory");
                     }
-                    fence_proxy_async_smem();
                 }
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&s->raw_empty[st]);
-                    mbar_arrive_cluster(full + rs * 8);
+                    mbar_arrive_cluster(full);
                 }
             }
         }
     } else if (warp >= 4 + kWeightWarps) {
         // ---- epilogue: lane = one output column, a quarter of a block's 128 to a warp ----
+        regs_up<112>();
         const int half = (warp - 4 - kWeightWarps) / 4, quarter = warp % 4;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
         const uint32_t empty = mapa(smem_addr(&s->acc_empty[0]), 0);
@@ -348,31 +359,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             acc_phase ^= 1;
             tc_fence_after();
-            // 16 rows at a time; gated: in turn for the two warps of a quarter
+            if (kSwiglu) {
+                // 32 rows at a time, in turn for the two warps of a quarter
 #pragma unroll 1
-            for (int c = kSwiglu ? half * 16 : 0; c < rows; c += kSwiglu ? 32 : 16) {
-                const float mine = lane < 16 && c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
-                uint64_t x[8], y[8];
-                if (kSwiglu)
-                    tmem_read16x2(lanes + c, lanes + kTileRows + c, x, y);
-                else
-                    tmem_read(lanes + half * kTileRows + c, x);
+                for (int c = half * 32; c < kTileRows; c += 64) {
+                    const bool last = c + 64 >= kTileRows;
+                    uint64_t x[16], y[16];
+                    if (c < rows) {
+                        tmem_read(lanes + c, x);
+                        tmem_read(lanes + kTileRows + c, y);
+                    }
+                    if (last) {
+                        hand_back(0);
+                        hand_back(1);
+                    }
+                    if (c >= rows) continue;
+                    const float scale = c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
+                    float* to = p.g.h + (r0 + c) * p.g.n + col;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float as = __shfl_sync(0xffffffffu, mine, j);
-                    const float2 a = unpack2(x[j / 2]);
-                    const float d = (j & 1 ? a.y : a.x) * (as * s0);
-                    if (kSwiglu) {
-                        const float2 b = unpack2(y[j / 2]);
-                        const float u = (j & 1 ? b.y : b.x) * (as * s1);
-                        if (on && c + j < rows) p.g.h[(r0 + c + j) * p.g.n + col] = gated_unit(d, u);
-                    } else if (on && c + j < rows) {
-                        static_cast<__nv_bfloat16*>(p.g.y)[(r0 + c + j) * p.g.n + col] = __float2bfloat16_rn(d);
+                    for (int j = 0; j < 32; ++j) {
+                        const float as = __shfl_sync(0xffffffffu, scale, j);
+                        const float2 a = unpack2(x[j / 2]), b = unpack2(y[j / 2]);
+                        const float gate = (j & 1 ? a.y : a.x) * (as * s0), up = (j & 1 ? b.y : b.x) * (as * s1);
+                        if (on && c + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit(gate, up);
                     }
                 }
+            } else {
+                // all rows into registers, so that the accumulator is free while they are stored
+                uint32_t v[kTileRows / 2];
+#pragma unroll
+                for (int c = 0; c < kTileRows; c += 32) {
+                    if (c >= rows) continue;
+                    const float scale = c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
+                    uint64_t x[16];
+                    tmem_read(lanes + half * kTileRows + c, x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 a = unpack2(x[j]);
+                        const float as0 = __shfl_sync(0xffffffffu, scale, 2 * j), as1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(a.x * (as0 * s0), a.y * (as1 * s0));
+                        v[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                }
+                hand_back(half);
+                uint16_t* to = static_cast<uint16_t*>(p.g.y) + r0 * p.g.n + col;
+#pragma unroll
+                for (int j = 0; j < kTileRows; ++j)
+                    if (on && j < rows) to[static_cast<long long>(j) * p.g.n] = static_cast<uint16_t>(v[j / 2] >> (j % 2 * 16));
             }
-            hand_back(kSwiglu ? 0 : half);
-            if (kSwiglu) hand_back(1);
         }
     }
     __syncwarp();
@@ -435,7 +469,7 @@ cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
     if (!gemm::make_map(&w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf) ||
         !gemm::make_map(&a, g.a, g.k, g.cap, g.E, kTileRows / 2) || !gemm::make_map(&a16, g.a, g.k, g.cap, g.E, kChunk))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + kStages * kStageBytes + kSlots * kRowsBytes + sizeof(Shared);
+    const size_t smem = 1024 + kStages * kStageBytes + kRowSlots * kRowsBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows - 1) / kTileRows) * ((g.n + kBlock - 1) / kBlock);
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);

@@ -12,9 +12,9 @@
 //
 // A pair of CTAs (one cluster, two SMs) owns a tile of two blocks of 256 weight
 // rows x up to 128 rows of an expert, in steps of 32, and walks k in steps of 128.  Per CTA:
-// a producer (TMA), four warps that convert each block's weights, two that
-// convert the rows, on the pair's first CTA two that feed the tensor cores (a block
-// each), eight that scale the sums and write them out.  For the gated product the blocks
+// a producer of weights and one of rows (TMA), four warps that convert each block's weights,
+// four that convert the rows, on the pair's first CTA two that feed the tensor cores (a
+// block each), eight that scale the sums and write them out.  For the gated product the blocks
 // are the gate and the up matrix.  Its activations leave as fp32, because the scale of a row
 // is known once the row is complete; a second kernel casts them.
 #include <cstdint>
@@ -43,16 +43,21 @@ constexpr int kHalf = 128;
 constexpr int kTileRows = 128;            // most rows of an expert in a tile
 constexpr int kBlockK = 128;              // int8: one 128-byte swizzled row
 constexpr int kWeightBytes = kHalf * kBlockK;          // a CTA's part of a block, 16 KB
-constexpr int kRowBytes = kTileRows / 2 * kBlockK;     // a CTA's part of the rows, 8 KB
-constexpr int kStageBytes = 2 * kWeightBytes + kRowBytes;
-constexpr int kStages = 4;
-constexpr int kHalfRows = kTileRows / 2 * 128;         // half a step of rows in fp16: 64 rows x 64 values
-constexpr int kRowsBytes = 2 * kHalfRows;              // a step of rows in fp16, 16 KB
-constexpr int kSlots = 2;                 // of converted steps of weights, in TMEM
-constexpr int kRowSlots = 4;              // of converted steps of rows, in shared memory
+constexpr int kStageBytes = 2 * kWeightBytes;
+constexpr int kStages = 3;                // of weights
+constexpr int kRowBytes = kTileRows / 2 * kBlockK;     // a CTA's part of a step of rows, 8 KB
+constexpr int kRowStages = 4;             // of rows: one to each warp that converts them
 constexpr int kChunk = 16;                // rows of the smaller box of a
-constexpr int kWeightWarps = 8, kEpilogueWarps = 8, kRowWarps = kRowSlots;
-constexpr int kThreads = (4 + kWeightWarps + kEpilogueWarps + kRowWarps) * kWarp;
+constexpr int kBatchBytes = 2 * kTileRows / 2 * 2 * kBlockK;  // a batch of rows in fp16: two steps of a full tile, 32 KB
+constexpr int kSlots = 2;                 // of converted steps of weights, in TMEM
+constexpr int kRowSlots = 3;              // of batches of converted rows, in shared memory
+constexpr int kWeightWarps = 8, kEpilogueWarps = 8;
+constexpr int kRowWarps = 4;              // a stage of rows each
+constexpr int kMostSteps = 8;             // of a batch of rows
+constexpr int kFirstEpilogue = 4 + kWeightWarps, kFirstRow = kFirstEpilogue + kEpilogueWarps;  // warps
+constexpr int kRelay = kFirstRow + kRowWarps;
+constexpr int kThreads = (kRelay + 4) * kWarp;  // whole warpgroups, whose registers are dealt out
+static_assert(kRowWarps == kRowStages && kRowWarps == 4, "a warp owns a stage of rows");
 constexpr int kTmemColumns = 512;
 constexpr int kSlotColumns = kBlockK / 2;              // TMEM columns of a step of weights
 constexpr int kWeightColumns = 2 * kTileRows;          // where they begin, behind both accumulators
@@ -63,11 +68,15 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t raw_full[kStages];       // this CTA's bytes have landed
+    uint64_t raw_full[kStages];       // this CTA's weights have landed
     uint64_t raw_empty[kStages];      // its converting warps have read them
+    uint64_t in_full[kRowStages];     // this CTA's rows have landed
+    uint64_t in_empty[kRowStages];    // the warp that converts them has read them
+    uint64_t go[kRowStages];          // the step's batch has a slot
+    uint64_t converted[kRowSlots];    // this CTA's part of a batch of rows is in shared memory
     uint64_t w_full[2][kSlots];       // leader's: a block's step is in both CTAs' TMEM
     uint64_t w_empty[2][kSlots];      // both: the MMAs that read it are done
-    uint64_t rows_full[kRowSlots];    // leader's: a step of rows is in both CTAs' shared memory
+    uint64_t rows_full[kRowSlots];    // leader's: a batch of rows is in both CTAs' shared memory
     uint64_t rows_empty[kRowSlots];   // both: both blocks' MMAs that read it are done
     uint64_t acc_full[2];             // both: a block's sums are in TMEM
     uint64_t acc_empty[2];            // leader's: the pair's epilogue warps have read them
@@ -109,6 +118,18 @@ __device__ __forceinline__ uint4 row_piece(uint32_t tile, int row, int piece) {
     return v;
 }
 
+// Steps of a batch of rows: as many as have room, by the rows of a tile (a multiple of 32).
+__device__ __forceinline__ int batch_steps(int width) { return width > 64 ? 2 : width > 32 ? 4 : kMostSteps; }
+
+// Several arrivals at once.
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
+    asm volatile(
+        "{\n\t.reg .b64 st;\n\t"
+        "mbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+        "r"(count)
+        : "memory");
+}
+
 // The block that accumulator `half` has of the pair's tile number `i`, or -1.
 __device__ __forceinline__ int block_of(int live, int blocks, int i, int half) {
     if (blocks == 2) return half < live ? half : -1;
@@ -122,8 +143,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t s_raw[];
     // swizzled tiles first, on a 1024-byte boundary, at the same offset in both CTAs
     uint8_t* s_stages = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
-    uint8_t* s_rows = s_stages + kStages * kStageBytes;
-    Shared* s = reinterpret_cast<Shared*>(s_rows + kRowSlots * kRowsBytes);
+    uint8_t* s_in = s_stages + kStages * kStageBytes;
+    uint8_t* s_rows = s_in + kRowStages * kRowBytes;
+    Shared* s = reinterpret_cast<Shared*>(s_rows + kRowSlots * kBatchBytes);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -131,14 +153,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s->raw_full[i], 1);
-            mbar_init(&s->raw_empty[i], kWeightWarps + 1);
+            mbar_init(&s->raw_empty[i], kWeightWarps);
         }
         for (int i = 0; i < kSlots; ++i)
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&s->w_full[h][i], kWeightWarps);  // half of them, in both CTAs
                 mbar_init(&s->w_empty[h][i], 1);
             }
+        for (int i = 0; i < kRowStages; ++i) {
+            mbar_init(&s->in_full[i], 1);
+            mbar_init(&s->in_empty[i], 1);
+            mbar_init(&s->go[i], 1);
+        }
         for (int i = 0; i < kRowSlots; ++i) {
+            mbar_init(&s->converted[i], kMostSteps);
             mbar_init(&s->rows_full[i], 2);
             mbar_init(&s->rows_empty[i], 2);
         }
@@ -174,56 +202,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // rows of a tile as the tensor cores take them
     const auto width = [&](const RowTile& t) { return (min(t.rows, kTileRows) + 31) / 32 * 32; };
 
-    if (warp < 4) regs_down<40>();
+    if (warp < 4) regs_down<32>();
     if (warp == 0) {
         if (lane == 0) {
-            // ---- producer: this CTA's half of the weights and of the rows ----
+            // ---- producer: this CTA's half of the weights ----
             uint32_t it = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const RowTile tl = walk.at(t);
-                const int n = width(tl), live = live_blocks(tl);
-                const int w0 = first_column(tl) + static_cast<int>(rank) * kHalf, a0 = tl.m0 + static_cast<int>(rank) * (n / 2);
+                const int live = live_blocks(tl), w0 = first_column(tl) + static_cast<int>(rank) * kHalf;
                 for (int b = 0; b < p.kb; ++b, ++it) {
                     const uint32_t st = it % kStages;
                     if (!(ok = wait_for(&s->raw_empty[st], it / kStages & 1 ^ 1, &s->waits))) break;
                     const uint32_t bar = smem_addr(&s->raw_full[st]), to = smem_addr(s_stages) + st * kStageBytes;
-                    mbar_arrive_expect_tx(&s->raw_full[st], live * kWeightBytes + n / 2 * kBlockK);
+                    mbar_arrive_expect_tx(&s->raw_full[st], live * kWeightBytes);
                     for (int i = 0; i < live; ++i)
                         tma_load_3d_alone(to + i * kWeightBytes, &map_w, b * kBlockK, kSwiglu ? w0 : w0 + i * kBlock,
                                           kSwiglu ? 2 * tl.e + i : tl.e, bar);
-                    if (n == kTileRows)
-                        tma_load_3d_alone(to + 2 * kWeightBytes, &map_a, b * kBlockK, a0, tl.e, bar);
-                    else
-                        for (int i = 0; i < n / 2; i += kChunk)
-                            tma_load_3d_alone(to + 2 * kWeightBytes + i * kBlockK, &map_a16, b * kBlockK, a0 + i, tl.e, bar);
                 }
             }
             // every stage has been read before the CTA may leave
             for (int i = 0; i < kStages && ok; ++i, ++it)
                 ok = wait_for(&s->raw_empty[it % kStages], it / kStages & 1 ^ 1, &s->waits);
         }
+    } else if (warp == 3) {
+        if (lane == 0) {
+            // ---- producer of rows: apart, because they have to be ahead of the weights ----
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const RowTile tl = walk.at(t);
+                const int n = width(tl), a0 = tl.m0 + static_cast<int>(rank) * (n / 2);
+                for (int b = 0; b < p.kb; ++b, ++it) {
+                    const uint32_t st = it % kRowStages;
+                    if (!(ok = wait_for(&s->in_empty[st], it / kRowStages & 1 ^ 1, &s->waits))) break;
+                    const uint32_t bar = smem_addr(&s->in_full[st]), to = smem_addr(s_in) + st * kRowBytes;
+                    mbar_arrive_expect_tx(&s->in_full[st], n / 2 * kBlockK);
+                    if (n == kTileRows)
+                        tma_load_3d_alone(to, &map_a, b * kBlockK, a0, tl.e, bar);
+                    else
+                        for (int i = 0; i < n / 2; i += kChunk)
+                            tma_load_3d_alone(to + i * kBlockK, &map_a16, b * kBlockK, a0 + i, tl.e, bar);
+                }
+            }
+            for (int i = 0; i < kRowStages && ok; ++i, ++it)
+                ok = wait_for(&s->in_empty[it % kRowStages], it / kRowStages & 1 ^ 1, &s->waits);
+        }
     } else if (warp == 1 || warp == 2) {
         if (rank == 0) {
             // ---- MMA: a warp for each block ----
             const int half = warp - 1;
-            uint32_t it = 0, mine = 0, acc_phase = 1;  // steps so far: all, and this block's
+            uint32_t batch = 0, mine = 0, acc_phase = 1;  // batches of rows so far, steps of this warp's blocks
             bool ok = true;
             for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
                 const RowTile tl = walk.at(t);
                 const int block = __shfl_sync(0xffffffffu, block_of(live_blocks(tl), blocks, i, half), 0);
-                const uint32_t idesc = f16_idesc(kBlock, __shfl_sync(0xffffffffu, width(tl), 0));
+                const int n = __shfl_sync(0xffffffffu, width(tl), 0), in_batch = batch_steps(n);
+                const uint32_t idesc = f16_idesc(kBlock, n), step_bytes = kBatchBytes / in_batch;
                 if (block >= 0) {
                     ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
                     acc_phase ^= 1;
                 }
-                for (int b = 0; b < p.kb && ok; ++b, ++it) {
-                    const uint32_t rs = it % kRowSlots, ws = mine % kSlots;
-                    ok = wait_cluster(&s->rows_full[rs], it / kRowSlots & 1, &s->waits);
+                for (int b = 0; b < p.kb && ok; ++b) {
+                    const uint32_t rs = batch % kRowSlots, ws = mine % kSlots;
+                    const int at = b % in_batch;
+                    if (at == 0) ok = wait_cluster(&s->rows_full[rs], batch / kRowSlots & 1, &s->waits);
                     if (block >= 0) ok = ok && wait_for(&s->w_full[half][ws], mine / kSlots & 1, &s->waits);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    uint64_t db = sw128_desc(smem_addr(s_rows) + rs * kRowsBytes);
+                    const bool end = at + 1 == in_batch || b + 1 == p.kb;
+                    uint64_t db = sw128_desc(smem_addr(s_rows) + rs * kBatchBytes + at * step_bytes);
                     asm volatile("" : "+l"(db));
                     tc_fence_after();
                     if (elect_one()) {
@@ -231,22 +279,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             const uint32_t a = tmem + kWeightColumns + (half * kSlots + ws) * kSlotColumns;
 #pragma unroll
                             for (int k = 0; k < kBlockK / 16; ++k)
-                                mma_f16_pair_tmem(tmem + half * kTileRows, a + k * 8, db + k / 4 * (kHalfRows >> 4) + k % 4 * 2,
+                                mma_f16_pair_tmem(tmem + half * kTileRows, a + k * 8, db + k / 4 * (step_bytes >> 5) + k % 4 * 2,
                                                   idesc, b > 0 || k > 0);
                             mma_commit_pair(smem_addr(&s->w_empty[half][ws]));
                             if (b + 1 == p.kb) mma_commit_pair(smem_addr(&s->acc_full[half]));
                         }
-                        mma_commit_pair(smem_addr(&s->rows_empty[rs]));
+                        if (end) mma_commit_pair(smem_addr(&s->rows_empty[rs]));
                     }
                     __syncwarp();
                     if (block >= 0) ++mine;
+                    if (end) ++batch;
                 }
             }
         }
-    } else if (warp >= 4 && warp < 4 + kWeightWarps) {
+    } else if (warp >= 4 && warp < kFirstEpilogue) {
         // ---- weights: thread = one weight row, 128 bytes a step -> 64 columns of TMEM.  Arrivals are relaxed: what they
         // announce is in TMEM, which the tcgen05 waits and fences on both sides put in order ----
-        regs_down<72>();
+        regs_down<64>();
         const int half = (warp - 4) / 4, quarter = warp % 4, row = quarter * kWarp + lane;
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + kWeightColumns + half * kSlots * kSlotColumns;
         const uint32_t full = mapa(smem_addr(&s->w_full[half][0]), 0);
@@ -285,28 +334,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&s->raw_empty[st]);
             }
         }
-    } else if (warp >= 4 + kWeightWarps + kEpilogueWarps) {
-        // ---- rows: a step to each of four warps in turn, 128 bytes of a row -> two halves of 64 fp16 in swizzled rows.
-        // Their arrival releases shared memory to the cluster, which takes longer than a step of the tensor cores
-        // (1000 cycles and more: two warps that shared every step made each of them as long), hence the turns ----
-        regs_down<72>();
-        const uint32_t rs = warp - (4 + kWeightWarps + kEpilogueWarps);  // warp and slot
-        const uint32_t full = mapa(smem_addr(&s->rows_full[rs]), 0);
-        uint32_t it = 0;
+    } else if (warp >= kRelay) {
+        regs_down<48>();
+        if (warp == kRelay && lane == 0) {
+            // ---- relay: batches of rows, as this CTA's part of each is complete, announced to the pair's first CTA.  That
+            // releases shared memory to the cluster, and an SM gets through one such release in some 1700 cycles
+            // however many warps ask for one, where the tensor cores take 1024 for a full step: hence the batches ----
+            const uint32_t full = mapa(smem_addr(&s->rows_full[0]), 0);
+            uint32_t batch = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const int in_batch = batch_steps(width(walk.at(t)));
+                for (int b = 0; b < p.kb; b += in_batch, ++batch) {
+                    const uint32_t rs = batch % kRowSlots;
+                    if (!(ok = wait_for(&s->converted[rs], batch / kRowSlots & 1, &s->waits))) break;
+                    mbar_arrive_cluster(full + rs * 8);
+                }
+            }
+        } else if (warp == kRelay + 1 && lane == 0) {
+            // ---- gate: each step's converting warp told that the step's batch has a slot.  A barrier tells phases apart by
+            // one bit, so the warps, which take some of the steps, could not wait for all of the slots in turn ----
+            uint32_t it = 0, batch = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const int in_batch = batch_steps(width(walk.at(t)));
+                for (int b = 0; b < p.kb; ++b, ++it) {
+                    const uint32_t st = it % kRowStages;
+                    if (b % in_batch == 0) {
+                        ok = wait_for(&s->rows_empty[batch % kRowSlots], batch / kRowSlots & 1 ^ 1, &s->waits);
+                        ++batch;
+                    }
+                    if (!(ok = ok && wait_for(&s->in_empty[st], it / kRowStages & 1 ^ 1, &s->waits))) break;
+                    mbar_arrive(&s->go[st]);
+                }
+            }
+        }
+    } else if (warp >= kFirstRow) {
+        // ---- rows: a step to each of four warps in turn, 128 bytes of a row -> two halves of 64 fp16 in swizzled rows ----
+        regs_down<48>();
+        const uint32_t st = warp - kFirstRow, from = smem_addr(s_in) + st * kRowBytes;  // the warp's stage
+        uint32_t batches = 0, steps = 0;  // before this tile
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
-            const int mine = width(walk.at(t)) / 2;  // rows of this CTA
-            for (int b = 0; b < p.kb; ++b, ++it) {
-                if (it % kRowSlots != rs) continue;
-                const uint32_t st = it % kStages;
-                ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits) &&
-                     wait_for(&s->rows_empty[rs], it / kRowSlots & 1 ^ 1, &s->waits);
-                ok = __all_sync(0xffffffffu, ok);
+            const int n = width(walk.at(t)), mine = n / 2, in_batch = batch_steps(n);  // mine: rows of this CTA
+            const uint32_t step_bytes = kBatchBytes / in_batch;
+            for (int b = (st - steps) % kRowStages; b < p.kb; b += kRowStages) {
+                const uint32_t batch = batches + b / in_batch, rs = batch % kRowSlots;
+                const uint32_t phase = (steps + b) / kRowStages & 1;
+                ok = __all_sync(0xffffffffu, wait_for(&s->go[st], phase, &s->waits) && wait_for(&s->in_full[st], phase, &s->waits));
                 if (!ok) break;
-                const uint32_t from = smem_addr(s_stages) + st * kStageBytes + 2 * kWeightBytes;
 #pragma unroll 1
                 for (int row = lane; row < mine; row += kWarp) {
-                    const uint32_t to = smem_addr(s_rows) + rs * kRowsBytes + row * 128;
+                    const uint32_t to = smem_addr(s_rows) + rs * kBatchBytes + b % in_batch * step_bytes + row * 128;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {  // 16 values
                         const uint4 x = row_piece(from, row, j);
@@ -318,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             to + j / 4 * kHalfRows + (((j % 4 * 2 + h) ^ (row & 7)) << 4)),
+                                             to + j / 4 * (step_bytes / 2) + (((j % 4 * 2 + h) ^ (row & 7)) << 4)),
                                          "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3])
                                          : "memory");
                     }
@@ -326,15 +405,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&s->raw_empty[st]);
-                    mbar_arrive_cluster(full);
+                    mbar_arrive(&s->in_empty[st]);
+                    // a tile's last batch may be short: its last step arrives for the ones that it lacks
+                    const int at = b % in_batch, each = kMostSteps / in_batch;
+                    mbar_arrive_many(&s->converted[rs], b + 1 == p.kb ? kMostSteps - at * each : each);
                 }
             }
+            batches += (p.kb + in_batch - 1) / in_batch;
+            steps += p.kb;
         }
-    } else if (warp >= 4 + kWeightWarps) {
+    } else if (warp >= kFirstEpilogue) {
         // ---- epilogue: lane = one output column, a quarter of a block's 128 to a warp ----
-        regs_up<112>();
-        const int half = (warp - 4 - kWeightWarps) / 4, quarter = warp % 4;
+        regs_up<120>();
+        const int half = (warp - kFirstEpilogue) / 4, quarter = warp % 4;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16);
         const uint32_t empty = mapa(smem_addr(&s->acc_empty[0]), 0);
         uint32_t acc_phase = 0;
@@ -353,6 +436,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float* ws = p.g.w_scales + static_cast<long long>(tl.e) * (kSwiglu ? 2 : 1) * p.g.n + col;
             const float s0 = on ? __ldg(ws) : 0.0f, s1 = on && kSwiglu ? __ldg(ws + p.g.n) : 0.0f;
             const int rows = min(tl.rows, kTileRows);
+            float scale[kTileRows / 32];  // of row 32 i + lane
+#pragma unroll
+            for (int c = 0; c < kTileRows; c += 32) scale[c / 32] = c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
             ok = wait_for(&s->acc_full[half], acc_phase, &s->waits);
             if (kSwiglu) ok = ok && wait_for(&s->acc_full[half ^ 1], acc_phase, &s->waits);
             ok = __all_sync(0xffffffffu, ok);
@@ -374,11 +460,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         hand_back(1);
                     }
                     if (c >= rows) continue;
-                    const float scale = c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
                     float* to = p.g.h + (r0 + c) * p.g.n + col;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float as = __shfl_sync(0xffffffffu, scale, j);
+                        const float as = __shfl_sync(0xffffffffu, c < 32 ? scale[0] : c < 64 ? scale[1] : c < 96 ? scale[2] : scale[3], j);
                         const float2 a = unpack2(x[j / 2]), b = unpack2(y[j / 2]);
                         const float gate = (j & 1 ? a.y : a.x) * (as * s0), up = (j & 1 ? b.y : b.x) * (as * s1);
                         if (on && c + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit(gate, up);
@@ -390,13 +475,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kTileRows; c += 32) {
                     if (c >= rows) continue;
-                    const float scale = c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;
                     uint64_t x[16];
                     tmem_read(lanes + half * kTileRows + c, x);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float2 a = unpack2(x[j]);
-                        const float as0 = __shfl_sync(0xffffffffu, scale, 2 * j), as1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
+                        const float as0 = __shfl_sync(0xffffffffu, scale[c / 32], 2 * j);
+                        const float as1 = __shfl_sync(0xffffffffu, scale[c / 32], 2 * j + 1);
                         const __nv_bfloat162 h = __floats2bfloat162_rn(a.x * (as0 * s0), a.y * (as1 * s0));
                         v[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
                     }
@@ -469,7 +554,7 @@ cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
     if (!gemm::make_map(&w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf) ||
         !gemm::make_map(&a, g.a, g.k, g.cap, g.E, kTileRows / 2) || !gemm::make_map(&a16, g.a, g.k, g.cap, g.E, kChunk))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + kStages * kStageBytes + kRowSlots * kRowsBytes + sizeof(Shared);
+    const size_t smem = 1024 + kStages * kStageBytes + kRowStages * kRowBytes + kRowSlots * kBatchBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows - 1) / kTileRows) * ((g.n + kBlock - 1) / kBlock);
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);

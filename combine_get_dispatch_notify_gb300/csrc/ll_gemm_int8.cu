@@ -130,6 +130,32 @@ __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) 
         : "memory");
 }
 
+// Matrix m (8 columns x 8 rows, lane T: column T / 4, rows 2 (T % 4) and the next) for m = a, b, c, d -> 16 bytes of row
+// lane / 4: the 8 columns of matrix lane % 4.
+__device__ __forceinline__ uint4 rows_of_matrices(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int lane) {
+    const uint32_t in[4] = {a, b, c, d};
+    uint32_t v[4];  // lane T: row T / 4, columns 2 (T % 4) and the next of matrix m
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(v[m]) : "r"(in[m]));
+    // 4 x 4 words between the four lanes of a row
+#pragma unroll
+    for (int s = 1; s <= 2; s *= 2) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t& lo = v[s == 1 ? 2 * i : i];
+            uint32_t& hi = v[s == 1 ? 2 * i + 1 : i + 2];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+            if (up)
+                lo = got;
+            else
+                hi = got;
+        }
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // The block that accumulator `half` has of the pair's tile number `i`, or -1.
 __device__ __forceinline__ int block_of(int live, int blocks, int i, int half) {
     if (blocks == 2) return half < live ? half : -1;
@@ -470,27 +496,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                // all rows into registers, so that the accumulator is free while they are stored
+                // All rows into registers, so that the accumulator is free while they are stored: as 8 x 8 matrices of
+                // columns and rows, which are then transposed between the lanes so that each stores 16 bytes of a row.
+                // (Columns stored by their lanes, 2 bytes each, took 9 us a tile, three quarters of its time at k = 512.)
                 uint32_t v[kTileRows / 2];
+                float ws[4];
 #pragma unroll
-                for (int c = 0; c < kTileRows; c += 32) {
-                    if (c >= rows) continue;
-                    uint64_t x[16];
-                    tmem_read(lanes + half * kTileRows + c, x);
+                for (int m = 0; m < 4; ++m) ws[m] = __shfl_sync(0xffffffffu, s0, 8 * m + lane / 4);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 a = unpack2(x[j]);
-                        const float as0 = __shfl_sync(0xffffffffu, scale[c / 32], 2 * j);
-                        const float as1 = __shfl_sync(0xffffffffu, scale[c / 32], 2 * j + 1);
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(a.x * (as0 * s0), a.y * (as1 * s0));
-                        v[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int c = 0; c < kTileRows; c += 32)
+                    if (c < rows) {
+                        uint64_t x[16];
+                        tmem_read_matrices(lanes + half * kTileRows + c, x);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float as0 = __shfl_sync(0xffffffffu, scale[c / 32], 8 * j + lane % 4 * 2);
+                            const float as1 = __shfl_sync(0xffffffffu, scale[c / 32], 8 * j + lane % 4 * 2 + 1);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const float2 d = unpack2(x[4 * j + m]);
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(d.x * (as0 * ws[m]), d.y * (as1 * ws[m]));
+                                v[c / 2 + 4 * j + m] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                        }
                     }
-                }
                 hand_back(half);
-                uint16_t* to = static_cast<uint16_t*>(p.g.y) + r0 * p.g.n + col;
+                const int to_col = col - lane + lane % 4 * 8;  // of this lane's 16 bytes
+                uint16_t* to = static_cast<uint16_t*>(p.g.y) + r0 * p.g.n + to_col;
 #pragma unroll
-                for (int j = 0; j < kTileRows; ++j)
-                    if (on && j < rows) to[static_cast<long long>(j) * p.g.n] = static_cast<uint16_t>(v[j / 2] >> (j % 2 * 16));
+                for (int c = 0; c < kTileRows; c += 8)
+                    if (c < rows) {
+                        const uint4 w = rows_of_matrices(v[c / 2], v[c / 2 + 1], v[c / 2 + 2], v[c / 2 + 3], lane);
+                        if (c + lane / 4 < rows && to_col < p.g.n) st_v4(to + static_cast<long long>(c + lane / 4) * p.g.n, w);
+                    }
             }
         }
     }

@@ -43,17 +43,16 @@ constexpr int kHalf = 128;
 constexpr int kTileRows = 128;            // most rows of an expert in a tile
 constexpr int kBlockK = 128;              // int8: one 128-byte swizzled row
 constexpr int kWeightBytes = kHalf * kBlockK;          // a CTA's part of a block, 16 KB
-constexpr int kStageBytes = 2 * kWeightBytes;
-constexpr int kStages = 3;                // of weights
-constexpr int kRowBytes = kTileRows / 2 * kBlockK;     // a CTA's part of a step of rows, 8 KB
+constexpr int kStages = 6;                // of weights, a block's step each
+constexpr int kRowBytes = kTileRows / 2 * kBlockK;     // a CTA's part of a stage of rows, 8 KB: one step of a full tile
 constexpr int kRowStages = 4;             // of rows: one to each warp that converts them
 constexpr int kChunk = 16;                // rows of the smaller box of a
-constexpr int kBatchBytes = 2 * kTileRows / 2 * 2 * kBlockK;  // a batch of rows in fp16: two steps of a full tile, 32 KB
+constexpr int kBatchBytes = 4 * kRowBytes;             // a batch of rows, two stages, in fp16: 32 KB
 constexpr int kSlots = 2;                 // of converted steps of weights, in TMEM
 constexpr int kRowSlots = 3;              // of batches of converted rows, in shared memory
 constexpr int kWeightWarps = 8, kEpilogueWarps = 8;
 constexpr int kRowWarps = 4;              // a stage of rows each
-constexpr int kMostSteps = 8;             // of a batch of rows
+constexpr int kBatchStages = 2;           // stages of rows of a batch
 constexpr int kFirstEpilogue = 4 + kWeightWarps, kFirstRow = kFirstEpilogue + kEpilogueWarps;  // warps
 constexpr int kRelay = kFirstRow + kRowWarps;
 constexpr int kThreads = (kRelay + 4) * kWarp;  // whole warpgroups, whose registers are dealt out
@@ -72,7 +71,7 @@ struct Shared {
     uint64_t raw_empty[kStages];      // its converting warps have read them
     uint64_t in_full[kRowStages];     // this CTA's rows have landed
     uint64_t in_empty[kRowStages];    // the warp that converts them has read them
-    uint64_t go[kRowStages];          // the step's batch has a slot
+    uint64_t go[kRowStages];          // the stage's batch has a slot
     uint64_t converted[kRowSlots];    // this CTA's part of a batch of rows is in shared memory
     uint64_t w_full[2][kSlots];       // leader's: a block's step is in both CTAs' TMEM
     uint64_t w_empty[2][kSlots];      // both: the MMAs that read it are done
@@ -118,8 +117,8 @@ __device__ __forceinline__ uint4 row_piece(uint32_t tile, int row, int piece) {
     return v;
 }
 
-// Steps of a batch of rows: as many as have room, by the rows of a tile (a multiple of 32).
-__device__ __forceinline__ int batch_steps(int width) { return width > 64 ? 2 : width > 32 ? 4 : kMostSteps; }
+// Steps of a stage of rows: as many as have room, by the rows of a tile (a multiple of 32).
+__device__ __forceinline__ int stage_steps(int width) { return width > 64 ? 1 : width > 32 ? 2 : 4; }
 
 // Several arrivals at once.
 __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
@@ -169,7 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t s_raw[];
     // swizzled tiles first, on a 1024-byte boundary, at the same offset in both CTAs
     uint8_t* s_stages = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
-    uint8_t* s_in = s_stages + kStages * kStageBytes;
+    uint8_t* s_in = s_stages + kStages * kWeightBytes;
     uint8_t* s_rows = s_in + kRowStages * kRowBytes;
     Shared* s = reinterpret_cast<Shared*>(s_rows + kRowSlots * kBatchBytes);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
@@ -192,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&s->go[i], 1);
         }
         for (int i = 0; i < kRowSlots; ++i) {
-            mbar_init(&s->converted[i], kMostSteps);
+            mbar_init(&s->converted[i], kBatchStages);
             mbar_init(&s->rows_full[i], 2);
             mbar_init(&s->rows_empty[i], 2);
         }
@@ -237,14 +236,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const RowTile tl = walk.at(t);
                 const int live = live_blocks(tl), w0 = first_column(tl) + static_cast<int>(rank) * kHalf;
-                for (int b = 0; b < p.kb; ++b, ++it) {
+                for (int b = 0; b < p.kb * live && ok; ++b, ++it) {
                     const uint32_t st = it % kStages;
                     if (!(ok = wait_for(&s->raw_empty[st], it / kStages & 1 ^ 1, &s->waits))) break;
-                    const uint32_t bar = smem_addr(&s->raw_full[st]), to = smem_addr(s_stages) + st * kStageBytes;
-                    mbar_arrive_expect_tx(&s->raw_full[st], live * kWeightBytes);
-                    for (int i = 0; i < live; ++i)
-                        tma_load_3d_alone(to + i * kWeightBytes, &map_w, b * kBlockK, kSwiglu ? w0 : w0 + i * kBlock,
-                                          kSwiglu ? 2 * tl.e + i : tl.e, bar);
+                    const int step = live == 2 ? b / 2 : b, i = live == 2 ? b % 2 : 0;
+                    mbar_arrive_expect_tx(&s->raw_full[st], kWeightBytes);
+                    tma_load_3d_alone(smem_addr(s_stages) + st * kWeightBytes, &map_w, step * kBlockK, kSwiglu ? w0 : w0 + i * kBlock,
+                                      kSwiglu ? 2 * tl.e + i : tl.e, smem_addr(&s->raw_full[st]));
                 }
             }
             // every stage has been read before the CTA may leave
@@ -258,17 +256,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const RowTile tl = walk.at(t);
-                const int n = width(tl), a0 = tl.m0 + static_cast<int>(rank) * (n / 2);
-                for (int b = 0; b < p.kb; ++b, ++it) {
+                const int n = width(tl), a0 = tl.m0 + static_cast<int>(rank) * (n / 2), in_stage = stage_steps(n);
+                for (int b0 = 0; b0 < p.kb; b0 += in_stage, ++it) {
                     const uint32_t st = it % kRowStages;
                     if (!(ok = wait_for(&s->in_empty[st], it / kRowStages & 1 ^ 1, &s->waits))) break;
-                    const uint32_t bar = smem_addr(&s->in_full[st]), to = smem_addr(s_in) + st * kRowBytes;
-                    mbar_arrive_expect_tx(&s->in_full[st], n / 2 * kBlockK);
-                    if (n == kTileRows)
-                        tma_load_3d_alone(to, &map_a, b * kBlockK, a0, tl.e, bar);
-                    else
-                        for (int i = 0; i < n / 2; i += kChunk)
-                            tma_load_3d_alone(to + i * kBlockK, &map_a16, b * kBlockK, a0 + i, tl.e, bar);
+                    const uint32_t bar = smem_addr(&s->in_full[st]);
+                    uint32_t to = smem_addr(s_in) + st * kRowBytes;
+                    const int steps = min(in_stage, p.kb - b0);
+                    mbar_arrive_expect_tx(&s->in_full[st], steps * (n / 2) * kBlockK);
+                    for (int b = b0; b < b0 + steps; ++b, to += n / 2 * kBlockK)
+                        if (n == kTileRows)
+                            tma_load_3d_alone(to, &map_a, b * kBlockK, a0, tl.e, bar);
+                        else
+                            for (int i = 0; i < n / 2; i += kChunk)
+                                tma_load_3d_alone(to + i * kBlockK, &map_a16, b * kBlockK, a0 + i, tl.e, bar);
                 }
             }
             for (int i = 0; i < kRowStages && ok; ++i, ++it)
@@ -283,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
                 const RowTile tl = walk.at(t);
                 const int block = __shfl_sync(0xffffffffu, block_of(live_blocks(tl), blocks, i, half), 0);
-                const int n = __shfl_sync(0xffffffffu, width(tl), 0), in_batch = batch_steps(n);
+                const int n = __shfl_sync(0xffffffffu, width(tl), 0), in_batch = kBatchStages * stage_steps(n);
                 const uint32_t idesc = f16_idesc(kBlock, n), step_bytes = kBatchBytes / in_batch;
                 if (block >= 0) {
                     ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
@@ -328,16 +329,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t it = 0, mine = 0;
         bool ok = true;
         for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
-            const int block = block_of(live_blocks(walk.at(t)), blocks, i, half);
-            for (int b = 0; b < p.kb; ++b, ++it) {
+            const int live = live_blocks(walk.at(t)), block = block_of(live, blocks, i, half);
+            for (int b = 0; b < p.kb * live; ++b, ++it) {
                 const uint32_t st = it % kStages, ws = mine % kSlots;
+                const bool own = block >= 0 && (live == 1 || b % 2 == block);
                 ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits);
-                if (block >= 0) ok = ok && wait_for(&s->w_empty[half][ws], mine / kSlots & 1 ^ 1, &s->waits);
+                if (own) ok = ok && wait_for(&s->w_empty[half][ws], mine / kSlots & 1 ^ 1, &s->waits);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (block >= 0) {
+                if (own) {
                     tc_fence_after();
-                    const uint32_t from = smem_addr(s_stages) + st * kStageBytes + block * kWeightBytes;
+                    const uint32_t from = smem_addr(s_stages) + st * kWeightBytes;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t v[32];
@@ -351,13 +353,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         tmem_write(to + ws * kSlotColumns + h * 32, v);
                     }
+                    // the bytes are in registers: their stage can be filled again while TMEM takes them
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->raw_empty[st]);
                     tmem_write_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(full + ws * 8);
                     ++mine;
+                } else if (lane == 0) {
+                    mbar_arrive(&s->raw_empty[st]);  // the other block's; every stage is waited for, a barrier tells phases apart by one bit
                 }
-                if (lane == 0) mbar_arrive(&s->raw_empty[st]);
             }
         }
     } else if (warp >= kRelay) {
@@ -370,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t batch = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const int in_batch = batch_steps(width(walk.at(t)));
+                const int in_batch = kBatchStages * stage_steps(width(walk.at(t)));
                 for (int b = 0; b < p.kb; b += in_batch, ++batch) {
                     const uint32_t rs = batch % kRowSlots;
                     if (!(ok = wait_for(&s->converted[rs], batch / kRowSlots & 1, &s->waits))) break;
@@ -378,15 +384,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == kRelay + 1 && lane == 0) {
-            // ---- gate: each step's converting warp told that the step's batch has a slot.  A barrier tells phases apart by
-            // one bit, so the warps, which take some of the steps, could not wait for all of the slots in turn ----
+            // ---- gate: each stage's converting warp told that the stage's batch has a slot.  A barrier tells phases apart by
+            // one bit, so the warps, which take some of the stages, could not wait for all of the slots in turn ----
             uint32_t it = 0, batch = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const int in_batch = batch_steps(width(walk.at(t)));
-                for (int b = 0; b < p.kb; ++b, ++it) {
+                const int in_stage = stage_steps(width(walk.at(t)));
+                for (int b = 0, g = 0; b < p.kb; b += in_stage, ++g, ++it) {
                     const uint32_t st = it % kRowStages;
-                    if (b % in_batch == 0) {
+                    if (g % kBatchStages == 0) {
                         ok = wait_for(&s->rows_empty[batch % kRowSlots], batch / kRowSlots & 1 ^ 1, &s->waits);
                         ++batch;
                     }
@@ -396,25 +402,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp >= kFirstRow) {
-        // ---- rows: a step to each of four warps in turn, 128 bytes of a row -> two halves of 64 fp16 in swizzled rows ----
+        // ---- rows: a stage to each of four warps in turn, 128 bytes of a row -> two halves of 64 fp16 in swizzled rows ----
         regs_down<48>();
         const uint32_t st = warp - kFirstRow, from = smem_addr(s_in) + st * kRowBytes;  // the warp's stage
-        uint32_t batches = 0, steps = 0;  // before this tile
+        uint32_t batches = 0, stages = 0;  // before this tile
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
-            const int n = width(walk.at(t)), mine = n / 2, in_batch = batch_steps(n);  // mine: rows of this CTA
-            const uint32_t step_bytes = kBatchBytes / in_batch;
-            for (int b = (st - steps) % kRowStages; b < p.kb; b += kRowStages) {
-                const uint32_t batch = batches + b / in_batch, rs = batch % kRowSlots;
-                const uint32_t phase = (steps + b) / kRowStages & 1;
+            const int n = width(walk.at(t)), mine = n / 2, in_stage = stage_steps(n);  // mine: rows of this CTA
+            const int all = (p.kb + in_stage - 1) / in_stage;                          // stages of this tile
+            const uint32_t step_bytes = kBatchBytes / (kBatchStages * in_stage);
+            for (int g = (st - stages) % kRowStages; g < all; g += kRowStages) {
+                const uint32_t batch = batches + g / kBatchStages, rs = batch % kRowSlots, phase = (stages + g) / kRowStages & 1;
                 ok = __all_sync(0xffffffffu, wait_for(&s->go[st], phase, &s->waits) && wait_for(&s->in_full[st], phase, &s->waits));
                 if (!ok) break;
+                const int lines = min(in_stage, p.kb - g * in_stage) * mine;
+                const uint32_t slot = smem_addr(s_rows) + rs * kBatchBytes + g % kBatchStages * in_stage * step_bytes;
 #pragma unroll 1
-                for (int row = lane; row < mine; row += kWarp) {
-                    const uint32_t to = smem_addr(s_rows) + rs * kBatchBytes + b % in_batch * step_bytes + row * 128;
+                for (int line = lane; line < lines; line += kWarp) {
+                    const int step = in_stage == 1 ? 0 : line / mine, row = line - step * mine;
+                    const uint32_t to = slot + step * step_bytes + row * 128;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {  // 16 values
-                        const uint4 x = row_piece(from, row, j);
+                    for (int j = 0; j < 8; ++j) {  // 16 values; steps are whole groups of eight rows apart, so `line` swizzles as `row`
+                        const uint4 x = row_piece(from, line, j);
                         uint32_t v[8];
                         widen(x.x, v[0], v[1]);
                         widen(x.y, v[2], v[3]);
@@ -432,13 +441,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&s->in_empty[st]);
-                    // a tile's last batch may be short: its last step arrives for the ones that it lacks
-                    const int at = b % in_batch, each = kMostSteps / in_batch;
-                    mbar_arrive_many(&s->converted[rs], b + 1 == p.kb ? kMostSteps - at * each : each);
+                    // a tile's last batch may be one stage short: its last stage arrives for that too
+                    mbar_arrive_many(&s->converted[rs], g + 1 == all ? kBatchStages - g % kBatchStages : 1);
                 }
             }
-            batches += (p.kb + in_batch - 1) / in_batch;
-            steps += p.kb;
+            batches += (all + kBatchStages - 1) / kBatchStages;
+            stages += all;
         }
     } else if (warp >= kFirstEpilogue) {
         // ---- epilogue: lane = one output column, a quarter of a block's 128 to a warp ----
@@ -592,7 +600,7 @@ cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
     if (!gemm::make_map(&w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf) ||
         !gemm::make_map(&a, g.a, g.k, g.cap, g.E, kTileRows / 2) || !gemm::make_map(&a16, g.a, g.k, g.cap, g.E, kChunk))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + kStages * kStageBytes + kRowStages * kRowBytes + kRowSlots * kBatchBytes + sizeof(Shared);
+    const size_t smem = 1024 + kStages * kWeightBytes + kRowStages * kRowBytes + kRowSlots * kBatchBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows - 1) / kTileRows) * ((g.n + kBlock - 1) / kBlock);
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);

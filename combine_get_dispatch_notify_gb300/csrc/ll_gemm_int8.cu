@@ -40,26 +40,32 @@ using gemm::Waits;
 
 constexpr int kBlock = 256;               // weight rows of a block; each CTA has half
 constexpr int kHalf = 128;
-constexpr int kTileRows = 128;            // most rows of an expert in a tile
 constexpr int kBlockK = 128;              // int8: one 128-byte swizzled row
-constexpr int kWeightBytes = kHalf * kBlockK;          // a CTA's part of a block, 16 KB
-constexpr int kStages = 6;                // of weights, a block's step each
-constexpr int kRowBytes = kTileRows / 2 * kBlockK;     // a CTA's part of a stage of rows, 8 KB: one step of a full tile
+constexpr int kWeightBytes = kHalf * kBlockK;          // a CTA's part of a block's step, 16 KB
 constexpr int kRowStages = 4;             // of rows: one to each warp that converts them
-constexpr int kChunk = 16;                // rows of the smaller box of a
-constexpr int kBatchBytes = 4 * kRowBytes;             // a batch of rows, two stages, in fp16: 32 KB
-constexpr int kSlots = 2;                 // of converted steps of weights, in TMEM
 constexpr int kRowSlots = 3;              // of batches of converted rows, in shared memory
+constexpr int kBatchStages = 2;           // stages of rows of a batch
+constexpr int kChunk = 16;                // rows of the smaller box of a
+// What depends on the most rows of a tile, 128 or 64: with 64 the room that rows and sums leave holds more weights in
+// flight and one more converted step of them.
+template <int kTileRows>
+struct Sizes {
+    static constexpr int kStages = kTileRows == 128 ? 6 : 10;         // of weights, a block's step each
+    static constexpr int kSlots = kTileRows == 128 ? 2 : 3;           // of converted steps of weights, in TMEM
+    static constexpr int kRowBytes = kTileRows / 2 * kBlockK;         // a CTA's part of a stage of rows: one step of a full tile
+    static constexpr int kBatchBytes = kBatchStages * 2 * kRowBytes;  // a batch of rows in fp16
+    // steps of a stage of rows: as many as have room, by the rows of a tile (a multiple of 32)
+    static __device__ __forceinline__ int stage_steps(int width) { return kTileRows / (width > 64 ? 128 : width > 32 ? 64 : 32); }
+};
+constexpr int kMostStages = 10, kMostSlots = 3;
 constexpr int kWeightWarps = 8, kEpilogueWarps = 8;
 constexpr int kRowWarps = 4;              // a stage of rows each
-constexpr int kBatchStages = 2;           // stages of rows of a batch
 constexpr int kFirstEpilogue = 4 + kWeightWarps, kFirstRow = kFirstEpilogue + kEpilogueWarps;  // warps
 constexpr int kRelay = kFirstRow + kRowWarps;
 constexpr int kThreads = (kRelay + 4) * kWarp;  // whole warpgroups, whose registers are dealt out
 static_assert(kRowWarps == kRowStages && kRowWarps == 4, "a warp owns a stage of rows");
 constexpr int kTmemColumns = 512;
 constexpr int kSlotColumns = kBlockK / 2;              // TMEM columns of a step of weights
-constexpr int kWeightColumns = 2 * kTileRows;          // where they begin, behind both accumulators
 
 struct Params {
     Int8GemmArgs g;
@@ -67,14 +73,14 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t raw_full[kStages];       // this CTA's weights have landed
-    uint64_t raw_empty[kStages];      // its converting warps have read them
+    uint64_t raw_full[kMostStages];   // this CTA's weights have landed
+    uint64_t raw_empty[kMostStages];  // its converting warps have read them
     uint64_t in_full[kRowStages];     // this CTA's rows have landed
     uint64_t in_empty[kRowStages];    // the warp that converts them has read them
     uint64_t go[kRowStages];          // the stage's batch has a slot
     uint64_t converted[kRowSlots];    // this CTA's part of a batch of rows is in shared memory
-    uint64_t w_full[2][kSlots];       // leader's: a block's step is in both CTAs' TMEM
-    uint64_t w_empty[2][kSlots];      // both: the MMAs that read it are done
+    uint64_t w_full[2][kMostSlots];   // leader's: a block's step is in both CTAs' TMEM
+    uint64_t w_empty[2][kMostSlots];  // both: the MMAs that read it are done
     uint64_t rows_full[kRowSlots];    // leader's: a batch of rows is in both CTAs' shared memory
     uint64_t rows_empty[kRowSlots];   // both: both blocks' MMAs that read it are done
     uint64_t acc_full[2];             // both: a block's sums are in TMEM
@@ -117,9 +123,6 @@ __device__ __forceinline__ uint4 row_piece(uint32_t tile, int row, int piece) {
     return v;
 }
 
-// Steps of a stage of rows: as many as have room, by the rows of a tile (a multiple of 32).
-__device__ __forceinline__ int stage_steps(int width) { return width > 64 ? 1 : width > 32 ? 2 : 4; }
-
 // Several arrivals at once.
 __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
     asm volatile(
@@ -161,10 +164,14 @@ __device__ __forceinline__ int block_of(int live, int blocks, int i, int half) {
     return (i & 1) == half ? 0 : -1;
 }
 
-template <bool kSwiglu>
+template <bool kSwiglu, int kTileRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ll_gemm_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                         const __grid_constant__ CUtensorMap map_a16, const Params p) {
+    using S = Sizes<kTileRows>;
+    constexpr int kStages = S::kStages, kSlots = S::kSlots, kRowBytes = S::kRowBytes, kBatchBytes = S::kBatchBytes;
+    constexpr int kWeightColumns = 2 * kTileRows;  // TMEM columns: the weights, behind both accumulators
+    static_assert(kWeightColumns + 2 * kSlots * kSlotColumns <= kTmemColumns && kStages <= kMostStages && kSlots <= kMostSlots, "");
     extern __shared__ uint8_t s_raw[];
     // swizzled tiles first, on a 1024-byte boundary, at the same offset in both CTAs
     uint8_t* s_stages = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
@@ -256,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const RowTile tl = walk.at(t);
-                const int n = width(tl), a0 = tl.m0 + static_cast<int>(rank) * (n / 2), in_stage = stage_steps(n);
+                const int n = width(tl), a0 = tl.m0 + static_cast<int>(rank) * (n / 2), in_stage = S::stage_steps(n);
                 for (int b0 = 0; b0 < p.kb; b0 += in_stage, ++it) {
                     const uint32_t st = it % kRowStages;
                     if (!(ok = wait_for(&s->in_empty[st], it / kRowStages & 1 ^ 1, &s->waits))) break;
@@ -284,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
                 const RowTile tl = walk.at(t);
                 const int block = __shfl_sync(0xffffffffu, block_of(live_blocks(tl), blocks, i, half), 0);
-                const int n = __shfl_sync(0xffffffffu, width(tl), 0), in_batch = kBatchStages * stage_steps(n);
+                const int n = __shfl_sync(0xffffffffu, width(tl), 0), in_batch = kBatchStages * S::stage_steps(n);
                 const uint32_t idesc = f16_idesc(kBlock, n), step_bytes = kBatchBytes / in_batch;
                 if (block >= 0) {
                     ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
@@ -326,11 +333,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int half = (warp - 4) / 4, quarter = warp % 4, row = quarter * kWarp + lane;
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + kWeightColumns + half * kSlots * kSlotColumns;
         const uint32_t full = mapa(smem_addr(&s->w_full[half][0]), 0);
-        uint32_t it = 0, mine = 0;
+        // Where every tile has two blocks, a warp passes over the other block's stages and arrives for both groups.  Elsewhere
+        // stages do not alternate, and every warp waits for each of them: a barrier tells phases apart by one bit.
+        const bool paired = kSwiglu || (blocks == 2 && columns % 2 == 0);
+        uint32_t it = paired ? half : 0, mine = 0;
         bool ok = true;
         for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
-            const int live = live_blocks(walk.at(t)), block = block_of(live, blocks, i, half);
-            for (int b = 0; b < p.kb * live; ++b, ++it) {
+            const int col = t % walk.tiles_n, live = kSwiglu ? 2 : min(blocks, columns - col * blocks);
+            const int block = block_of(live, blocks, i, half);
+            for (int b = paired ? half : 0; b < p.kb * live; b += paired ? 2 : 1, it += paired ? 2 : 1) {
                 const uint32_t st = it % kStages, ws = mine % kSlots;
                 const bool own = block >= 0 && (live == 1 || b % 2 == block);
                 ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits);
@@ -355,14 +366,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     // the bytes are in registers: their stage can be filled again while TMEM takes them
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->raw_empty[st]);
+                    if (lane == 0) mbar_arrive_many(&s->raw_empty[st], paired ? 2 : 1);
                     tmem_write_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(full + ws * 8);
                     ++mine;
                 } else if (lane == 0) {
-                    mbar_arrive(&s->raw_empty[st]);  // the other block's; every stage is waited for, a barrier tells phases apart by one bit
+                    mbar_arrive(&s->raw_empty[st]);  // the other block's
                 }
             }
         }
@@ -376,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t batch = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const int in_batch = kBatchStages * stage_steps(width(walk.at(t)));
+                const int in_batch = kBatchStages * S::stage_steps(width(walk.at(t)));
                 for (int b = 0; b < p.kb; b += in_batch, ++batch) {
                     const uint32_t rs = batch % kRowSlots;
                     if (!(ok = wait_for(&s->converted[rs], batch / kRowSlots & 1, &s->waits))) break;
@@ -389,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0, batch = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const int in_stage = stage_steps(width(walk.at(t)));
+                const int in_stage = S::stage_steps(width(walk.at(t)));
                 for (int b = 0, g = 0; b < p.kb; b += in_stage, ++g, ++it) {
                     const uint32_t st = it % kRowStages;
                     if (g % kBatchStages == 0) {
@@ -408,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t batches = 0, stages = 0;  // before this tile
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
-            const int n = width(walk.at(t)), mine = n / 2, in_stage = stage_steps(n);  // mine: rows of this CTA
+            const int n = width(walk.at(t)), mine = n / 2, in_stage = S::stage_steps(n);  // mine: rows of this CTA
             const int all = (p.kb + in_stage - 1) / in_stage;                          // stages of this tile
             const uint32_t step_bytes = kBatchBytes / (kBatchStages * in_stage);
             for (int g = (st - stages) % kRowStages; g < all; g += kRowStages) {
@@ -494,10 +505,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         hand_back(1);
                     }
                     if (c >= rows) continue;
+                    float of_rows = scale[0];  // the scales of these rows
+#pragma unroll
+                    for (int k = 1; k < kTileRows / 32; ++k)
+                        if (c == 32 * k) of_rows = scale[k];
                     float* to = p.g.h + (r0 + c) * p.g.n + col;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float as = __shfl_sync(0xffffffffu, c < 32 ? scale[0] : c < 64 ? scale[1] : c < 96 ? scale[2] : scale[3], j);
+                        const float as = __shfl_sync(0xffffffffu, of_rows, j);
                         const float2 a = unpack2(x[j / 2]), b = unpack2(y[j / 2]);
                         const float gate = (j & 1 ? a.y : a.x) * (as * s0), up = (j & 1 ? b.y : b.x) * (as * s1);
                         if (on && c + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit(gate, up);
@@ -591,8 +606,9 @@ __global__ void __launch_bounds__(kCastThreads) cast_rows_kernel(const Int8GemmA
     }
 }
 
-template <bool kSwiglu>
+template <bool kSwiglu, int kTileRows>
 cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
+    using S = Sizes<kTileRows>;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const Params p = {g, (g.k + kBlockK - 1) / kBlockK};
@@ -600,11 +616,17 @@ cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
     if (!gemm::make_map(&w, g.w, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kHalf) ||
         !gemm::make_map(&a, g.a, g.k, g.cap, g.E, kTileRows / 2) || !gemm::make_map(&a16, g.a, g.k, g.cap, g.E, kChunk))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + kStages * kWeightBytes + kRowStages * kRowBytes + kRowSlots * kBatchBytes + sizeof(Shared);
+    const size_t smem = 1024 + S::kStages * kWeightBytes + kRowStages * S::kRowBytes + kRowSlots * S::kBatchBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows - 1) / kTileRows) * ((g.n + kBlock - 1) / kBlock);
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
-    return launch_pdl(ll_gemm_int8_kernel<kSwiglu>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, w, a, a16, p);
+    return launch_pdl(ll_gemm_int8_kernel<kSwiglu, kTileRows>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, w, a, a16, p);
+}
+
+// Tiles of 64 rows where no expert can have more.
+template <bool kSwiglu>
+cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
+    return g.cap <= 64 ? launch<kSwiglu, 64>(g, stream) : launch<kSwiglu, 128>(g, stream);
 }
 
 }  // namespace

@@ -8,7 +8,8 @@
 // value's.  Bound by HBM: a token is read once and written K times at half its
 // width, 2 H + K H bytes.  A scale needs the whole row, so a row is one team's:
 // 32 threads hold up to 2048 columns in registers, 128 up to 8192, and what is
-// longer is read a second time for its cast.
+// longer is read a second time for its cast.  The cast row goes through shared
+// memory and from there to every slot by one bulk copy each.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -79,7 +80,14 @@ __global__ void __launch_bounds__(kThreads) ll_dispatch_int8_kernel(const Args p
     constexpr int kTeams = kThreads / kTeam, kWarps = kTeam / kWarp;
     constexpr int kHeld = kTeam * kLaneCols * kPasses;
     __shared__ uint32_t s_max[2][kWarps];
+    __shared__ alignas(128) uint8_t s_row[kTeams][2][kHeld];  // the team's cast rows: two take turns
     const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, lane = threadIdx.x % kWarp;
+    const auto sync = [] {
+        if (kWarps == 1)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
     griddep_launch_dependents();
     griddep_wait();  // x, the ids and the row map are complete from here on
     int turn = 0;
@@ -100,27 +108,29 @@ __global__ void __launch_bounds__(kThreads) ll_dispatch_int8_kernel(const Args p
         for (int i = 0; i < kPasses; ++i) m = max_bits(m, held[i]);
         for (int col = kHeld + tid * kLaneCols; col < p.H; col += kTeam * kLaneCols) m = max_bits(m, load(x, col, p.H));
         m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        // the copies out of this buffer, of the token before the last one, have read it
+        if (tid < kWarp) bulk_wait_read<1>();
+        // two places take turns: passing this token's barrier says that the last one's maxima have been read
+        if (kWarps > 1 && lane == 0) s_max[turn][tid / kWarp] = m;
+        sync();
         if (kWarps > 1) {
-            // two places take turns: passing this token's barrier says that the last one's maxima have been read
-            if (lane == 0) s_max[turn][tid / kWarp] = m;
-            __syncthreads();
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) m = max(m, s_max[turn][i]);
         }
         const float scale = row_scale(__uint_as_float(m << 16));
         const bool finite = m < 0x7f80u;
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        uint4 q[kPasses];
+        uint8_t* out = s_row[team][turn];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) q[i] = finite ? cast(held[i], scale) : zero;
-        for (int k = 0; k < p.K; ++k) {
-            const long long r = __shfl_sync(0xffffffffu, row, k);
-            if (r < 0) continue;
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int col = (i * kTeam + tid) * kLaneCols;
-                if (col < p.H) st_v4(p.recv_x + r * p.H + col, q[i]);
-            }
+        for (int i = 0; i < kPasses; ++i) {
+            const int col = (i * kTeam + tid) * kLaneCols;
+            if (col < p.H) *reinterpret_cast<uint4*>(out + col) = finite ? cast(held[i], scale) : zero;
+        }
+        fence_proxy_async_smem();
+        sync();
+        if (tid < kWarp) {
+            if (row >= 0) bulk_s2g(p.recv_x + row * p.H, out, min(p.H, kHeld));
+            bulk_commit();
         }
         for (int col = kHeld + tid * kLaneCols; col - tid * kLaneCols < p.H; col += kTeam * kLaneCols) {
             const uint4 more = finite ? cast(load(x, col, p.H), scale) : zero;
@@ -135,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) ll_dispatch_int8_kernel(const Args p
                 reinterpret_cast<int2*>(p.src_info)[row] = make_int2(static_cast<int>(t / p.T), static_cast<int>(t % p.T));
         }
     }
+    if (tid < kWarp) bulk_wait_all();
 }
 
 template <int kTeam>
@@ -143,7 +154,7 @@ cudaError_t launch(const Args& p, cudaStream_t stream) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     const long long want = (p.tokens + kThreads / kTeam - 1) / (kThreads / kTeam), most = sms * 8LL;
     return launch_pdl(ll_dispatch_int8_kernel<kTeam>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                      dim3(kThreads), 0, stream, 0, false, p);
+                      dim3(kThreads), 0, stream, 0, true, p);
 }
 
 }  // namespace

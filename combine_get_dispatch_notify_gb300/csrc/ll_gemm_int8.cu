@@ -571,8 +571,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-// ---- the gated product's rows, cast ----
-constexpr int kCastThreads = 128;
+// ---- the gated product's rows, cast: a CTA to a row, which it holds in registers up to 4096 columns ----
+constexpr int kCastThreads = 256;
+constexpr int kCastPasses = 4;  // of four columns a thread
 
 __global__ void __launch_bounds__(kCastThreads) cast_rows_kernel(const Int8GemmArgs p) {
     __shared__ uint32_t s_max[2][kCastThreads / kWarp];
@@ -580,16 +581,26 @@ __global__ void __launch_bounds__(kCastThreads) cast_rows_kernel(const Int8GemmA
     griddep_wait();
     int turn = 0;
     for (long long r = blockIdx.x; r < static_cast<long long>(p.E) * p.cap; r += gridDim.x) {
-        const int e = static_cast<int>(r / p.cap), m = static_cast<int>(r % p.cap);
+        const int e = static_cast<int>(r / p.cap), m = static_cast<int>(r - static_cast<long long>(e) * p.cap);
         if (m >= __ldg(p.count + e)) continue;
-        const float* h = p.h + r * p.n;
+        const float4* h = reinterpret_cast<const float4*>(p.h + r * p.n);
+        const int pieces = p.n / 4, held = kCastThreads * kCastPasses;
+        float4 v[kCastPasses];
         uint32_t most = 0;  // bits of the largest magnitude; NaN is above them all
-        for (int c = threadIdx.x * 4; c < p.n; c += kCastThreads * 4) {
-            const float4 v = *reinterpret_cast<const float4*>(h + c);
-            most = max(max(most, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y)))),
-                       max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+        const auto larger = [&](const float4& x) {
+            most = max(max(most, max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y)))),
+                       max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
+        };
+#pragma unroll
+        for (int i = 0; i < kCastPasses; ++i) {
+            const int c = i * kCastThreads + threadIdx.x;
+            v[i] = c < pieces ? h[c] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+#pragma unroll
+        for (int i = 0; i < kCastPasses; ++i) larger(v[i]);
+        for (int c = held + threadIdx.x; c < pieces; c += kCastThreads) larger(h[c]);
         most = __reduce_max_sync(0xffffffffu, most);
+        // two places take turns: passing this row's barrier says that the last one's maxima have been read
         if (threadIdx.x % kWarp == 0) s_max[turn][threadIdx.x / kWarp] = most;
         __syncthreads();
 #pragma unroll
@@ -597,11 +608,16 @@ __global__ void __launch_bounds__(kCastThreads) cast_rows_kernel(const Int8GemmA
         turn ^= 1;
         const float scale = row_scale(__uint_as_float(most));
         const bool finite = most < 0x7f800000u;
-        for (int c = threadIdx.x * 4; c < p.n; c += kCastThreads * 4) {
-            const float4 v = *reinterpret_cast<const float4*>(h + c);
-            const uint32_t q = finite ? pack_int8x4(v.x / scale, v.y / scale, v.z / scale, v.w / scale) : 0u;
-            *reinterpret_cast<uint32_t*>(static_cast<int8_t*>(p.y) + r * p.n + c) = q;
+        uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<int8_t*>(p.y) + r * p.n);
+        const auto cast = [&](const float4& x) {
+            return finite ? pack_int8x4(x.x / scale, x.y / scale, x.z / scale, x.w / scale) : 0u;
+        };
+#pragma unroll
+        for (int i = 0; i < kCastPasses; ++i) {
+            const int c = i * kCastThreads + threadIdx.x;
+            if (c < pieces) y[c] = cast(v[i]);
         }
+        for (int c = held + threadIdx.x; c < pieces; c += kCastThreads) y[c] = cast(h[c]);
         if (threadIdx.x == 0) p.y_scales[r] = scale;
     }
 }

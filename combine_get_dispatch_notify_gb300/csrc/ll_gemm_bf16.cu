@@ -55,10 +55,9 @@ constexpr int kTmemColumns = 512;
 constexpr int kOutCols = 32, kOutRows = 32;    // of a warp's box of output
 constexpr int kOutBytes = kOutCols * kOutRows * 2;
 
-// Stages and bytes of an epilogue warp's buffers: where sums are widened (fp32 output) or gate and up come in on the way
-// out, a stage is given up for twice the buffers.
-template <Bf16Form kForm, bool kOut16>
-constexpr bool kWide = kForm == Bf16Form::kDswiglu || (kForm == Bf16Form::kWgrad && !kOut16);
+// Where gate and up come in on the way out, a stage is given up for twice the buffers of an epilogue warp.
+template <Bf16Form kForm>
+constexpr bool kWide = kForm == Bf16Form::kDswiglu;
 constexpr int kMostStages = 4;
 
 struct Params {
@@ -181,8 +180,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr bool kWgrad = kForm == Bf16Form::kWgrad;
     constexpr bool kSwiglu = kForm == Bf16Form::kSwiglu, kDswiglu = kForm == Bf16Form::kDswiglu;
     constexpr bool kAcrossA = kWgrad || kForm == Bf16Form::kDgrad || kDswiglu;  // its rows of memory run across the contraction
-    constexpr int kStages = kWide<kForm, kOut16> ? 3 : 4;
-    constexpr int kBufBytes = kWide<kForm, kOut16> ? 4 * kOutBytes : 2 * kOutBytes;  // of an epilogue warp
+    constexpr int kStages = kWide<kForm> ? 3 : 4;
+    constexpr int kBufBytes = kWide<kForm> ? 4 * kOutBytes : 2 * kOutBytes;  // of an epilogue warp
     extern __shared__ uint8_t s_raw[];
     // stages first, on a 1024-byte boundary as the swizzle needs, at the same offset in both CTAs
     uint8_t* s_tiles = s_raw + ((1024u - (smem_addr(s_raw) & 1023u)) & 1023u);
@@ -374,24 +373,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         if (kWgrad) {
             // thread = one output row
-            constexpr int kCols = kOut16 ? 64 : 32;  // of one store: 128 bytes a row
-            constexpr int kBoxes = kWide<kForm, kOut16> ? 2 : 1;
-            uint32_t turn = 0;
+            constexpr int kCols = 64;  // of one store in bf16: 128 bytes a row
             const auto store = [&](const uint4 (&v)[8], int x, int y, int e) {
                 if (x >= p.g.k || y >= p.g.n) return;
-                const uint32_t to = buf + turn % kBoxes * (2 * kOutBytes);
-                ++turn;
-                if (lane == 0) bulk_wait_read<kBoxes - 1>();  // the store before has left this buffer
+                if (lane == 0) bulk_wait_read<0>();  // the store before has left the buffer
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)),
                                  "r"(v[j].x), "r"(v[j].y), "r"(v[j].z), "r"(v[j].w)
                                  : "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&map_out, to, x, y, e);
+                    tma_store_3d(&map_out, buf, x, y, e);
                     bulk_commit();
                 }
             };
@@ -423,19 +418,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kTileRows / kCols; ++c) store(v[c], tl.b0 + c * kCols, y, tl.e);
                 } else {
-#pragma unroll 1
-                    for (int c = 0; c < kTileRows; c += kCols) {
+                    // From registers to memory: through shared memory, which the operands keep busy, 32 experts x 512 rows, 4096
+                    // x 7168, took 1020 us.  Two neighbouring lanes trade pairs of columns, so that each stores 16 bytes and
+                    // the four lanes of a row 64 in a line.
+                    float* out = static_cast<float*>(p.g.out) + (static_cast<long long>(tl.e) * p.g.n + y + lane / 4) * p.g.k;
+#pragma unroll 2
+                    for (int c = 0; c < kTileRows; c += 32) {
                         uint64_t x[16];
-                        if (any) tmem_read(d + c, x);
-                        uint4 v[8];
+                        if (any) tmem_read_matrices(d + c, x);
+                        if (any && c + 32 == kTileRows) hand_back(half);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 f = any ? unpack2(x[j]) : make_float2(0.0f, 0.0f);
-                            reinterpret_cast<uint32_t*>(v)[2 * j] = __float_as_uint(f.x);
-                            reinterpret_cast<uint32_t*>(v)[2 * j + 1] = __float_as_uint(f.y);
+                        for (int j = 0; j < 4; j += 2) {
+                            const int col = tl.b0 + c + 8 * (j + lane % 2) + lane % 4 / 2 * 4;
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const uint64_t lo = any ? x[4 * j + m] : 0, hi = any ? x[4 * j + 4 + m] : 0;
+                                const uint64_t got = __shfl_xor_sync(0xffffffffu, lane % 2 ? lo : hi, 1);
+                                const float2 first = unpack2(lane % 2 ? got : lo), second = unpack2(lane % 2 ? hi : got);
+                                if (col < p.g.k && y + 8 * m + lane / 4 < p.g.n)
+                                    *reinterpret_cast<float4*>(out + static_cast<long long>(8 * m) * p.g.k + col) =
+                                        make_float4(first.x, first.y, second.x, second.y);
+                            }
                         }
-                        if (any && c + kCols == kTileRows) hand_back(half);
-                        store(v, tl.b0 + c, y, tl.e);
                     }
                 }
             }
@@ -535,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float2 a = unpack2(x[j]), b = unpack2(y[j]);
-                            h[j] = pack_bf16(make_float2(gated_unit(a.x, b.x), gated_unit(a.y, b.y)));
+                            h[j] = pack_bf16(make_float2(gated_unit<true>(a.x, b.x), gated_unit<true>(a.y, b.y)));
                             g[j] = pack_bf16(a);
                             u[j] = pack_bf16(b);
                         }
@@ -566,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int m = 0; m < 4; ++m) {
                                 const float2 f = unpack2(x[4 * j + m]), a = unpack_bf16(g[m]), b = unpack_bf16(u[m]);
-                                const float2 lo = gated_unit_gradient(f.x, a.x, b.x), hi = gated_unit_gradient(f.y, a.y, b.y);
+                                const float2 lo = gated_unit_gradient<true>(f.x, a.x, b.x), hi = gated_unit_gradient<true>(f.y, a.y, b.y);
                                 g[m] = pack_bf16(make_float2(lo.x, hi.x));
                                 u[m] = pack_bf16(make_float2(lo.y, hi.y));
                             }
@@ -652,8 +656,7 @@ cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
         const bool none = g.cap == 0;
         ok = make_map_bf16(&a, none ? g.out : g.rows, g.n, none ? 1 : g.cap, none ? 1 : g.E, kBlockK) &&
              make_map_bf16(&b, none ? g.out : g.other, g.k, none ? 1 : g.cap, none ? 1 : g.E, kBlockK) &&
-             (kOut16 ? make_map_bf16(&out, g.out, g.k, g.n, g.E, kWarp)
-                     : gemm::make_map(&out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.out, g.k, g.n, g.E, kWarp));
+             (!kOut16 || make_map_bf16(&out, g.out, g.k, g.n, g.E, kWarp));
     } else {
         const long long rows = static_cast<long long>(g.E) * g.cap;
         ok = make_map_bf16(&a, g.other, g.k, g.n, g.E * (kSwiglu ? 2 : 1), kTransposed ? kBlockK : kHalf) &&
@@ -663,7 +666,7 @@ cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
         if (halves != nullptr) ok = ok && make_out_map(&gate_up, halves, p.out_n, rows, 1, true);
     }
     if (!ok) return cudaErrorInvalidValue;
-    constexpr bool wide = kWide<kForm, kOut16>;
+    constexpr bool wide = kWide<kForm>;
     const size_t smem = 1024 + (wide ? 3 : 4) * kStageBytes + kEpilogueWarps * (wide ? 4 : 2) * kOutBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) *

@@ -515,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float as = __shfl_sync(0xffffffffu, of_rows, j);
                         const float2 a = unpack2(x[j / 2]), b = unpack2(y[j / 2]);
                         const float gate = (j & 1 ? a.y : a.x) * (as * s0), up = (j & 1 ? b.y : b.x) * (as * s1);
-                        if (on && c + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit(gate, up);
+                        if (on && c + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit<false>(gate, up);
                     }
                 }
             } else {

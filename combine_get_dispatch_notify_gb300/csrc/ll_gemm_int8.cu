@@ -234,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // rows of a tile as the tensor cores take them
     const auto width = [&](const RowTile& t) { return (min(t.rows, kTileRows) + 31) / 32 * 32; };
 
-    if (warp < 4) regs_down<32>();
+    if (warp < 4) regs_down<40>();
     if (warp == 0) {
         if (lane == 0) {
             // ---- producer: this CTA's half of the weights ----

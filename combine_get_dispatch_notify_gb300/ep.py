@@ -806,6 +806,8 @@ def ep_ll_gemm_swiglu_int8(a, a_scales, w, w_scales, count, y, y_scales, workspa
             _t(count, torch.int32, (E,), "count"), _t(y, torch.int8, (E, cap, n), "y"),
             _t(y_scales, torch.float32, (E, cap), "y_scales"))
     ws, nws = _workspace(workspace, ep_ll_gemm_swiglu_int8_workspace_bytes(shape))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _here(status, a, a_scales, w, w_scales, count, y, y_scales, workspace)
     _check("ep_ll_gemm_swiglu_int8",
            lib().ep_ll_gemm_swiglu_int8(ctypes.byref(shape), *args, ws, nws, _t(status, torch.int32, (1,), "status"),

@@ -5,7 +5,9 @@ import pytest
 import torch
 
 import experts_ref as ref
+import oracle
 from combine_get_dispatch_notify_gb300 import ep
+from combine_get_dispatch_notify_gb300.workloads import Workload, gen_routing
 from test_gpu_ll_int8 import BF16, ROUTES, placed
 
 pytestmark = pytest.mark.gpu
@@ -126,3 +128,23 @@ def test_repeats_on_streams_and_in_a_graph():
     assert ep.ep_sync_status(status) == ep.EP_OK
     for other in (b, c):
         assert torch.equal(a[0], other[0]) and torch.equal(a[1], other[1])
+
+
+@pytest.mark.parametrize("K", [4, 9])
+def test_an_expert_picked_twice_by_a_token(K):
+    """Slots of one token may name the same expert: they have rows, gradients and weights of their own."""
+    R, T, H, E = 2, 60, 136, 6
+    wl = Workload("m", R=R, T=T, H=H, E=E, K=K, C=1, seed=5, routing="replace")
+    idx, wt = gen_routing(wl)
+    assert any(len(set(r)) < K for r in idx.view(-1, K).tolist())
+    cap = R * T * K
+    slot = torch.from_numpy(oracle.ll_layout(oracle.load(), R, T, K, E, cap, idx.numpy())["slot_pos"])
+    shape = ep.EpShape.make(R, T, K, E, H, 1)
+    gen = torch.Generator().manual_seed(6)
+    g, y = torch.randn(R, T, H, generator=gen).to(BF16), torch.randn(E, cap, H, generator=gen).to(BF16)
+    gy, gw = torch.zeros(E, cap, H, dtype=BF16, device="cuda"), torch.zeros(R, T, K, device="cuda")
+    assert run(shape, cap, g.cuda(), y.cuda(), idx.cuda(), wt.cuda(), slot.cuda(), gy, gw) == ep.EP_OK
+    at = idx.view(-1, K), slot.view(-1, K).long()
+    assert torch.equal(gy.cpu()[at], (g.view(-1, 1, H).float() * wt.view(-1, K, 1)).to(BF16))
+    terms = g.view(-1, 1, H).double() * y[at].double()
+    ref.close_fp32("grad_topk_w", gw.view(-1, K).cpu(), terms.sum(-1), terms.abs().sum(-1) * ref.sum_error(H))

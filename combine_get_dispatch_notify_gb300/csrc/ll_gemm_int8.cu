@@ -158,12 +158,6 @@ __device__ __forceinline__ uint4 rows_of_matrices(uint32_t a, uint32_t b, uint32
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// The block that accumulator `half` has of the pair's tile number `i`, or -1.
-__device__ __forceinline__ int block_of(int live, int blocks, int i, int half) {
-    if (blocks == 2) return half < live ? half : -1;
-    return (i & 1) == half ? 0 : -1;
-}
-
 template <bool kSwiglu, int kTileRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ll_gemm_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
@@ -185,7 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s->raw_full[i], 1);
-            mbar_init(&s->raw_empty[i], kWeightWarps);
+            mbar_init(&s->raw_empty[i], kWeightWarps / 2);
         }
         for (int i = 0; i < kSlots; ++i)
             for (int h = 0; h < 2; ++h) {
@@ -226,11 +220,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int blocks = kSwiglu ? 2 : blocks_of_tiles(row_tiles, columns, pairs);
     walk.tiles_n = kSwiglu ? columns : (columns + blocks - 1) / blocks;
     const int tiles = row_tiles * walk.tiles_n;
-    // first output column of a tile, and its blocks that hold any
+    // first output column of a tile (its second block may lie past the last one)
     const auto first_column = [&](const RowTile& t) { return t.col * (kSwiglu ? 1 : blocks) * kBlock; };
-    const auto live_blocks = [&](const RowTile& t) {
-        return kSwiglu ? 2 : min(blocks, (p.g.n - first_column(t) + kBlock - 1) / kBlock);
-    };
+    // Steps of weights, all of the pair's tiles in turn.  Where tiles have two blocks, the first group of converting warps,
+    // the first MMA warp and the first accumulator have the first block's and the second ones the second's.  Where
+    // they have one, the groups take every other step, the first MMA warp does them all, and the accumulators take turns by
+    // tile.  Either way unit number 2 i + g, in the order of the loads, is the i-th of group g.
+    const uint32_t steps = tiles > pair ? static_cast<uint32_t>((tiles - pair + pairs - 1) / pairs) * p.kb : 0;
     // rows of a tile as the tensor cores take them
     const auto width = [&](const RowTile& t) { return (min(t.rows, kTileRows) + 31) / 32 * 32; };
 
@@ -242,13 +238,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const RowTile tl = walk.at(t);
-                const int live = live_blocks(tl), w0 = first_column(tl) + static_cast<int>(rank) * kHalf;
-                for (int b = 0; b < p.kb * live && ok; ++b, ++it) {
+                const int w0 = first_column(tl) + static_cast<int>(rank) * kHalf;
+                for (int u = 0; u < p.kb * blocks; ++u, ++it) {
                     const uint32_t st = it % kStages;
                     if (!(ok = wait_for(&s->raw_empty[st], it / kStages & 1 ^ 1, &s->waits))) break;
-                    const int step = live == 2 ? b / 2 : b, i = live == 2 ? b % 2 : 0;
+                    const int b = blocks == 2 ? u / 2 : u, i = blocks == 2 ? u % 2 : 0;
                     mbar_arrive_expect_tx(&s->raw_full[st], kWeightBytes);
-                    tma_load_3d_alone(smem_addr(s_stages) + st * kWeightBytes, &map_w, step * kBlockK, kSwiglu ? w0 : w0 + i * kBlock,
+                    tma_load_3d_alone(smem_addr(s_stages) + st * kWeightBytes, &map_w, b * kBlockK, kSwiglu ? w0 : w0 + i * kBlock,
                                       kSwiglu ? 2 * tl.e + i : tl.e, smem_addr(&s->raw_full[st]));
                 }
             }
@@ -283,25 +279,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = wait_for(&s->in_empty[it % kRowStages], it / kRowStages & 1 ^ 1, &s->waits);
         }
     } else if (warp == 1 || warp == 2) {
-        if (rank == 0) {
-            // ---- MMA: a warp for each block ----
-            const int half = warp - 1;
-            uint32_t batch = 0, mine = 0, acc_phase = 1;  // batches of rows so far, steps of this warp's blocks
+        const uint32_t half = warp - 1;
+        if (rank == 0 && half < static_cast<uint32_t>(blocks)) {
+            // ---- MMA ----
+            uint32_t batch = 0, it = 0;  // batches of rows and steps so far
             bool ok = true;
-            for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
-                const RowTile tl = walk.at(t);
-                const int block = __shfl_sync(0xffffffffu, block_of(live_blocks(tl), blocks, i, half), 0);
-                const int n = __shfl_sync(0xffffffffu, width(tl), 0), in_batch = kBatchStages * S::stage_steps(n);
+            for (uint32_t t = pair, i = 0; t < static_cast<uint32_t>(tiles) && ok; t += pairs, ++i) {
+                const int n = __shfl_sync(0xffffffffu, width(walk.at(t)), 0), in_batch = kBatchStages * S::stage_steps(n);
                 const uint32_t idesc = f16_idesc(kBlock, n), step_bytes = kBatchBytes / in_batch;
-                if (block >= 0) {
-                    ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
-                    acc_phase ^= 1;
-                }
-                for (int b = 0; b < p.kb && ok; ++b) {
-                    const uint32_t rs = batch % kRowSlots, ws = mine % kSlots;
+                const uint32_t acc = blocks == 2 ? half : i & 1, before = blocks == 2 ? i : i / 2;  // its tiles before this one
+                ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[acc], before & 1 ^ 1, &s->waits));
+                for (int b = 0; b < p.kb && ok; ++b, ++it) {
+                    const uint32_t rs = batch % kRowSlots, g = blocks == 2 ? half : it & 1, unit = blocks == 2 ? it : it / 2;
+                    const uint32_t ws = unit % kSlots;
                     const int at = b % in_batch;
                     if (at == 0) ok = wait_cluster(&s->rows_full[rs], batch / kRowSlots & 1, &s->waits);
-                    if (block >= 0) ok = ok && wait_for(&s->w_full[half][ws], mine / kSlots & 1, &s->waits);
+                    ok = ok && wait_for(&s->w_full[g][ws], unit / kSlots & 1, &s->waits);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const bool end = at + 1 == in_batch || b + 1 == p.kb;
@@ -309,73 +302,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     asm volatile("" : "+l"(db));
                     tc_fence_after();
                     if (elect_one()) {
-                        if (block >= 0) {
-                            const uint32_t a = tmem + kWeightColumns + (half * kSlots + ws) * kSlotColumns;
+                        const uint32_t a = tmem + kWeightColumns + (g * kSlots + ws) * kSlotColumns;
 #pragma unroll
-                            for (int k = 0; k < kBlockK / 16; ++k)
-                                mma_f16_pair_tmem(tmem + half * kTileRows, a + k * 8, db + k / 4 * (step_bytes >> 5) + k % 4 * 2,
-                                                  idesc, b > 0 || k > 0);
-                            mma_commit_pair(smem_addr(&s->w_empty[half][ws]));
-                            if (b + 1 == p.kb) mma_commit_pair(smem_addr(&s->acc_full[half]));
-                        }
+                        for (int k = 0; k < kBlockK / 16; ++k)
+                            mma_f16_pair_tmem(tmem + acc * kTileRows, a + k * 8, db + k / 4 * (step_bytes >> 5) + k % 4 * 2, idesc,
+                                              b > 0 || k > 0);
+                        mma_commit_pair(smem_addr(&s->w_empty[g][ws]));
                         if (end) mma_commit_pair(smem_addr(&s->rows_empty[rs]));
+                        if (end && blocks == 1) mma_commit_pair(smem_addr(&s->rows_empty[rs]));  // for the other warp
+                        if (b + 1 == p.kb) mma_commit_pair(smem_addr(&s->acc_full[acc]));
                     }
                     __syncwarp();
-                    if (block >= 0) ++mine;
                     if (end) ++batch;
                 }
             }
         }
     } else if (warp >= 4 && warp < kFirstEpilogue) {
-        // ---- weights: thread = one weight row, 128 bytes a step -> 64 columns of TMEM.  Arrivals are relaxed: what they
+        // ---- weights: two groups of four warps; thread = one weight row, 128 bytes a step -> 64 columns of TMEM.  Arrivals are relaxed: what they
         // announce is in TMEM, which the tcgen05 waits and fences on both sides put in order ----
         regs_down<64>();
-        const int half = (warp - 4) / 4, quarter = warp % 4, row = quarter * kWarp + lane;
-        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * kWarp) << 16) + kWeightColumns + half * kSlots * kSlotColumns;
-        const uint32_t full = mapa(smem_addr(&s->w_full[half][0]), 0);
-        // Where every tile has two blocks, a warp passes over the other block's stages and arrives for both groups.  Elsewhere
-        // stages do not alternate, and every warp waits for each of them: a barrier tells phases apart by one bit.
-        const bool paired = kSwiglu || (blocks == 2 && columns % 2 == 0);
-        uint32_t it = paired ? half : 0, mine = 0;
-        bool ok = true;
-        for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
-            const int col = t % walk.tiles_n, live = kSwiglu ? 2 : min(blocks, columns - col * blocks);
-            const int block = block_of(live, blocks, i, half);
-            for (int b = paired ? half : 0; b < p.kb * live; b += paired ? 2 : 1, it += paired ? 2 : 1) {
-                const uint32_t st = it % kStages, ws = mine % kSlots;
-                const bool own = block >= 0 && (live == 1 || b % 2 == block);
-                ok = wait_for(&s->raw_full[st], it / kStages & 1, &s->waits);
-                if (own) ok = ok && wait_for(&s->w_empty[half][ws], mine / kSlots & 1 ^ 1, &s->waits);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (own) {
-                    tc_fence_after();
-                    const uint32_t from = smem_addr(s_stages) + st * kWeightBytes;
+        const uint32_t g = (warp - 4) / 4, quarter = warp % 4;
+        const int row = quarter * kWarp + lane;
+        const uint32_t to = tmem + (quarter * kWarp << 16) + kWeightColumns + g * kSlots * kSlotColumns;
+        const uint32_t full = mapa(smem_addr(&s->w_full[g][0]), 0);
+        const uint32_t units = blocks == 2 ? steps : (steps + 1 - g) / 2;
+        for (uint32_t u = 0; u < units; ++u) {
+            const uint32_t st = (2 * u + g) % kStages, ws = u % kSlots;
+            const bool ok = wait_for(&s->raw_full[st], (2 * u + g) / kStages & 1, &s->waits) &&
+                            wait_for(&s->w_empty[g][ws], u / kSlots & 1 ^ 1, &s->waits);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t from = smem_addr(s_stages) + st * kWeightBytes;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t v[32];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint4 x = row_piece(from, row, 4 * h + j);
-                            widen(x.x, v[8 * j], v[8 * j + 1]);
-                            widen(x.y, v[8 * j + 2], v[8 * j + 3]);
-                            widen(x.z, v[8 * j + 4], v[8 * j + 5]);
-                            widen(x.w, v[8 * j + 6], v[8 * j + 7]);
-                        }
-                        tmem_write(to + ws * kSlotColumns + h * 32, v);
-                    }
-                    // the bytes are in registers: their stage can be filled again while TMEM takes them
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_many(&s->raw_empty[st], paired ? 2 : 1);
-                    tmem_write_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(full + ws * 8);
-                    ++mine;
-                } else if (lane == 0) {
-                    mbar_arrive(&s->raw_empty[st]);  // the other block's
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 x = row_piece(from, row, 4 * h + j);
+                    widen(x.x, v[8 * j], v[8 * j + 1]);
+                    widen(x.y, v[8 * j + 2], v[8 * j + 3]);
+                    widen(x.z, v[8 * j + 4], v[8 * j + 5]);
+                    widen(x.w, v[8 * j + 6], v[8 * j + 7]);
                 }
+                tmem_write(to + ws * kSlotColumns + h * 32, v);
             }
+            // the bytes are in registers: their stage can be filled again while TMEM takes them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->raw_empty[st]);
+            tmem_write_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(full + ws * 8);
         }
     } else if (warp >= kRelay) {
         regs_down<48>();
@@ -473,8 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
             const RowTile tl = walk.at(t);
-            const int block = kSwiglu ? 0 : block_of(live_blocks(tl), blocks, i, half);
-            if (block < 0) continue;
+            if (blocks == 1 && (i & 1) != half) continue;
+            const int block = kSwiglu || blocks == 1 ? 0 : half;
             const int col = first_column(tl) + block * kBlock + static_cast<int>(rank) * kHalf + quarter * kWarp + lane;
             const bool on = col < p.g.n;
             const long long r0 = static_cast<long long>(tl.e) * p.g.cap + tl.m0;

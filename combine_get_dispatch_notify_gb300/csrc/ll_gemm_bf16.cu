@@ -64,7 +64,7 @@ struct Params {
     Bf16GemmArgs g;
     int kb;                // steps of the contraction (forms over rows)
     int out_n;             // columns of the output (of each half of it)
-    int blocks, tiles_m, tiles_n;  // kWgrad: blocks of a tile, tiles of output rows and columns
+    int tiles_m, tiles_n;  // kWgrad: tiles of output rows and columns
 };
 
 struct Shared {
@@ -127,7 +127,7 @@ struct Tiles {
     static constexpr bool kWgrad = kForm == Bf16Form::kWgrad;
     const Params& p;
     RowTiles<kTileRows> walk;
-    int blocks;  // of a tile (1: a tile is one block, the two accumulators take turns)
+    int blocks = 2;  // of a tile (1: a tile is one block, the two accumulators take turns)
 
     __device__ __forceinline__ Tile at(int t) {
         Tile r;
@@ -155,8 +155,16 @@ struct Tiles {
         }
         return r;
     }
-    // Steps of 64 of the contraction.
-    __device__ __forceinline__ int steps(const Tile& t) const { return kWgrad ? (t.rows + kBlockK - 1) / kBlockK : p.kb; }
+    // Steps of 64 of the contraction in a stage: two where a tile is one block and has up to 128 rows, so that as many bytes
+    // of the weights are in flight as with two blocks (eight experts with one row each, 2048 -> 7168: 55 us, with
+    // one step to a stage 60).
+    __device__ __forceinline__ int in_stage(const Tile& t) const {
+        return kForm != Bf16Form::kSwiglu && !kWgrad && blocks == 1 && t.rows <= kTileRows / 2 ? 2 : 1;
+    }
+    // Stages of a tile.
+    __device__ __forceinline__ int stages(const Tile& t) const {
+        return kWgrad ? (t.rows + kBlockK - 1) / kBlockK : (p.kb + in_stage(t) - 1) / in_stage(t);
+    }
 };
 // The block that accumulator `half` has of the pair's tile number `i`, or -1.
 __device__ __forceinline__ int block_of(const Tile& t, int blocks, int i, int half) {
@@ -212,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and weights are complete from here on
     griddep_launch_dependents();
-    Tiles<kForm> list{p, RowTiles<kTileRows>{p.g.count, s->first, p.g.E, p.g.cap}, kWgrad ? p.blocks : 2};
+    Tiles<kForm> list{p, RowTiles<kTileRows>{p.g.count, s->first, p.g.E, p.g.cap}};
     if (!kWgrad && warp == 1) list.walk.fill(s->first, lane);
     tc_fence_before();
     __syncthreads();
@@ -237,14 +245,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t full = mapa(smem_addr(&s->full[0]), 0);
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const Tile tl = list.at(t);
-                const int steps = list.steps(tl);
+                const int stages = list.stages(tl), in_stage = list.in_stage(tl);
                 const int n = kWgrad ? kTileRows : (tl.rows + 31) / 32 * 32;  // rows of the second operand
                 const int a0 = tl.a0 + static_cast<int>(rank) * kHalf;
                 const int b0 = (kWgrad ? tl.b0 : tl.m0) + static_cast<int>(rank) * (n / 2);
-                const uint32_t bytes = tl.blocks * kOperand + n / 2 * 128;  // of each CTA
-                for (int b = 0; b < steps; ++b) {
+                const uint32_t each = tl.blocks * kOperand + n / 2 * 128;  // bytes of a step, of each CTA
+                for (int b = 0; b < stages; ++b) {
                     if (!(ok = wait_for(&s->empty[st.at], st.phase, &s->waits))) break;
                     uint32_t bar = full + st.at * sizeof(uint64_t);
+                    const int steps = in_stage == 1 ? 1 : min(2, p.kb - 2 * b);
+                    const uint32_t bytes = steps * each;
                     if (kWgrad && (tl.rows - b * kBlockK < kBlockK) && tl.rows % 16 != 0) {
                         bar = mapa(smem_addr(&s->landed[st.at]), rank);
                         mbar_arrive_expect_tx(&s->landed[st.at], bytes);
@@ -252,24 +262,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(&s->full[st.at], 2 * bytes);
                         if (kWgrad) mbar_arrive(&s->full[st.at]);
                     }
-                    const uint32_t to = smem_addr(s_tiles) + st.at * kStageBytes, tb = to + 2 * kOperand;
-                    const int c = b * kBlockK;
-                    for (int i = 0; i < tl.blocks; ++i) {
-                        const uint32_t ta = to + i * kOperand;
-                        if (kSwiglu) {
-                            tma_load_3d(ta, &map_a, c, a0, 2 * tl.e + i, bar);
-                        } else if (kAcrossA) {
-                            for (int j = 0; j < 2; ++j) tma_load_3d(ta + j * kBox, &map_a, a0 + i * kBlock + j * 64, c, tl.e, bar);
-                        } else {
-                            tma_load_3d(ta, &map_a, c, a0 + i * kBlock, tl.e, bar);
+                    uint32_t ta = smem_addr(s_tiles) + st.at * kStageBytes, tb = ta + 2 * kOperand;
+                    for (int step = 0; step < steps; ++step, tb += kBox) {
+                        const int c = (b * in_stage + step) * kBlockK;
+                        for (int i = 0; i < tl.blocks; ++i, ta += kOperand) {
+                            if (kSwiglu) {
+                                tma_load_3d(ta, &map_a, c, a0, 2 * tl.e + i, bar);
+                            } else if (kAcrossA) {
+                                for (int j = 0; j < 2; ++j)
+                                    tma_load_3d(ta + j * kBox, &map_a, a0 + i * kBlock + j * 64, c, tl.e, bar);
+                            } else {
+                                tma_load_3d(ta, &map_a, c, a0 + i * kBlock, tl.e, bar);
+                            }
                         }
-                    }
-                    if (kWgrad) {
-                        for (int j = 0; j < 2; ++j) tma_load_3d(tb + j * kBox, &map_b, b0 + j * 64, c, tl.e, bar);
-                    } else if (n == kTileRows) {
-                        tma_load_3d(tb, &map_b, c, b0, tl.e, bar);
-                    } else {
-                        for (int i = 0; i < n / 2; i += kChunk) tma_load_3d(tb + i * 128, &map_b16, c, b0 + i, tl.e, bar);
+                        if (kWgrad) {
+                            for (int j = 0; j < 2; ++j) tma_load_3d(tb + j * kBox, &map_b, b0 + j * 64, c, tl.e, bar);
+                        } else if (n == kTileRows) {
+                            tma_load_3d(tb, &map_b, c, b0, tl.e, bar);
+                        } else {
+                            for (int i = 0; i < n / 2; i += kChunk) tma_load_3d(tb + i * 128, &map_b16, c, b0 + i, tl.e, bar);
+                        }
                     }
                     st.next();
                 }
@@ -285,13 +297,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
                 const Tile tl = list.at(t);
-                const int steps = __shfl_sync(0xffffffffu, list.steps(tl), 0);
-                if (steps == 0) continue;
+                const int stages = __shfl_sync(0xffffffffu, list.stages(tl), 0);
+                const int in_stage = __shfl_sync(0xffffffffu, list.in_stage(tl), 0);
+                if (stages == 0) continue;
                 const int block = __shfl_sync(0xffffffffu, block_of(tl, list.blocks, i, half), 0);
                 if (block < 0) {
                     // the other warp's tile: only this one's arrivals (a barrier tells phases apart by one bit, so a wait
                     // may not be left out)
-                    for (int b = 0; b < steps && ok; ++b, st.next()) {
+                    for (int b = 0; b < stages && ok; ++b, st.next()) {
                         ok = __all_sync(0xffffffffu, wait_for(&s->full[st.at], st.phase, &s->waits));
                         if (ok && elect_one()) mma_commit_pair(smem_addr(&s->empty[st.at]));
                         __syncwarp();
@@ -301,12 +314,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int rows = __shfl_sync(0xffffffffu, tl.rows, 0);
                 const uint32_t idesc = bf16_idesc(kBlock, kWgrad ? kTileRows : (rows + 31) / 32 * 32, kAcrossA, kWgrad);
                 const bool ragged = kWgrad && rows % 16 != 0;
-                const int last = kWgrad ? (rows - (steps - 1) * kBlockK + 15) / 16 : kBlockK / 16;  // MMAs of the last step
+                const int last = kWgrad ? (rows - (stages - 1) * kBlockK + 15) / 16 : kBlockK / 16;  // MMAs of the last step
                 ok = __all_sync(0xffffffffu, wait_for(&s->acc_empty[half], acc_phase, &s->waits));
                 acc_phase ^= 1;
                 const uint32_t d = tmem + half * kTileRows;
-                for (int b = 0; b < steps && ok; ++b) {
-                    const bool end = b + 1 == steps;
+                for (int b = 0; b < stages && ok; ++b) {
+                    const bool end = b + 1 == stages;
                     const bool there = ragged && end ? wait_cluster(&s->full[st.at], st.phase, &s->waits)
                                                      : wait_for(&s->full[st.at], st.phase, &s->waits);
                     ok = __all_sync(0xffffffffu, there);
@@ -323,6 +336,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < kBlockK / 16; ++k)
                             if (!kWgrad || !end || k < last)
                                 mma_f16_pair(d, da + k * (kAcrossA ? 128 : 2), db + k * (kWgrad ? 128 : 2), idesc, b > 0 || k > 0);
+                        if (!kWgrad && in_stage == 2 && 2 * b + 1 < p.kb) {
+#pragma unroll
+                            for (int k = 0; k < kBlockK / 16; ++k)
+                                mma_f16_pair(d, da + (kOperand >> 4) + k * (kAcrossA ? 128 : 2), db + (kBox >> 4) + k * 2, idesc, true);
+                        }
                         mma_commit_pair(smem_addr(&s->empty[st.at]));
                         if (end) mma_commit_pair(smem_addr(&s->acc_full[half]));
                     }
@@ -337,9 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const Tile tl = list.at(t);
-                const int steps = list.steps(tl), left = tl.rows - (steps - 1) * kBlockK;
+                const int stages = list.stages(tl), left = tl.rows - (stages - 1) * kBlockK;
                 if (tl.rows % 16 != 0) {
-                    st.skip(steps - 1);
+                    st.skip(stages - 1);
                     ok = __all_sync(0xffffffffu, wait_for(&s->landed[st.at], phases >> st.at & 1, &s->waits));
                     if (!ok) break;
                     phases ^= 1u << st.at;
@@ -353,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive_cluster(mapa(smem_addr(&s->full[st.at]), 0));
                     st.next();
                 } else {
-                    st.skip(steps);
+                    st.skip(stages);
                 }
             }
         }
@@ -646,8 +664,7 @@ cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
     const int inner = kTransposed ? g.n : g.k;  // forms over rows: the contraction
     p.out_n = kWgrad || kTransposed ? g.k : g.n;
     p.kb = over(inner, kBlockK);
-    p.blocks = 2;
-    p.tiles_m = over(g.n, p.blocks * kBlock);
+    p.tiles_m = over(g.n, 2 * kBlock);
     p.tiles_n = over(g.k, kTileRows);
     CUtensorMap a = {}, b = {}, b16 = {}, out = {}, gate_up = {};
     bool ok;

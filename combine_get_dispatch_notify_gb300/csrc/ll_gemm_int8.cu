@@ -17,6 +17,11 @@
 // block each), eight that scale the sums and write them out.  For the gated product the blocks
 // are the gate and the up matrix.  Its activations leave as fp32, because the scale of a row
 // is known once the row is complete; a second kernel casts them.
+//
+// Measured, 32 experts with about 1024 rows each: gated, 7168 -> 2 x 2048, 1280 to 1310 us with the cast, plain,
+// 2048 -> 7168, 617 to 646 (1.47 to 1.56 PFLOP/s; tensor pipe about 60 % busy, half of the issue slots: the chain from bytes
+// through TMEM to the tensor cores bounds it).  64 experts with about 64 rows: 361 to 369 and 178 us, 5.1 to 5.3
+// TB/s of weights.  8 experts with one row: 64 and 41 us, of which some 25 and 20 do not grow with k.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>

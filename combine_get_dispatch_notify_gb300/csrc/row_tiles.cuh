@@ -31,12 +31,21 @@ struct RowTiles {
 
     // Fills `to` (one warp).
     __device__ __forceinline__ void fill(int* to, int lane) const {
+        constexpr int kAhead = 8;  // groups whose counts are asked for together
         const int groups = (E + kWarp - 1) / kWarp;
         int base = 0;
-        for (int i = 0; i < groups; ++i) {
-            if (lane == 0) to[i] = base;
-            const int at = i * kWarp + lane;
-            base += static_cast<int>(__reduce_add_sync(0xffffffffu, at < E ? (rows_of(at) + kTileM - 1) / kTileM : 0));
+        for (int i0 = 0; i0 < groups; i0 += kAhead) {
+            int n[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int at = (i0 + i) * kWarp + lane;
+                n[i] = at < E ? (rows_of(at) + kTileM - 1) / kTileM : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (lane == 0 && i0 + i < groups) to[i0 + i] = base;
+                base += static_cast<int>(__reduce_add_sync(0xffffffffu, n[i]));
+            }
         }
         if (lane == 0) to[groups] = base;
     }

@@ -134,7 +134,7 @@ template <Bf16Form kForm>
 struct Tiles {
     static constexpr bool kWgrad = kForm == Bf16Form::kWgrad;
     const Params& p;
-    RowTiles<kTileRows> walk;
+    RowTiles<kTileRows, kForm == Bf16Form::kSwiglu> walk;
     int blocks = 2;  // of a tile (1: a tile is one block, the two accumulators take turns)
 
     __device__ __forceinline__ Tile at(int t) {
@@ -151,7 +151,7 @@ struct Tiles {
             const RowTile w = walk.at(t);
             r.e = w.e;
             r.m0 = w.m0;
-            r.rows = min(w.rows, kTileRows);
+            r.rows = w.rows;
             r.b0 = 0;
             if (kForm == Bf16Form::kSwiglu) {
                 r.a0 = w.col * kBlock;
@@ -228,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and weights are complete from here on
     griddep_launch_dependents();
-    Tiles<kForm> list{p, RowTiles<kTileRows>{p.g.count, s->first, p.g.E, p.g.cap}};
+    Tiles<kForm> list{p, RowTiles<kTileRows, kSwiglu>{p.g.count, s->first, p.g.E, p.g.cap}};
     if (!kWgrad && warp == 1) list.walk.fill(s->first, lane);
     tc_fence_before();
     __syncthreads();

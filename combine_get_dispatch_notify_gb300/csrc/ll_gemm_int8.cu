@@ -213,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 4) tmem_alloc_pair(&s->tmem, kTmemColumns);
     griddep_wait();  // counts, rows and scales are complete from here on
     griddep_launch_dependents();
-    RowTiles<kTileRows> walk{p.g.count, s->first, p.g.E, p.g.cap};
+    RowTiles<kTileRows, false> walk{p.g.count, s->first, p.g.E, p.g.cap};
     if (warp == 1) walk.fill(s->first, lane);
     tc_fence_before();
     __syncthreads();
@@ -233,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // tile.  Either way unit number 2 i + g, in the order of the loads, is the i-th of group g.
     const uint32_t steps = tiles > pair ? static_cast<uint32_t>((tiles - pair + pairs - 1) / pairs) * p.kb : 0;
     // rows of a tile as the tensor cores take them
-    const auto width = [&](const RowTile& t) { return (min(t.rows, kTileRows) + 31) / 32 * 32; };
+    const auto width = [&](const RowTile& t) { return (t.rows + 31) / 32 * 32; };
 
     if (warp < 4) regs_down<40>();
     if (warp == 0) {
@@ -462,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const long long r0 = static_cast<long long>(tl.e) * p.g.cap + tl.m0;
             const float* ws = p.g.w_scales + static_cast<long long>(tl.e) * (kSwiglu ? 2 : 1) * p.g.n + col;
             const float s0 = on ? __ldg(ws) : 0.0f, s1 = on && kSwiglu ? __ldg(ws + p.g.n) : 0.0f;
-            const int rows = min(tl.rows, kTileRows);
+            const int rows = tl.rows;
             float scale[kTileRows / 32];  // of row 32 i + lane
 #pragma unroll
             for (int c = 0; c < kTileRows; c += 32) scale[c / 32] = c + lane < rows ? __ldg(p.g.a_scales + r0 + c + lane) : 0.0f;

@@ -1,5 +1,5 @@
 // Walk over the tiles of ragged experts: experts in order, then tiles of rows,
-// then tiles of columns.  For kernels whose tile height is kTileM for every expert.
+// then tiles of columns.
 #pragma once
 
 #include <cstdint>
@@ -12,12 +12,17 @@ namespace ep {
 constexpr int kRowGroups = 8192 / kWarp;  // most groups of 32 experts
 
 struct RowTile {
-    int e, m0, col, rows;  // expert, first row, tile of columns, valid rows of the expert from m0 on
+    int e, m0, col, rows;  // expert, first row, tile of columns, rows
 };
 
 // `first` (shared memory, kRowGroups + 2 words) holds the tiles of rows before each group of 32 experts; a walk goes on
 // from the expert of its last tile.
-template <int kTileM>
+//
+// An expert's tiles have kTileM rows and its last one the rest, or (kEven) all of them about as many, in steps of 32.  A last
+// tile of a few rows is bound by its weights' bytes and costs half of a whole one; even tiles have more bytes a row all of them.
+// 32 experts, 7168 / 2048, about 512 rows each (1024), half of the experts with a few more: gated 586 us evenly, 625 not
+// (1153, 1151), but the rows' gradient 665 and 607 (1322, 1184), the last product 320 and 310 (663, 622).
+template <int kTileM, bool kEven>
 struct RowTiles {
     const int32_t* count;
     const int* first;
@@ -59,16 +64,16 @@ struct RowTiles {
             e = group * kWarp;
             before = first[group];
         }
-        int rows;
+        int rows, n;
         for (;;) {
             rows = rows_of(e);
-            const int n = (rows + kTileM - 1) / kTileM;
+            n = (rows + kTileM - 1) / kTileM;
             if (before + n > want) break;
             before += n;
             ++e;
         }
-        const int m0 = (want - before) * kTileM;
-        return RowTile{e, m0, t - want * tiles_n, rows - m0};
+        const int height = kEven ? ((rows + n - 1) / n + 31) / 32 * 32 : kTileM, m0 = (want - before) * height;
+        return RowTile{e, m0, t - want * tiles_n, min(height, rows - m0)};
     }
 };
 

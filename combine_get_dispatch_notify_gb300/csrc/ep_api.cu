@@ -244,7 +244,7 @@ bool gemm_shape_bf16_ok(const ep_gemm_shape_t* s) {
 // written all the same.
 ep_status_t ll_gemm_bf16(const ep_gemm_shape_t* s, Bf16Form form, const uint16_t* rows, const uint16_t* other,
                          const uint16_t* gate_up, const int32_t* count, void* out, uint16_t* gate_up_out, bool out_bf16,
-                         int32_t* status, cudaStream_t stream) {
+                         int32_t* status, cudaStream_t stream, const PairStall& stall = PairStall()) {
     if (!gemm_shape_bf16_ok(s)) return EP_ERR_INVALID_ARG;
     const bool wgrad = form == Bf16Form::kWgrad;
     const long long cap_rows = static_cast<long long>(s->num_experts) * s->capacity;
@@ -255,7 +255,7 @@ ep_status_t ll_gemm_bf16(const ep_gemm_shape_t* s, Bf16Form form, const uint16_t
         return EP_ERR_INVALID_ARG;
     if (cap_rows == 0 && !wgrad) return EP_OK;
     return from_cuda(launch_ll_gemm_bf16(Bf16GemmArgs{form, s->num_experts, s->capacity, s->n, s->k, rows, other, gate_up,
-                                                      count, out, gate_up_out, out_bf16, status},
+                                                      count, out, gate_up_out, out_bf16, status, stall},
                                          stream));
 }
 
@@ -266,7 +266,8 @@ size_t swiglu_int8_workspace(const ep_gemm_shape_t* s) {
 // Checks shared by the two int8 products; `halves` is 2 when w holds a gate and an up matrix.
 ep_status_t ll_gemm_int8(const ep_gemm_shape_t* s, int halves, const int8_t* a, const float* a_scales, const int8_t* w,
                          const float* w_scales, const int32_t* count, void* y, float* y_scales, void* workspace,
-                         size_t workspace_bytes, int32_t* status, cudaStream_t stream) {
+                         size_t workspace_bytes, int32_t* status, cudaStream_t stream,
+                         const PairStall& stall = PairStall()) {
     if (!gemm_shape_ok(s, halves == 2 ? 16 : 8)) return EP_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(s->num_experts) * s->capacity;
     if (!array_ok(a, rows, 16) || !array_ok(a_scales, rows, 16) || !aligned16(w) || !aligned16(w_scales) ||
@@ -278,7 +279,7 @@ ep_status_t ll_gemm_int8(const ep_gemm_shape_t* s, int halves, const int8_t* a, 
     if (rows == 0) return EP_OK;
     return from_cuda(launch_ll_gemm_int8(Int8GemmArgs{s->num_experts, s->capacity, s->n, s->k, a, a_scales, w, w_scales,
                                                       count, y, halves == 2 ? y_scales : nullptr,
-                                                      static_cast<float*>(workspace), status},
+                                                      static_cast<float*>(workspace), status, stall},
                                          stream));
 }
 
@@ -996,6 +997,30 @@ ep_status_t ep_ll_gemm_swiglu_int8(const ep_gemm_shape_t* shape, const int8_t* a
                                    cudaStream_t stream) {
     return ep::ll_gemm_int8(shape, 2, a, a_scales, w, w_scales, count, y, y_scales, workspace, workspace_bytes, status,
                             stream);
+}
+
+ep_status_t ep_debug_ll_gemm_bf16_stall(const ep_gemm_shape_t* shape, int32_t form, const uint16_t* rows,
+                                        const uint16_t* other, const uint16_t* gate_up, const int32_t* count, void* out,
+                                        uint16_t* gate_up_out, int32_t* status, int32_t stall_pair, int32_t stall_tile,
+                                        int32_t wait_limit_us, cudaStream_t stream) {
+    if (form < 0 || form > 5 || stall_pair < -1 || stall_tile < 0 || stall_tile > (1 << 20) || wait_limit_us < 1 ||
+        wait_limit_us > 2000000 || (form != 1 && gate_up_out != nullptr))
+        return EP_ERR_INVALID_ARG;
+    const ep::Bf16Form forms[6] = {ep::Bf16Form::kPlain,   ep::Bf16Form::kSwiglu, ep::Bf16Form::kDgrad,
+                                   ep::Bf16Form::kDswiglu, ep::Bf16Form::kWgrad,  ep::Bf16Form::kWgrad};
+    return ep::ll_gemm_bf16(shape, forms[form], rows, other, gate_up, count, out, gate_up_out, form != 4, status, stream,
+                            ep::PairStall{wait_limit_us, stall_pair, stall_tile});
+}
+
+ep_status_t ep_debug_ll_gemm_int8_stall(const ep_gemm_shape_t* shape, const int8_t* a, const float* a_scales,
+                                        const int8_t* w, const float* w_scales, const int32_t* count, void* y,
+                                        float* y_scales, void* workspace, size_t workspace_bytes, int32_t* status,
+                                        int32_t stall_pair, int32_t stall_tile, int32_t wait_limit_us,
+                                        cudaStream_t stream) {
+    if (stall_pair < -1 || stall_tile < 0 || stall_tile > (1 << 20) || wait_limit_us < 1 || wait_limit_us > 2000000)
+        return EP_ERR_INVALID_ARG;
+    return ep::ll_gemm_int8(shape, y_scales != nullptr ? 2 : 1, a, a_scales, w, w_scales, count, y, y_scales, workspace,
+                            workspace_bytes, status, stream, ep::PairStall{wait_limit_us, stall_pair, stall_tile});
 }
 
 ep_status_t ep_sync_status(const int32_t* status, cudaStream_t stream) {

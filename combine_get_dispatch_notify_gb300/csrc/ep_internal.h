@@ -193,6 +193,13 @@ cudaError_t launch_ll_dispatch_int8(const Shape& sh, const uint16_t* x, const in
                                     const int32_t* slot_pos, int cap, int8_t* recv_x, float* recv_x_scales,
                                     int32_t* recv_src_info, int32_t* status, cudaStream_t stream);
 
+// Testing hook of the experts' bf16 and int8 products: a limit for every device wait, and a pair of CTAs fed no products
+// from that tile of its own on.
+struct PairStall {
+    int wait_limit_us = 2000000;
+    int pair = -1, tile = 0;
+};
+
 // Experts' bf16 products (see ep_ll_gemm_bf16 and its neighbours for the forms).
 enum class Bf16Form { kPlain, kSwiglu, kDgrad, kDswiglu, kWgrad };
 struct Bf16GemmArgs {
@@ -206,6 +213,7 @@ struct Bf16GemmArgs {
     uint16_t* gate_up_out;  // kSwiglu, may be NULL
     bool out_bf16;      // kWgrad
     int32_t* status;
+    PairStall stall;
 };
 cudaError_t launch_ll_gemm_bf16(const Bf16GemmArgs& g, cudaStream_t stream);
 
@@ -222,6 +230,7 @@ struct Int8GemmArgs {
     float* y_scales;
     float* h;
     int32_t* status;
+    PairStall stall;
 };
 cudaError_t launch_ll_gemm_int8(const Int8GemmArgs& g, cudaStream_t stream);
 

@@ -88,7 +88,7 @@ struct Shared {
 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
-    return gemm::wait_for<false>(bar, parity, w);
+    return gemm::wait_for<true>(bar, parity, w);  // the limit is read only once a wait is slow
 }
 // At cluster scope: what another CTA's threads wrote before they arrived is visible.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Waits* w) {
@@ -96,7 +96,7 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Wai
     do {
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait_cluster(bar, parity)) return true;
-    } while (globaltimer_ns() - start < gemm::kWaitLimitNs);
+    } while (globaltimer_ns() - start < w->limit_us * 1000LL);
     *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
     return false;
 }
@@ -219,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kEpilogueWarps; ++i)
             for (int j = 0; j < 2; ++j) mbar_init(&s->loaded[i][j], 1);
-        s->waits = Waits{0, 0};
+        s->waits = Waits{0, p.g.stall.wait_limit_us};
         fence_mbarrier_init();
         prefetch_tensormap(&map_a);
         prefetch_tensormap(&map_b);
@@ -305,6 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
                 const Tile tl = list.at(t);
+                if (pair == p.g.stall.pair && i >= p.g.stall.tile) break;  // testing hook
                 const int stages = __shfl_sync(0xffffffffu, list.stages(tl), 0);
                 const int in_stage = __shfl_sync(0xffffffffu, list.in_stage(tl), 0);
                 if (stages == 0) continue;

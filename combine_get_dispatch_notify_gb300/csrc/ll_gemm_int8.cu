@@ -96,7 +96,7 @@ struct Shared {
 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
-    return gemm::wait_for<false>(bar, parity, w);
+    return gemm::wait_for<true>(bar, parity, w);  // the limit is read only once a wait is slow
 }
 // At cluster scope: what another CTA's threads wrote before they arrived is visible.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Waits* w) {
@@ -104,7 +104,7 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Wai
     do {
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait_cluster(bar, parity)) return true;
-    } while (globaltimer_ns() - start < gemm::kWaitLimitNs);
+    } while (globaltimer_ns() - start < w->limit_us * 1000LL);
     *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
     return false;
 }
@@ -205,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&s->acc_full[i], 1);
             mbar_init(&s->acc_empty[i], kSwiglu ? 2 * kEpilogueWarps : kEpilogueWarps);  // of the pair
         }
-        s->waits = Waits{0, 0};
+        s->waits = Waits{0, p.g.stall.wait_limit_us};
         fence_mbarrier_init();
         prefetch_tensormap(&map_w);
         prefetch_tensormap(&map_a);
@@ -290,6 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t batch = 0, it = 0;  // batches of rows and steps so far
             bool ok = true;
             for (uint32_t t = pair, i = 0; t < static_cast<uint32_t>(tiles) && ok; t += pairs, ++i) {
+                if (pair == p.g.stall.pair && static_cast<int>(i) >= p.g.stall.tile) break;  // testing hook
                 const int n = __shfl_sync(0xffffffffu, width(walk.at(t)), 0), in_batch = kBatchStages * S::stage_steps(n);
                 const uint32_t idesc = f16_idesc(kBlock, n), step_bytes = kBatchBytes / in_batch;
                 const uint32_t acc = blocks == 2 ? half : i & 1, before = blocks == 2 ? i : i / 2;  // its tiles before this one

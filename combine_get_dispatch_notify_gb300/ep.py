@@ -128,6 +128,8 @@ _SIGS = {
     "ep_ll_gemm_int8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 7 + [_vp]),
     "ep_ll_gemm_swiglu_int8_workspace_bytes": (_sz, [ctypes.POINTER(EpGemmShape)]),
     "ep_ll_gemm_swiglu_int8": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_sz, _vp, _vp]),
+    "ep_debug_ll_gemm_bf16_stall": (_i32, [ctypes.POINTER(EpGemmShape), _i32] + [_vp] * 7 + [_i32] * 3 + [_vp]),
+    "ep_debug_ll_gemm_int8_stall": (_i32, [ctypes.POINTER(EpGemmShape)] + [_vp] * 8 + [_sz, _vp] + [_i32] * 3 + [_vp]),
     "ep_sync_status": (_i32, [_vp, _vp]),
     "ep_debug_notify_dispatch_stall": (_i32, [ctypes.POINTER(EpShape)] + [_vp] * 16 +
                                        [_sz, _vp, _i32, _i32, _vp]),
@@ -812,6 +814,45 @@ def ep_ll_gemm_swiglu_int8(a, a_scales, w, w_scales, count, y, y_scales, workspa
     _check("ep_ll_gemm_swiglu_int8",
            lib().ep_ll_gemm_swiglu_int8(ctypes.byref(shape), *args, ws, nws, _t(status, torch.int32, (1,), "status"),
                                         _stream(stream)))
+
+
+def ep_debug_ll_gemm_bf16_stall(form: int, n: int, k: int, rows, other, gate_up, count, out, gate_up_out, status,
+                                stall_pair: int, stall_tile: int, wait_limit_us: int, stream=None) -> None:
+    """Testing hook: the bf16 product of ``form`` (0 plain, 1 gated, 2 rows' gradient, 3 gradient
+    through the activation, 4 and 5 weights' gradient in fp32 and bf16) of weights [n, k] with one
+    pair of CTAs fed no products from its tile ``stall_tile`` on and every device wait bounded by
+    ``wait_limit_us``; the status word then reports a timeout and the context stays usable."""
+    bf16 = torch.bfloat16
+    E, cap = rows.shape[:2]
+    wgrad, halves = form in (4, 5), form == 3
+    out_dim = {0: n, 1: n, 2: k, 3: k}.get(form)
+    other_shape = (E, cap, k) if wgrad else (E, 2, n, k) if form == 1 else (E, n, k)
+    out_shape = (E, n, k) if wgrad else (E, cap, 2, out_dim) if halves else (E, cap, out_dim)
+    args = (_i32(form), _t(rows, bf16, (E, cap, k if form < 2 else n), "rows"), _t(other, bf16, other_shape, "other"),
+            _t(gate_up, bf16, (E, cap, 2, k), "gate_up", nullable=not halves), _t(count, torch.int32, (E,), "count"),
+            _t(out, torch.float32 if form == 4 else bf16, out_shape, "out"),
+            _t(gate_up_out, bf16, (E, cap, 2, n), "gate_up_out", nullable=True), _t(status, torch.int32, (1,), "status"),
+            _i32(stall_pair), _i32(stall_tile), _i32(wait_limit_us))
+    _check("ep_debug_ll_gemm_bf16_stall",
+           lib().ep_debug_ll_gemm_bf16_stall(ctypes.byref(EpGemmShape(E, cap, n, k)), *args, _stream(stream)))
+
+
+def ep_debug_ll_gemm_int8_stall(a, a_scales, w, w_scales, count, y, y_scales, workspace, status, stall_pair: int,
+                                stall_tile: int, wait_limit_us: int, stream=None) -> None:
+    """Testing hook: :func:`ep_ll_gemm_swiglu_int8` (:func:`ep_ll_gemm_int8` where ``y_scales`` is
+    None) stalled as in :func:`ep_debug_ll_gemm_bf16_stall`."""
+    gated = y_scales is not None
+    E, cap, n, k = _gemm_dims(a, w, 4 if gated else 3)
+    two = (2,) if gated else ()
+    shape = EpGemmShape(E, cap, n, k)
+    ws, nws = _workspace(workspace, ep_ll_gemm_swiglu_int8_workspace_bytes(shape)) if gated else (None, _sz(0))
+    rc = lib().ep_debug_ll_gemm_int8_stall(
+        ctypes.byref(shape), _t(a, torch.int8, (E, cap, k), "a"), _t(a_scales, torch.float32, (E, cap), "a_scales"),
+        _t(w, torch.int8, (E, *two, n, k), "w"), _t(w_scales, torch.float32, (E, *two, n), "w_scales"),
+        _t(count, torch.int32, (E,), "count"), _t(y, torch.int8 if gated else torch.bfloat16, (E, cap, n), "y"),
+        _t(y_scales, torch.float32, (E, cap), "y_scales", nullable=True), ws, nws, _t(status, torch.int32, (1,), "status"),
+        _i32(stall_pair), _i32(stall_tile), _i32(wait_limit_us), _stream(stream))
+    _check("ep_debug_ll_gemm_int8_stall", rc)
 
 
 def ep_sync_status(status, stream=None) -> int:

@@ -910,6 +910,29 @@ ep_status_t ep_debug_ll_gemm_fp8_stall(const ep_gemm_shape_t* shape, const uint8
                                        float* y_scales, int32_t* status, int32_t stall_cta, int32_t stall_tile,
                                        int32_t wait_limit_us, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Testing hooks for failure detection in the experts' bf16 and int8 products:
+ * the calls with every device wait bounded by `wait_limit_us` microseconds (1 ..
+ * 2e6) and the tensor cores of pair of CTAs `stall_pair` (-1: none) left without
+ * products from its tile number `stall_tile` (0 .. 2^20) on.  Whatever waits
+ * for those products gives up, sets EP_DEV_TIMEOUT and exits, so the context stays
+ * usable.  A pair without that many tiles finishes normally.  Output
+ * contents are undefined after a stalled run.
+ *   form  0 ep_ll_gemm_bf16, 1 ep_ll_gemm_swiglu_bf16, 2 ep_ll_gemm_dgrad_bf16,
+ *         3 ep_ll_gemm_dswiglu_bf16, 4 ep_ll_gemm_wgrad_bf16 into fp32, 5 into bf16;
+ *         rows is that call's first array, other its weights (4, 5: a)
+ *   y_scales  NULL: ep_ll_gemm_int8, else ep_ll_gemm_swiglu_int8
+ */
+ep_status_t ep_debug_ll_gemm_bf16_stall(const ep_gemm_shape_t* shape, int32_t form, const uint16_t* rows,
+                                        const uint16_t* other, const uint16_t* gate_up, const int32_t* count, void* out,
+                                        uint16_t* gate_up_out, int32_t* status, int32_t stall_pair, int32_t stall_tile,
+                                        int32_t wait_limit_us, cudaStream_t stream);
+ep_status_t ep_debug_ll_gemm_int8_stall(const ep_gemm_shape_t* shape, const int8_t* a, const float* a_scales,
+                                        const int8_t* w, const float* w_scales, const int32_t* count, void* y,
+                                        float* y_scales, void* workspace, size_t workspace_bytes, int32_t* status,
+                                        int32_t stall_pair, int32_t stall_tile, int32_t wait_limit_us,
+                                        cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -173,3 +173,22 @@ def test_channel_cast():
     assert int(q.abs().max()) == 127 and (q[0, 1, 5] == 0).all() and float(s[0, 1, 5]) > 0
     # half a step, and the roundings of scale and quotient
     assert ((q.double() * s.double().unsqueeze(-1) - w.double()).abs() <= s.double().unsqueeze(-1) * (0.5 + 2.0 ** -15)).all()
+
+
+def test_stall_hooks_refuse_bad_arguments(ep):
+    L, inv = ep.lib(), ep.EP_ERR_INVALID_ARG
+    good = ctypes.byref(ep.EpGemmShape(2, 4, 16, 32))
+    bf16 = lambda form, p, *stall: L.ep_debug_ll_gemm_bf16_stall(good, form, *p, *stall, vp(0))  # noqa: E731
+    p = [FAKE, FAKE, FAKE, FAKE, FAKE2, NUL, FAKE]  # rows, other, gate_up, count, out, gate_up_out, status
+    i8 = lambda p, *stall: L.ep_debug_ll_gemm_int8_stall(good, *p[:8], 1 << 20, p[8], *stall, vp(0))  # noqa: E731
+    q = [FAKE] * 9
+    for stall in ((-2, 0, 1000), (0, -1, 1000), (0, (1 << 20) + 1, 1000), (0, 0, 0), (0, 0, 2000001)):
+        assert bf16(0, p, *stall) == inv and i8(q, *stall) == inv
+    for form in (-1, 6):
+        assert bf16(form, p, 0, 0, 1000) == inv
+    assert bf16(0, p[:5] + [FAKE] + p[6:], 0, 0, 1000) == inv  # only the gated product has a second output
+    assert bf16(3, p[:2] + [NUL] + p[3:], 0, 0, 1000) == inv
+    for i in (0, 1, 3, 4, 6):
+        assert bf16(0, p[:i] + [NUL] + p[i + 1:], 0, 0, 1000) == inv
+    for i in (0, 1, 2, 3, 4, 5, 7, 8):
+        assert i8(q[:i] + [NUL] + q[i + 1:], 0, 0, 1000) == inv

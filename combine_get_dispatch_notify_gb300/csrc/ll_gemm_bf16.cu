@@ -215,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], kSwiglu ? 2 * kEpilogueWarps : kEpilogueWarps);  // of the pair
+            mbar_init(&s->acc_empty[i], kSwiglu || kDswiglu ? 2 * kEpilogueWarps : kEpilogueWarps);  // of the pair
         }
         for (int i = 0; i < kEpilogueWarps; ++i)
             for (int j = 0; j < 2; ++j) mbar_init(&s->loaded[i][j], 1);
@@ -394,9 +394,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t buf = smem_addr(s_out + (warp - 4) * kBufBytes);
         uint32_t acc_phase = 0;
         bool ok = true;
+        // kDswiglu: a tile of one block is shared by all eight warps, so where a block has four of its own they arrive twice
+        const bool shared = kDswiglu && list.blocks == 1;
         const auto hand_back = [&](int h) {
             tc_fence_before();
             if (lane == 0) mbar_arrive_cluster_relaxed(empty + h * 8);
+            if (kDswiglu && !shared && lane == 0) mbar_arrive_cluster_relaxed(empty + h * 8);
         };
         if (kWgrad) {
             // thread = one output row
@@ -527,8 +530,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t loads = 0;  // kDswiglu: boxes of gate and up asked for
             for (int t = pair, i = 0; t < tiles && ok; t += pairs, ++i) {
                 const Tile tl = list.at(t);
-                const int block = kSwiglu ? 0 : block_of(tl, list.blocks, i, half);
+                const int block = kSwiglu || shared ? 0 : block_of(tl, list.blocks, i, half);
                 if (block < 0) continue;
+                const int acc = shared ? i & 1 : half;
                 const int col = tl.a0 + block * kBlock + static_cast<int>(rank) * kHalf + quarter * kWarp;
                 const bool on = col < p.out_n;
                 const auto load = [&](int c) {  // kDswiglu: gate and up of the rows from c on, into the next set of buffers
@@ -543,15 +547,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                               smem_addr(&s->loaded[warp - 4][set]));
                     }
                 };
-                if (kDswiglu && on) load(0);
-                ok = wait_for(&s->acc_full[half], acc_phase, &s->waits);
+                // kDswiglu: the boxes of 32 rows that this warp has (shared: in turn for the two warps of a quarter), the first two
+                // asked for ahead
+                const int first = shared ? half * kOutRows : 0, stride = shared ? 2 * kOutRows : kOutRows;
+                uint32_t now = loads;
+                if (kDswiglu && on && first < tl.rows) {
+                    load(first);
+                    if (first + stride < tl.rows) load(first + stride);
+                }
+                ok = wait_for(&s->acc_full[acc], shared ? i >> 1 & 1 : acc_phase, &s->waits);
                 if (kSwiglu) ok = ok && wait_for(&s->acc_full[half ^ 1], acc_phase, &s->waits);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 acc_phase ^= 1;
                 tc_fence_after();
-                if (!on) {
-                    hand_back(half);
+                if (!on || (kDswiglu && first >= tl.rows)) {
+                    hand_back(acc);
                     if (kSwiglu) hand_back(half ^ 1);
                     continue;
                 }
@@ -580,13 +591,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     hand_back(1);
                 } else if (kDswiglu) {
 #pragma unroll 1
-                    for (int c = 0; c < tl.rows; c += kOutRows) {
-                        const uint32_t now = loads - 1;  // this box's number
-                        if (c + kOutRows < tl.rows) load(c + kOutRows);
+                    for (int c = first; c < tl.rows; c += stride, ++now) {
+                        if (c > first && c + stride < tl.rows) load(c + stride);
                         const uint32_t box = buf + (now & 1) * 2 * kOutBytes;
                         uint64_t x[16];
-                        tmem_read_matrices(lanes + half * kTileRows + c, x);
-                        if (c + kOutRows >= tl.rows) hand_back(half);
+                        tmem_read_matrices(lanes + acc * kTileRows + c, x);
+                        if (c + stride >= tl.rows) hand_back(acc);
                         ok = __all_sync(0xffffffffu, wait_for(&s->loaded[warp - 4][now & 1], now >> 1 & 1, &s->waits));
                         if (!ok) break;
 #pragma unroll

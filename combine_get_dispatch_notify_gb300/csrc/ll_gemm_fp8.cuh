@@ -65,6 +65,22 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* 
     return wait_slow<kStall>(bar, parity, w);
 }
 
+// The same in few instructions, for kernels with many waits (unrolled, the two loops above made up two thirds of such a one,
+// and a short call fetches all of it): the limit is read only once a wait is slow.
+__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, Waits* w) {
+    long long start = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (i % 64 != 0) continue;
+        const long long now = globaltimer_ns();
+        if (start == 0) start = now;
+        if (now - start > w->limit_us * 1000LL) break;
+    }
+    *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
+    return false;
+}
+
 // The tiles of a kernel: experts in order, then row tiles, then weight tiles.
 // `first` holds the tiles before each group of 32 experts; a role walks on
 // from the expert of its last tile.

@@ -20,8 +20,8 @@
 //
 // Measured, 32 experts with about 1024 rows each: gated, 7168 -> 2 x 2048, 1280 to 1310 us with the cast, plain,
 // 2048 -> 7168, 617 to 646 (1.47 to 1.56 PFLOP/s; tensor pipe about 60 % busy, half of the issue slots: the chain from bytes
-// through TMEM to the tensor cores bounds it).  64 experts with about 64 rows: 361 to 369 and 178 us, 5.1 to 5.3
-// TB/s of weights.  8 experts with one row: 64 and 41 us, of which some 25 and 20 do not grow with k.
+// through TMEM to the tensor cores bounds it).  64 experts with 64 rows: 338 and 157 us, 5.6 and 6.0 TB/s of weights.
+// 8 experts with one row, in a captured graph: 46 and 27 us, of which 12 (5 of them the cast) and 7 at k = 128.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -96,7 +96,7 @@ struct Shared {
 };
 
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Waits* w) {
-    return gemm::wait_for<true>(bar, parity, w);  // the limit is read only once a wait is slow
+    return gemm::wait_small(bar, parity, w);
 }
 // At cluster scope: what another CTA's threads wrote before they arrived is visible.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Waits* w) {
@@ -418,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int line = lane; line < lines; line += kWarp) {
                     const int step = in_stage == 1 ? 0 : line / mine, row = line - step * mine;
                     const uint32_t to = slot + step * step_bytes + row * 128;
-#pragma unroll
+#pragma unroll (kTileRows == 64 ? 2 : 8)
                     for (int j = 0; j < 8; ++j) {  // 16 values; steps are whole groups of eight rows apart, so `line` swizzles as `row`
                         const uint4 x = row_piece(from, line, j);
                         uint32_t v[8];
@@ -477,31 +477,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             acc_phase ^= 1;
             tc_fence_after();
             if (kSwiglu) {
-                // 32 rows at a time, in turn for the two warps of a quarter
+                // 32 rows at a time, in turn for the two warps of a quarter.  Short calls find none of their instructions on the SM:
+                // few rows go through a small loop (8 experts with one row, both products in turn 78 -> 73 us; 1024 rows 1332 -> 1429)
+                constexpr int kPart = kTileRows == 64 ? 8 : 32;
 #pragma unroll 1
                 for (int c = half * 32; c < kTileRows; c += 64) {
-                    const bool last = c + 64 >= kTileRows;
-                    uint64_t x[16], y[16];
-                    if (c < rows) {
-                        tmem_read(lanes + c, x);
-                        tmem_read(lanes + kTileRows + c, y);
-                    }
-                    if (last) {
-                        hand_back(0);
-                        hand_back(1);
-                    }
-                    if (c >= rows) continue;
                     float of_rows = scale[0];  // the scales of these rows
 #pragma unroll
                     for (int k = 1; k < kTileRows / 32; ++k)
                         if (c == 32 * k) of_rows = scale[k];
-                    float* to = p.g.h + (r0 + c) * p.g.n + col;
+#pragma unroll 1
+                    for (int part = 0; part < 32; part += kPart) {
+                        const int r = c + part;
+                        uint64_t x[kPart / 2], y[kPart / 2];
+                        if (r < rows) tmem_read2(lanes + r, lanes + kTileRows + r, x, y);
+                        if (c + 64 >= kTileRows && part + kPart == 32) {
+                            hand_back(0);
+                            hand_back(1);
+                        }
+                        if (r >= rows) continue;
+                        float* to = p.g.h + (r0 + r) * p.g.n + col;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float as = __shfl_sync(0xffffffffu, of_rows, j);
-                        const float2 a = unpack2(x[j / 2]), b = unpack2(y[j / 2]);
-                        const float gate = (j & 1 ? a.y : a.x) * (as * s0), up = (j & 1 ? b.y : b.x) * (as * s1);
-                        if (on && c + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit<false>(gate, up);
+                        for (int j = 0; j < kPart; ++j) {
+                            const float as = __shfl_sync(0xffffffffu, of_rows, part + j);
+                            const float2 a = unpack2(x[j / 2]), b = unpack2(y[j / 2]);
+                            const float gate = (j & 1 ? a.y : a.x) * (as * s0), up = (j & 1 ? b.y : b.x) * (as * s1);
+                            if (on && r + j < rows) to[static_cast<long long>(j) * p.g.n] = gated_unit<false>(gate, up);
+                        }
                     }
                 }
             } else {

@@ -138,6 +138,25 @@ __device__ __forceinline__ void tmem_read(uint32_t addr, uint64_t (&x)[8]) {
         : "memory");
 }
 
+// As many columns from each of two places.
+__device__ __forceinline__ void tmem_read2(uint32_t addr0, uint32_t addr1, uint64_t (&x)[4], uint64_t (&y)[4]) {
+    asm volatile(
+        "{\n\t.reg .b32 r<16>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {r0, r1, r2, r3, r4, r5, r6, r7}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {r8, r9, r10, r11, r12, r13, r14, r15}, [%9];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {r0, r1}; mov.b64 %1, {r2, r3}; mov.b64 %2, {r4, r5}; mov.b64 %3, {r6, r7};\n\t"
+        "mov.b64 %4, {r8, r9}; mov.b64 %5, {r10, r11}; mov.b64 %6, {r12, r13}; mov.b64 %7, {r14, r15};\n\t"
+        "}"
+        : "=l"(x[0]), "=l"(x[1]), "=l"(x[2]), "=l"(x[3]), "=l"(y[0]), "=l"(y[1]), "=l"(y[2]), "=l"(y[3])
+        : "r"(addr0), "r"(addr1)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_read2(uint32_t addr0, uint32_t addr1, uint64_t (&x)[16], uint64_t (&y)[16]) {
+    tmem_read(addr0, x);
+    tmem_read(addr1, y);
+}
+
 // 16 columns from each of two places, as 8 pairs each.
 __device__ __forceinline__ void tmem_read16x2(uint32_t addr0, uint32_t addr1, uint64_t (&x)[8], uint64_t (&y)[8]) {
     asm volatile(

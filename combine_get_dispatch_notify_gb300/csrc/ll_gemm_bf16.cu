@@ -233,7 +233,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     griddep_wait();  // counts, rows and weights are complete from here on
     griddep_launch_dependents();
     Tiles<kForm> list{p, RowTiles<kTileRows, kSwiglu>{p.g.count, s->first, p.g.E, p.g.cap}};
-    if (!kWgrad && warp == 1) list.walk.fill(s->first, lane);
+    const int columns = (p.out_n + kBlock - 1) / kBlock;
+    if (!kWgrad && warp == 1) list.walk.fill(s->first, lane, columns, pairs);
     tc_fence_before();
     __syncthreads();
     cluster_wait_acquire();
@@ -241,7 +242,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s->tmem;
     int tiles = p.g.E * p.tiles_m * p.tiles_n;
     if (!kWgrad) {
-        const int row_tiles = list.walk.row_tiles(), columns = (p.out_n + kBlock - 1) / kBlock;
+        list.walk.start();
+        const int row_tiles = list.walk.row_tiles();
         if (!kSwiglu) list.blocks = blocks_of_tiles(row_tiles, columns, pairs);
         list.walk.tiles_n = kSwiglu ? columns : (columns + list.blocks - 1) / list.blocks;
         tiles = row_tiles * list.walk.tiles_n;
@@ -709,7 +711,7 @@ cudaError_t launch(const Bf16GemmArgs& g, cudaStream_t stream) {
     const size_t smem = 1024 + (wide ? 3 : 4) * kStageBytes + kEpilogueWarps * (wide ? 4 : 2) * kOutBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
     const long long most = static_cast<long long>(g.E) *
-                           (kWgrad ? p.tiles_m * p.tiles_n : over(g.cap, kTileRows) * over(p.out_n, kBlock));
+                           (kWgrad ? p.tiles_m * p.tiles_n : over(g.cap, kTileRows / 2) * over(p.out_n, kBlock));
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
     return launch_pdl(ll_gemm_bf16_kernel<kForm, kOut16>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, a, b, b16,
                       out, gate_up, p);

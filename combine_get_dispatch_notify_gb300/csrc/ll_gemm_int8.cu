@@ -218,13 +218,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     griddep_wait();  // counts, rows and scales are complete from here on
     griddep_launch_dependents();
     RowTiles<kTileRows, false> walk{p.g.count, s->first, p.g.E, p.g.cap};
-    if (warp == 1) walk.fill(s->first, lane);
+    const int columns = (p.g.n + kBlock - 1) / kBlock;
+    if (warp == 1) walk.fill(s->first, lane, columns, pairs);
     tc_fence_before();
     __syncthreads();
     cluster_wait_acquire();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
-    const int columns = (p.g.n + kBlock - 1) / kBlock, row_tiles = walk.row_tiles();
+    walk.start();
+    const int row_tiles = walk.row_tiles();
     const int blocks = kSwiglu ? 2 : blocks_of_tiles(row_tiles, columns, pairs);
     walk.tiles_n = kSwiglu ? columns : (columns + blocks - 1) / blocks;
     const int tiles = row_tiles * walk.tiles_n;
@@ -622,7 +624,7 @@ cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + S::kStages * kWeightBytes + kRowStages * S::kRowBytes + kRowSlots * S::kBatchBytes + sizeof(Shared);
     // an upper bound of the tiles: the counts are on the device
-    const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows - 1) / kTileRows) * ((g.n + kBlock - 1) / kBlock);
+    const long long most = static_cast<long long>(g.E) * ((g.cap + kTileRows / 2 - 1) / (kTileRows / 2)) * ((g.n + kBlock - 1) / kBlock);
     const int pairs = static_cast<int>(most < sms / 2 ? most : sms / 2);
     return launch_pdl(ll_gemm_int8_kernel<kSwiglu, kTileRows>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, w, a, a16, p);
 }

@@ -35,6 +35,8 @@ SHAPES = {
     "counts_past_the_capacity": (64, 64, 10, [11, 1 << 30, -1, -(1 << 31), 10]),
     "all_empty": (48, 40, 16, [0, 0, 0]),
     "many_experts": (24, 40, 9, [i % 10 for i in range(300)]),
+    "many_tiles_of_all_sizes": (264, 72, 300, [255, 256, 257, 300, 31, 33, 129, 0] * 20),
+    "many_longer_experts": (24, 40, 140, [i * 7 % 141 for i in range(300)]),
     "more_tiles_than_sms": (1032, 64, 520, [520] * 24),
 }
 

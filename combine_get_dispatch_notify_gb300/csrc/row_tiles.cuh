@@ -20,8 +20,9 @@ struct RowTile {
 //
 // Tiles have kTileM rows, or half as many where that takes no more rounds of tiles.  With few tiles an expert of many rows is
 // what a call waits for, and its halves go to two places: 24 experts by Zipf popularity (220, 126, 112 rows and fewer),
-// 1160 / 520, bf16: gradient through the activation 22.6 -> 14.7 us, rows' gradient 19.6 -> 15.0, gated 19.9 -> 15.4, last
-// product 12.9 -> 10.0.  With more rounds every row of weights would be read twice as often.
+// 1160 / 520, bf16: gradient through the activation 22.6 -> 16.0 us, rows' gradient 19.6 -> 16.3, gated 19.9 -> 15.7, last
+// product 12.9 -> 10.8.  16 experts with 200 rows, 2048 / 1024, where it takes more: last product 19.0 -> 24.4, rows' gradient 33 -> 46.
+// Two experts with 256 rows, 7168 / 2048: gated 68 -> 59, but gradient through the activation 48 -> 58.
 //
 // An expert's last tile has the rest of its rows, or (kEven) all of its tiles about as many, in steps of 32.  A last
 // tile of a few rows is bound by its weights' bytes and costs half of a whole one; even tiles have more bytes a row all of them.

@@ -84,6 +84,7 @@ struct Shared {
     uint64_t loaded[kEpilogueWarps][2];  // kDswiglu: gate and up are in the warp's buffers
     int first[kRowGroups + 2];     // tiles before each group of 32 experts
     uint32_t tmem;
+    uint32_t asked;  // kWgrad: stages that this CTA's producer has asked for so far
     Waits waits;
 };
 
@@ -97,6 +98,25 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Wai
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait_cluster(bar, parity)) return true;
     } while (globaltimer_ns() - start < w->limit_us * 1000LL);
+    *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
+    return false;
+}
+
+// For waits that may be for something many tiles ahead, which take as long as the call does: the limit is for the time in which
+// the CTA's ring stands still, and begins again with every stage that its producer has asked for.
+__device__ __forceinline__ bool wait_while_moving(uint64_t* bar, uint32_t parity, Waits* w, const uint32_t* asked) {
+    long long start = 0;
+    uint32_t seen = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (i % 64 != 0) continue;
+        const long long now = globaltimer_ns();
+        const uint32_t moved = *reinterpret_cast<const volatile uint32_t*>(asked);
+        if (start == 0 || moved != seen) start = now;
+        seen = moved;
+        if (now - start > w->limit_us * 1000LL) break;
+    }
     *reinterpret_cast<volatile int*>(&w->ran_out) = 1;
     return false;
 }
@@ -219,6 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kEpilogueWarps; ++i)
             for (int j = 0; j < 2; ++j) mbar_init(&s->loaded[i][j], 1);
+        s->asked = 0;
         s->waits = Waits{0, p.g.stall.wait_limit_us};
         fence_mbarrier_init();
         prefetch_tensormap(&map_a);
@@ -254,6 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (warp == 0 && lane == 0) {
             // ---- producer ----
             Ring<kStages> st(1);  // a fresh barrier passes a wait for phase 1
+            uint32_t asked = 0;
             bool ok = true;
             const uint32_t full = mapa(smem_addr(&s->full[0]), 0);
             for (int t = pair; t < tiles && ok; t += pairs) {
@@ -296,6 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < n / 2; i += kChunk) tma_load_3d(tb + i * 128, &map_b16, c, b0 + i, tl.e, bar);
                         }
                     }
+                    if (kWgrad) *reinterpret_cast<volatile uint32_t*>(&s->asked) = ++asked;
                     st.next();
                 }
             }
@@ -363,7 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 3 && kWgrad) {
-            // ---- relay: the step that ends an expert's rows, zeroed behind the last of them ----
+            // ---- relay: the step that ends an expert's rows, zeroed behind the last of them.  Experts whose rows end with 16 are
+            // passed over, so the next such step may be the call's last ----
             Ring<kStages> st(0);
             uint32_t phases = 0;  // of the landed barriers, a bit each
             bool ok = true;
@@ -372,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int stages = list.stages(tl), left = tl.rows - (stages - 1) * kBlockK;
                 if (tl.rows % 16 != 0) {
                     st.skip(stages - 1);
-                    ok = __all_sync(0xffffffffu, wait_for(&s->landed[st.at], phases >> st.at & 1, &s->waits));
+                    ok = __all_sync(0xffffffffu, wait_while_moving(&s->landed[st.at], phases >> st.at & 1, &s->waits, &s->asked));
                     if (!ok) break;
                     phases ^= 1u << st.at;
                     uint8_t* to = s_tiles + st.at * kStageBytes;
@@ -431,7 +455,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (block < 0) continue;
                 const bool any = tl.rows > 0;  // without rows the gradient is 0 and the tensor cores have nothing
                 if (any) {
-                    ok = __all_sync(0xffffffffu, wait_for(&s->acc_full[half], acc_phase, &s->waits));
+                    // the second accumulator may have been passed over for as many tiles as there are columns of them
+                    ok = __all_sync(0xffffffffu, wait_while_moving(&s->acc_full[half], acc_phase, &s->waits, &s->asked));
                     if (!ok) break;
                     acc_phase ^= 1;
                     tc_fence_after();

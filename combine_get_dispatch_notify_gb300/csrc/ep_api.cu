@@ -183,6 +183,25 @@ bool array_ok(const void* p, long long n, unsigned align) {
     return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (align - 1u)) == 0;
 }
 
+// An array by its place, for the calls whose outputs may not overlap: their kernels still read an input, or another output's
+// neighbours, when the first results are written.
+struct Array {
+    const void* p;
+    long long bytes;
+};
+bool overlap(const Array& a, const Array& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// The first `outputs` arrays overlap none of the others.
+template <int kArrays>
+bool outputs_apart(const Array (&arrays)[kArrays], int outputs) {
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < kArrays; ++j)
+            if (overlap(arrays[i], arrays[j])) return false;
+    return true;
+}
+
 ep_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
 
 bool make_route(const Shape& sh, const ep_route_t* r, RouteCfg* out) {
@@ -250,10 +269,21 @@ ep_status_t ll_gemm_bf16(const ep_gemm_shape_t* s, Bf16Form form, const uint16_t
     const long long cap_rows = static_cast<long long>(s->num_experts) * s->capacity;
     if (!array_ok(rows, cap_rows, 16) || !array_ok(other, wgrad ? cap_rows : 1, 16) || !aligned4(count) ||
         !array_ok(out, wgrad ? 1 : cap_rows, 16) || (gate_up_out != nullptr && !aligned16(gate_up_out)) ||
-        (form == Bf16Form::kDswiglu && (!array_ok(gate_up, cap_rows, 16) || (gate_up == out && cap_rows > 0))) ||
-        !aligned4(status))
+        (form == Bf16Form::kDswiglu && !array_ok(gate_up, cap_rows, 16)) || !aligned4(status))
         return EP_ERR_INVALID_ARG;
     if (cap_rows == 0 && !wgrad) return EP_OK;
+    // columns of the rows, of the output and, where there is one, of the other array with two halves
+    const bool forward = form == Bf16Form::kPlain || form == Bf16Form::kSwiglu;
+    const long long n = s->n, k = s->k, weights = s->num_experts * n * k * 2, row = 2 * cap_rows;
+    const Array arrays[] = {
+        {out, wgrad ? (out_bf16 ? weights : 2 * weights) : row * (forward ? n : form == Bf16Form::kDswiglu ? 2 * k : k)},
+        {status, 4},
+        {gate_up_out, row * 2 * n},
+        {rows, row * (forward ? k : n)},
+        {other, wgrad ? row * k : form == Bf16Form::kSwiglu ? 2 * weights : weights},
+        {form == Bf16Form::kDswiglu ? gate_up : nullptr, row * 2 * k},
+        {count, s->num_experts * 4LL}};
+    if (!outputs_apart(arrays, 3)) return EP_ERR_INVALID_ARG;
     return from_cuda(launch_ll_gemm_bf16(Bf16GemmArgs{form, s->num_experts, s->capacity, s->n, s->k, rows, other, gate_up,
                                                       count, out, gate_up_out, out_bf16, status, stall},
                                          stream));
@@ -277,6 +307,17 @@ ep_status_t ll_gemm_int8(const ep_gemm_shape_t* s, int halves, const int8_t* a, 
                         workspace_bytes < swiglu_int8_workspace(s)))
         return EP_ERR_INVALID_ARG;
     if (rows == 0) return EP_OK;
+    const long long n = s->n, k = s->k, weights = s->num_experts * n * k * halves;
+    const Array arrays[] = {{y, rows * n * (halves == 2 ? 1 : 2)},
+                            {status, 4},
+                            {halves == 2 ? y_scales : nullptr, rows * 4},
+                            {halves == 2 ? workspace : nullptr, rows * n * 4},
+                            {a, rows * k},
+                            {a_scales, rows * 4},
+                            {w, weights},
+                            {w_scales, s->num_experts * n * halves * 4},
+                            {count, s->num_experts * 4LL}};
+    if (!outputs_apart(arrays, 4)) return EP_ERR_INVALID_ARG;
     return from_cuda(launch_ll_gemm_int8(Int8GemmArgs{s->num_experts, s->capacity, s->n, s->k, a, a_scales, w, w_scales,
                                                       count, y, halves == 2 ? y_scales : nullptr,
                                                       static_cast<float*>(workspace), status, stall},
@@ -924,6 +965,10 @@ ep_status_t ep_ll_combine_backward(const ep_shape_t* shape, const uint16_t* grad
         !ep::array_ok(grad_topk_w, tokens, 4) || !ep::aligned4(status))
         return EP_ERR_INVALID_ARG;
     if (tokens == 0) return EP_OK;
+    const long long H = sh.H, slots = tokens * sh.K;
+    const ep::Array arrays[] = {{grad_y, rows * H * 2},  {grad_topk_w, slots * 4}, {status, 4},   {grad_combined, tokens * H * 2},
+                                {y, rows * H * 2},       {topk_idx, slots * 8},    {topk_w, slots * 4}, {slot_pos, slots * 4}};
+    if (!ep::outputs_apart(arrays, 3)) return EP_ERR_INVALID_ARG;
     return ep::from_cuda(ep::launch_ll_combine_backward(sh, grad_combined, y, expert_capacity, topk_idx, topk_w, slot_pos,
                                                         grad_y, grad_topk_w, status, stream));
 }

@@ -665,6 +665,7 @@ ep_status_t ep_ll_gemm_swiglu_fp8(const ep_gemm_shape_t* shape, const uint8_t* a
  *   grad_topk_w      out fp32 [R][T][K], every element written (0 for a slot without a row)
  * A slot with an id or position past its range sets EP_DEV_INCONSISTENT and
  * counts as one without a row.  Slots hold rows of their own (ep_ll_layout's do).
+ * Outputs that overlap an input or each other (grad_y in the place of y) are EP_ERR_INVALID_ARG.
  */
 ep_status_t ep_ll_combine_backward(const ep_shape_t* shape, const uint16_t* grad_combined, const uint16_t* y,
                                    int32_t expert_capacity, const int64_t* topk_idx, const float* topk_w,
@@ -683,6 +684,10 @@ ep_status_t ep_ll_combine_backward(const ep_shape_t* shape, const uint16_t* grad
  * num_experts * capacity below 2^31, and capacity * n, capacity * k and n * k
  * below 2^38.  A device wait that runs out sets EP_DEV_TIMEOUT (the outputs are
  * then unspecified).
+ *
+ * Outputs may overlap no input and not each other, because results are written while other
+ * columns of the same rows are still to be read: gradients in the place of what they are
+ * made from are EP_ERR_INVALID_ARG (where the capacity is not 0).
  */
 
 /* EP_OK when `shape` obeys the rules above, else EP_ERR_INVALID_ARG. */
@@ -725,7 +730,7 @@ ep_status_t ep_ll_gemm_dgrad_bf16(const ep_gemm_shape_t* shape, const uint16_t* 
  *   grad_y        in  bf16 bits [num_experts][capacity][n]
  *   w             in  bf16 bits [num_experts][n][k]  (the block's last matrix)
  *   gate_up       in  bf16 bits [num_experts][capacity][2][k]  of ep_ll_gemm_swiglu_bf16
- *   grad_gate_up  out bf16 bits [num_experts][capacity][2][k]; may not be gate_up
+ *   grad_gate_up  out bf16 bits [num_experts][capacity][2][k]
  */
 ep_status_t ep_ll_gemm_dswiglu_bf16(const ep_gemm_shape_t* shape, const uint16_t* grad_y, const uint16_t* w,
                                     const uint16_t* gate_up, const int32_t* count, uint16_t* grad_gate_up,
@@ -771,7 +776,8 @@ ep_status_t ep_ll_dispatch_int8(const ep_shape_t* shape, const uint16_t* x, cons
  * The sum is held in fp32, which is exact while it stays within 2^24 (so for k
  * <= 1024 always), and rounds like any fp32 sum beyond.  Rows behind an
  * expert's count and experts without rows as for ep_ll_gemm_fp8; shapes obey
- * ep_check_gemm_shape.
+ * ep_check_gemm_shape.  Outputs and the workspace may overlap no input and not each
+ * other: EP_ERR_INVALID_ARG (where the capacity is not 0).
  *
  * ep_ll_gemm_int8: y = bf16(p)
  *   a         in  int8 [num_experts][capacity][k]

@@ -1092,6 +1092,12 @@ class MoETrainLayer:
         (fp32 or bf16, the weights' shapes), every element of them."""
         sh, cap, F = self.shape, self.expert_capacity, self.ffn
         E, H = sh.num_experts, sh.hidden
+        # views with another order of the same sizes would hide a wrong shape from the calls; and nothing is launched for one
+        bf16 = torch.bfloat16
+        _t(w13, bf16, (E, 2, F, H), "w13")
+        _t(w2, bf16, (E, H, F), "w2")
+        for t, shape, name in ((grad_w13, (E, 2, F, H), "grad_w13"), (grad_w2, (E, H, F), "grad_w2")):
+            _t(t, bf16 if t is not None and t.dtype == bf16 else torch.float32, shape, name)
         ep_ll_combine_backward(sh, grad_out, self.y, cap, self.topk_idx, self.topk_w, self.slot_pos, self.grad_y,
                                self.grad_topk_w, self.status, stream)
         ep_route_backward(sh, self.route, logits, self.topk_idx, self.grad_topk_w, grad_logits, self.status, stream)

@@ -11,7 +11,7 @@
 // longer is read a second time for its cast.  The cast row goes through shared
 // memory and from there to every slot by one bulk copy each (16-byte stores by every
 // thread: 416 us where this takes 383).  2048 tokens x 7168 to 8 slots take 31 us, 32768 tokens
-// 383 us (6.1 TB/s, 91 % of the copy rate).
+// 376 to 383 us (6.1 to 6.3 TB/s, 91 to 93 % of the copy rate).
 #include <cstdint>
 #include <cuda_runtime.h>
 

@@ -23,13 +23,20 @@
 // step of 64: its last 16 rows are then zeroed behind them in shared memory, in both
 // operands, because what lies there may be a NaN.
 //
-// Bound by the tensor cores where experts have hundreds of rows (gated, 32 experts with 1024 rows
-// each, 7168 -> 2 x 2048: 1031 to 1048 us in a burst, 1.84 to 1.87 PFLOP/s; its loads alone take 653, its
-// products without most of the loads 895), by the weights' bytes where they have few (8 experts with one row: 75 us,
-// 6.3 TB/s, 94 with the launch).  In the same bursts: rows' gradient 1008 to 1050 us, weight gradient in
-// bf16 1057 to 1090, last product 549 to 564.  Rows that are not a multiple of 256 cost more than
+// The tensor cores' fp32 sums come out short, as if what lies below a sum's last bit were cut off and not rounded: of n terms
+// by about n 2^-30 of their magnitude (weight gradients of normal values, fp32, error against 64 bits: 4.7e-7 at 512 rows, 2.1e-6
+// at 2048, 9.1e-6 at 8192, 3.8e-5 at 32768; the library's bf16 product gives the same).  A result in bf16 is rounded far more;
+// fp32 gradients of long experts carry that error, because a second sum beside the first would take the room that the second
+// block of a tile has.
+//
+// Bound by the tensor cores where experts have hundreds of rows, by the weights' bytes where they have few.  One call by itself
+// with its launch, caches emptied before it, 32 experts with exactly 1024 rows, 7168 / 2048 (the longer times where the calls
+// before brought the card to its power limit): gated 1026 to 1048 us (1.84 to 1.88 PFLOP/s; its loads alone take 653, its
+// products without most of the loads 895), last product 549 to 564 (1.71 to 1.75), gradient through the activation 630 to 648
+// (1.49 to 1.53), rows' gradient 1008 to 1087 (1.77 to 1.91), weight gradient in bf16 1057 to 1260 (1.53 to 1.82).  Rows that are not a multiple of 256 cost more than
 // their share, because an expert's last tile reads all of its weights again: about 1024 rows, half of
-// the experts with a few more, 1151 to 1174 us.
+// the experts with a few more, gated 1145 to 1199 us.  8 experts with one row: gated 74 us in a captured graph (6.4 TB/s), last
+// product 38 (6.1); by themselves with their launches 94 and 55, and 113 to 117 the two of them among other calls.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -479,8 +486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kTileRows / kCols; ++c) store(v[c], tl.b0 + c * kCols, y, tl.e);
                 } else {
                     // From registers to memory: through shared memory, which the operands keep busy, 32 experts x 512 rows, 4096
-                    // x 7168, took 1020 us.  Two neighbouring lanes trade pairs of columns, so that each stores 16 bytes and
-                    // the four lanes of a row 64 in a line.
+                    // x 7168, took 1020 us, so 932.  Products and stores add up all the same (0.84 us a row and 500 us; the stores' bytes
+                    // alone take 555), since both accumulators fill together and are handed back with their last columns.  Two
+                    // neighbouring lanes trade pairs of columns, so that each stores 16 bytes and the four lanes of a row 64 in a line.
                     float* out = static_cast<float*>(p.g.out) + (static_cast<long long>(tl.e) * p.g.n + y + lane / 4) * p.g.k;
 #pragma unroll 2
                     for (int c = 0; c < kTileRows; c += 32) {

@@ -7,7 +7,8 @@
 // bytes cross memory as int8 and become fp16 on the SM: weights in registers on their way
 // into TMEM, from where they are the tensor cores' first operand, an expert's rows on
 // their way from one place of shared memory to another.  Products are exact and sums are
-// fp32: exact too as long as they stay within 2^24.  A byte b becomes a number without a
+// fp32: exact too as long as they stay within 2^24, and beyond that short by a few parts in
+// 10^6 at k = 7168, as the tensor cores add (ll_gemm_bf16.cu).  A byte b becomes a number without a
 // conversion instruction: b + 128 in the low bits of 1024 makes the fp16 number 1152 + b.
 //
 // A pair of CTAs (one cluster, two SMs) owns a tile of two blocks of 256 weight
@@ -18,10 +19,12 @@
 // are the gate and the up matrix.  Its activations leave as fp32, because the scale of a row
 // is known once the row is complete; a second kernel casts them.
 //
-// Measured, 32 experts with about 1024 rows each: gated, 7168 -> 2 x 2048, 1280 to 1310 us with the cast, plain,
-// 2048 -> 7168, 617 to 646 (1.47 to 1.56 PFLOP/s; tensor pipe about 60 % busy, half of the issue slots: the chain from bytes
-// through TMEM to the tensor cores bounds it).  64 experts with 64 rows: 338 and 157 us, 5.6 and 6.0 TB/s of weights.
-// 8 experts with one row, in a captured graph: 46 and 27 us, of which 12 (5 of them the cast) and 7 at k = 128.
+// Measured, gated (7168 -> 2 x 2048, with the cast) and plain (2048 -> 7168).  One call by itself with its launch, caches
+// emptied before it: 32 experts with about 1024 rows 1270 and 587 us (1.51 and 1.64 PFLOP/s; tensor pipe 65 % busy, more than
+// half of the issue slots: the chain from bytes through TMEM to the tensor cores bounds it); 64 experts with about 64 rows 360
+// and 177 us, 5.2 and 5.3 TB/s of weights; 8 experts with one row 62 and 41.  Both of them one after the other: 1926 to 1958 us,
+// and 1975 to 2072 in long runs, where the power limit takes the clock from 2070 to 1940 MHz; 516 to 526; 75 to 77.  8 experts
+// with one row in a captured graph: 46 and 27 us, of which 12 (5 of them the cast) and 7 at k = 128.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -629,7 +632,11 @@ cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
     return launch_pdl(ll_gemm_int8_kernel<kSwiglu, kTileRows>, dim3(2 * pairs), dim3(kThreads), smem, stream, 0, true, w, a, a16, p);
 }
 
-// Tiles of 64 rows where no expert can have more.
+// Tiles of 64 rows where no expert can have more.  The host knows the capacity, not the rows, and a kernel's shared memory and
+// TMEM are laid out for its tiles.  So few rows in buffers of a larger capacity go through tiles of 128, with fewer
+// weights in flight and the epilogue of many rows: one row to each of 8 experts, both products, 75 us at a capacity of 16, 77 at
+// 64, 85 at 72, 87 at 128 (16 tokens of 32 experts: 237, 239, 252, 254), and 101 (269) at 1280, where the cast also
+// passes over 40960 rows' places.
 template <bool kSwiglu>
 cudaError_t launch(const Int8GemmArgs& g, cudaStream_t stream) {
     return g.cap <= 64 ? launch<kSwiglu, 64>(g, stream) : launch<kSwiglu, 128>(g, stream);
